@@ -12,6 +12,13 @@
  * dspark_schedule_pack and dspark_verify_scatter produce the same results as the two pairs of
  * calls with fewer kernel launches; dspark_observe accumulates calibration counters.
  *
+ * Between pack and verify the target model runs over the packed rows. Its operators that must
+ * know about ragged windows are here too:
+ *
+ *   dspark_append    the rows' keys and values -> rotated, quantised, into a paged 8-bit cache
+ *   dspark_attend    the rows' queries -> attention over that cache
+ *   dspark_rotate    rotary positions over rows of heads, and their inverse
+ *
  * Source of the method: "DSpark in SGLang: Speculative Decoding with Confidence-Driven,
  * Variable-Length Verification" (LMSYS blog, as summarised by papercache.org), sections
  * "A2 method details" (confidence scheduler, verify modes, ragged verify over full CUDA graphs,
@@ -75,12 +82,17 @@ extern "C" {
 #define DSPARK_STATUS_BAD_LENGTH     0x80 /* accept_len / out_len outside range: clamped         */
 #define DSPARK_STATUS_STALL         0x100 /* a bounded in-kernel wait gave up: this call's verify
                                              results are invalid (not expected in operation)   */
+#define DSPARK_STATUS_BAD_PAGE      0x200 /* a page id or block outside the cache: not stored, or
+                                             its tokens not attended to                        */
+#define DSPARK_STATUS_BAD_VALUE     0x400 /* a non-finite key or value: stored as 0              */
 
 /* ---- limits of the library ----------------------------------------------------------- */
 #define DSPARK_MAX_GAMMA        32     /* block width                                         */
 #define DSPARK_MAX_CANDIDATES   16384  /* B*(gamma-1): the scheduler sorts them in one CTA    */
 #define DSPARK_MAX_BATCH        8192   /* B for schedule and pack (single-CTA scans)          */
 #define DSPARK_MAX_TIERS        1024
+#define DSPARK_MAX_HEAD         1024   /* head size of dspark_rotate                          */
+#define DSPARK_MAX_CACHE_HEAD   256    /* head size of a cache, a multiple of 16              */
 
 typedef enum { DSPARK_BF16 = 0, DSPARK_F32 = 1 } dspark_dtype;
 
@@ -392,6 +404,145 @@ int dspark_verify_noalloc(dspark_mode mode, int stochastic,
                           uint64_t seed, uint64_t step, int32_t* accept_len, int32_t* committed,
                           int32_t* ceiling_len, float* row_prob, int32_t* status,
                           cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * dspark_rope — rotary positions. Pair j (of rot / 2) of a head turns by the angle
+ * position * f_j; turns[j] = f_j / (2 pi) * 2^64 is that frequency as a 64-bit fraction of a
+ * turn per position, so the angle modulo one turn is an exact integer product for every int32
+ * position. Elements past the first `rot` of a head are not rotated.
+ *   half layout (interleaved = 0):  pair j = elements (j, j + rot/2)
+ *   interleaved (interleaved = 1):  pair j = elements (2j, 2j + 1)
+ *   (a, b) -> mscale * (a cos - b sin, b cos + a sin)
+ * turns is a DEVICE array [rot/2], 8-byte aligned; the struct is read during the call only.
+ *
+ * dspark_rope_turns — fills a HOST array turns[rot/2] (a host function; copy it to the device
+ * once) with f_j = base^(-2j/rot), scaled for contexts longer than the trained one:
+ *   DSPARK_ROPE_PLAIN     f_j
+ *   DSPARK_ROPE_LINEAR    f_j / factor (every position divided)
+ *   DSPARK_ROPE_BY_PARTS  with r_j = trained * f_j / (2 pi) turns over the trained context and
+ *                         k = clamp((r_j - slow) / (fast - slow), 0, 1):
+ *                         (1 - k) f_j / factor + k f_j ("NTK-by-parts", Peng et al., "YaRN:
+ *                         Efficient Context Window Extension", 2023, which also sets
+ *                         mscale = 0.1 ln(factor) + 1)
+ * factor is read by the last two, trained / slow / fast by the last. Errors: rot odd or outside
+ * [0, DSPARK_MAX_HEAD], base <= 1, factor < 1, trained <= 0, slow < 0 or fast <= slow.
+ * ------------------------------------------------------------------------------------- */
+typedef struct {
+    const uint64_t* turns;
+    int32_t         rot;
+    int32_t         interleaved;
+    float           mscale;
+} dspark_rope;
+typedef enum { DSPARK_ROPE_PLAIN = 0, DSPARK_ROPE_LINEAR = 1, DSPARK_ROPE_BY_PARTS = 2 } dspark_rope_scaling;
+int dspark_rope_turns(int rot, double base, dspark_rope_scaling scaling, double factor,
+                      double trained, double slow, double fast, uint64_t* turns);
+
+/* ---------------------------------------------------------------------------------------
+ * dspark_rotate — y = x with every head of every row rotated by its row's position; inverse != 0
+ * turns by -position with the same mscale, which is the gradient with respect to x (and, for
+ * mscale 1, undoes the rotation). Products in fp32, one rounding to the type of y.
+ * Row r's head h starts at element r * stride + h * dim. y may be x (same stride: in place);
+ * otherwise the two must not overlap and y's unrotated elements are copied.
+ *
+ * x, y [rows, heads, dim] bf16 or fp32 (dtype) with row strides x_stride, y_stride >= heads*dim
+ * elements; positions [rows] int32, any value. Limits: rows >= 0, 1 <= dim <= DSPARK_MAX_HEAD.
+ * Sixteen-byte aligned rows with dim % 16 == 0 and rot % 16 == 0 take 16-byte accesses.
+ * ------------------------------------------------------------------------------------- */
+int dspark_rotate(const void* x, int64_t x_stride, void* y, int64_t y_stride, dspark_dtype dtype,
+                  int rows, int heads, int dim, const int32_t* positions,
+                  const dspark_rope* rope, int inverse, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * dspark_cache — keys and values of many requests in pages, 8 bits per element.
+ *   k, v       [n_pages, heads, page, dim]  e4m3 codes (1 sign, 4 exponent, 3 mantissa bits,
+ *                                           largest 448), 16-byte aligned
+ *   k_scale,
+ *   v_scale    [n_pages, heads] fp32, positive and finite: element = code * scale of its block
+ *              (a block is one page's slots of one head)
+ *   table      [B, width] int32: table[b, j] is the page of request b's tokens
+ *              j * page .. (j + 1) * page - 1
+ * page is 16, 32, 64 or 128 tokens; dim a multiple of 16 up to DSPARK_MAX_CACHE_HEAD. All
+ * pointers are DEVICE pointers; the struct is read during the call only.
+ *
+ * dspark_append — the packed rows' keys and values into the cache. Row r with
+ * b = row_req[r] >= 0 is token t = lengths[b] + row_pos[r] of request b: slot t % page of page
+ * table[b, t / page]. Its key is rotated at position t (rope NULL: not), its value is not.
+ * For every (block, K or V) that the call writes, with x the call's elements for it in fp32:
+ *   a non-finite element counts as 0 (DSPARK_STATUS_BAD_VALUE)
+ *   fresh  = the smallest power of two 2^e, e >= -64, with max|x| <= 448 * 2^e
+ *   scale  = fresh                       if the block's first written slot is slot 0
+ *            max(block's scale, fresh)   otherwise: the slots before it are retained tokens
+ *   retained codes := e4m3(code * (old scale / scale)); new codes := e4m3(x / scale), both
+ *   rounded to nearest even. Slots past the written ones keep their (stale) codes.
+ * So the rows of rejected drafts need no clean-up: the next step's rows overwrite them.
+ * lengths is not advanced; repeating a call repeats its result.
+ * q != NULL: the rows' queries [rows, q_heads, dim], rotated the same way, go to q_out (the same
+ * shape and type; q_out may be q), products in fp32, one rounding; q_out's rows without a
+ * request are left as they are.
+ *
+ * Rows are as dspark_pack writes them: a request's rows consecutive, row_pos 0, 1, 2, ...;
+ * row_req -1 is padding. No two requests of a call may write one page, and a page that is written
+ * must not be shared with another request.
+ * k, v [rows, heads, dim], bf16 or fp32 (dtype), row strides in elements as in dspark_rotate;
+ * row_req, row_pos [rows] int32; lengths [B] int32, tokens in the cache before this call's rows.
+ * A request or position out of range (row_req >= B, row_pos < 0) flags DSPARK_STATUS_BAD_ROWS, a
+ * length that is negative or passes int32 DSPARK_STATUS_BAD_LENGTH, a page id outside
+ * [0, n_pages) or a block >= width DSPARK_STATUS_BAD_PAGE; those rows are not stored.
+ * One kernel; a block belongs to one CTA: no atomics, the same bits every time.
+ * ------------------------------------------------------------------------------------- */
+typedef struct {
+    void*          k;
+    void*          v;
+    float*         k_scale;
+    float*         v_scale;
+    const int32_t* table;
+    int32_t        n_pages;
+    int32_t        heads;
+    int32_t        page;
+    int32_t        dim;
+    int32_t        width;
+} dspark_cache;
+int dspark_append(const dspark_cache* cache, const dspark_rope* rope, const void* k,
+                  int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                  int64_t q_stride, void* q_out, int64_t q_out_stride, int q_heads,
+                  dspark_dtype dtype, int rows, const int32_t* row_req, const int32_t* row_pos,
+                  const int32_t* lengths, int B, int32_t* status, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * dspark_attend — attention of the packed rows over the cache, after dspark_append stored their
+ * keys and values. Row cu_seqlens[b] + i of request b is at position p = lengths[b] + i and sees
+ * the tokens t of request b with t <= p and, window > 0, t > p - window. Query head h reads
+ * cache head h / (q_heads / heads).
+ *   s_t = scale * <q, K_t>,  out = sum_t exp(s_t) V_t / sum_t exp(s_t),  lse = ln sum_t exp(s_t)
+ * A row that sees nothing gets out = 0 and lse = -inf. Tokens in a page whose id lies outside
+ * [0, n_pages), or in a block >= width, are not seen (DSPARK_STATUS_BAD_PAGE); pages wholly
+ * before every row's window are not looked at (their entries may be stale). A negative length
+ * counts as 0 (DSPARK_STATUS_BAD_LENGTH); a request whose rows lie outside [0, rows) or run
+ * backwards gets nothing written (DSPARK_STATUS_BAD_ROWS). What stale slots hold, NaN codes
+ * included, does not matter; NaN codes in a token that some row of the call sees may reach
+ * every row of its request (dspark_append writes none).
+ * Rows at or past cu_seqlens[B] are not written.
+ *
+ * q, out [rows, q_heads, dim] bf16 or fp32 (dtype), row strides in elements >= q_heads * dim;
+ * cu_seqlens [B+1], lengths [B] int32 (the same lengths the append had); scale finite;
+ * lse [rows, q_heads] fp32 or NULL; status as everywhere. q_heads is a multiple of heads.
+ * workspace: at least dspark_attend_workspace_bytes(heads, dim) bytes of device scratch, 16-byte
+ * aligned, no clearing needed, rewritten by every call; calls that share it must not overlap.
+ *
+ * Precision: bf16 with dim 64 or 128 runs on the tensor cores, q as two e4m3 pieces (its eight
+ * mantissa bits exactly, down to 2^-17 of a row's largest element), the softmax weights as two
+ * pieces (relative error below 2^-8, 6e-4 rms: under bf16's own), sums in fp32. fp32, and other
+ * dims, run in fp32 throughout.
+ * ------------------------------------------------------------------------------------- */
+int dspark_attend(const dspark_cache* cache, const void* q, int64_t q_stride, void* out,
+                  int64_t out_stride, int q_heads, dspark_dtype dtype, int rows,
+                  const int32_t* cu_seqlens, const int32_t* lengths, int B, float scale,
+                  int window, float* lse, void* workspace, size_t workspace_bytes,
+                  int32_t* status, cudaStream_t stream);
+
+/* Bytes of device workspace dspark_attend needs; a value that depends on the sizes only. Returns
+ * 0 and sets dspark_last_error on invalid sizes. */
+size_t dspark_attend_workspace_bytes(int heads, int dim);
 
 /* Message of the last failed call on this host thread ("" if none). Never NULL. */
 const char* dspark_last_error(void);

@@ -8,5 +8,6 @@ package is the ctypes binding (`_binding`), the in-tree build (`build`), a buffe
 runner (`step`) and the seeded synthetic workloads (`synth`).
 """
 from ._binding import (BF16, CAP_ACCEPT, COMPACT, F32, MODES, STATIC, CostTable, DSparkError,  # noqa: F401
-                       dspark_pack, dspark_scatter, dspark_schedule, dspark_verify,
+                       PagedCache, Rope, dspark_append, dspark_attend,
+                       dspark_attend_workspace_bytes, dspark_pack, dspark_rotate, dspark_scatter, dspark_schedule, dspark_verify,
                        dspark_verify_workspace_bytes, last_error, lib, version)

@@ -28,6 +28,11 @@ STATUS_BAD_ROWS = 0x20
 STATUS_BAD_TOKEN = 0x40
 STATUS_BAD_LENGTH = 0x80
 STATUS_STALL = 0x100
+STATUS_BAD_PAGE = 0x200
+STATUS_BAD_VALUE = 0x400
+
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BY_PARTS = 0, 1, 2
+ROPE_SCALINGS = {"none": ROPE_PLAIN, "linear": ROPE_LINEAR, "by_parts": ROPE_BY_PARTS}
 
 STREAM_AUTO, STREAM_REGISTER, STREAM_BULK = 0, 1, 2
 
@@ -42,6 +47,8 @@ _LIB = None
 _p = ctypes.c_void_p
 _i = ctypes.c_int
 _u64 = ctypes.c_uint64
+_i64 = ctypes.c_int64
+_d = ctypes.c_double
 
 
 class DSparkError(RuntimeError):
@@ -53,6 +60,18 @@ class DSparkError(RuntimeError):
 class _Cost(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_double), ("alpha", ctypes.c_void_p), ("alpha_len", ctypes.c_int32),
                 ("theta", ctypes.c_void_p), ("theta_len", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("heads", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("width", ctypes.c_int32)]
 
 
 SYMBOLS = {
@@ -70,6 +89,13 @@ SYMBOLS = {
     "dspark_verify_noalloc": ([_i, _i, _p, _i, _p, _i, _i, _p, _p, _p, _i, _i, ctypes.c_float,
                                _u64, _u64, _p, _p, _p, _p, _p, _p], _i),
     "dspark_observe": ([_p, _p, _p, _i, _i, _i, _p, _p, _p, _p], _i),
+    "dspark_rope_turns": ([_i, _d, _i, _d, _d, _d, _d, _p], _i),
+    "dspark_rotate": ([_p, _i64, _p, _i64, _i, _i, _i, _i, _p, ctypes.POINTER(_Rope), _i, _p], _i),
+    "dspark_append": ([ctypes.POINTER(_Cache), ctypes.POINTER(_Rope), _p, _i64, _p, _i64, _p, _i64,
+                       _p, _i64, _i, _i, _i, _p, _p, _p, _i, _p, _p], _i),
+    "dspark_attend": ([ctypes.POINTER(_Cache), _p, _i64, _p, _i64, _i, _i, _i, _p, _p, _i,
+                       ctypes.c_float, _i, _p, _p, ctypes.c_size_t, _p, _p], _i),
+    "dspark_attend_workspace_bytes": ([_i, _i], ctypes.c_size_t),
     "dspark_graph_begin": ([_p], _i),
     "dspark_graph_end": ([_p, ctypes.POINTER(_p)], _i),
     "dspark_graph_launch": ([_p, _p], _i),
@@ -296,12 +322,12 @@ def dspark_verify_workspace_bytes(B: int, gamma: int, V: int, stochastic: bool) 
     return int(lib().dspark_verify_workspace_bytes(B, gamma, V, int(bool(stochastic))))
 
 
-def _dtype_code(t: torch.Tensor) -> int:
+def _dtype_code(t: torch.Tensor, name: str = "logits") -> int:
     if t.dtype == torch.bfloat16:
         return BF16
     if t.dtype == torch.float32:
         return F32
-    raise ValueError(f"logits must be bfloat16 or float32, got {t.dtype}")
+    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
 def _verify_args(mode, target, block_tokens, accept_len, committed, workspace, stochastic,
@@ -419,6 +445,170 @@ def utilisation(util) -> float:
     """Committed tokens over the acceptance ceiling, from dspark_observe's counters."""
     c, ceil = int(util[0]), int(util[1])
     return c / ceil if ceil else 0.0
+
+
+# ---- the target forward's ragged operators: rotary positions, paged cache, attention -------
+def rope_turns(rot: int, base: float = 10000.0, scaling="none", factor: float = 1.0,
+               trained: float = 1.0, slow: float = 1.0, fast: float = 32.0):
+    """dspark_rope_turns: the frequencies of rot / 2 pairs as 64-bit fractions of a turn per
+    position, a host array (numpy uint64) to copy to the device once (Rope does)."""
+    import numpy as np
+    code = ROPE_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    out = np.zeros(max(int(rot) // 2, 1), np.uint64)
+    _check("dspark_rope_turns",
+           lib().dspark_rope_turns(int(rot), float(base), code, float(factor), float(trained),
+                                   float(slow), float(fast), out.ctypes.data))
+    return out[:int(rot) // 2]
+
+
+class Rope:
+    """A rotation of the first 2 * len(turns) elements of every head: `turns` is an int64 (or
+    uint64) CUDA tensor of dspark_rope_turns' values, `mscale` the factor on cos and sin."""
+
+    def __init__(self, turns: torch.Tensor, mscale: float = 1.0, interleaved: bool = False):
+        if turns.dtype not in (torch.int64, torch.uint64):
+            raise ValueError(f"turns must be int64 or uint64, got {turns.dtype}")
+        self.turns = turns
+        self.mscale = float(mscale)
+        self.interleaved = bool(interleaved)
+        self._c = _Rope(_ptr(turns, "turns"), 2 * turns.numel(), int(interleaved), self.mscale)
+
+    @classmethod
+    def make(cls, rot: int, base: float = 10000.0, *, scaling="none", factor: float = 1.0,
+             trained: float = 1.0, slow: float = 1.0, fast: float = 32.0, mscale=None,
+             interleaved: bool = False, device="cuda"):
+        """The rope of these frequencies; mscale None: 0.1 ln(factor) + 1 by parts, else 1."""
+        import math
+        import numpy as np
+        turns = rope_turns(rot, base, scaling, factor, trained, slow, fast)
+        if mscale is None:
+            by_parts = scaling in ("by_parts", ROPE_BY_PARTS)
+            mscale = 0.1 * math.log(factor) + 1.0 if by_parts else 1.0
+        return cls(torch.as_tensor(turns.view(np.int64)).to(device), mscale, interleaved)
+
+    @property
+    def c(self):
+        return self._c
+
+
+class PagedCache:
+    """An 8-bit paged key/value cache (dspark_cache) over the caller's tensors: k and v
+    [n_pages, heads, page, dim] float8_e4m3fn (or uint8 codes), k_scale and v_scale
+    [n_pages, heads] float32, table [B, width] int32."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor, table: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must both be [n_pages, heads, page, dim]")
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise ValueError(f"{name} must be float8_e4m3fn or uint8, got {t.dtype}")
+        if table.dim() != 2:
+            raise ValueError("table must be [B, width]")
+        n, heads, page, dim = k.shape
+        self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
+        self.n_pages, self.heads, self.page, self.dim = n, heads, page, dim
+        self.B, self.width = table.shape
+        scales = dict(dtype=torch.float32, numel=n * heads)
+        self._c = _Cache(_ptr(k, "k"), _ptr(v, "v"), _ptr(k_scale, "k_scale", **scales),
+                         _ptr(v_scale, "v_scale", **scales), _ptr(table, "table", torch.int32),
+                         n, heads, page, dim, self.width)
+
+    @classmethod
+    def empty(cls, n_pages: int, heads: int, page: int, dim: int, table: torch.Tensor):
+        """A zeroed cache of n_pages pages on the table's device."""
+        dev = table.device
+        pages = [torch.zeros(n_pages, heads, page, dim, dtype=torch.uint8, device=dev)
+                 .view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.ones(n_pages, heads, dtype=torch.float32, device=dev) for _ in range(2)]
+        return cls(*pages, *scales, table)
+
+    @property
+    def c(self):
+        return self._c
+
+
+def _heads(t: torch.Tensor, name: str, dtype=None, rows=None, heads=None, dim=None):
+    """(pointer, row stride) of rows of heads: [rows, heads, dim], the heads of a row dense, rows
+    at any stride (a slice of a projection's output)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, dim]")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    r, h, d = t.shape
+    if (rows is not None and r != rows) or (heads is not None and h != heads) or \
+            (dim is not None and d != dim):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {dim}], got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    if r > 1 and s0 < h * d:
+        raise ValueError(f"{name}: rows overlap")
+    return ctypes.c_void_p(t.data_ptr()), s0 if r > 1 else h * d
+
+
+def dspark_rotate(x: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, rope: Rope, *,
+                  inverse: bool = False, stream=None, prepare: bool = False):
+    """y = x rotated by each row's position; inverse: rotated back, which is the gradient."""
+    xp, xs = _heads(x, "x")
+    rows, heads, dim = x.shape
+    yp, ys = _heads(y, "y", x.dtype, rows, heads, dim)
+    args = (xp, xs, yp, ys, _dtype_code(x, "x"), rows, heads, dim,
+            _ptr(positions, "positions", torch.int32, numel=rows, required=rows > 0),
+            ctypes.byref(rope.c), int(bool(inverse)), _stream(stream))
+    return _call("dspark_rotate", args, prepare)
+
+
+def dspark_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, row_req: torch.Tensor,
+                  row_pos: torch.Tensor, lengths: torch.Tensor, *, rope: Optional[Rope] = None,
+                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """The packed rows' keys (rotated) and values into the cache; q, if given, rotated to q_out."""
+    kp, ks = _heads(k, "k", None, None, cache.heads, cache.dim)
+    rows = k.shape[0]
+    vp, vs = _heads(v, "v", k.dtype, rows, cache.heads, cache.dim)
+    if (q is None) != (q_out is None):
+        raise ValueError("give both q and q_out or neither")
+    qp, qs, op, os_, hq = None, 0, None, 0, 0
+    if q is not None:
+        qp, qs = _heads(q, "q", k.dtype, rows, None, cache.dim)
+        hq = q.shape[1]
+        op, os_ = _heads(q_out, "q_out", k.dtype, rows, hq, cache.dim)
+    args = (ctypes.byref(cache.c), ctypes.byref(rope.c) if rope is not None else None,
+            kp, ks, vp, vs, qp, qs, op, os_, hq, _dtype_code(k, "k"), rows,
+            _ptr(row_req, "row_req", torch.int32, min_numel=rows, required=rows > 0),
+            _ptr(row_pos, "row_pos", torch.int32, min_numel=rows, required=rows > 0),
+            _ptr(lengths, "lengths", torch.int32, numel=cache.B), cache.B,
+            _ptr(status, "status", torch.int32, min_numel=1, required=False), _stream(stream))
+    return _call("dspark_append", args, prepare)
+
+
+def dspark_attend_workspace_bytes(heads: int, dim: int) -> int:
+    return int(lib().dspark_attend_workspace_bytes(int(heads), int(dim)))
+
+
+def dspark_attend(cache: PagedCache, q: torch.Tensor, out: torch.Tensor, cu_seqlens: torch.Tensor,
+                  lengths: torch.Tensor, workspace: torch.Tensor, *,
+                  scale: Optional[float] = None, window: int = 0,
+                  lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                  stream=None, prepare: bool = False):
+    """Attention of the packed rows over the cache; scale None: 1 / sqrt(dim); window 0: every
+    token up to the row's own."""
+    qp, qs = _heads(q, "q", None, None, None, cache.dim)
+    rows, hq, dim = q.shape
+    op, os_ = _heads(out, "out", q.dtype, rows, hq, dim)
+    if lengths.numel() != cache.B:
+        raise ValueError(f"lengths must have {cache.B} elements, got {lengths.numel()}")
+    args = (ctypes.byref(cache.c), qp, qs, op, os_, hq, _dtype_code(q, "q"), rows,
+            _ptr(cu_seqlens, "cu_seqlens", torch.int32, min_numel=cache.B + 1),
+            _ptr(lengths, "lengths", torch.int32), cache.B,
+            float(dim) ** -0.5 if scale is None else float(scale), int(window),
+            _ptr(lse, "lse", torch.float32, min_numel=rows * hq, required=False),
+            _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+            _ptr(status, "status", torch.int32, min_numel=1, required=False), _stream(stream))
+    return _call("dspark_attend", args, prepare)
 
 
 NOALLOC_SCRATCH_BYTES = 4 << 20
