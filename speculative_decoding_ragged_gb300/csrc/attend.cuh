@@ -33,6 +33,9 @@ __device__ __forceinline__ float max_nan(float a, float b)
 
 size_t attend_workspace_bytes(int dim);
 int launch_attend(const AttendCall& A, int dtype, cudaStream_t stream);
+// The tensor-core kernel: whether it serves a call, and its launch.
+bool attend_mma_serves(const AttendCall& A, int dtype);
+int launch_attend_mma(const AttendCall& A, cudaStream_t stream);
 
 // Request b's packed rows [row0, row0 + w) and its length, checked: w = 0 for one whose rows are
 // not within the buffer. *bits collects what was wrong.

@@ -186,10 +186,9 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(AttendCall A)
 
 }  // namespace
 
-size_t attend_workspace_bytes(int) { return 16; }
-
 int launch_attend(const AttendCall& A, int dtype, cudaStream_t stream)
 {
+    if (attend_mma_serves(A, dtype)) return launch_attend_mma(A, stream);
     auto kernel = dtype == DSPARK_BF16 ? attend_any_kernel<DSPARK_BF16> : attend_any_kernel<DSPARK_F32>;
     return launch_pdl("attend", kernel, dim3(static_cast<unsigned>(A.rows), static_cast<unsigned>(A.c.heads)),
                       dim3(kWarps * 32), 0, stream, A);

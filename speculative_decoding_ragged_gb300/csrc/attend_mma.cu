@@ -1,0 +1,1094 @@
+// attend_mma.cu — dspark_attend on the tensor cores: bf16 queries over the e4m3 cache, head
+// sizes 64 and 128.
+//
+// Mathematics. For a row r (one position, one query head) and tokens t with block scales ks, vs:
+//   x_t = log2(e) scale q.K_t + log2 vs_t,   w_t = 2^(x_t - m),   O = sum_t w_t Vcode_t,
+//   l = sum_t w_t / vs_t,   out = O / l,     lse = ln 2 (m + log2 l).
+// Putting the value's scale into the exponent makes every product of the value side a plain
+// product of codes, keeps w_t <= 1 whatever the blocks' scales, and costs nothing: it is the
+// addend of the multiply-add that scales the score.
+//
+// The cache stays in its 8 bits all the way into the tensor cores (kind::f8f6f4). What is not
+// 8-bit is split into e4m3 pieces that accumulate into the same fp32 sums: a bf16 query element
+// has 8 significant bits, an e4m3 piece 4, so two pieces (over a power of two per row) hold it
+// exactly down to 2^-17 of the row's largest; a weight in two pieces is within 2^-8 (6e-4 rms,
+// below the rounding of the bf16 result). Compared with widening K and V to 16 bits in shared
+// memory this needs no conversion of the cache and moves half the shared-memory bytes; the
+// second piece doubles the 8-bit products, which run at twice the 16-bit rate.
+//
+// Work. A unit is (request, cache head, 128 of its rows); its visible tokens come in tiles of
+// 128. All tiles of all units form one line, which the persistent grid (two CTAs per SM) cuts
+// into equal runs, so one long request and many short ones balance alike; every CTA computes the
+// cut from cu_seqlens and lengths on the device. A unit cut by a run's end leaves (m, l, O) parts
+// in the workspace that attend_join_kernel joins.
+//
+// A CTA: warp 4 loads pages with TMA (one box per page and K or V, swizzled), warp 5 issues the
+// products, warps 0-3 do the softmax with one TMEM lane (row) per thread. Rows are at most 128
+// lanes; a unit of at most 64 or 32 rows (decode and verify) puts 2 or 4 copies of them in the
+// lanes and each copy takes 1/2 or 1/4 of every tile's tokens, so all four warps share the
+// softmax; the copies' products write their own lanes only (the instruction's lane mask) and
+// join at the unit's end like parts.
+// The weights overlay the scores in TMEM: 128 + dim columns, so two CTAs fit and one's softmax
+// runs under the other's products.
+//
+// Bound: HBM for decode and verify (2 dim bytes per token and cache head; the products take
+// 1024 of about 1400 cycles that a tile's 32 KB take to arrive), for prompts the softmax's
+// instruction issue next to the products.
+#include <cuda.h>
+
+#include "attend.cuh"
+#include "rope.cuh"
+
+namespace dspark {
+namespace {
+
+constexpr int kTile = 128;                   // tokens per tile, rows per unit
+constexpr int kSoftThreads = 128;
+constexpr int kThreads = 192;
+constexpr int kMaxCtas = 304;                // parts the workspace holds: two CTAs on 152 SMs
+constexpr int kBlocks = kTile / 16;          // most blocks in a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -1e30f;              // a row's reference before it has seen a token
+// Weights are stored as 2^(x - m + kShift) where m may lag the true maximum by kLag: at most
+// 2^8.5 < 448, and a weight keeps two full pieces down to 2^-12 of the largest.
+constexpr float kShift = 6.0f;
+constexpr float kLag = 2.5f;
+constexpr long long kWaitCycles = 1ll << 31;
+
+// What the join needs to know of a CTA's run.
+struct RunMeta {
+    int64_t total;      // tiles of the whole call
+    int64_t unit_end;   // global tile where the cut unit ends
+    int cut;            // 1: the run's last unit starts here and continues in the next runs
+    int slot;           // the part it left here
+    int row0, rows;     // the unit's first packed row and its rows (position, head) ...
+    int flat0, head0;   // ... from this flat index, first query head
+};
+
+struct Workspace {
+    RunMeta* meta;      // [kMaxCtas]
+    float2* ml;         // [kMaxCtas][2][kTile]
+    float* o;           // [kMaxCtas][2][kTile][dim]
+};
+__host__ __device__ inline Workspace workspace_of(void* ws, int)
+{
+    char* p = static_cast<char*>(ws);
+    Workspace w;
+    w.meta = reinterpret_cast<RunMeta*>(p);
+    w.ml = reinterpret_cast<float2*>(p + kMaxCtas * sizeof(RunMeta));
+    w.o = reinterpret_cast<float*>(p + kMaxCtas * (sizeof(RunMeta) + 2 * kTile * sizeof(float2)));
+    return w;
+}
+
+// ---- PTX -----------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_addr(const void* p)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+// Bounded wait for the phase of this parity. Once any thread of the CTA has given up (about a
+// second), *stalled is set and every wait returns false, so that all roles leave their loops.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* stalled)
+{
+    if (mbar_try(bar, parity)) return true;
+    const long long deadline = clock64() + kWaitCycles;
+    while (!mbar_try(bar, parity)) {
+        if (*stalled) return false;
+        if (clock64() > deadline) { *stalled = 1; return false; }
+    }
+    return true;
+}
+// The same bound, but not cut short by another wait's end: for what is in flight.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, volatile int* stalled)
+{
+    const long long deadline = clock64() + kWaitCycles;
+    while (!mbar_try(bar, parity))
+        if (clock64() > deadline) { *stalled = 1; return; }
+}
+// A page's box of the [rows, dim] tensor of codes -> shared memory.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The barrier's arrival follows the completion of every product this thread issued before.
+__device__ __forceinline__ void tc_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 ::"r"(bar) : "memory");
+}
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem], lanes of quarter i untouched where off<i> is all ones.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                       uint32_t off0, uint32_t off1, uint32_t off2, uint32_t off3)
+{
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n"
+        "}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(off0), "r"(off1), "r"(off2),
+        "r"(off3) : "memory");
+}
+__device__ __forceinline__ void tc_ld32(uint32_t addr, float* x)
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const float* x)
+{
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// ---- the line of tiles ---------------------------------------------------------------------
+struct Shape {                   // a unit's visible tiles [a, z]
+    int a, z;
+};
+__device__ __forceinline__ Shape unit_tiles(const AttendCall& A, int w, int len, int qt)
+{
+    const int i0 = qt * kTile / A.group;
+    const int64_t last = min(static_cast<int64_t>(qt + 1) * kTile, static_cast<int64_t>(w) * A.group) - 1;
+    const int i1 = static_cast<int>(last / A.group);
+    const int p0 = len + i0;
+    const int lo = A.window > 0 && p0 >= A.window ? p0 - A.window + 1 : 0;
+    return {lo / kTile, (len + i1) / kTile};
+}
+__device__ __forceinline__ int row_tiles(const AttendCall& A, int w)
+{
+    return static_cast<int>((static_cast<int64_t>(w) * A.group + kTile - 1) / kTile);
+}
+__device__ __forceinline__ int64_t head_tiles(const AttendCall& A, int w, int len)
+{
+    int64_t n = 0;
+    const int nq = row_tiles(A, w);
+    for (int qt = 0; qt < nq; ++qt) {
+        const Shape s = unit_tiles(A, w, len, qt);
+        n += s.z - s.a + 1;
+    }
+    return n;
+}
+
+// The units of one run in order, the same in every role.
+struct Walk {
+    int b, h, qt, nq;
+    int row0, w, len;
+    int a, z, k0, n;             // the unit's tiles [a, z]; this piece: n tiles from k0
+    int64_t left;                // tiles of the run from this piece on
+
+    __device__ __forceinline__ void request(const AttendCall& A)
+    {
+        int bits = 0;
+        while (true) {           // the next request with rows; there is one while left > 0
+            request_rows(A, b, &row0, &w, &len, &bits);
+            if (w > 0 || b + 1 >= A.B) break;
+            ++b;
+        }
+        nq = row_tiles(A, w);
+    }
+    __device__ __forceinline__ void unit(const AttendCall& A, int skip)
+    {
+        const Shape s = unit_tiles(A, w, len, qt);
+        a = s.a;
+        z = s.z;
+        k0 = a + skip;
+        n = static_cast<int>(min(static_cast<int64_t>(z - k0 + 1), left));
+    }
+    __device__ __forceinline__ void start(const AttendCall& A, int b0, int64_t off, int64_t tiles)
+    {
+        b = b0;
+        left = tiles;
+        request(A);
+        const int64_t per = head_tiles(A, w, len);
+        h = static_cast<int>(off / per);
+        off -= h * per;
+        qt = 0;
+        while (true) {
+            const Shape s = unit_tiles(A, w, len, qt);
+            if (off < s.z - s.a + 1) break;
+            off -= s.z - s.a + 1;
+            ++qt;
+        }
+        unit(A, static_cast<int>(off));
+    }
+    // false at the run's end
+    __device__ __forceinline__ bool next(const AttendCall& A)
+    {
+        left -= n;
+        if (left <= 0) return false;
+        if (++qt == nq) {
+            qt = 0;
+            if (++h == A.c.heads) {
+                h = 0;
+                ++b;
+                request(A);
+            }
+        }
+        unit(A, 0);
+        return true;
+    }
+    __device__ __forceinline__ int rows(const AttendCall& A) const
+    {
+        return static_cast<int>(min(static_cast<int64_t>(kTile),
+                                    static_cast<int64_t>(w) * A.group - static_cast<int64_t>(qt) * kTile));
+    }
+};
+
+// A block's numbers in a tile: score factor, exponent addend, 1 / value scale.
+struct __align__(16) BlockNums {
+    float ks, bias, inv, pad;
+};
+
+constexpr uint32_t kSmemAlign = 1024;        // the 128-byte swizzle's period
+template <int D>
+struct Smem {
+    static constexpr int kSlot = kTile * D;              // one tile's K or V; 1024-byte aligned in order
+    static constexpr int kSlots = D == 128 ? 4 : 8;      // K and V alternate
+    uint8_t q[2][kTile * D];                             // the queries' two pieces
+    uint8_t ring[kSlots][kSlot];
+    BlockNums nums[kSlots / 2][kBlocks];
+    float2 ml[kTile];
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t s_full, p_full, pv_done, q_full;
+    int64_t scan[kThreads / 32];
+    int64_t run_off;
+    int64_t total;
+    int run_b;
+    uint32_t tmem;
+    int stalled;       // a wait gave up: every role leaves its loop
+    int quit;          // the same, as the softmax warps agreed on it at a barrier
+};
+
+// K-major and MN-major operands share the TMA swizzle: rows of D bytes, groups of 8 rows.
+template <int D>
+__device__ __forceinline__ uint64_t operand(uint32_t addr)
+{
+    constexpr uint64_t swizzle = D == 128 ? 2 : 4;       // 128- or 64-byte
+    return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (1ull << 16) |
+           (static_cast<uint64_t>(8 * D / 16) << 32) | (1ull << 46) | (swizzle << 61);
+}
+
+// ---- softmax -------------------------------------------------------------------------------
+struct Row {
+    float f;              // score factor: scale log2(e) 2^e of the row's pieces
+    int lo, span;         // sees tokens [lo, lo + span]
+    float m, l;
+};
+
+// One chunk's (32 tokens) exponents from its scores, in place.
+template <bool MASK>
+__device__ __forceinline__ void exponents(float* x, const Row& r, const BlockNums& n0,
+                                          const BlockNums& n1, int token)
+{
+    const float f0 = r.f * n0.ks, f1 = r.f * n1.ks;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        x[j] = fmaf(x[j], f0, n0.bias);
+        x[j + 16] = fmaf(x[j + 16], f1, n1.bias);
+    }
+    if (MASK) {
+        const uint32_t at = static_cast<uint32_t>(token - r.lo), span = static_cast<uint32_t>(r.span);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (at + j > span) x[j] = -INFINITY;
+    }
+}
+__device__ __forceinline__ float max32(const float* x)
+{
+    float a = x[0], b = x[1], c = x[2], d = x[3];
+#pragma unroll
+    for (int j = 4; j < 32; j += 4) {
+        a = fmaxf(a, x[j]);
+        b = fmaxf(b, x[j + 1]);
+        c = fmaxf(c, x[j + 2]);
+        d = fmaxf(d, x[j + 3]);
+    }
+    return fmaxf(fmaxf(a, b), fmaxf(c, d));
+}
+// A pair of weights in two e4m3 pieces each. The weights go through fp16 (11 bits, 2^-12: a
+// sixteenth of what the pieces are off by); the remainder is exact there.
+__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo)
+{
+    uint32_t w, back, rest;
+    uint16_t h, s;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(w));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(w), "r"(back));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(s) : "r"(rest));
+    *hi = h;
+    *lo = s;
+}
+// Exponents -> weights, their sum, and the pieces (8 words each) at p[0..7], p[8..15].
+__device__ __forceinline__ void weights(float* x, Row& r, const BlockNums& n0, const BlockNums& n1,
+                                        uint32_t* p)
+{
+    const float ref = r.m - kShift;
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        x[j] = ex2_approx(x[j] - ref);
+        s0 += x[j];
+    }
+#pragma unroll
+    for (int j = 16; j < 32; ++j) {
+        x[j] = ex2_approx(x[j] - ref);
+        s1 += x[j];
+    }
+    r.l += s0 * n0.inv + s1 * n1.inv;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        uint32_t h0, h1, l0, l1;
+        split2(x[4 * k], x[4 * k + 1], &h0, &l0);
+        split2(x[4 * k + 2], x[4 * k + 3], &h1, &l1);
+        p[k] = h0 | (h1 << 16);
+        p[8 + k] = l0 | (l1 << 16);
+    }
+}
+
+// One tile for one row copy: scores in TMEM -> weights in TMEM. C copies: this thread's chunks
+// are [q0, q0 + 4 / C).
+template <int D, int C>
+__device__ __forceinline__ void soften(Smem<D>& sm, Row& r, uint32_t lanes, const BlockNums* nums,
+                                       int page, int token0, int q0, bool mask, bool first)
+{
+    constexpr int N = 4 / C;
+    const uint32_t s_addr = sm.tmem + lanes;
+    float x[32];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int q = q0 + i;
+        tc_ld32(s_addr + 32 * q, x);
+        tc_wait_ld();
+        const BlockNums n0 = nums[32 * q / page], n1 = nums[(32 * q + 16) / page];
+        if (mask) exponents<true>(x, r, n0, n1, token0 + 32 * q);
+        else exponents<false>(x, r, n0, n1, 0);
+        top = fmaxf(top, max32(x));
+    }
+    if (first) {
+        r.m = fmaxf(top, kNone);
+    } else {
+        const bool grow = top > r.m + kLag;
+        if (__any_sync(0xffffffffu, grow)) {
+            float g = 1.0f;
+            if (grow) {
+                g = ex2_approx(r.m - top);
+                r.m = top;
+                r.l *= g;
+            }
+            const uint32_t o_addr = sm.tmem + lanes + kTile;
+            float o[32];
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+                tc_ld32(o_addr + d, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] *= g;
+                tc_st32(o_addr + d, o);
+            }
+            tc_wait_st();
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int q = q0 + i;
+        const BlockNums n0 = nums[32 * q / page], n1 = nums[(32 * q + 16) / page];
+        if (N > 1) {
+            tc_ld32(s_addr + 32 * q, x);
+            tc_wait_ld();
+            if (mask) exponents<true>(x, r, n0, n1, token0 + 32 * q);
+            else exponents<false>(x, r, n0, n1, 0);
+        }
+        uint32_t p[16];
+        weights(x, r, n0, n1, p);
+        tc_st16(s_addr + 16 * q, p);       // behind every chunk still to be read
+    }
+    tc_wait_st();
+}
+
+// This thread's row of the queries as two pieces in shared memory; returns the row's exponent.
+template <int D>
+__device__ __forceinline__ int load_query(const AttendCall& A, Smem<D>& sm, int t, bool live,
+                                          int64_t row, int head)
+{
+    uint4 v[D / 8];
+    const uint16_t* src = static_cast<const uint16_t*>(A.q) + row * A.q_stride +
+                          static_cast<int64_t>(head) * D;
+    if (!live) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    } else if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) v[i] = reinterpret_cast<const uint4*>(src)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = src[8 * i + 2 * k] | (static_cast<uint32_t>(src[8 * i + 2 * k + 1]) << 16);
+            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    // the magnitudes' bits order like the magnitudes, NaN above all
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            top = max(top, w[k] & 0x7fffu);
+            top = max(top, (w[k] >> 16) & 0x7fffu);
+        }
+    }
+    const bool fine = top < 0x7f80u;
+    const int e = fine ? scale_exponent(__uint_as_float(top << 16)) : 0;
+    const float inv = exp2i(-e);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint4 u = v[2 * c + k / 2];
+            const uint32_t w0 = (k & 1) ? u.z : u.x, w1 = (k & 1) ? u.w : u.y;
+            const float y[4] = {bf16_lo(w0) * inv, bf16_hi(w0) * inv, bf16_lo(w1) * inv, bf16_hi(w1) * inv};
+            float z[4];
+            hi[k] = e4m3x4(y[0], y[1], y[2], y[3]);
+            e4m3x4_to_f32(hi[k], z);
+            lo[k] = e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
+            if (!fine) hi[k] = 0x7f7f7f7fu;          // NaN: the row answers NaN
+        }
+        const int swz = D == 128 ? (c ^ (t & 7)) : (c ^ ((t >> 1) & 3));
+        *reinterpret_cast<uint4*>(&sm.q[0][t * D + swz * 16]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(&sm.q[1][t * D + swz * 16]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    return e;
+}
+
+// A finished piece: the copies' sums joined and written, as results or as a part.
+template <int D>
+__device__ __forceinline__ void finish(const AttendCall& A, Smem<D>& sm, const Row& r, uint32_t lanes,
+                                       int t, int copies, const Walk& wk, bool whole, int part,
+                                       const Workspace& ws)
+{
+    const int RT = kTile / copies;
+    const int row = t % RT, sub = t / RT;
+    float m = r.m, l = r.l;
+    if (copies > 1) {
+        sm.ml[t] = make_float2(r.m, r.l);
+        soft_sync();
+        for (int c = 0; c < copies; ++c) m = fmaxf(m, sm.ml[row + c * RT].x);
+        l = 0.0f;
+        for (int c = 0; c < copies; ++c) {
+            const float2 o = sm.ml[row + c * RT];
+            l += o.y * ex2_approx(o.x - m);
+        }
+    }
+    float g = copies > 1 ? ex2_approx(r.m - m) : 1.0f;
+    if (whole) g = l == 0.0f ? 0.0f : g / l;       // a row that saw nothing: zeros
+    const bool live = row < wk.rows(A);
+    const int flat = wk.qt * kTile + row;
+    const int64_t prow = wk.row0 + flat / A.group;
+    const int head = wk.h * A.group + flat % A.group;
+    if (live && sub == 0) {
+        if (!whole)
+            ws.ml[part * kTile + row] = make_float2(m, l);
+        else if (A.lse != nullptr)
+            A.lse[prow * A.q_heads + head] = l == 0.0f ? -INFINITY : (m - kShift + log2f(l)) * kLn2;
+    }
+    uint16_t* out = static_cast<uint16_t*>(A.out) + prow * A.out_stride + static_cast<int64_t>(head) * D;
+    float* po = ws.o + (static_cast<int64_t>(part) * kTile + row) * D;
+    const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+    float4* stage = reinterpret_cast<float4*>(sm.q[0]);    // 128 x 32 floats: the queries are done
+    const uint32_t o_addr = sm.tmem + lanes + kTile;
+#pragma unroll 1
+    for (int d0 = 0; d0 < D; d0 += 32) {
+        float o[32];
+        tc_ld32(o_addr + d0, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] *= g;
+        int n = 32, d = d0;
+        if (copies > 1) {
+            n = 32 / copies;
+            d = d0 + sub * n;
+            soft_sync();                       // the stage's last readers are done
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                stage[t * 8 + (j ^ (t & 7))] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            soft_sync();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {      // 16 or 8 of the chunk's columns
+                if (j * 4 >= n) break;
+                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int c = 0; c < copies; ++c) {
+                    const int from = row + c * RT;
+                    const float4 v = stage[from * 8 + ((sub * (n / 4) + j) ^ (from & 7))];
+                    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+                }
+                o[4 * j] = s.x; o[4 * j + 1] = s.y; o[4 * j + 2] = s.z; o[4 * j + 3] = s.w;
+            }
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j * 8 >= n) break;
+            const float* y = o + 8 * j;
+            if (!whole) {
+                *reinterpret_cast<float4*>(po + d + 8 * j) = make_float4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<float4*>(po + d + 8 * j + 4) = make_float4(y[4], y[5], y[6], y[7]);
+            } else if (vec) {
+                store8<DSPARK_BF16>(out + d + 8 * j, y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) store1<DSPARK_BF16>(out, d + 8 * j + i, y[i]);
+            }
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
+                  const __grid_constant__ CUtensorMap v_map)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(
+        raw + ((kSmemAlign - (smem_addr(raw) & (kSmemAlign - 1))) & (kSmemAlign - 1)));
+    constexpr int kSlots = Smem<D>::kSlots;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Workspace ws = workspace_of(A.ws, D);
+
+    if (tid == 0) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(smem_addr(&sm.full[s]), 1);
+            mbar_init(smem_addr(&sm.empty[s]), 1);
+        }
+        mbar_init(smem_addr(&sm.s_full), 1);
+        mbar_init(smem_addr(&sm.p_full), kSoftThreads);
+        mbar_init(smem_addr(&sm.pv_done), 1);
+        mbar_init(smem_addr(&sm.q_full), kSoftThreads);
+        sm.stalled = 0;
+        sm.quit = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;"
+                     ::"r"(smem_addr(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_fence_before();
+    }
+    pdl_wait_and_trigger();
+
+    // The cut: each thread counts the tiles of a stretch of requests, a scan over the threads
+    // gives the total and the stretch that holds this CTA's first tile.
+    int bits = 0;
+    const int per = (A.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        int row0, w, len;
+        request_rows(A, b, &row0, &w, &len, &bits);
+        mine += head_tiles(A, w, len) * A.c.heads;
+    }
+    if (blockIdx.x == 0 && bits) raise_status(A.status, bits);
+    int64_t upto = mine;
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += y;
+    }
+    if (lane == 31) sm.scan[warp] = upto;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sm.scan[w];
+        total += sm.scan[w];
+    }
+    const int64_t t0 = total * blockIdx.x / gridDim.x, t1 = total * (blockIdx.x + 1) / gridDim.x;
+    const int64_t from = before + upto - mine;
+    if (t0 < t1 && t0 >= from && t0 < from + mine) {
+        int64_t off = t0 - from;
+        int b = b0;
+        for (; b < b1; ++b) {
+            int row0, w, len, ignored = 0;
+            request_rows(A, b, &row0, &w, &len, &ignored);
+            const int64_t n = head_tiles(A, w, len) * A.c.heads;
+            if (off < n) break;
+            off -= n;
+        }
+        sm.run_b = b;
+        sm.run_off = off;
+    }
+    if (tid == 0) ws.meta[blockIdx.x].cut = 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    volatile int* stalled = &sm.stalled;
+    if (t0 < t1) {
+        Walk wk;
+        wk.start(A, sm.run_b, sm.run_off, t1 - t0);
+        if (warp == 4) {
+            // ---- pages in ----
+            const int per_tile = kTile / A.c.page;
+            const uint32_t box = static_cast<uint32_t>(A.c.page) * D;
+            const int beyond = A.c.n_pages * A.c.heads * A.c.page;     // a row past the tensor: zeros
+            int it = 0;
+            int bad = 0, issued = 0;
+            bool ok = true;
+            do {
+                const int32_t* table = A.c.table + static_cast<int64_t>(wk.b) * A.c.width;
+                const int total_blocks = (wk.len + wk.w + A.c.page - 1) / A.c.page;
+                const int p0 = wk.len + wk.qt * kTile / A.group;
+                const int lo = A.window > 0 && p0 >= A.window ? p0 - A.window + 1 : 0;
+                // 32 blocks at a time, one per lane; the next 32 are fetched while these load
+                const int first_block = wk.k0 * per_tile;
+                int base = first_block;
+                auto id_of = [&](int j) -> int {        // -1: dead, not there, or not a page
+                    if (j >= total_blocks || (j + 1) * A.c.page <= lo) return -1;
+                    const int id = j < A.c.width ? table[j] : -1;
+                    if (id < 0 || id >= A.c.n_pages) { bad = 1; return -1; }
+                    return id;
+                };
+                auto nums_of = [&](int id) -> float2 {
+                    if (id < 0) return make_float2(0.0f, 0.0f);
+                    const int64_t bh = static_cast<int64_t>(id) * A.c.heads + wk.h;
+                    return make_float2(A.c.k_scale[bh], A.c.v_scale[bh]);
+                };
+                const int end_block = (wk.k0 + wk.n) * per_tile;
+                int id = base + lane < end_block ? id_of(base + lane) : -1;
+                float2 sc = nums_of(id);
+                int next_id = -1;
+                float2 next_sc = make_float2(0.0f, 0.0f);
+                for (int k = 0; ok && k < wk.n; ++k, ++it) {
+                    const int j0 = first_block + k * per_tile - base;   // this tile's first lane
+                    if (j0 == 0 && base + 32 + lane < end_block) next_id = id_of(base + 32 + lane);
+                    if (j0 == per_tile || (per_tile == 32 && j0 == 0)) next_sc = nums_of(next_id);
+                    const int src = j0 + (lane & (per_tile - 1));
+                    const int my_id = __shfl_sync(0xffffffffu, id, src);
+                    const float ks = __shfl_sync(0xffffffffu, sc.x, src);
+                    const float vs = __shfl_sync(0xffffffffu, sc.y, src);
+                    const int block = base + src;
+                    const bool there = lane < per_tile && block < total_blocks;
+                    const int count = __popc(__ballot_sync(0xffffffffu, there));
+                    const int row = my_id < 0 ? beyond : (my_id * A.c.heads + wk.h) * A.c.page;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int use = 2 * it + kv;
+                        const int s = use % kSlots;
+                        const uint32_t full = smem_addr(&sm.full[s]);
+                        if (use >= kSlots)
+                            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.empty[s]),
+                                                                   ((use / kSlots) & 1) ^ 1, stalled));
+                        if (!ok) break;
+                        if (kv == 1 && lane < per_tile) {
+                            BlockNums n;
+                            n.ks = my_id < 0 ? 0.0f : ks;
+                            n.bias = my_id < 0 ? -INFINITY : log2f(vs);
+                            n.inv = my_id < 0 ? 0.0f : 1.0f / vs;
+                            n.pad = 0.0f;
+                            sm.nums[it % (kSlots / 2)][lane] = n;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_expect_tx(full, count * box);
+                        __syncwarp();
+                        if (there)
+                            tma_load(smem_addr(sm.ring[s]) + lane * box, kv ? &v_map : &k_map, row, full);
+                        issued = use + 1;
+                    }
+                    if (j0 + per_tile == 32) {
+                        base += 32;
+                        id = next_id;
+                        sc = next_sc;
+                        next_id = -1;
+                    }
+                }
+            } while (ok && wk.next(A));
+            if (bad) raise_status(A.status, DSPARK_STATUS_BAD_PAGE);
+            // every started copy lands before the CTA may leave
+            __syncwarp();
+            for (int s = 0; s < kSlots && s < issued; ++s)
+                drain(smem_addr(&sm.full[s]), ((issued - 1 - s) / kSlots) & 1, stalled);
+        } else if (warp == 5) {
+            // ---- products ----
+            if (lane == 0) {
+                constexpr uint32_t kIdesc = (1u << 4) | (kTile / 16 << 24);
+                constexpr uint32_t kIdescQK = kIdesc | (kTile / 8 << 17);
+                constexpr uint32_t kIdescPV = kIdesc | (D / 8 << 17) | (1u << 16);   // V: dim contiguous
+                const uint32_t s_addr = sm.tmem, o_addr = sm.tmem + kTile;
+                int it = 0, piece = 0;
+                bool ok = true;
+                do {
+                    const int rows = wk.rows(A);
+                    const int copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+                    ok = mbar_wait(smem_addr(&sm.q_full), piece & 1, stalled);
+                    for (int k = 0; ok && k < wk.n; ++k, ++it) {
+                        const int use = 2 * it;
+                        const int sk = use % kSlots, sv = (use + 1) % kSlots;
+                        const uint32_t round = (use / kSlots) & 1;
+                        // the scores' columns hold the last tile's weights until its products end
+                        ok = mbar_wait(smem_addr(&sm.full[sk]), round, stalled) &&
+                             (it == 0 || mbar_wait(smem_addr(&sm.pv_done), (it - 1) & 1, stalled));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t kb = operand<D>(smem_addr(sm.ring[sk]));
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const uint64_t qa = operand<D>(smem_addr(sm.q[p]));
+#pragma unroll
+                            for (int s = 0; s < D / 32; ++s)
+                                mma_ss(s_addr, qa + 2 * s, kb + 2 * s, kIdescQK, p > 0 || s > 0);
+                        }
+                        tc_commit(smem_addr(&sm.empty[sk]));
+                        tc_commit(smem_addr(&sm.s_full));
+                        ok = mbar_wait(smem_addr(&sm.p_full), it & 1, stalled) &&
+                             mbar_wait(smem_addr(&sm.full[sv]), round, stalled);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vb = operand<D>(smem_addr(sm.ring[sv]));
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            // chunk s belongs to copy s * copies / 4
+                            uint32_t off[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                off[i] = i * copies / 4 == s * copies / 4 ? 0u : 0xffffffffu;
+                            const uint32_t fresh = k == 0 && (s * copies) % 4 == 0;
+#pragma unroll
+                            for (int p = 0; p < 2; ++p)
+                                mma_ts(o_addr, s_addr + 16 * s + 8 * p, vb + s * (32 * D / 16), kIdescPV,
+                                       p > 0 || !fresh, off[0], off[1], off[2], off[3]);
+                        }
+                        tc_commit(smem_addr(&sm.empty[sv]));
+                        tc_commit(smem_addr(&sm.pv_done));
+                    }
+                    ++piece;
+                } while (ok && wk.next(A));
+                // the last products' arrivals on the slots' barriers land before the CTA leaves
+                if (it > 0) {
+                    const int use = 2 * (it - 1);
+                    drain(smem_addr(&sm.empty[use % kSlots]), (use / kSlots) & 1, stalled);
+                    drain(smem_addr(&sm.empty[(use + 1) % kSlots]), (use / kSlots) & 1, stalled);
+                }
+            }
+            __syncwarp();
+        } else {
+            // ---- softmax ----
+            const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+            int it = 0, piece = 0;
+            int64_t at = t0;
+            bool ok = true;
+            do {
+                const int rows = wk.rows(A);
+                const int copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+                const int RT = kTile / copies;
+                const int row = min(tid % RT, rows - 1);
+                const int flat = wk.qt * kTile + row;
+                const int i = flat / A.group;
+                const int e = load_query<D>(A, sm, tid, tid % RT < rows, wk.row0 + i,
+                                            wk.h * A.group + flat - i * A.group);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(smem_addr(&sm.q_full));
+                Row r;
+                r.f = A.scale * kLog2e * exp2i(e);
+                const int pos = wk.len + i;
+                r.lo = A.window > 0 && pos >= A.window ? pos - A.window + 1 : 0;
+                r.span = pos - r.lo;
+                r.m = kNone;
+                r.l = 0.0f;
+                // tiles that every row sees whole need no mask: those within [hi lo, lo pos]
+                const int i0 = wk.qt * kTile / A.group;
+                const int i1 = (wk.qt * kTile + rows - 1) / A.group;
+                const int p0 = wk.len + i0, p1 = wk.len + i1;
+                const int lo1 = A.window > 0 && p1 >= A.window ? p1 - A.window + 1 : 0;
+                const int stored = wk.len + wk.w;
+                for (int k = 0; k < wk.n; ++k, ++it) {
+                    const int token0 = (wk.k0 + k) * kTile;
+                    const int use = 2 * it + 1;
+                    const int s = use % kSlots;
+                    ok = mbar_wait(smem_addr(&sm.full[s]), (use / kSlots) & 1, stalled) &&
+                         mbar_wait(smem_addr(&sm.s_full), it & 1, stalled);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const BlockNums* nums = sm.nums[it % (kSlots / 2)];
+                    const bool mask = token0 + kTile - 1 > p0 || token0 < lo1;
+                    const bool first = k == 0;
+                    if (copies == 4)
+                        soften<D, 4>(sm, r, lanes, nums, A.c.page, token0, warp, mask, first);
+                    else if (copies == 2)
+                        soften<D, 2>(sm, r, lanes, nums, A.c.page, token0, (warp >> 1) * 2, mask, first);
+                    else
+                        soften<D, 1>(sm, r, lanes, nums, A.c.page, token0, 0, mask, first);
+                    tc_fence_before();
+                    if (token0 + kTile > stored) {      // slots past the last token: 0 x NaN is NaN
+                        if (token0 + tid >= stored) {
+                            uint4* v = reinterpret_cast<uint4*>(&sm.ring[s][tid * D]);
+#pragma unroll
+                            for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    mbar_arrive(smem_addr(&sm.p_full));
+                }
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done), (it - 1) & 1, stalled));
+                // a warp whose waits gave up leaves; agree on it before finish()'s barriers
+                if (lane == 0 && !ok) *reinterpret_cast<volatile int*>(&sm.quit) = 1;
+                soft_sync();
+                if (*reinterpret_cast<volatile int*>(&sm.quit)) break;
+                tc_fence_after();
+                const bool whole = wk.k0 == wk.a && wk.k0 + wk.n - 1 == wk.z;
+                const int part = blockIdx.x * 2 + (piece > 0);
+                finish<D>(A, sm, r, lanes, tid, copies, wk, whole, part, ws);
+                if (tid == 0 && !whole && wk.k0 == wk.a) {
+                    RunMeta& m = ws.meta[blockIdx.x];
+                    m.total = total;
+                    m.unit_end = at + (wk.z - wk.a + 1);
+                    m.slot = piece > 0;
+                    m.row0 = wk.row0;
+                    m.rows = rows;
+                    m.flat0 = wk.qt * kTile;
+                    m.head0 = wk.h * A.group;
+                    m.cut = 1;
+                }
+                at += wk.n;
+                ++piece;
+                soft_sync();                   // the stage is free before the next queries enter it
+            } while (wk.next(A));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && sm.stalled) raise_status(A.status, DSPARK_STATUS_STALL);
+    if (warp == 5)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(sm.tmem));
+}
+
+// Joins the parts of each cut unit: one warp per row, each CTA of a column takes every kJoinY-th
+// group of rows.
+constexpr int kJoinWarps = 4;
+constexpr int kJoinY = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendCall A, int ctas)
+{
+    pdl_wait_and_trigger();
+    const Workspace ws = workspace_of(A.ws, D);
+    const RunMeta m = ws.meta[blockIdx.x];
+    if (!m.cut) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c0 = blockIdx.x;
+    auto start = [&](int c) -> int64_t { return m.total * c / ctas; };
+    int c1 = c0 + 1;                          // one past the last run that holds a part
+    {
+        int lo = c0 + 1, hi = ctas;           // the first run that starts at or past the unit's end
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (start(mid) < m.unit_end) lo = mid + 1; else hi = mid;
+        }
+        c1 = lo;
+    }
+    auto part = [&](int c) -> int { return c * 2 + (c == c0 ? m.slot : 0); };
+    for (int row = blockIdx.y * kJoinWarps + warp; row < m.rows; row += kJoinY * kJoinWarps) {
+        float top = kNone, sum = 0.0f;
+        for (int c = c0 + lane; c < c1; c += 32)
+            if (start(c) < start(c + 1)) top = fmaxf(top, ws.ml[part(c) * kTile + row].x);
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int cb = c0; cb < c1; cb += 32) {
+            const int c = cb + lane;
+            float f = 0.0f;
+            int p = -1;
+            if (c < c1 && start(c) < start(c + 1)) {
+                p = part(c);
+                const float2 ml = ws.ml[p * kTile + row];
+                f = exp2f(ml.x - top);
+                sum += f * ml.y;
+            }
+            const int n = min(32, c1 - cb);
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+                const int pk = __shfl_sync(0xffffffffu, p, k);
+                const float fk = __shfl_sync(0xffffffffu, f, k);
+                if (pk < 0 || lane * 4 >= D) continue;
+                const float4 o = *reinterpret_cast<const float4*>(
+                    ws.o + (static_cast<int64_t>(pk) * kTile + row) * D + lane * 4);
+                acc.x = fmaf(fk, o.x, acc.x);
+                acc.y = fmaf(fk, o.y, acc.y);
+                acc.z = fmaf(fk, o.z, acc.z);
+                acc.w = fmaf(fk, o.w, acc.w);
+            }
+        }
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int flat = m.flat0 + row;
+        const int64_t prow = m.row0 + flat / A.group;
+        const int head = m.head0 + flat % A.group;
+        if (lane * 4 < D) {
+            uint16_t* out = static_cast<uint16_t*>(A.out) + prow * A.out_stride +
+                            static_cast<int64_t>(head) * D + lane * 4;
+            const uint32_t a = pack_bf16(acc.x * inv, acc.y * inv), b = pack_bf16(acc.z * inv, acc.w * inv);
+            out[0] = static_cast<uint16_t>(a);
+            out[1] = static_cast<uint16_t>(a >> 16);
+            out[2] = static_cast<uint16_t>(b);
+            out[3] = static_cast<uint16_t>(b >> 16);
+        }
+        if (lane == 0 && A.lse != nullptr)
+            A.lse[prow * A.q_heads + head] = sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * kLn2;
+    }
+}
+
+// cuTensorMapEncodeTiled, found through the runtime (the library does not link libcuda).
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                             CUtensorMapFloatOOBfill);
+EncodeFn encode_fn()
+{
+    static const EncodeFn fn = []() -> EncodeFn {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) != cudaSuccess || q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+int encode(CUtensorMap* map, void* codes, const dspark_cache& c)
+{
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return fail(DSPARK_ERR_CUDA, "dspark attend: cuTensorMapEncodeTiled not found");
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.dim),
+                                static_cast<cuuint64_t>(c.n_pages) * c.heads * c.page};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.dim)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(c.dim), static_cast<cuuint32_t>(c.page)};
+    const cuuint32_t ones[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, ones,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(DSPARK_ERR_CUDA, "dspark attend: cuTensorMapEncodeTiled returned %d", static_cast<int>(r));
+    return DSPARK_OK;
+}
+
+template <int D>
+int launch(const AttendCall& A, cudaStream_t stream)
+{
+    DeviceInfo dev;
+    int rc = current_device(&dev);
+    if (rc != DSPARK_OK) return rc;
+    const size_t smem = sizeof(Smem<D>) + kSmemAlign;
+    static bool ready[64] = {};               // opt-in to large shared memory, once per device
+    if (!ready[dev.device]) {
+        const cudaError_t e = cudaFuncSetAttribute(attend_mma_kernel<D>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return fail(DSPARK_ERR_CUDA, "dspark attend: %s", cudaGetErrorString(e));
+        }
+        ready[dev.device] = true;
+    }
+    CUtensorMap k_map, v_map;
+    rc = encode(&k_map, A.c.k, A.c);
+    if (rc == DSPARK_OK) rc = encode(&v_map, A.c.v, A.c);
+    if (rc != DSPARK_OK) return rc;
+    const int ctas = min(2 * dev.sm_count, kMaxCtas);
+    rc = launch_pdl("attend", attend_mma_kernel<D>, dim3(ctas), dim3(kThreads), smem, stream, A, k_map, v_map);
+    if (rc != DSPARK_OK) return rc;
+    return launch_pdl("attend join", attend_join_kernel<D>, dim3(ctas, kJoinY), dim3(kJoinWarps * 32), 0,
+                      stream, A, ctas);
+}
+
+}  // namespace
+
+bool attend_mma_serves(const AttendCall& A, int dtype)
+{
+    return dtype == DSPARK_BF16 && (A.c.dim == 64 || A.c.dim == 128) && A.c.n_pages > 0;
+}
+
+size_t attend_workspace_bytes(int dim)
+{
+    if (dim != 64 && dim != 128) return 16;
+    return kMaxCtas * (sizeof(RunMeta) + 2 * kTile * (sizeof(float2) + dim * sizeof(float)));
+}
+
+int launch_attend_mma(const AttendCall& A, cudaStream_t stream)
+{
+    return A.c.dim == 128 ? launch<128>(A, stream) : launch<64>(A, stream);
+}
+
+}  // namespace dspark
