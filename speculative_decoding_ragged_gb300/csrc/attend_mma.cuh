@@ -1,0 +1,435 @@
+// attend_mma.cuh — what the two tensor-core attention kernels share: the PTX they are written in,
+// the cut of the work into equal runs, the parts left in the workspace.
+//
+// Mathematics. For a row r (one position, one query head) and tokens t with block scales ks, vs:
+//   x_t = log2(e) scale q.K_t + log2 vs_t,   w_t = 2^(x_t - m),   O = sum_t w_t Vcode_t,
+//   l = sum_t w_t / vs_t,   out = O / l,     lse = ln 2 (m + log2 l).
+// Putting the value's scale into the exponent makes every product of the value side a plain
+// product of codes, keeps w_t <= 1 whatever the blocks' scales, and costs nothing: it is the
+// addend of the multiply-add that scales the score.
+//
+// The cache stays in its 8 bits all the way into the tensor cores (kind::f8f6f4). What is not
+// 8-bit is split into e4m3 pieces whose products add up in fp32: a bf16 query element has 8
+// significant bits, an e4m3 piece 4, so two pieces (over a power of two per row) hold it exactly
+// down to 2^-17 of the row's largest; a weight in two pieces is within 2^-8 (6e-4 rms, below the
+// rounding of the bf16 result). Compared with widening K and V to 16 bits in shared memory this
+// needs no conversion of the cache and moves half the shared-memory bytes; the second piece
+// doubles the 8-bit products, which run at twice the 16-bit rate.
+//
+// Work. A unit is (request, cache head, up to R of its rows); its visible tokens come in tiles of
+// 128. All tiles of all units form one line, which the persistent grid (two CTAs per SM) cuts
+// into equal runs, so one long request and many short ones balance alike; every CTA computes the
+// cut from cu_seqlens and lengths on the device. A unit cut by a run's end leaves (m, l, O) parts
+// in the workspace that attend_join_kernel joins, in a fixed order: no atomics, the same bits
+// every time.
+#pragma once
+
+#include <cuda.h>
+
+#include "attend.cuh"
+#include "rope.cuh"
+
+namespace dspark {
+
+constexpr int kTile = 128;                   // tokens per tile
+constexpr int kMaxCtas = 304;                // parts the workspace holds: two CTAs on 152 SMs
+constexpr int kBlocks = kTile / 16;          // most blocks in a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -1e30f;              // a row's reference before it has seen a token
+// Weights are stored as 2^(x - m + kShift) where m may lag the true maximum by kLag: at most
+// 2^8.5 < 448, and a weight keeps two full pieces down to 2^-12 of the largest.
+constexpr float kShift = 6.0f;
+constexpr float kLag = 2.5f;
+constexpr long long kWaitCycles = 1ll << 31;
+constexpr uint32_t kSmemAlign = 1024;        // the 128-byte swizzle's period
+
+// What the join needs to know of a CTA's run.
+struct RunMeta {
+    int64_t total;      // places on the whole line
+    int64_t unit_end;   // the place where the cut unit ends
+    int cut;            // 1: the run's last unit starts here and continues in the next runs
+    int slot;           // the part it left here
+    int row0, rows;     // the request's first packed row; the unit's rows (position, head) ...
+    int flat0, head0;   // ... from this flat index on, first query head
+};
+
+struct Workspace {
+    RunMeta* meta;      // [kMaxCtas]
+    float2* ml;         // [kMaxCtas][2][kTile]
+    float* o;           // [kMaxCtas][2][kTile][dim]
+};
+__host__ __device__ inline Workspace workspace_of(void* ws)
+{
+    char* p = static_cast<char*>(ws);
+    Workspace w;
+    w.meta = reinterpret_cast<RunMeta*>(p);
+    w.ml = reinterpret_cast<float2*>(p + kMaxCtas * sizeof(RunMeta));
+    w.o = reinterpret_cast<float*>(p + kMaxCtas * (sizeof(RunMeta) + 2 * kTile * sizeof(float2)));
+    return w;
+}
+
+int encode_cache(CUtensorMap* map, void* codes, const dspark_cache& c);
+int launch_attend_join(const AttendCall& A, int ctas, cudaStream_t stream);
+int launch_attend_narrow(const AttendCall& A, int ctas, int device, cudaStream_t stream);
+int launch_attend_wide(const AttendCall& A, int ctas, int device, cudaStream_t stream);
+
+// ---- PTX -----------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_addr(const void* p)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+// Bounded wait for the phase of this parity. Once any thread of the CTA has given up (about a
+// second), *stalled is set and every wait returns false, so that all roles leave their loops.
+// The loop is out of line: the kernels run each part of their code a few times from a cold
+// instruction cache, which costs about 16 cycles an instruction, so code size is time.
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* stalled)
+{
+    const long long deadline = clock64() + kWaitCycles;
+    while (!mbar_try(bar, parity)) {
+        if (*stalled) return false;
+        if (clock64() > deadline) { *stalled = 1; return false; }
+    }
+    return true;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* stalled)
+{
+    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, stalled);
+}
+// The same bound, but not cut short by another wait's end: for what is in flight.
+static __device__ __noinline__ void drain(uint32_t bar, uint32_t parity, volatile int* stalled)
+{
+    const long long deadline = clock64() + kWaitCycles;
+    while (!mbar_try(bar, parity))
+        if (clock64() > deadline) { *stalled = 1; return; }
+}
+// True in one lane of the warp, which runs converged here.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " elect.sync _|p, 0xffffffff;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n" : "=r"(yes));
+    return yes != 0;
+}
+// A page's box of the [rows, dim] tensor of codes -> shared memory.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The barrier's arrival follows the completion of every product this thread issued before.
+__device__ __forceinline__ void tc_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 ::"r"(bar) : "memory");
+}
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem], lanes of quarter i untouched where off<i> is all ones.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                       uint32_t off0, uint32_t off1, uint32_t off2, uint32_t off3)
+{
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n"
+        "}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(off0), "r"(off1), "r"(off2),
+        "r"(off3) : "memory");
+}
+__device__ __forceinline__ void tc_ld32(uint32_t addr, float* x)
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const float* x)
+{
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+
+// K-major and MN-major operands share the TMA swizzle: rows of BYTES (128 or 64), groups of 8 rows.
+template <int BYTES>
+__device__ __forceinline__ uint64_t operand(uint32_t addr)
+{
+    constexpr uint64_t swizzle = BYTES == 128 ? 2 : 4;   // 128- or 64-byte
+    return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (1ull << 16) |
+           (static_cast<uint64_t>(8 * BYTES / 16) << 32) | (1ull << 46) | (swizzle << 61);
+}
+
+// A block's numbers in a tile: score factor, exponent addend, 1 / value scale.
+struct __align__(16) BlockNums {
+    float ks, bias, inv, pad;
+};
+
+// Two weights in two e4m3 pieces each. The weights go through fp16 (11 bits, 2^-12: a sixteenth
+// of what the pieces are off by); the remainder is exact there.
+template <bool LOW = false>      // the second piece times 2^4, where it has a column of its own
+__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo)
+{
+    uint32_t w, back, rest;
+    uint16_t h, s;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(w));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(w), "r"(back));
+    if (LOW) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(rest), "r"(0x4c004c00u));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(s) : "r"(rest));
+    *hi = h;
+    *lo = s;
+}
+
+// ---- the line of tiles ---------------------------------------------------------------------
+// A unit of n tiles takes kUnitCost + n places on the line: starting and finishing a unit costs a
+// CTA about as much as that many tiles, and runs of equal length should take equal time. Tile k is
+// at place kUnitCost + k of its unit.
+constexpr int kUnitCost = 2;
+
+struct Shape {                   // a unit's visible tiles [a, z]
+    int a, z;
+};
+// The tiles that some row of a request's qt-th R rows sees. The divisions by the group are spared
+// where the unit holds the request's first or last rows: for decode and verify, always.
+template <int R>
+static __device__ __noinline__ Shape unit_tiles(const AttendCall& A, int w, int len, int qt)
+{
+    const int i0 = qt == 0 ? 0 : qt * R / A.group;
+    const int i1 = static_cast<int64_t>(qt + 1) * R >= static_cast<int64_t>(w) * A.group
+                       ? w - 1 : ((qt + 1) * R - 1) / A.group;
+    const int p0 = len + i0;
+    const int lo = A.window > 0 && p0 >= A.window ? p0 - A.window + 1 : 0;
+    return {lo / kTile, (len + i1) / kTile};
+}
+template <int R>
+__device__ __forceinline__ int row_tiles(const AttendCall& A, int w)
+{
+    return static_cast<int>((static_cast<int64_t>(w) * A.group + R - 1) / R);
+}
+// The places that one head of a request takes on the line.
+template <int R>
+static __device__ __noinline__ int64_t head_places(const AttendCall& A, int w, int len)
+{
+    int64_t n = 0;
+    const int nq = row_tiles<R>(A, w);
+#pragma unroll 1
+    for (int qt = 0; qt < nq; ++qt) {
+        const Shape s = unit_tiles<R>(A, w, len, qt);
+        n += s.z - s.a + 1 + kUnitCost;
+    }
+    return n;
+}
+// Where run i of `ctas` starts on a line of `total` places.
+static __device__ __noinline__ int64_t run_start(int64_t total, int i, int ctas)
+{
+    if (total < (1 << 22))       // 32-bit division where the product fits: the usual case
+        return static_cast<uint32_t>(total) * static_cast<uint32_t>(i) / static_cast<uint32_t>(ctas);
+    return total * i / ctas;
+}
+
+// The units of one run in order.
+template <int R>
+struct Walk {
+    int b, h, qt, nq;
+    int row0, w, len;
+    int a, z, k0, n;             // the unit's tiles [a, z]; this piece: n tiles from k0
+    int64_t unit;                // the unit's first place on the line
+    int64_t end;                 // the run's end on the line
+
+    __device__ __forceinline__ void piece(const AttendCall& A, int64_t from)
+    {
+        const Shape s = unit_tiles<R>(A, w, len, qt);
+        a = s.a;
+        z = s.z;
+        const int64_t first = unit + kUnitCost, nt = z - a + 1;      // the place of the first tile
+        const int k = from > first ? static_cast<int>(from - first) : 0;
+        k0 = a + k;
+        const int64_t stop = end - first < nt ? end - first : nt;
+        n = static_cast<int>(stop - k);                               // <= 0: nothing of it here
+    }
+    __device__ __forceinline__ bool last() const { return end - (unit + kUnitCost + z - a + 1) <= kUnitCost; }
+    // The next unit of the run; only if !last().
+    __device__ __forceinline__ void next(const AttendCall& A)
+    {
+        unit += kUnitCost + z - a + 1;
+        if (++qt == nq) {
+            qt = 0;
+            if (++h == A.c.heads) {
+                h = 0;
+                int bits = 0;
+#pragma unroll 1
+                do {             // there is one with rows before the run's end
+                    ++b;
+                    request_rows(A, b, &row0, &w, &len, &bits);
+                } while (w <= 0 && b + 1 < A.B);
+                nq = row_tiles<R>(A, w);
+            }
+        }
+        piece(A, unit);
+    }
+    __device__ __forceinline__ int rows(const AttendCall& A) const
+    {
+        return static_cast<int>(min(static_cast<int64_t>(R),
+                                    static_cast<int64_t>(w) * A.group - static_cast<int64_t>(qt) * R));
+    }
+    __device__ __forceinline__ bool whole() const { return k0 == a && n == z - a + 1; }
+    __device__ __forceinline__ int64_t unit_end() const { return unit + kUnitCost + z - a + 1; }
+    // The first token that some row of the unit sees.
+    __device__ __forceinline__ int first_seen(const AttendCall& A) const
+    {
+        const int p0 = len + (qt == 0 ? 0 : qt * R / A.group);
+        return A.window > 0 && p0 >= A.window ? p0 - A.window + 1 : 0;
+    }
+};
+
+// The cut, by a whole CTA of NT threads: each thread counts the places of a stretch of requests, a
+// scan over the threads gives the total and the stretch that holds the run's first place; that
+// thread writes the walk's start (n <= 0: the run holds no tile). The caller synchronises before
+// the walk is read.
+template <int R>
+struct Cut {
+    int64_t scan[32];
+    Walk<R> walk;
+};
+template <int R, int NT>
+__device__ __forceinline__ int64_t cut_line(const AttendCall& A, Cut<R>& cut)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int bits = 0;
+    const int per = (A.B + NT - 1) / NT;
+    const int b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
+    int64_t mine = 0, off = 0, t0 = 0, t1 = 0, total = 0;
+    if (tid == 0) cut.walk.n = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+            int row0, w, len;
+            request_rows(A, b, &row0, &w, &len, &bits);
+            const int64_t per_head = head_places<R>(A, w, len);
+            const int64_t all = per_head * A.c.heads;
+            if (pass == 0) { mine += all; continue; }
+            if (off >= all) { off -= all; continue; }
+            Walk<R>& k = cut.walk;
+            const int h = all < INT32_MAX
+                              ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(per_head))
+                              : static_cast<int>(off / per_head);
+            off -= h * per_head;
+            int qt = 0;
+#pragma unroll 1
+            while (true) {
+                const Shape s = unit_tiles<R>(A, w, len, qt);
+                const int n = s.z - s.a + 1 + kUnitCost;
+                if (off < n) break;
+                off -= n;
+                ++qt;
+            }
+            k.b = b;
+            k.h = h;
+            k.qt = qt;
+            k.nq = row_tiles<R>(A, w);
+            k.row0 = row0;
+            k.w = w;
+            k.len = len;
+            k.unit = t0 - off;
+            k.end = t1;
+            k.piece(A, t0);
+            break;
+        }
+        if (pass) break;
+        int64_t upto = mine;
+#pragma unroll 1
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += y;
+        }
+        if (lane == 31) cut.scan[warp] = upto;
+        __syncthreads();
+        int64_t before = 0;
+#pragma unroll 1
+        for (int w = 0; w < NT / 32; ++w) {
+            const int64_t s = cut.scan[w];
+            if (w < warp) before += s;
+            total += s;
+        }
+        const int64_t from = before + upto - mine;
+        t0 = run_start(total, blockIdx.x, gridDim.x);
+        t1 = run_start(total, blockIdx.x + 1, gridDim.x);
+        if (!(t0 < t1 && t0 >= from && t0 < from + mine)) break;
+        off = t0 - from;
+    }
+    if (blockIdx.x == 0 && bits) raise_status(A.status, bits);
+    return total;
+}
+
+}  // namespace dspark

@@ -1,0 +1,838 @@
+// attend_narrow.cu — dspark_attend on the tensor cores for decode and verify: units of at most 32
+// rows (window positions x query heads of one cache head).
+//
+// With few rows the products are turned round: the tile's 128 tokens (for the scores) and the
+// head's elements (for the sums) fill the 128 lanes of the instruction, the rows are its columns:
+//   S^T [128 tokens, 2 NR] = K [128, D] (Q_hi, Q_lo)^T       O^T [D, 2 NR] += V^T [D, 128] (W_hi, W_lo)
+// NR = 8, 16 or 32 by the unit's rows, so the products cost what the rows need (256 cycles a tile
+// at NR = 32 where 128 row lanes would cost 1024) and K and V are read from shared memory once.
+// The two pieces are separate columns and are added when they are read.
+// A thread's lane is a token: block scales are per-thread scalars, the rows' factors and
+// references broadcast reads. The softmax needs no reduction over lanes in the common case: every
+// thread checks its own exponents against the rows' references (one barrier with a vote), and
+// only a tile that passes one by kLag, or a unit's first, finds the true maxima. The row sums stay
+// in registers, one partial sum per row and thread, until the unit ends.
+//
+// A CTA: warps 0-7 do the softmax, two threads per token with half of the rows each (two groups
+// of four warps that never meet), warp 8 loads pages with TMA, warp 9 issues the products one tile
+// of scores ahead, warp 10 walks the run's units, describes them to the others and prepares their
+// queries. Scores and sums are double buffered in TMEM (256 columns), the ring holds 2.5 tiles of
+// K and V, two CTAs per SM.
+//
+// Bound by HBM: 2 D bytes per token and cache head. What else showed in clock stamps was cold
+// code (about 16 cycles per instruction the first time), hence one walker, rolled loops where
+// registers allow them, and half the rows per thread.
+#include <type_traits>
+
+#include "attend_mma.cuh"
+
+namespace dspark {
+namespace {
+
+constexpr int kRows = 32;
+constexpr int kSoftThreads = 256;
+constexpr int kThreads = 352;
+constexpr int kP = 64;                       // bytes of a token's row of weights: two pieces of 32
+constexpr int kPieces = 8;                   // described pieces
+// Weights are 2^(x - m + kUp) where m may lag the true maximum by kBehind: at most 2^8.5 < 448.
+// The second piece has columns of its own and is scaled by 2^4 more, so a weight is within 2^-8 of
+// itself or 2^-16 of the largest. A wide margin for m makes rescaling rare.
+constexpr float kUp = 2.0f;
+constexpr float kBehind = 6.5f;
+constexpr float kLowBack = 0.0625f;
+
+// A run's part of one unit.
+struct Piece {
+    int b, h, len, w;
+    int row0, flat0;     // the request's first packed row; the unit's first (position, head)
+    int rows;
+    int k0, n;           // tiles
+    int first_seen;
+    int whole, cut;      // nothing of the unit is elsewhere; it starts here and goes on elsewhere
+    int last;
+    int i0, g0;          // position and head of the unit's first row
+    int64_t unit_end;    // on the line of tiles
+};
+struct RowInfo {
+    int64_t out;         // element offset of the row's results
+    int64_t lse;
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kSlot = kTile * D;              // one tile's K or V
+    static constexpr int kSlots = D == 128 ? 5 : 10;     // K and V alternate
+    static constexpr int kNums = kSlots / 2 + 2;         // tiles whose numbers may still be read
+    uint8_t ring[kSlots][kSlot];
+    uint8_t q[2][2 * kRows * D];                         // two units' queries: hi rows, lo rows
+    uint8_t p[kTile * kP];                               // the weights, a row per token
+    BlockNums nums[kNums][kBlocks];
+    Piece piece[kPieces];
+    RowInfo info[4][kRows];                              // four units' rows
+    int2 see[4][kRows];                                  // first token seen, and how many past it
+    float f[4][kRows];                                   // score factors: scale log2(e) 2^e
+    RowInfo now_info[kRows];                             // the softmax's own copies of its unit's
+    __align__(16) int2 now_see[kRows];
+    __align__(16) float2 row[kRows];                                   // factor, reference - kUp (0: none seen)
+    __align__(16) float grow[kRows];                                   // 2^(old reference - new)
+    float part[4][kRows];                                // per-warp maxima or sums
+    int unseen[2];                                       // a row of the half has seen nothing yet
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t piece_full[kPieces], info_full[4], q_full[2], q_empty[2];
+    uint64_t s_full[2], pv_done[2], p_full;
+    Cut<kRows> cut;
+    uint32_t tmem;
+    int stalled;         // a wait gave up: every role leaves its loop
+};
+
+// TMEM columns: scores at 64 * (tile & 1), sums at 128 + 64 * (unit & 1).
+constexpr uint32_t kSums = 128;
+
+__device__ __forceinline__ int columns_of(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+
+// V^T as the first operand: its 128 lanes are the head's elements. Of a 64-wide head the second 64
+// lanes read the first ones again (the stride between swizzle atoms is 0) and are ignored.
+template <int D>
+__device__ __forceinline__ uint64_t v_operand(uint64_t v)
+{
+    return D == 128 ? v : v & ~(0x3fffull << 16);
+}
+
+template <int N>
+__device__ __forceinline__ void tc_ld(uint32_t addr, float* x)
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    if (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7])
+                     : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tc_st4(uint32_t addr, const float* x)
+{
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+// The four warps of a half: a barrier, and a barrier with a vote.
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+__device__ __forceinline__ bool half_any(int half, bool yes)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n"
+        " .reg .pred p, q;\n"
+        " setp.ne.u32 p, %1, 0;\n"
+        " barrier.cta.red.or.pred q, %2, 128, p;\n"
+        " selp.u32 %0, 1, 0, q;\n"
+        "}\n" : "=r"(r) : "r"(static_cast<uint32_t>(yes)), "r"(3 + half) : "memory");
+    return r != 0;
+}
+
+// v[0..N) of every lane, combined over the warp's 32 lanes: lane i gets row i % N. Each step
+// halves the rows a lane keeps, so N - 1 exchanges do what N full reductions would.
+template <int N, bool MAX>
+__device__ __forceinline__ float reduce_rows(float* v, int lane)
+{
+    auto both = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+#pragma unroll
+    for (int h = N / 2; h > 0; h >>= 1) {
+        const bool up = (lane & h) != 0;
+#pragma unroll
+        for (int j = 0; j < h; ++j) {
+            const float send = up ? v[j] : v[j + h], keep = up ? v[j + h] : v[j];
+            v[j] = both(keep, __shfl_xor_sync(0xffffffffu, send, h));
+        }
+    }
+    float y = v[0];
+#pragma unroll
+    for (int off = N; off < 32; off <<= 1) y = both(y, __shfl_xor_sync(0xffffffffu, y, off));
+    return y;
+}
+
+struct Token {
+    BlockNums n;
+    int t;
+};
+
+// One tile, this thread's token, HR rows from r0: scores in TMEM -> weights in shared memory;
+// l[j] += this token's weights.
+template <int D, int HR>
+__device__ __forceinline__ bool soften(Smem<D>& sm, const int2* see, int half, float* l, uint32_t s_addr,
+                                       uint32_t o_addr, const Token& k, bool mask, bool first, int it,
+                                       volatile int* stalled)
+{
+    constexpr int NR = 2 * HR;
+    constexpr int N = HR < 8 ? HR : 8;
+    const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3;
+    const int r0 = half * HR;
+    const float4* row2 = reinterpret_cast<const float4*>(sm.row + r0);
+    const int4* see2 = reinterpret_cast<const int4*>(see + r0);
+    float x[HR];
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+#pragma unroll
+        for (int c = 0; c < HR; c += N) {
+            float lo[N];
+            tc_ld<N>(s_addr + r0 + c, x + c);
+            tc_ld<N>(s_addr + NR + r0 + c, lo);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[c + j] += lo[j];
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < HR; r += 2) {
+            const float4 c = row2[r / 2];        // two rows' factor and reference
+            x[r] = fmaf(x[r], c.x * k.n.ks, k.n.bias - c.y);
+            x[r + 1] = fmaf(x[r + 1], c.z * k.n.ks, k.n.bias - c.w);
+            top = fmaxf(top, fmaxf(x[r], x[r + 1]));
+        }
+        if (mask) {
+            top = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < HR; r += 2) {
+                const int4 s = see2[r / 2];
+                if (static_cast<uint32_t>(k.t - s.x) > static_cast<uint32_t>(s.y)) x[r] = -INFINITY;
+                if (static_cast<uint32_t>(k.t - s.z) > static_cast<uint32_t>(s.w)) x[r + 1] = -INFINITY;
+                top = fmaxf(top, fmaxf(x[r], x[r + 1]));
+            }
+        }
+        if (pass) break;
+        if (!half_any(half, top > kUp + kBehind || sm.unseen[half])) break;
+        // The rows' maxima, as exponents over the present references; new references for the rows
+        // that passed theirs by too much and those that see their first tokens.
+        const float most = reduce_rows<HR, true>(x, lane);
+        if (lane < HR) sm.part[warp][r0 + lane] = most;
+        half_sync(half);
+        if ((tid & 127) < 32) {
+            const int r = r0 + (lane & (HR - 1));
+            const float over = fmaxf(fmaxf(sm.part[0][r], sm.part[1][r]), fmaxf(sm.part[2][r], sm.part[3][r]));
+            const float old = sm.row[r].y;
+            const bool none = old == 0.0f;
+            float y = old;
+            if (over > -INFINITY && (none || over > kUp + kBehind)) {
+                y = old + over - kUp;
+                if (y == 0.0f) y = 1e-30f;       // 0 stands for none
+            }
+            __syncwarp();
+            if (lane < HR) {
+                sm.grow[r] = none ? 1.0f : ex2_approx(old - y);
+                sm.row[r].y = y;
+            }
+            const bool any = __any_sync(0xffffffffu, y == 0.0f);
+            if (lane == 0) sm.unseen[half] = any;
+        }
+        half_sync(half);
+        if (first) continue;
+        // the tiles before this one have to be in the sums before these are scaled
+        if (it > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done[(it - 1) & 1]),
+                                                         ((it - 1) >> 1) & 1, stalled)))
+            return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < HR; c += 4) {
+            float o[4], lo[4];
+            tc_ld<4>(o_addr + r0 + c, o);
+            tc_ld<4>(o_addr + NR + r0 + c, lo);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[j] *= sm.grow[r0 + c + j];
+                lo[j] *= sm.grow[r0 + c + j];
+            }
+            tc_st4(o_addr + r0 + c, o);
+            tc_st4(o_addr + NR + r0 + c, lo);
+        }
+        tc_wait_st();
+#pragma unroll
+        for (int r = 0; r < HR; ++r) l[r] *= sm.grow[r0 + r];
+    }
+    // the last tile's products read the weights that these replace
+    if (it > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done[(it - 1) & 1]),
+                                                     ((it - 1) >> 1) & 1, stalled)))
+        return false;
+    uint32_t hi[HR / 4], lo[HR / 4];
+#pragma unroll
+    for (int c = 0; c < HR / 4; ++c) {
+        float* y = x + 4 * c;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y[j] = ex2_approx(y[j]);
+            l[4 * c + j] = fmaf(y[j], k.n.inv, l[4 * c + j]);
+        }
+        uint32_t h0, h1, l0, l1;
+        split2<true>(y[0], y[1], &h0, &l0);
+        split2<true>(y[2], y[3], &h1, &l1);
+        hi[c] = h0 | (h1 << 16);
+        lo[c] = l0 | (l1 << 16);
+    }
+    const int token = tid & 127;
+    uint8_t* p = &sm.p[token * kP];
+    const int swz = (token >> 1) & 3;            // the 64-byte swizzle: 16-byte chunks
+    uint8_t* ph = p + (((r0 >> 4) ^ swz) << 4) + (r0 & 15);
+    uint8_t* pl = p + ((((NR + r0) >> 4) ^ swz) << 4) + ((NR + r0) & 15);
+    if (HR == 16) {
+        *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    } else if (HR == 8) {
+        *reinterpret_cast<uint2*>(ph) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(pl) = make_uint2(lo[0], lo[1]);
+    } else {
+        *reinterpret_cast<uint32_t*>(ph) = hi[0];
+        *reinterpret_cast<uint32_t*>(pl) = lo[0];
+    }
+    return true;
+}
+
+// A finished piece: sums over the threads, results or a part written. Lane d holds element d.
+template <int D, int HR>
+__device__ __forceinline__ void finish(const AttendCall& A, Smem<D>& sm, const RowInfo* info, int half,
+                                       float* l, uint32_t o_addr, int rows, bool whole, int part,
+                                       const Workspace& ws)
+{
+    constexpr int NR = 2 * HR;
+    const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3;
+    const int r0 = half * HR;
+    const float mine = reduce_rows<HR, false>(l, lane);
+    if (lane < HR) sm.part[warp][r0 + lane] = mine;
+    half_sync(half);
+    const int r = r0 + (tid & 127);
+    if ((tid & 127) < HR && r < rows) {
+        const float sum = (sm.part[0][r] + sm.part[1][r]) + (sm.part[2][r] + sm.part[3][r]);
+        const float m = sm.row[r].y;             // reference - kUp, as the weights are
+        if (!whole)
+            ws.ml[part * kTile + r] = make_float2(sum == 0.0f ? kNone : m, sum);
+        else if (A.lse != nullptr)
+            A.lse[info[r].lse] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        sm.grow[r] = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;    // nothing seen: zeros
+    }
+    half_sync(half);
+    const int d = tid & 127;
+    uint16_t* out = static_cast<uint16_t*>(A.out) + d;
+    float* po = ws.o + static_cast<int64_t>(part) * kTile * D + d;
+#pragma unroll 1
+    for (int c = r0; c < r0 + HR; c += 4) {
+        if (c >= rows) break;
+        float o[4], lo[4];
+        int64_t at[4];
+        tc_ld<4>(o_addr + c, o);
+        tc_ld<4>(o_addr + NR + c, lo);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) at[j] = info[c + j].out;
+        const float4 g = *reinterpret_cast<const float4*>(sm.grow + c);
+        tc_wait_ld();
+        o[0] = fmaf(lo[0], kLowBack, o[0]) * g.x;
+        o[1] = fmaf(lo[1], kLowBack, o[1]) * g.y;
+        o[2] = fmaf(lo[2], kLowBack, o[2]) * g.z;
+        o[3] = fmaf(lo[3], kLowBack, o[3]) * g.w;
+        if (D == 128 || d < D) {                 // D = 64: lanes 64.. repeat the first ones
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (whole && c + j < rows) store1<DSPARK_BF16>(out, at[j], o[j]);
+                if (!whole && c + j < rows) po[(c + j) * D] = o[j];
+            }
+        }
+    }
+}
+
+// One pass of 32 lanes over a unit's queries, as two pieces in shared memory: a lane takes 16
+// elements of row `row` (of D / 16 such segments), the row's factor and what the softmax needs to
+// know of it go to slot `slot`. Rows past the unit's are zeros.
+template <int D>
+static __device__ __noinline__ void load_queries(const AttendCall& A, Smem<D>& sm, const Piece& pc, int slot,
+                                                 uint8_t* q, int row, int nr)
+{
+    constexpr int S = D / 16;
+    const int seg = threadIdx.x & (S - 1);
+    const bool live = row < pc.rows;
+    int i = pc.i0, g = pc.g0 + (live ? row : pc.rows - 1);
+    if (g >= A.group) {
+        const int more = g / A.group;
+        i += more;
+        g -= more * A.group;
+    }
+    const int64_t prow = pc.row0 + i;
+    const int head = pc.h * A.group + g;
+    const uint16_t* at = static_cast<const uint16_t*>(A.q) + prow * A.q_stride + static_cast<int64_t>(head) * D + seg * 16;
+    uint4 v[2];
+    if ((reinterpret_cast<uintptr_t>(at) & 15u) == 0) {
+        v[0] = reinterpret_cast<const uint4*>(at)[0];
+        v[1] = reinterpret_cast<const uint4*>(at)[1];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = at[8 * j + 2 * k] | (static_cast<uint32_t>(at[8 * j + 2 * k + 1]) << 16);
+            v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t top = 0;                            // magnitudes' bits order like them, NaN above all
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (!live) w[k] = 0;
+        top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+    }
+#pragma unroll
+    for (int off = 1; off < S; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const bool fine = top < 0x7f80u;
+    const int e = fine ? scale_exponent(__uint_as_float(top << 16)) : 0;
+    const float inv = exp2i(-e);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float y[4] = {bf16_lo(w[2 * k]) * inv, bf16_hi(w[2 * k]) * inv,
+                            bf16_lo(w[2 * k + 1]) * inv, bf16_hi(w[2 * k + 1]) * inv};
+        float z[4];
+        hi[k] = e4m3x4(y[0], y[1], y[2], y[3]);
+        e4m3x4_to_f32(hi[k], z);
+        lo[k] = e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int rr = p * nr + row;
+        const int chunk = seg ^ (D == 128 ? rr & 7 : (rr >> 1) & 3);
+        *reinterpret_cast<uint4*>(q + rr * D + chunk * 16) =
+            p ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    }
+    if (seg == 0) {
+        const int pos = pc.len + i;
+        const int first = A.window > 0 && pos >= A.window ? pos - A.window + 1 : 0;
+        sm.info[slot][row].out = prow * A.out_stride + static_cast<int64_t>(head) * D;
+        sm.info[slot][row].lse = prow * A.q_heads + head;
+        sm.see[slot][row] = make_int2(first, pos - first);
+        // a query that is not finite makes its row's factor, hence its results, NaN
+        sm.f[slot][row] = fine ? A.scale * kLog2e * exp2i(e) : __int_as_float(0x7fc00000);
+    }
+}
+
+__device__ __forceinline__ void describe(const AttendCall& A, const Walk<kRows>& wk, Piece& p)
+{
+    p.b = wk.b;
+    p.h = wk.h;
+    p.len = wk.len;
+    p.w = wk.w;
+    p.row0 = wk.row0;
+    p.flat0 = wk.qt * kRows;
+    p.rows = wk.rows(A);
+    p.i0 = p.flat0 == 0 ? 0 : p.flat0 / A.group;
+    p.g0 = p.flat0 - p.i0 * A.group;
+    p.k0 = wk.k0;
+    p.n = wk.n;
+    p.first_seen = wk.first_seen(A);
+    p.whole = wk.whole();
+    p.cut = wk.k0 == wk.a && !p.whole;
+    p.last = wk.last();
+    p.unit_end = wk.unit_end();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(
+        raw + ((kSmemAlign - (smem_addr(raw) & (kSmemAlign - 1))) & (kSmemAlign - 1)));
+    constexpr int kSlots = Smem<D>::kSlots;
+    constexpr int kNums = Smem<D>::kNums;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Workspace ws = workspace_of(A.ws);
+
+    if (tid < kSlots) {
+        mbar_init(smem_addr(&sm.full[tid]), 1);
+        mbar_init(smem_addr(&sm.empty[tid]), 1);
+    } else if (tid >= 32 && tid < 32 + kPieces) {
+        const int s = tid - 32;
+        mbar_init(smem_addr(&sm.piece_full[s]), 1);
+        if (s < 4) mbar_init(smem_addr(&sm.info_full[s]), 32);
+        if (s < 2) {
+            mbar_init(smem_addr(&sm.q_full[s]), 32);
+            mbar_init(smem_addr(&sm.q_empty[s]), 1);
+            mbar_init(smem_addr(&sm.s_full[s]), 1);
+            mbar_init(smem_addr(&sm.pv_done[s]), 1);
+        }
+        if (s == 2) mbar_init(smem_addr(&sm.p_full), kSoftThreads);
+        if (s == 3) sm.stalled = 0;
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;"
+                     ::"r"(smem_addr(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_fence_before();
+    }
+    pdl_wait_and_trigger();
+    const int64_t total = cut_line<kRows, kThreads>(A, sm.cut);
+    if (tid == 0) ws.meta[blockIdx.x].cut = 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    volatile int* stalled = &sm.stalled;
+    if (sm.cut.walk.n > 0) {
+        if (warp == 10) {
+            // ---- the walk: pieces described up to three ahead; queries from the second on ----
+            Walk<kRows> wk = sm.cut.walk;
+            int described = 0;
+            bool more = true, ok = true;
+#pragma unroll 1
+            for (int piece = 0; ok; ++piece) {
+#pragma unroll 1
+                while (more && described <= piece + 2) {
+                    if (lane == 0) {
+                        describe(A, wk, sm.piece[described & (kPieces - 1)]);
+                        mbar_arrive(smem_addr(&sm.piece_full[described & (kPieces - 1)]));
+                    }
+                    __syncwarp();
+                    ++described;
+                    more = !wk.last();
+                    if (more) wk.next(A);
+                }
+                if (piece == described) break;
+                const Piece& pc = sm.piece[piece & (kPieces - 1)];
+                if (piece > 0) {
+                    const int nr = columns_of(pc.rows);
+                    if (piece >= 2)
+                        ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.q_empty[piece & 1]),
+                                                               ((piece >> 1) & 1) ^ 1, stalled));
+                    if (!ok) break;
+                    constexpr int S = D / 16;
+#pragma unroll 1
+                    for (int r = lane / S; r < nr; r += 32 / S)
+                        load_queries<D>(A, sm, pc, piece & 3, sm.q[piece & 1], r, nr);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(smem_addr(&sm.q_full[piece & 1]));
+                    mbar_arrive(smem_addr(&sm.info_full[piece & 3]));
+                }
+            }
+        } else if (warp == 8) {
+            // ---- pages in ----
+            const int per_tile = kTile / A.c.page;
+            const uint32_t box = static_cast<uint32_t>(A.c.page) * D;
+            const int beyond = A.c.n_pages * A.c.heads * A.c.page;     // a row past the tensor: zeros
+            int bad = 0, issued = 0, slot = 0, num = 0;
+            uint32_t phase = 0;                              // parity of this use of the slot
+            bool ok = true;
+#pragma unroll 1
+            for (int piece = 0; ok; ++piece) {
+                const Piece& pc = sm.piece[piece & (kPieces - 1)];
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.piece_full[piece & (kPieces - 1)]),
+                                                       (piece / kPieces) & 1, stalled));
+                if (!ok) break;
+                const int h = pc.h, n = pc.n, lo = pc.first_seen;
+                const bool last = pc.last;
+                const int32_t* table = A.c.table + static_cast<int64_t>(pc.b) * A.c.width;
+                const int total_blocks = (pc.len + pc.w + A.c.page - 1) / A.c.page;
+                // 32 blocks at a time, one per lane; the next 32 are fetched while these load
+                int base = pc.k0 * per_tile;
+                const int end_block = base + n * per_tile;
+                auto id_of = [&](int j) -> int {        // -1: dead, not there, or not a page
+                    if (j >= end_block || j >= total_blocks || (j + 1) * A.c.page <= lo) return -1;
+                    const int id = j < A.c.width ? table[j] : -1;
+                    if (id < 0 || id >= A.c.n_pages) { bad = 1; return -1; }
+                    return id;
+                };
+                int id = -1, next_id = id_of(base + lane), j0 = 32;
+                float2 sc = make_float2(0.0f, 0.0f);
+                base -= 32;
+#pragma unroll 1
+                for (int k = 0; k < n; ++k) {
+                    if (j0 == 32) {                          // the next 32 blocks
+                        j0 = 0;
+                        base += 32;
+                        id = next_id;
+                        if (id >= 0) {
+                            const int64_t bh = static_cast<int64_t>(id) * A.c.heads + h;
+                            sc = make_float2(A.c.k_scale[bh], A.c.v_scale[bh]);
+                        }
+                        next_id = id_of(base + 32 + lane);
+                    }
+                    const int src = j0 + (lane & (per_tile - 1));
+                    const int my_id = __shfl_sync(0xffffffffu, id, src);
+                    const bool there = lane < per_tile && base + src < total_blocks;
+                    const int count = __popc(__ballot_sync(0xffffffffu, there));
+                    const int row = my_id < 0 ? beyond : (my_id * A.c.heads + h) * A.c.page;
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (issued >= kSlots)
+                            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.empty[slot]), phase ^ 1u, stalled));
+                        if (!ok) break;
+                        const uint32_t full = smem_addr(&sm.full[slot]);
+                        if (kv == 1) {
+                            const float ks = __shfl_sync(0xffffffffu, sc.x, src);
+                            const float vs = __shfl_sync(0xffffffffu, sc.y, src);
+                            BlockNums b;
+                            b.ks = my_id < 0 ? 0.0f : ks;
+                            b.bias = my_id < 0 ? -INFINITY : __log2f(vs);
+                            b.inv = my_id < 0 ? 0.0f : ex2_approx(-b.bias);
+                            b.pad = 0.0f;
+                            if (lane < per_tile) sm.nums[num][lane] = b;
+                            if (++num == kNums) num = 0;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_expect_tx(full, count * box);
+                        __syncwarp();
+                        if (there)
+                            tma_load(smem_addr(sm.ring[slot]) + lane * box, kv ? &v_map : &k_map, row, full);
+                        ++issued;
+                        if (++slot == kSlots) { slot = 0; phase ^= 1u; }
+                    }
+                    if (!ok) break;
+                    j0 += per_tile;
+                }
+                if (last) break;
+            }
+            if (bad) raise_status(A.status, DSPARK_STATUS_BAD_PAGE);
+            // every started copy lands before the CTA may leave
+            __syncwarp();
+#pragma unroll 1
+            for (int s = 0; s < kSlots && s < issued; ++s)
+                drain(smem_addr(&sm.full[s]), ((issued - 1 - s) / kSlots) & 1, stalled);
+        } else if (warp == 9) {
+            // ---- products: the warp runs as one, an elected lane issues ----
+            const bool leader = elect_one();
+            constexpr uint32_t kIdesc = (1u << 4) | (kTile / 16 << 24);
+            // V^T: the head's elements are contiguous, and so are the weights' rows
+            constexpr uint32_t kIdescPV = kIdesc | (1u << 15) | (1u << 16);
+            const uint32_t tmem = sm.tmem;
+            const uint64_t ring0 = operand<D>(smem_addr(sm.ring[0]));
+            const uint64_t q_op = operand<D>(smem_addr(sm.q[0]));
+            const uint64_t p_op = operand<kP>(smem_addr(sm.p));
+            constexpr uint32_t kStep = Smem<D>::kSlot / 16;
+            constexpr uint32_t kQStep = sizeof(sm.q[0]) / 16;
+            // the scores run one tile ahead of the sums: their own place in the pieces
+            int pa = -1, left_a = 0, it_a = 0, slot_a = 0;
+            uint32_t phase_a = 0, columns_a = 0;
+            bool last_a = false, ready = true, ok = true;
+            auto test = [&](uint32_t bar, uint32_t parity, bool wait) -> bool {
+                return __all_sync(0xffffffffu, mbar_try(bar, parity) || (wait && mbar_wait_slow(bar, parity, stalled)));
+            };
+            // the scores of tile it_a; unless `wait`, only if everything is there already
+            auto scores = [&](bool wait) -> bool {
+                if (left_a == 0) {
+                    if (ready) { ++pa; ready = false; }
+                    const int s = pa & (kPieces - 1);
+                    if (!test(smem_addr(&sm.piece_full[s]), (pa / kPieces) & 1, wait)) return false;
+                    if (!test(smem_addr(&sm.q_full[pa & 1]), (pa >> 1) & 1, wait)) return false;
+                    ready = true;
+                    left_a = sm.piece[s].n;
+                    last_a = sm.piece[s].last;
+                    columns_a = columns_of(sm.piece[s].rows) >> 2 << 17;
+                }
+                if (!test(smem_addr(&sm.full[slot_a]), phase_a, wait)) return false;
+                tc_fence_after();
+                --left_a;
+                if (leader) {
+                    const uint64_t a = ring0 + slot_a * kStep, b = q_op + (pa & 1) * kQStep;
+#pragma unroll
+                    for (int s = 0; s < D / 32; ++s)
+                        mma_ss(tmem + 64 * (it_a & 1), a + 2 * s, b + 2 * s, kIdesc | columns_a, s > 0);
+                    tc_commit(smem_addr(&sm.s_full[it_a & 1]));
+                    tc_commit(smem_addr(&sm.empty[slot_a]));
+                    if (left_a == 0) tc_commit(smem_addr(&sm.q_empty[pa & 1]));
+                }
+                __syncwarp();
+                slot_a += 2;
+                if (slot_a >= kSlots) { slot_a -= kSlots; phase_a ^= 1u; }
+                ++it_a;
+                return true;
+            };
+            int it = 0, piece = -1, left = 0, slot = 1;
+            uint32_t phase = 0, idesc = 0, o_addr = 0;
+            bool last = false, fresh = true;
+#pragma unroll 1
+            while (true) {
+                // this tile's scores by all means, the next one's if they can start
+#pragma unroll 1
+                while (it_a <= it + 1 && !(last_a && left_a == 0)) {
+                    const bool must = it_a == it;
+                    if (!scores(must)) { ok = !must; break; }
+                }
+                if (!ok) break;
+                if (left == 0) {
+                    const Piece& pc = sm.piece[++piece & (kPieces - 1)];
+                    left = pc.n;
+                    last = pc.last;
+                    idesc = kIdescPV | (columns_of(pc.rows) >> 2 << 17);
+                    o_addr = tmem + kSums + 64 * (piece & 1);
+                    fresh = true;
+                }
+                ok = test(smem_addr(&sm.p_full), it & 1, true) && test(smem_addr(&sm.full[slot]), phase, true);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint64_t a = v_operand<D>(ring0 + slot * kStep);
+#pragma unroll
+                    for (int s = 0; s < kTile / 32; ++s)
+                        mma_ss(o_addr, a + s * (32 * D / 16), p_op + s * (32 * kP / 16), idesc, !fresh || s > 0);
+                    tc_commit(smem_addr(&sm.pv_done[it & 1]));
+                    tc_commit(smem_addr(&sm.empty[slot]));
+                }
+                __syncwarp();
+                fresh = false;
+                slot += 2;
+                if (slot >= kSlots) { slot -= kSlots; phase ^= 1u; }
+                ++it;
+                if (--left == 0 && last) break;
+            }
+            // the last products' arrivals on the barriers land before the CTA leaves
+            if (it > 0) {
+                const int uk = 2 * (it - 1), uv = uk + 1;
+                drain(smem_addr(&sm.empty[uk % kSlots]), (uk / kSlots) & 1, stalled);
+                drain(smem_addr(&sm.empty[uv % kSlots]), (uv / kSlots) & 1, stalled);
+                drain(smem_addr(&sm.q_empty[piece & 1]), (piece >> 1) & 1, stalled);
+            }
+            __syncwarp();
+        } else {
+            // ---- softmax ----
+            const int half = warp >> 2;
+            const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+            const int token = tid & 127;
+            const int my_block = token / A.c.page;
+            int it = 0, piece = 0, slot = 1, num = 0;
+            uint32_t phase = 0;
+            bool ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.piece_full[0]), 0, stalled));
+            if (ok) {                            // the first unit's queries: all eight warps
+                const int nr = columns_of(sm.piece[0].rows);
+                constexpr int S = D / 16;
+                if (warp * 32 / S < nr) load_queries<D>(A, sm, sm.piece[0], 0, sm.q[0], tid / S, nr);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            asm volatile("bar.sync 5, 256;" ::: "memory");
+            if (warp == 0) {
+                mbar_arrive(smem_addr(&sm.q_full[0]));
+                mbar_arrive(smem_addr(&sm.info_full[0]));
+            }
+            auto run_piece = [&](auto tag) -> bool {
+                constexpr int HR = decltype(tag)::value;
+                const Piece& pc = sm.piece[piece & (kPieces - 1)];
+                const RowInfo* info = sm.now_info;
+                const int2* see = sm.now_see;
+                const int n = pc.n, rows = pc.rows;
+                float l[HR];
+#pragma unroll
+                for (int r = 0; r < HR; ++r) l[r] = 0.0f;
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.info_full[piece & 3]),
+                                                             (piece >> 2) & 1, stalled));
+                // copied: the walk may describe the piece after the next three over these
+                if (token < HR) {
+                    const int r = half * HR + token;
+                    sm.row[r] = make_float2(sm.f[piece & 3][r], 0.0f);
+                    sm.now_info[r] = sm.info[piece & 3][r];
+                    sm.now_see[r] = sm.see[piece & 3][r];
+                }
+                if (token == 0) sm.unseen[half] = 1;
+                // tiles that every row sees whole need no mask
+                const int first_pos = sm.see[piece & 3][0].x + sm.see[piece & 3][0].y;
+                const int last_lo = sm.see[piece & 3][rows - 1].x;
+                half_sync(half);
+                const int stored = pc.len + pc.w;
+                const uint32_t o_addr = sm.tmem + lanes + kSums + 64 * (piece & 1);
+                // a warp whose wait gave up goes on to the piece's end, where the warps agree on it:
+                // they share the barriers within
+                Token t;
+                t.t = pc.k0 * kTile + token;
+#pragma unroll 1
+                for (int k = 0; k < n; ++k, ++it, t.t += kTile) {
+                    const int token0 = t.t - token;
+                    ok = ok && mbar_wait(smem_addr(&sm.full[slot]), phase, stalled) &&
+                         mbar_wait(smem_addr(&sm.s_full[it & 1]), (it >> 1) & 1, stalled);
+                    ok = __all_sync(0xffffffffu, ok);
+                    tc_fence_after();
+                    t.n = sm.nums[num][my_block];
+                    if (++num == kNums) num = 0;
+                    const bool mask = token0 + kTile - 1 > first_pos || token0 < last_lo;
+                    ok = soften<D, HR>(sm, see, half, l, sm.tmem + lanes + 64 * (it & 1), o_addr, t, mask, k == 0,
+                                       it, stalled) && ok;
+                    tc_fence_before();
+                    if (t.t >= stored) {         // a slot past the last token: 0 x NaN is NaN
+                        uint4* v = reinterpret_cast<uint4*>(&sm.ring[slot][token * D + half * (D / 2)]);
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) v[c] = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if (ok) mbar_arrive(smem_addr(&sm.p_full));
+                    slot += 2;
+                    if (slot >= kSlots) { slot -= kSlots; phase ^= 1u; }
+                }
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done[(it - 1) & 1]),
+                                                             ((it - 1) >> 1) & 1, stalled));
+                if (half_any(half, !ok)) return false;
+                tc_fence_after();
+                finish<D, HR>(A, sm, info, half, l, o_addr, rows, pc.whole, blockIdx.x * 2 + (piece > 0), ws);
+                return true;
+            };
+#pragma unroll 1
+            for (; ok; ++piece) {
+                const Piece& pc = sm.piece[piece & (kPieces - 1)];
+                // the roles before this one have seen the description; so has this thread, by them
+                if (piece > 0)
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.piece_full[piece & (kPieces - 1)]),
+                                                           (piece / kPieces) & 1, stalled));
+                if (half_any(half, !ok)) break;
+                const int nr = columns_of(pc.rows);
+                ok = nr == 8 ? run_piece(std::integral_constant<int, 4>{})
+                   : nr == 16 ? run_piece(std::integral_constant<int, 8>{})
+                              : run_piece(std::integral_constant<int, 16>{});
+                if (!ok) break;
+                if (tid == 0 && pc.cut) {
+                    RunMeta& m = ws.meta[blockIdx.x];
+                    m.total = total;
+                    m.unit_end = pc.unit_end;
+                    m.slot = piece > 0;
+                    m.row0 = pc.row0;
+                    m.rows = pc.rows;
+                    m.flat0 = pc.flat0;
+                    m.head0 = pc.h * A.group;
+                    m.cut = 1;
+                }
+                if (pc.last) break;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && sm.stalled) raise_status(A.status, DSPARK_STATUS_STALL);
+    if (warp == 9)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(sm.tmem));
+}
+
+template <int D>
+int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
+{
+    const size_t smem = sizeof(Smem<D>) + kSmemAlign;
+    static bool ready[64] = {};               // opt-in to large shared memory, once per device
+    if (!ready[device]) {
+        const cudaError_t e = cudaFuncSetAttribute(attend_narrow_kernel<D>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return fail(DSPARK_ERR_CUDA, "dspark attend: %s", cudaGetErrorString(e));
+        }
+        ready[device] = true;
+    }
+    CUtensorMap k_map, v_map;
+    int rc = encode_cache(&k_map, A.c.k, A.c);
+    if (rc == DSPARK_OK) rc = encode_cache(&v_map, A.c.v, A.c);
+    if (rc != DSPARK_OK) return rc;
+    return launch_pdl("attend", attend_narrow_kernel<D>, dim3(ctas), dim3(kThreads), smem, stream, A,
+                      k_map, v_map);
+}
+
+}  // namespace
+
+int launch_attend_narrow(const AttendCall& A, int ctas, int device, cudaStream_t stream)
+{
+    return A.c.dim == 128 ? launch<128>(A, ctas, device, stream) : launch<64>(A, ctas, device, stream);
+}
+
+}  // namespace dspark

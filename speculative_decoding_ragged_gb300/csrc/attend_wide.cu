@@ -1,312 +1,22 @@
-// attend_mma.cu — dspark_attend on the tensor cores: bf16 queries over the e4m3 cache, head
-// sizes 64 and 128.
-//
-// Mathematics. For a row r (one position, one query head) and tokens t with block scales ks, vs:
-//   x_t = log2(e) scale q.K_t + log2 vs_t,   w_t = 2^(x_t - m),   O = sum_t w_t Vcode_t,
-//   l = sum_t w_t / vs_t,   out = O / l,     lse = ln 2 (m + log2 l).
-// Putting the value's scale into the exponent makes every product of the value side a plain
-// product of codes, keeps w_t <= 1 whatever the blocks' scales, and costs nothing: it is the
-// addend of the multiply-add that scales the score.
-//
-// The cache stays in its 8 bits all the way into the tensor cores (kind::f8f6f4). What is not
-// 8-bit is split into e4m3 pieces that accumulate into the same fp32 sums: a bf16 query element
-// has 8 significant bits, an e4m3 piece 4, so two pieces (over a power of two per row) hold it
-// exactly down to 2^-17 of the row's largest; a weight in two pieces is within 2^-8 (6e-4 rms,
-// below the rounding of the bf16 result). Compared with widening K and V to 16 bits in shared
-// memory this needs no conversion of the cache and moves half the shared-memory bytes; the
-// second piece doubles the 8-bit products, which run at twice the 16-bit rate.
-//
-// Work. A unit is (request, cache head, 128 of its rows); its visible tokens come in tiles of
-// 128. All tiles of all units form one line, which the persistent grid (two CTAs per SM) cuts
-// into equal runs, so one long request and many short ones balance alike; every CTA computes the
-// cut from cu_seqlens and lengths on the device. A unit cut by a run's end leaves (m, l, O) parts
-// in the workspace that attend_join_kernel joins.
+// attend_wide.cu — dspark_attend on the tensor cores for prompts and large groups: units of up to
+// 128 rows, one row per TMEM lane.
 //
 // A CTA: warp 4 loads pages with TMA (one box per page and K or V, swizzled), warp 5 issues the
-// products, warps 0-3 do the softmax with one TMEM lane (row) per thread. Rows are at most 128
-// lanes; a unit of at most 64 or 32 rows (decode and verify) puts 2 or 4 copies of them in the
-// lanes and each copy takes 1/2 or 1/4 of every tile's tokens, so all four warps share the
-// softmax; the copies' products write their own lanes only (the instruction's lane mask) and
-// join at the unit's end like parts.
+// products, warps 0-3 do the softmax with one TMEM lane (row) per thread. A unit of at most 64 or
+// 32 rows puts 2 or 4 copies of them in the lanes and each copy takes 1/2 or 1/4 of every tile's
+// tokens, so all four warps share the softmax; the copies' products write their own lanes only
+// (the instruction's lane mask) and join at the unit's end like parts.
 // The weights overlay the scores in TMEM: 128 + dim columns, so two CTAs fit and one's softmax
 // runs under the other's products.
-//
-// Bound: HBM for decode and verify (2 dim bytes per token and cache head; the products take
-// 1024 of about 1400 cycles that a tile's 32 KB take to arrive), for prompts the softmax's
-// instruction issue next to the products.
-#include <cuda.h>
-
-#include "attend.cuh"
-#include "rope.cuh"
+#include "attend_mma.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kTile = 128;                   // tokens per tile, rows per unit
+constexpr int kRows = 128;
 constexpr int kSoftThreads = 128;
 constexpr int kThreads = 192;
-constexpr int kMaxCtas = 304;                // parts the workspace holds: two CTAs on 152 SMs
-constexpr int kBlocks = kTile / 16;          // most blocks in a tile
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNone = -1e30f;              // a row's reference before it has seen a token
-// Weights are stored as 2^(x - m + kShift) where m may lag the true maximum by kLag: at most
-// 2^8.5 < 448, and a weight keeps two full pieces down to 2^-12 of the largest.
-constexpr float kShift = 6.0f;
-constexpr float kLag = 2.5f;
-constexpr long long kWaitCycles = 1ll << 31;
 
-// What the join needs to know of a CTA's run.
-struct RunMeta {
-    int64_t total;      // tiles of the whole call
-    int64_t unit_end;   // global tile where the cut unit ends
-    int cut;            // 1: the run's last unit starts here and continues in the next runs
-    int slot;           // the part it left here
-    int row0, rows;     // the unit's first packed row and its rows (position, head) ...
-    int flat0, head0;   // ... from this flat index, first query head
-};
-
-struct Workspace {
-    RunMeta* meta;      // [kMaxCtas]
-    float2* ml;         // [kMaxCtas][2][kTile]
-    float* o;           // [kMaxCtas][2][kTile][dim]
-};
-__host__ __device__ inline Workspace workspace_of(void* ws, int)
-{
-    char* p = static_cast<char*>(ws);
-    Workspace w;
-    w.meta = reinterpret_cast<RunMeta*>(p);
-    w.ml = reinterpret_cast<float2*>(p + kMaxCtas * sizeof(RunMeta));
-    w.o = reinterpret_cast<float*>(p + kMaxCtas * (sizeof(RunMeta) + 2 * kTile * sizeof(float2)));
-    return w;
-}
-
-// ---- PTX -----------------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t smem_addr(const void* p)
-{
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n"
-        " .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n"
-        "}\n"
-        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-    return done != 0;
-}
-// Bounded wait for the phase of this parity. Once any thread of the CTA has given up (about a
-// second), *stalled is set and every wait returns false, so that all roles leave their loops.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* stalled)
-{
-    if (mbar_try(bar, parity)) return true;
-    const long long deadline = clock64() + kWaitCycles;
-    while (!mbar_try(bar, parity)) {
-        if (*stalled) return false;
-        if (clock64() > deadline) { *stalled = 1; return false; }
-    }
-    return true;
-}
-// The same bound, but not cut short by another wait's end: for what is in flight.
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, volatile int* stalled)
-{
-    const long long deadline = clock64() + kWaitCycles;
-    while (!mbar_try(bar, parity))
-        if (clock64() > deadline) { *stalled = 1; return; }
-}
-// A page's box of the [rows, dim] tensor of codes -> shared memory.
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// The barrier's arrival follows the completion of every product this thread issued before.
-__device__ __forceinline__ void tc_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 ::"r"(bar) : "memory");
-}
-// D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile(
-        "{\n"
-        " .reg .pred p;\n"
-        " setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
-}
-// D[tmem] (+)= A[tmem] B[smem], lanes of quarter i untouched where off<i> is all ones.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc,
-                                       uint32_t off0, uint32_t off1, uint32_t off2, uint32_t off3)
-{
-    asm volatile(
-        "{\n"
-        " .reg .pred p;\n"
-        " setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n"
-        "}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(off0), "r"(off1), "r"(off2),
-        "r"(off3) : "memory");
-}
-__device__ __forceinline__ void tc_ld32(uint32_t addr, float* x)
-{
-    uint32_t* r = reinterpret_cast<uint32_t*>(x);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void tc_st32(uint32_t addr, const float* x)
-{
-    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-        ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
-}
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-        ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]) : "memory");
-}
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// ---- the line of tiles ---------------------------------------------------------------------
-struct Shape {                   // a unit's visible tiles [a, z]
-    int a, z;
-};
-__device__ __forceinline__ Shape unit_tiles(const AttendCall& A, int w, int len, int qt)
-{
-    const int i0 = qt * kTile / A.group;
-    const int64_t last = min(static_cast<int64_t>(qt + 1) * kTile, static_cast<int64_t>(w) * A.group) - 1;
-    const int i1 = static_cast<int>(last / A.group);
-    const int p0 = len + i0;
-    const int lo = A.window > 0 && p0 >= A.window ? p0 - A.window + 1 : 0;
-    return {lo / kTile, (len + i1) / kTile};
-}
-__device__ __forceinline__ int row_tiles(const AttendCall& A, int w)
-{
-    return static_cast<int>((static_cast<int64_t>(w) * A.group + kTile - 1) / kTile);
-}
-__device__ __forceinline__ int64_t head_tiles(const AttendCall& A, int w, int len)
-{
-    int64_t n = 0;
-    const int nq = row_tiles(A, w);
-    for (int qt = 0; qt < nq; ++qt) {
-        const Shape s = unit_tiles(A, w, len, qt);
-        n += s.z - s.a + 1;
-    }
-    return n;
-}
-
-// The units of one run in order, the same in every role.
-struct Walk {
-    int b, h, qt, nq;
-    int row0, w, len;
-    int a, z, k0, n;             // the unit's tiles [a, z]; this piece: n tiles from k0
-    int64_t left;                // tiles of the run from this piece on
-
-    __device__ __forceinline__ void request(const AttendCall& A)
-    {
-        int bits = 0;
-        while (true) {           // the next request with rows; there is one while left > 0
-            request_rows(A, b, &row0, &w, &len, &bits);
-            if (w > 0 || b + 1 >= A.B) break;
-            ++b;
-        }
-        nq = row_tiles(A, w);
-    }
-    __device__ __forceinline__ void unit(const AttendCall& A, int skip)
-    {
-        const Shape s = unit_tiles(A, w, len, qt);
-        a = s.a;
-        z = s.z;
-        k0 = a + skip;
-        n = static_cast<int>(min(static_cast<int64_t>(z - k0 + 1), left));
-    }
-    __device__ __forceinline__ void start(const AttendCall& A, int b0, int64_t off, int64_t tiles)
-    {
-        b = b0;
-        left = tiles;
-        request(A);
-        const int64_t per = head_tiles(A, w, len);
-        h = static_cast<int>(off / per);
-        off -= h * per;
-        qt = 0;
-        while (true) {
-            const Shape s = unit_tiles(A, w, len, qt);
-            if (off < s.z - s.a + 1) break;
-            off -= s.z - s.a + 1;
-            ++qt;
-        }
-        unit(A, static_cast<int>(off));
-    }
-    // false at the run's end
-    __device__ __forceinline__ bool next(const AttendCall& A)
-    {
-        left -= n;
-        if (left <= 0) return false;
-        if (++qt == nq) {
-            qt = 0;
-            if (++h == A.c.heads) {
-                h = 0;
-                ++b;
-                request(A);
-            }
-        }
-        unit(A, 0);
-        return true;
-    }
-    __device__ __forceinline__ int rows(const AttendCall& A) const
-    {
-        return static_cast<int>(min(static_cast<int64_t>(kTile),
-                                    static_cast<int64_t>(w) * A.group - static_cast<int64_t>(qt) * kTile));
-    }
-};
-
-// A block's numbers in a tile: score factor, exponent addend, 1 / value scale.
-struct __align__(16) BlockNums {
-    float ks, bias, inv, pad;
-};
-
-constexpr uint32_t kSmemAlign = 1024;        // the 128-byte swizzle's period
 template <int D>
 struct Smem {
     static constexpr int kSlot = kTile * D;              // one tile's K or V; 1024-byte aligned in order
@@ -317,23 +27,11 @@ struct Smem {
     float2 ml[kTile];
     uint64_t full[kSlots], empty[kSlots];
     uint64_t s_full, p_full, pv_done, q_full;
-    int64_t scan[kThreads / 32];
-    int64_t run_off;
-    int64_t total;
-    int run_b;
+    Cut<kRows> cut;
     uint32_t tmem;
     int stalled;       // a wait gave up: every role leaves its loop
     int quit;          // the same, as the softmax warps agreed on it at a barrier
 };
-
-// K-major and MN-major operands share the TMA swizzle: rows of D bytes, groups of 8 rows.
-template <int D>
-__device__ __forceinline__ uint64_t operand(uint32_t addr)
-{
-    constexpr uint64_t swizzle = D == 128 ? 2 : 4;       // 128- or 64-byte
-    return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (1ull << 16) |
-           (static_cast<uint64_t>(8 * D / 16) << 32) | (1ull << 46) | (swizzle << 61);
-}
 
 // ---- softmax -------------------------------------------------------------------------------
 struct Row {
@@ -371,20 +69,6 @@ __device__ __forceinline__ float max32(const float* x)
         d = fmaxf(d, x[j + 3]);
     }
     return fmaxf(fmaxf(a, b), fmaxf(c, d));
-}
-// A pair of weights in two e4m3 pieces each. The weights go through fp16 (11 bits, 2^-12: a
-// sixteenth of what the pieces are off by); the remainder is exact there.
-__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo)
-{
-    uint32_t w, back, rest;
-    uint16_t h, s;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(w));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(w), "r"(back));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(s) : "r"(rest));
-    *hi = h;
-    *lo = s;
 }
 // Exponents -> weights, their sum, and the pieces (8 words each) at p[0..7], p[8..15].
 __device__ __forceinline__ void weights(float* x, Row& r, const BlockNums& n0, const BlockNums& n1,
@@ -536,7 +220,7 @@ __device__ __forceinline__ int load_query(const AttendCall& A, Smem<D>& sm, int 
 // A finished piece: the copies' sums joined and written, as results or as a part.
 template <int D>
 __device__ __forceinline__ void finish(const AttendCall& A, Smem<D>& sm, const Row& r, uint32_t lanes,
-                                       int t, int copies, const Walk& wk, bool whole, int part,
+                                       int t, int copies, const Walk<kRows>& wk, bool whole, int part,
                                        const Workspace& ws)
 {
     const int RT = kTile / copies;
@@ -560,7 +244,7 @@ __device__ __forceinline__ void finish(const AttendCall& A, Smem<D>& sm, const R
     const int head = wk.h * A.group + flat % A.group;
     if (live && sub == 0) {
         if (!whole)
-            ws.ml[part * kTile + row] = make_float2(m, l);
+            ws.ml[part * kTile + row] = make_float2(m - kShift, l);
         else if (A.lse != nullptr)
             A.lse[prow * A.q_heads + head] = l == 0.0f ? -INFINITY : (m - kShift + log2f(l)) * kLn2;
     }
@@ -617,7 +301,7 @@ __device__ __forceinline__ void finish(const AttendCall& A, Smem<D>& sm, const R
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
-attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
+attend_wide_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map)
 {
     extern __shared__ __align__(16) unsigned char raw[];
@@ -625,7 +309,7 @@ attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
         raw + ((kSmemAlign - (smem_addr(raw) & (kSmemAlign - 1))) & (kSmemAlign - 1)));
     constexpr int kSlots = Smem<D>::kSlots;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Workspace ws = workspace_of(A.ws, D);
+    const Workspace ws = workspace_of(A.ws);
 
     if (tid == 0) {
         for (int s = 0; s < kSlots; ++s) {
@@ -648,54 +332,20 @@ attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
     }
     pdl_wait_and_trigger();
 
-    // The cut: each thread counts the tiles of a stretch of requests, a scan over the threads
-    // gives the total and the stretch that holds this CTA's first tile.
-    int bits = 0;
-    const int per = (A.B + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        int row0, w, len;
-        request_rows(A, b, &row0, &w, &len, &bits);
-        mine += head_tiles(A, w, len) * A.c.heads;
-    }
-    if (blockIdx.x == 0 && bits) raise_status(A.status, bits);
-    int64_t upto = mine;
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += y;
-    }
-    if (lane == 31) sm.scan[warp] = upto;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += sm.scan[w];
-        total += sm.scan[w];
-    }
-    const int64_t t0 = total * blockIdx.x / gridDim.x, t1 = total * (blockIdx.x + 1) / gridDim.x;
-    const int64_t from = before + upto - mine;
-    if (t0 < t1 && t0 >= from && t0 < from + mine) {
-        int64_t off = t0 - from;
-        int b = b0;
-        for (; b < b1; ++b) {
-            int row0, w, len, ignored = 0;
-            request_rows(A, b, &row0, &w, &len, &ignored);
-            const int64_t n = head_tiles(A, w, len) * A.c.heads;
-            if (off < n) break;
-            off -= n;
-        }
-        sm.run_b = b;
-        sm.run_off = off;
-    }
+    const int64_t total = cut_line<kRows, kThreads>(A, sm.cut);
     if (tid == 0) ws.meta[blockIdx.x].cut = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
 
     volatile int* stalled = &sm.stalled;
-    if (t0 < t1) {
-        Walk wk;
-        wk.start(A, sm.run_b, sm.run_off, t1 - t0);
+    Walk<kRows> wk = sm.cut.walk;
+    auto next_piece = [&]() -> bool {
+        if (wk.last()) return false;
+        wk.next(A);
+        return true;
+    };
+    if (wk.n > 0) {
         if (warp == 4) {
             // ---- pages in ----
             const int per_tile = kTile / A.c.page;
@@ -707,8 +357,7 @@ attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
             do {
                 const int32_t* table = A.c.table + static_cast<int64_t>(wk.b) * A.c.width;
                 const int total_blocks = (wk.len + wk.w + A.c.page - 1) / A.c.page;
-                const int p0 = wk.len + wk.qt * kTile / A.group;
-                const int lo = A.window > 0 && p0 >= A.window ? p0 - A.window + 1 : 0;
+                const int lo = wk.first_seen(A);
                 // 32 blocks at a time, one per lane; the next 32 are fetched while these load
                 const int first_block = wk.k0 * per_tile;
                 int base = first_block;
@@ -771,7 +420,7 @@ attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
                         next_id = -1;
                     }
                 }
-            } while (ok && wk.next(A));
+            } while (ok && next_piece());
             if (bad) raise_status(A.status, DSPARK_STATUS_BAD_PAGE);
             // every started copy lands before the CTA may leave
             __syncwarp();
@@ -831,7 +480,7 @@ attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
                         tc_commit(smem_addr(&sm.pv_done));
                     }
                     ++piece;
-                } while (ok && wk.next(A));
+                } while (ok && next_piece());
                 // the last products' arrivals on the slots' barriers land before the CTA leaves
                 if (it > 0) {
                     const int use = 2 * (it - 1);
@@ -844,7 +493,6 @@ attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
             // ---- softmax ----
             const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
             int it = 0, piece = 0;
-            int64_t at = t0;
             bool ok = true;
             do {
                 const int rows = wk.rows(A);
@@ -905,13 +553,13 @@ attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
                 soft_sync();
                 if (*reinterpret_cast<volatile int*>(&sm.quit)) break;
                 tc_fence_after();
-                const bool whole = wk.k0 == wk.a && wk.k0 + wk.n - 1 == wk.z;
+                const bool whole = wk.whole();
                 const int part = blockIdx.x * 2 + (piece > 0);
                 finish<D>(A, sm, r, lanes, tid, copies, wk, whole, part, ws);
                 if (tid == 0 && !whole && wk.k0 == wk.a) {
                     RunMeta& m = ws.meta[blockIdx.x];
                     m.total = total;
-                    m.unit_end = at + (wk.z - wk.a + 1);
+                    m.unit_end = wk.unit_end();
                     m.slot = piece > 0;
                     m.row0 = wk.row0;
                     m.rows = rows;
@@ -919,10 +567,9 @@ attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
                     m.head0 = wk.h * A.group;
                     m.cut = 1;
                 }
-                at += wk.n;
                 ++piece;
                 soft_sync();                   // the stage is free before the next queries enter it
-            } while (wk.next(A));
+            } while (next_piece());
         }
     }
     tc_fence_before();
@@ -933,162 +580,34 @@ attend_mma_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(sm.tmem));
 }
 
-// Joins the parts of each cut unit: one warp per row, each CTA of a column takes every kJoinY-th
-// group of rows.
-constexpr int kJoinWarps = 4;
-constexpr int kJoinY = 8;
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendCall A, int ctas)
+int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 {
-    pdl_wait_and_trigger();
-    const Workspace ws = workspace_of(A.ws, D);
-    const RunMeta m = ws.meta[blockIdx.x];
-    if (!m.cut) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = blockIdx.x;
-    auto start = [&](int c) -> int64_t { return m.total * c / ctas; };
-    int c1 = c0 + 1;                          // one past the last run that holds a part
-    {
-        int lo = c0 + 1, hi = ctas;           // the first run that starts at or past the unit's end
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (start(mid) < m.unit_end) lo = mid + 1; else hi = mid;
-        }
-        c1 = lo;
-    }
-    auto part = [&](int c) -> int { return c * 2 + (c == c0 ? m.slot : 0); };
-    for (int row = blockIdx.y * kJoinWarps + warp; row < m.rows; row += kJoinY * kJoinWarps) {
-        float top = kNone, sum = 0.0f;
-        for (int c = c0 + lane; c < c1; c += 32)
-            if (start(c) < start(c + 1)) top = fmaxf(top, ws.ml[part(c) * kTile + row].x);
-        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int cb = c0; cb < c1; cb += 32) {
-            const int c = cb + lane;
-            float f = 0.0f;
-            int p = -1;
-            if (c < c1 && start(c) < start(c + 1)) {
-                p = part(c);
-                const float2 ml = ws.ml[p * kTile + row];
-                f = exp2f(ml.x - top);
-                sum += f * ml.y;
-            }
-            const int n = min(32, c1 - cb);
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-                const int pk = __shfl_sync(0xffffffffu, p, k);
-                const float fk = __shfl_sync(0xffffffffu, f, k);
-                if (pk < 0 || lane * 4 >= D) continue;
-                const float4 o = *reinterpret_cast<const float4*>(
-                    ws.o + (static_cast<int64_t>(pk) * kTile + row) * D + lane * 4);
-                acc.x = fmaf(fk, o.x, acc.x);
-                acc.y = fmaf(fk, o.y, acc.y);
-                acc.z = fmaf(fk, o.z, acc.z);
-                acc.w = fmaf(fk, o.w, acc.w);
-            }
-        }
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const int flat = m.flat0 + row;
-        const int64_t prow = m.row0 + flat / A.group;
-        const int head = m.head0 + flat % A.group;
-        if (lane * 4 < D) {
-            uint16_t* out = static_cast<uint16_t*>(A.out) + prow * A.out_stride +
-                            static_cast<int64_t>(head) * D + lane * 4;
-            const uint32_t a = pack_bf16(acc.x * inv, acc.y * inv), b = pack_bf16(acc.z * inv, acc.w * inv);
-            out[0] = static_cast<uint16_t>(a);
-            out[1] = static_cast<uint16_t>(a >> 16);
-            out[2] = static_cast<uint16_t>(b);
-            out[3] = static_cast<uint16_t>(b >> 16);
-        }
-        if (lane == 0 && A.lse != nullptr)
-            A.lse[prow * A.q_heads + head] = sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * kLn2;
-    }
-}
-
-// cuTensorMapEncodeTiled, found through the runtime (the library does not link libcuda).
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                             CUtensorMapFloatOOBfill);
-EncodeFn encode_fn()
-{
-    static const EncodeFn fn = []() -> EncodeFn {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess || q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            return nullptr;
-        }
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
-}
-
-int encode(CUtensorMap* map, void* codes, const dspark_cache& c)
-{
-    const EncodeFn fn = encode_fn();
-    if (fn == nullptr) return fail(DSPARK_ERR_CUDA, "dspark attend: cuTensorMapEncodeTiled not found");
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.dim),
-                                static_cast<cuuint64_t>(c.n_pages) * c.heads * c.page};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.dim)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(c.dim), static_cast<cuuint32_t>(c.page)};
-    const cuuint32_t ones[2] = {1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, ones,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        return fail(DSPARK_ERR_CUDA, "dspark attend: cuTensorMapEncodeTiled returned %d", static_cast<int>(r));
-    return DSPARK_OK;
-}
-
-template <int D>
-int launch(const AttendCall& A, cudaStream_t stream)
-{
-    DeviceInfo dev;
-    int rc = current_device(&dev);
-    if (rc != DSPARK_OK) return rc;
     const size_t smem = sizeof(Smem<D>) + kSmemAlign;
     static bool ready[64] = {};               // opt-in to large shared memory, once per device
-    if (!ready[dev.device]) {
-        const cudaError_t e = cudaFuncSetAttribute(attend_mma_kernel<D>,
+    if (!ready[device]) {
+        const cudaError_t e = cudaFuncSetAttribute(attend_wide_kernel<D>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
         if (e != cudaSuccess) {
             cudaGetLastError();
             return fail(DSPARK_ERR_CUDA, "dspark attend: %s", cudaGetErrorString(e));
         }
-        ready[dev.device] = true;
+        ready[device] = true;
     }
     CUtensorMap k_map, v_map;
-    rc = encode(&k_map, A.c.k, A.c);
-    if (rc == DSPARK_OK) rc = encode(&v_map, A.c.v, A.c);
+    int rc = encode_cache(&k_map, A.c.k, A.c);
+    if (rc == DSPARK_OK) rc = encode_cache(&v_map, A.c.v, A.c);
     if (rc != DSPARK_OK) return rc;
-    const int ctas = min(2 * dev.sm_count, kMaxCtas);
-    rc = launch_pdl("attend", attend_mma_kernel<D>, dim3(ctas), dim3(kThreads), smem, stream, A, k_map, v_map);
-    if (rc != DSPARK_OK) return rc;
-    return launch_pdl("attend join", attend_join_kernel<D>, dim3(ctas, kJoinY), dim3(kJoinWarps * 32), 0,
-                      stream, A, ctas);
+    return launch_pdl("attend", attend_wide_kernel<D>, dim3(ctas), dim3(kThreads), smem, stream, A,
+                      k_map, v_map);
 }
 
 }  // namespace
 
-bool attend_mma_serves(const AttendCall& A, int dtype)
+int launch_attend_wide(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 {
-    return dtype == DSPARK_BF16 && (A.c.dim == 64 || A.c.dim == 128) && A.c.n_pages > 0;
-}
-
-size_t attend_workspace_bytes(int dim)
-{
-    if (dim != 64 && dim != 128) return 16;
-    return kMaxCtas * (sizeof(RunMeta) + 2 * kTile * (sizeof(float2) + dim * sizeof(float)));
-}
-
-int launch_attend_mma(const AttendCall& A, cudaStream_t stream)
-{
-    return A.c.dim == 128 ? launch<128>(A, stream) : launch<64>(A, stream);
+    return A.c.dim == 128 ? launch<128>(A, ctas, device, stream) : launch<64>(A, ctas, device, stream);
 }
 
 }  // namespace dspark
