@@ -19,6 +19,8 @@ struct AttendCall {
     float scale;
     int window;
     float* lse;
+    int reach;                 // tokens that the page table reaches
+    int last_tile;             // the last 128-token tile of them
     void* ws;
     int32_t* status;
 };
@@ -38,7 +40,7 @@ bool attend_mma_serves(const AttendCall& A, int dtype);
 int launch_attend_mma(const AttendCall& A, cudaStream_t stream);
 
 // Request b's packed rows [row0, row0 + w) and its length, checked: w = 0 for one whose rows are
-// not within the buffer. *bits collects what was wrong.
+// not within the buffer. *bits collects what was wrong, tokens past the page table included.
 __device__ __forceinline__ void request_rows(const AttendCall& A, int b, int* row0, int* w,
                                              int* len, int* bits)
 {
@@ -50,6 +52,7 @@ __device__ __forceinline__ void request_rows(const AttendCall& A, int b, int* ro
     *len = n;
     if (r0 < 0 || r1 < r0 || r1 > A.rows) { *w = 0; *bits |= DSPARK_STATUS_BAD_ROWS; }
     else if (n > INT32_MAX - 256 - *w) { *w = 0; *bits |= DSPARK_STATUS_BAD_LENGTH; }
+    else if (*w > 0 && n + *w > A.reach) *bits |= DSPARK_STATUS_BAD_PAGE;
 }
 
 }  // namespace dspark

@@ -5,60 +5,67 @@
 namespace dspark {
 namespace {
 
-// Joins the parts of each cut unit: one warp per row, each CTA of a column takes every kJoinY-th
-// group of rows.
-constexpr int kJoinWarps = 4;
-constexpr int kJoinY = 8;
+// Joins the parts of each cut unit: the runs that a unit's places cross, but the first, share its
+// rows (a unit cut once is joined by one CTA, one cut 37 times by 37). A warp takes a row: its
+// lanes first read the parts' references and sums, then dim / 4 lanes add up the parts, 16 loads
+// in flight.
+constexpr int kJoinWarps = 16;
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendCall A, int ctas)
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendCall A)
 {
     pdl_wait_and_trigger();
     const Workspace ws = workspace_of(A.ws);
     const RunMeta m = ws.meta[blockIdx.x];
     if (!m.cut) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = blockIdx.x;
-    auto start = [&](int c) -> int64_t { return run_start(m.total, c, ctas); };
-    int c1 = c0 + 1;                          // one past the last run that holds a part
-    {
-        int lo = c0 + 1, hi = ctas;           // the first run that starts at or past the unit's end
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (start(mid) < m.unit_end) lo = mid + 1; else hi = mid;
-        }
-        c1 = lo;
-    }
-    auto part = [&](int c) -> int { return c * 2 + (c == c0 ? m.slot : 0); };
-    for (int row = blockIdx.y * kJoinWarps + warp; row < m.rows; row += kJoinY * kJoinWarps) {
+    const int c0 = (m.unit + kUnitCost) / m.run;             // the run of the unit's first tile
+    const int c1 = (m.end + m.run - 1) / m.run;              // one past the run of its last
+    // in the first run an earlier unit's piece may come before
+    const int part0 = 2 * c0 + (c0 * m.run < m.unit ? 1 : 0);
+    const int shares = c1 - c0 - 1, share = static_cast<int>(blockIdx.x) - c0 - 1;
+#pragma unroll 1
+    for (int row = share * kJoinWarps + warp; row < m.rows; row += shares * kJoinWarps) {
         float top = kNone, sum = 0.0f;
+#pragma unroll 1
         for (int c = c0 + lane; c < c1; c += 32)
-            if (start(c) < start(c + 1)) top = fmaxf(top, ws.ml[part(c) * kTile + row].x);
+            top = fmaxf(top, ws.ml[(c == c0 ? part0 : 2 * c) * kTile + row].x);
+#pragma unroll
         for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
         for (int cb = c0; cb < c1; cb += 32) {
             const int c = cb + lane;
             float f = 0.0f;
-            int p = -1;
-            if (c < c1 && start(c) < start(c + 1)) {
-                p = part(c);
-                const float2 ml = ws.ml[p * kTile + row];
+            if (c < c1) {
+                const float2 ml = ws.ml[(c == c0 ? part0 : 2 * c) * kTile + row];
                 f = exp2f(ml.x - top);
                 sum += f * ml.y;
             }
             const int n = min(32, c1 - cb);
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-                const int pk = __shfl_sync(0xffffffffu, p, k);
-                const float fk = __shfl_sync(0xffffffffu, f, k);
-                if (pk < 0 || lane * 4 >= D) continue;
-                const float4 o = *reinterpret_cast<const float4*>(
-                    ws.o + (static_cast<int64_t>(pk) * kTile + row) * D + lane * 4);
-                acc.x = fmaf(fk, o.x, acc.x);
-                acc.y = fmaf(fk, o.y, acc.y);
-                acc.z = fmaf(fk, o.z, acc.z);
-                acc.w = fmaf(fk, o.w, acc.w);
+            const int d = lane * 4 < D ? lane * 4 : 0;
+#pragma unroll 1
+            for (int k0 = 0; k0 < n; k0 += 16) {
+                float4 o[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int ck = min(cb + k0 + k, c1 - 1);
+                    if (k0 + k < n)
+                        o[k] = *reinterpret_cast<const float4*>(
+                            ws.o + (static_cast<int64_t>(ck == c0 ? part0 : 2 * ck) * kTile + row) * D + d);
+                    else
+                        o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+                    acc.x = fmaf(fk, o[k].x, acc.x);
+                    acc.y = fmaf(fk, o[k].y, acc.y);
+                    acc.z = fmaf(fk, o[k].z, acc.z);
+                    acc.w = fmaf(fk, o[k].w, acc.w);
+                }
             }
         }
+#pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         const int flat = m.flat0 + row;
@@ -121,7 +128,7 @@ int encode_cache(CUtensorMap* map, void* codes, const dspark_cache& c)
 int launch_attend_join(const AttendCall& A, int ctas, cudaStream_t stream)
 {
     return launch_pdl("attend join", A.c.dim == 128 ? attend_join_kernel<128> : attend_join_kernel<64>,
-                      dim3(ctas, kJoinY), dim3(kJoinWarps * 32), 0, stream, A, ctas);
+                      dim3(ctas), dim3(kJoinWarps * 32), 0, stream, A);
 }
 
 bool attend_mma_serves(const AttendCall& A, int dtype)

@@ -44,12 +44,11 @@ constexpr float kLag = 2.5f;
 constexpr long long kWaitCycles = 1ll << 31;
 constexpr uint32_t kSmemAlign = 1024;        // the 128-byte swizzle's period
 
-// What the join needs to know of a CTA's run.
+// What the join needs to know of the unit that a run's start cut.
 struct RunMeta {
-    int64_t total;      // places on the whole line
-    int64_t unit_end;   // the place where the cut unit ends
-    int cut;            // 1: the run's last unit starts here and continues in the next runs
-    int slot;           // the part it left here
+    int cut;            // 0: the run starts with a unit's beginning, or holds no tile
+    int unit, end;      // the unit's places on the line
+    int run;            // places per run
     int row0, rows;     // the request's first packed row; the unit's rows (position, head) ...
     int flat0, head0;   // ... from this flat index on, first query head
 };
@@ -253,23 +252,32 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t*
 // ---- the line of tiles ---------------------------------------------------------------------
 // A unit of n tiles takes kUnitCost + n places on the line: starting and finishing a unit costs a
 // CTA about as much as that many tiles, and runs of equal length should take equal time. Tile k is
-// at place kUnitCost + k of its unit.
+// at place kUnitCost + k of its unit. Run i holds the places [i * run, (i + 1) * run). The host
+// makes sure that a line's length fits an int (places_fit).
 constexpr int kUnitCost = 2;
 
 struct Shape {                   // a unit's visible tiles [a, z]
     int a, z;
 };
-// The tiles that some row of a request's qt-th R rows sees. The divisions by the group are spared
-// where the unit holds the request's first or last rows: for decode and verify, always.
+// The tiles that some row of a request's qt-th R rows sees and the page table reaches (one tile at
+// least). The divisions by the group are spared where the unit holds the request's first or last
+// rows: for decode and verify, always.
 template <int R>
-static __device__ __noinline__ Shape unit_tiles(const AttendCall& A, int w, int len, int qt)
+static __device__ __noinline__ Shape some_unit_tiles(const AttendCall& A, int w, int len, int qt)
 {
     const int i0 = qt == 0 ? 0 : qt * R / A.group;
     const int i1 = static_cast<int64_t>(qt + 1) * R >= static_cast<int64_t>(w) * A.group
                        ? w - 1 : ((qt + 1) * R - 1) / A.group;
     const int p0 = len + i0;
     const int lo = A.window > 0 && p0 >= A.window ? p0 - A.window + 1 : 0;
-    return {lo / kTile, (len + i1) / kTile};
+    return {min(lo / kTile, A.last_tile), min((len + i1) / kTile, A.last_tile)};
+}
+template <int R>
+__device__ __forceinline__ Shape unit_tiles(const AttendCall& A, int w, int len, int qt)
+{
+    if (static_cast<int64_t>(w) * A.group > R) return some_unit_tiles<R>(A, w, len, qt);
+    const int lo = A.window > 0 && len >= A.window ? len - A.window + 1 : 0;      // the only unit
+    return {min(lo / kTile, A.last_tile), min((len + w - 1) / kTile, A.last_tile)};
 }
 template <int R>
 __device__ __forceinline__ int row_tiles(const AttendCall& A, int w)
@@ -278,9 +286,9 @@ __device__ __forceinline__ int row_tiles(const AttendCall& A, int w)
 }
 // The places that one head of a request takes on the line.
 template <int R>
-static __device__ __noinline__ int64_t head_places(const AttendCall& A, int w, int len)
+__device__ __forceinline__ int head_places(const AttendCall& A, int w, int len)
 {
-    int64_t n = 0;
+    int n = 0;
     const int nq = row_tiles<R>(A, w);
 #pragma unroll 1
     for (int qt = 0; qt < nq; ++qt) {
@@ -289,12 +297,12 @@ static __device__ __noinline__ int64_t head_places(const AttendCall& A, int w, i
     }
     return n;
 }
-// Where run i of `ctas` starts on a line of `total` places.
-static __device__ __noinline__ int64_t run_start(int64_t total, int i, int ctas)
+// Whether a call's line fits an int, whatever the lengths.
+template <int R>
+inline bool places_fit(const AttendCall& A)
 {
-    if (total < (1 << 22))       // 32-bit division where the product fits: the usual case
-        return static_cast<uint32_t>(total) * static_cast<uint32_t>(i) / static_cast<uint32_t>(ctas);
-    return total * i / ctas;
+    const int64_t units = (static_cast<int64_t>(A.rows) * A.q_heads) / R + static_cast<int64_t>(A.B) * A.c.heads;
+    return units * (A.last_tile + 1 + kUnitCost) <= INT32_MAX / 2;
 }
 
 // The units of one run in order.
@@ -303,25 +311,25 @@ struct Walk {
     int b, h, qt, nq;
     int row0, w, len;
     int a, z, k0, n;             // the unit's tiles [a, z]; this piece: n tiles from k0
-    int64_t unit;                // the unit's first place on the line
-    int64_t end;                 // the run's end on the line
+    int unit;                    // the unit's first place on the line
+    int stop;                    // the run's end on the line
 
-    __device__ __forceinline__ void piece(const AttendCall& A, int64_t from)
+    __device__ __forceinline__ void piece(const AttendCall& A, int from)
     {
         const Shape s = unit_tiles<R>(A, w, len, qt);
         a = s.a;
         z = s.z;
-        const int64_t first = unit + kUnitCost, nt = z - a + 1;      // the place of the first tile
-        const int k = from > first ? static_cast<int>(from - first) : 0;
+        const int first = unit + kUnitCost;                          // the place of the first tile
+        const int k = from > first ? from - first : 0;
         k0 = a + k;
-        const int64_t stop = end - first < nt ? end - first : nt;
-        n = static_cast<int>(stop - k);                               // <= 0: nothing of it here
+        n = min(stop - first, z - a + 1) - k;                        // <= 0: nothing of it here
     }
-    __device__ __forceinline__ bool last() const { return end - (unit + kUnitCost + z - a + 1) <= kUnitCost; }
+    __device__ __forceinline__ int end() const { return unit + kUnitCost + z - a + 1; }
+    __device__ __forceinline__ bool last() const { return stop - end() <= kUnitCost; }
     // The next unit of the run; only if !last().
     __device__ __forceinline__ void next(const AttendCall& A)
     {
-        unit += kUnitCost + z - a + 1;
+        unit = end();
         if (++qt == nq) {
             qt = 0;
             if (++h == A.c.heads) {
@@ -343,7 +351,6 @@ struct Walk {
                                     static_cast<int64_t>(w) * A.group - static_cast<int64_t>(qt) * R));
     }
     __device__ __forceinline__ bool whole() const { return k0 == a && n == z - a + 1; }
-    __device__ __forceinline__ int64_t unit_end() const { return unit + kUnitCost + z - a + 1; }
     // The first token that some row of the unit sees.
     __device__ __forceinline__ int first_seen(const AttendCall& A) const
     {
@@ -355,81 +362,97 @@ struct Walk {
 // The cut, by a whole CTA of NT threads: each thread counts the places of a stretch of requests, a
 // scan over the threads gives the total and the stretch that holds the run's first place; that
 // thread writes the walk's start (n <= 0: the run holds no tile). The caller synchronises before
-// the walk is read.
+// the walk is read. Returns the places per run.
 template <int R>
 struct Cut {
-    int64_t scan[32];
+    int scan[32];
     Walk<R> walk;
 };
+// Thread-serial part of the cut: the run [t0, t1) starts `off` places into the requests from b on.
+// `k` holds request b already, and `per_head` its places per head.
+template <int R>
+__device__ __forceinline__ void find_start(const AttendCall& A, Walk<R>& k, int per_head, int off, int t0, int t1)
+{
+    int bits = 0;
+#pragma unroll 1
+    while (off >= per_head * A.c.heads) {        // only where a thread counts several requests
+        off -= per_head * A.c.heads;
+        ++k.b;
+        request_rows(A, k.b, &k.row0, &k.w, &k.len, &bits);
+        per_head = head_places<R>(A, k.w, k.len);
+    }
+    k.h = static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(per_head));
+    off -= k.h * per_head;
+    k.nq = row_tiles<R>(A, k.w);
+    k.stop = t1;
+    k.qt = 0;
+    k.unit = t0 - off;
+    k.piece(A, t0);
+#pragma unroll 1
+    while (k.end() <= t0) {                      // several units of rows: the one that holds t0
+        ++k.qt;
+        k.unit = k.end();
+        k.piece(A, t0);
+    }
+}
 template <int R, int NT>
-__device__ __forceinline__ int64_t cut_line(const AttendCall& A, Cut<R>& cut)
+__device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R>& cut)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int bits = 0;
     const int per = (A.B + NT - 1) / NT;
     const int b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
-    int64_t mine = 0, off = 0, t0 = 0, t1 = 0, total = 0;
+    int mine = 0, per_head = 1;
+    Walk<R> k;
     if (tid == 0) cut.walk.n = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            int row0, w, len;
-            request_rows(A, b, &row0, &w, &len, &bits);
-            const int64_t per_head = head_places<R>(A, w, len);
-            const int64_t all = per_head * A.c.heads;
-            if (pass == 0) { mine += all; continue; }
-            if (off >= all) { off -= all; continue; }
-            Walk<R>& k = cut.walk;
-            const int h = all < INT32_MAX
-                              ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(per_head))
-                              : static_cast<int>(off / per_head);
-            off -= h * per_head;
-            int qt = 0;
-#pragma unroll 1
-            while (true) {
-                const Shape s = unit_tiles<R>(A, w, len, qt);
-                const int n = s.z - s.a + 1 + kUnitCost;
-                if (off < n) break;
-                off -= n;
-                ++qt;
-            }
-            k.b = b;
-            k.h = h;
-            k.qt = qt;
-            k.nq = row_tiles<R>(A, w);
-            k.row0 = row0;
-            k.w = w;
-            k.len = len;
-            k.unit = t0 - off;
-            k.end = t1;
-            k.piece(A, t0);
-            break;
-        }
-        if (pass) break;
-        int64_t upto = mine;
-#pragma unroll 1
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += y;
-        }
-        if (lane == 31) cut.scan[warp] = upto;
-        __syncthreads();
-        int64_t before = 0;
-#pragma unroll 1
-        for (int w = 0; w < NT / 32; ++w) {
-            const int64_t s = cut.scan[w];
-            if (w < warp) before += s;
-            total += s;
-        }
-        const int64_t from = before + upto - mine;
-        t0 = run_start(total, blockIdx.x, gridDim.x);
-        t1 = run_start(total, blockIdx.x + 1, gridDim.x);
-        if (!(t0 < t1 && t0 >= from && t0 < from + mine)) break;
-        off = t0 - from;
+    for (int b = b1 - 1; b >= b0; --b) {         // downwards: the walk is left at the first one
+        k.b = b;
+        request_rows(A, b, &k.row0, &k.w, &k.len, &bits);
+        per_head = head_places<R>(A, k.w, k.len);
+        mine += per_head * A.c.heads;
+    }
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+    }
+    if (lane == 31) cut.scan[warp] = upto;
+    __syncthreads();
+    int sums = lane < NT / 32 ? cut.scan[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sums, d);
+        if (lane >= d) sums += y;
+    }
+    static_assert(NT / 32 <= 16, "the second scan covers 16 warps");
+    const int total = __shfl_sync(0xffffffffu, sums, NT / 32 - 1);
+    const int before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+    const int from = (warp > 0 ? before : 0) + upto - mine;
+    const int run = static_cast<int>((static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x);
+    const int t0 = min(static_cast<int>(blockIdx.x) * run, total), t1 = min(t0 + run, total);
+    if (t0 < t1 && t0 >= from && t0 < from + mine) {
+        find_start<R>(A, k, per_head, t0 - from, t0, t1);
+        cut.walk = k;
     }
     if (blockIdx.x == 0 && bits) raise_status(A.status, bits);
-    return total;
+    return run;
+}
+// The run's entry for the join, by one thread.
+template <int R>
+__device__ __forceinline__ void write_meta(const AttendCall& A, const Workspace& ws, const Walk<R>& k, int run)
+{
+    RunMeta m;
+    m.cut = k.n > 0 && k.k0 > k.a;
+    m.unit = k.unit;
+    m.end = k.end();
+    m.run = run;
+    m.row0 = k.row0;
+    m.rows = k.rows(A);
+    m.flat0 = k.qt * R;
+    m.head0 = k.h * A.group;
+    ws.meta[blockIdx.x] = m;
 }
 
 }  // namespace dspark

@@ -48,10 +48,9 @@ struct Piece {
     int rows;
     int k0, n;           // tiles
     int first_seen;
-    int whole, cut;      // nothing of the unit is elsewhere; it starts here and goes on elsewhere
+    int whole;           // nothing of the unit is elsewhere
     int last;
     int i0, g0;          // position and head of the unit's first row
-    int64_t unit_end;    // on the line of tiles
 };
 struct RowInfo {
     int64_t out;         // element offset of the row's results
@@ -427,9 +426,7 @@ __device__ __forceinline__ void describe(const AttendCall& A, const Walk<kRows>&
     p.n = wk.n;
     p.first_seen = wk.first_seen(A);
     p.whole = wk.whole();
-    p.cut = wk.k0 == wk.a && !p.whole;
     p.last = wk.last();
-    p.unit_end = wk.unit_end();
 }
 
 template <int D>
@@ -469,13 +466,13 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
         tc_fence_before();
     }
     pdl_wait_and_trigger();
-    const int64_t total = cut_line<kRows, kThreads>(A, sm.cut);
-    if (tid == 0) ws.meta[blockIdx.x].cut = 0;
+    const int run = cut_line<kRows, kThreads>(A, sm.cut);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
 
     volatile int* stalled = &sm.stalled;
+    if (tid == 0) write_meta<kRows>(A, ws, sm.cut.walk, run);
     if (sm.cut.walk.n > 0) {
         if (warp == 10) {
             // ---- the walk: pieces described up to three ahead; queries from the second on ----
@@ -782,17 +779,6 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                    : nr == 16 ? run_piece(std::integral_constant<int, 8>{})
                               : run_piece(std::integral_constant<int, 16>{});
                 if (!ok) break;
-                if (tid == 0 && pc.cut) {
-                    RunMeta& m = ws.meta[blockIdx.x];
-                    m.total = total;
-                    m.unit_end = pc.unit_end;
-                    m.slot = piece > 0;
-                    m.row0 = pc.row0;
-                    m.rows = pc.rows;
-                    m.flat0 = pc.flat0;
-                    m.head0 = pc.h * A.group;
-                    m.cut = 1;
-                }
                 if (pc.last) break;
             }
         }
@@ -820,6 +806,8 @@ int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
         }
         ready[device] = true;
     }
+    if (!places_fit<kRows>(A))
+        return fail(DSPARK_ERR_UNSUPPORTED, "dspark_attend: rows, heads and pages beyond what one call can cut");
     CUtensorMap k_map, v_map;
     int rc = encode_cache(&k_map, A.c.k, A.c);
     if (rc == DSPARK_OK) rc = encode_cache(&v_map, A.c.v, A.c);

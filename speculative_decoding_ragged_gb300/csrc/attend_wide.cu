@@ -332,8 +332,7 @@ attend_wide_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
     }
     pdl_wait_and_trigger();
 
-    const int64_t total = cut_line<kRows, kThreads>(A, sm.cut);
-    if (tid == 0) ws.meta[blockIdx.x].cut = 0;
+    const int run = cut_line<kRows, kThreads>(A, sm.cut);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -345,6 +344,7 @@ attend_wide_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
         wk.next(A);
         return true;
     };
+    if (tid == 0) write_meta<kRows>(A, ws, wk, run);
     if (wk.n > 0) {
         if (warp == 4) {
             // ---- pages in ----
@@ -556,17 +556,6 @@ attend_wide_kernel(AttendCall A, const __grid_constant__ CUtensorMap k_map,
                 const bool whole = wk.whole();
                 const int part = blockIdx.x * 2 + (piece > 0);
                 finish<D>(A, sm, r, lanes, tid, copies, wk, whole, part, ws);
-                if (tid == 0 && !whole && wk.k0 == wk.a) {
-                    RunMeta& m = ws.meta[blockIdx.x];
-                    m.total = total;
-                    m.unit_end = wk.unit_end();
-                    m.slot = piece > 0;
-                    m.row0 = wk.row0;
-                    m.rows = rows;
-                    m.flat0 = wk.qt * kTile;
-                    m.head0 = wk.h * A.group;
-                    m.cut = 1;
-                }
                 ++piece;
                 soft_sync();                   // the stage is free before the next queries enter it
             } while (next_piece());
@@ -595,6 +584,8 @@ int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
         }
         ready[device] = true;
     }
+    if (!places_fit<kRows>(A))
+        return fail(DSPARK_ERR_UNSUPPORTED, "dspark_attend: rows, heads and pages beyond what one call can cut");
     CUtensorMap k_map, v_map;
     int rc = encode_cache(&k_map, A.c.k, A.c);
     if (rc == DSPARK_OK) rc = encode_cache(&v_map, A.c.v, A.c);

@@ -150,6 +150,9 @@ int dspark_attend(const dspark_cache* cache, const void* q, int64_t q_stride, vo
     A.scale = scale;
     A.window = window;
     A.lse = lse;
+    const int64_t reach = static_cast<int64_t>(cache->width) * cache->page;
+    A.reach = static_cast<int>(reach < INT32_MAX ? reach : INT32_MAX);
+    A.last_tile = static_cast<int>((reach > 0 ? reach - 1 : 0) / 128);
     A.ws = workspace;
     A.status = status;
     return dspark::launch_attend(A, static_cast<int>(dtype), stream);
