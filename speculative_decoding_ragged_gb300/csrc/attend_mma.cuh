@@ -254,7 +254,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t*
 // CTA about as much as that many tiles, and runs of equal length should take equal time. Tile k is
 // at place kUnitCost + k of its unit. Run i holds the places [i * run, (i + 1) * run). The host
 // makes sure that a line's length fits an int (places_fit).
-constexpr int kUnitCost = 2;
+constexpr int kUnitCost = 4;
 
 struct Shape {                   // a unit's visible tiles [a, z]
     int a, z;

@@ -1,11 +1,11 @@
 // attend_narrow.cu — dspark_attend on the tensor cores for decode and verify: units of at most 32
-// rows (window positions x query heads of one cache head).
+// rows (window positions x query heads of one cache head): 8, 16 or 32, by the call.
 //
 // With few rows the products are turned round: the tile's 128 tokens (for the scores) and the
 // head's elements (for the sums) fill the 128 lanes of the instruction, the rows are its columns:
-//   S^T [128 tokens, 2 NR] = K [128, D] (Q_hi, Q_lo)^T       O^T [D, 2 NR] += V^T [D, 128] (W_hi, W_lo)
-// NR = 8, 16 or 32 by the unit's rows, so the products cost what the rows need (256 cycles a tile
-// at NR = 32 where 128 row lanes would cost 1024) and K and V are read from shared memory once.
+//   S^T [128 tokens, 2 R] = K [128, D] (Q_hi, Q_lo)^T       O^T [D, 2 R] += V^T [D, 128] (W_hi, W_lo)
+// so the products cost what the rows need (about 600 cycles a tile at R = 32, where 128 row lanes
+// cost 1400) and K and V are read from shared memory once.
 // The two pieces are separate columns and are added when they are read.
 // A thread's lane is a token: block scales are per-thread scalars, the rows' factors and
 // references broadcast reads. The softmax needs no reduction over lanes in the common case: every
@@ -22,14 +22,11 @@
 // Bound by HBM: 2 D bytes per token and cache head. What else showed in clock stamps was cold
 // code (about 16 cycles per instruction the first time), hence one walker, rolled loops where
 // registers allow them, and half the rows per thread.
-#include <type_traits>
-
 #include "attend_mma.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kRows = 32;
 constexpr int kSoftThreads = 256;
 constexpr int kThreads = 352;
 constexpr int kP = 64;                       // bytes of a token's row of weights: two pieces of 32
@@ -57,29 +54,30 @@ struct RowInfo {
     int64_t lse;
 };
 
-template <int D>
+template <int D, int R>
 struct Smem {
     static constexpr int kSlot = kTile * D;              // one tile's K or V
     static constexpr int kSlots = D == 128 ? 5 : 10;     // K and V alternate
     static constexpr int kNums = kSlots / 2 + 2;         // tiles whose numbers may still be read
     uint8_t ring[kSlots][kSlot];
-    uint8_t q[2][2 * kRows * D];                         // two units' queries: hi rows, lo rows
+    uint8_t q[2][2 * R * D];                         // two units' queries: hi rows, lo rows
     uint8_t p[kTile * kP];                               // the weights, a row per token
     BlockNums nums[kNums][kBlocks];
     Piece piece[kPieces];
-    RowInfo info[4][kRows];                              // four units' rows
-    int2 see[4][kRows];                                  // first token seen, and how many past it
-    float f[4][kRows];                                   // score factors: scale log2(e) 2^e
-    RowInfo now_info[kRows];                             // the softmax's own copies of its unit's
-    __align__(16) int2 now_see[kRows];
-    __align__(16) float2 row[kRows];                                   // factor, reference - kUp (0: none seen)
-    __align__(16) float grow[kRows];                                   // 2^(old reference - new)
-    float part[4][kRows];                                // per-warp maxima or sums
+    RowInfo info[4][R];                              // four units' rows
+    int2 see[4][R];                                  // first token seen, and how many past it
+    float f[4][R];                                   // score factors: scale log2(e) 2^e
+    RowInfo now_info[R];                             // the softmax's own copies of its unit's
+    __align__(16) int2 now_see[R];
+    __align__(16) float now_f[R];
+    __align__(16) float ref[R];                      // kUp - reference (0: nothing seen yet)
+    __align__(16) float grow[R];                     // 2^(old reference - new)
+    float4 part[R];                                  // the four warps' maxima or sums
     int unseen[2];                                       // a row of the half has seen nothing yet
     uint64_t full[kSlots], empty[kSlots];
     uint64_t piece_full[kPieces], info_full[4], q_full[2], q_empty[2];
     uint64_t s_full[2], pv_done[2], p_full;
-    Cut<kRows> cut;
+    Cut<R> cut;
     uint32_t tmem;
     int stalled;         // a wait gave up: every role leaves its loop
 };
@@ -87,7 +85,37 @@ struct Smem {
 // TMEM columns: scores at 64 * (tile & 1), sums at 128 + 64 * (unit & 1).
 constexpr uint32_t kSums = 128;
 
-__device__ __forceinline__ int columns_of(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// Packed fp32 pairs: one instruction for two.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 
 // V^T as the first operand: its 128 lanes are the head's elements. Of a 64-wide head the second 64
 // lanes read the first ones again (the stride between swizzle atoms is 0) and are ignored.
@@ -134,7 +162,7 @@ __device__ __forceinline__ bool half_any(int half, bool yes)
 // v[0..N) of every lane, combined over the warp's 32 lanes: lane i gets row i % N. Each step
 // halves the rows a lane keeps, so N - 1 exchanges do what N full reductions would.
 template <int N, bool MAX>
-__device__ __forceinline__ float reduce_rows(float* v, int lane)
+__device__ __forceinline__ float reduce_some(float* v, int lane)
 {
     auto both = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
 #pragma unroll
@@ -151,92 +179,118 @@ __device__ __forceinline__ float reduce_rows(float* v, int lane)
     for (int off = N; off < 32; off <<= 1) y = both(y, __shfl_xor_sync(0xffffffffu, y, off));
     return y;
 }
+// HR rows' values of a warp -> its column of part[r0 ..].
+template <int HR, bool MAX>
+__device__ __forceinline__ void reduce_rows(float4* part, float* v, int lane, int warp)
+{
+    const float y = reduce_some<HR, MAX>(v, lane);
+    if (lane < HR) reinterpret_cast<float*>(part + lane)[warp] = y;
+}
 
 struct Token {
     BlockNums n;
     int t;
 };
 
-// One tile, this thread's token, HR rows from r0: scores in TMEM -> weights in shared memory;
-// l[j] += this token's weights.
-template <int D, int HR>
-__device__ __forceinline__ bool soften(Smem<D>& sm, const int2* see, int half, float* l, uint32_t s_addr,
-                                       uint32_t o_addr, const Token& k, bool mask, bool first, int it,
-                                       volatile int* stalled)
+// One tile, this thread's token, half of the R rows: scores in TMEM -> weights in shared memory;
+// l += this token's weights.
+template <int D, int R>
+__device__ __forceinline__ bool soften(Smem<D, R>& sm, int half, uint64_t* l, uint32_t s_addr, uint32_t o_addr,
+                                       const Token& k, bool mask, bool first, int it, volatile int* stalled)
 {
-    constexpr int NR = 2 * HR;
-    constexpr int N = HR < 8 ? HR : 8;
+    constexpr int HR = R / 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3;
     const int r0 = half * HR;
-    const float4* row2 = reinterpret_cast<const float4*>(sm.row + r0);
-    const int4* see2 = reinterpret_cast<const int4*>(see + r0);
-    float x[HR];
+    const float4* f4 = reinterpret_cast<const float4*>(sm.now_f + r0);
+    const float4* ref4 = reinterpret_cast<const float4*>(sm.ref + r0);
+    const uint64_t ks2 = pack2(k.n.ks, k.n.ks), bias2 = pack2(k.n.bias, k.n.bias);
+    uint64_t x[HR / 2];                       // pairs of rows
 #pragma unroll 1
     for (int pass = 0;; ++pass) {
+        constexpr int N = HR < 8 ? HR : 8;
 #pragma unroll
-        for (int c = 0; c < HR; c += N) {
-            float lo[N];
-            tc_ld<N>(s_addr + r0 + c, x + c);
-            tc_ld<N>(s_addr + NR + r0 + c, lo);
+        for (int c = 0; c < HR; c += N) {        // the two pieces' columns, added
+            float hi[N], lo[N];
+            tc_ld<N>(s_addr + r0 + c, hi);
+            tc_ld<N>(s_addr + R + r0 + c, lo);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < N; ++j) x[c + j] += lo[j];
+            for (int j = 0; j < N; j += 2)
+                x[(c + j) / 2] = add2(pack2(hi[j], hi[j + 1]), pack2(lo[j], lo[j + 1]));
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < HR; r += 2) {
-            const float4 c = row2[r / 2];        // two rows' factor and reference
-            x[r] = fmaf(x[r], c.x * k.n.ks, k.n.bias - c.y);
-            x[r + 1] = fmaf(x[r + 1], c.z * k.n.ks, k.n.bias - c.w);
-            top = fmaxf(top, fmaxf(x[r], x[r + 1]));
-        }
+        for (int r = 0; r < HR; r += 4) {
+                const float4 f = f4[r / 4], ref = ref4[r / 4];
+                x[r / 2] = fma2(x[r / 2], mul2(pack2(f.x, f.y), ks2), add2(bias2, pack2(ref.x, ref.y)));
+                x[r / 2 + 1] = fma2(x[r / 2 + 1], mul2(pack2(f.z, f.w), ks2), add2(bias2, pack2(ref.z, ref.w)));
+                const float2 a = unpack2(x[r / 2]), b = unpack2(x[r / 2 + 1]);
+                top = fmaxf(top, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
+            }
         if (mask) {
             top = -INFINITY;
+            const int4* see2 = reinterpret_cast<const int4*>(sm.now_see + r0);
 #pragma unroll
             for (int r = 0; r < HR; r += 2) {
-                const int4 s = see2[r / 2];
-                if (static_cast<uint32_t>(k.t - s.x) > static_cast<uint32_t>(s.y)) x[r] = -INFINITY;
-                if (static_cast<uint32_t>(k.t - s.z) > static_cast<uint32_t>(s.w)) x[r + 1] = -INFINITY;
-                top = fmaxf(top, fmaxf(x[r], x[r + 1]));
-            }
+                    const int4 s = see2[r / 2];
+                    float2 a = unpack2(x[r / 2]);
+                    if (static_cast<uint32_t>(k.t - s.x) > static_cast<uint32_t>(s.y)) a.x = -INFINITY;
+                    if (static_cast<uint32_t>(k.t - s.z) > static_cast<uint32_t>(s.w)) a.y = -INFINITY;
+                    x[r / 2] = pack2(a.x, a.y);
+                    top = fmaxf(top, fmaxf(a.x, a.y));
+                }
         }
         if (pass) break;
-        if (!half_any(half, top > kUp + kBehind || sm.unseen[half])) break;
+        if (!first && !half_any(half, top > kUp + kBehind || sm.unseen[half])) break;
         // The rows' maxima, as exponents over the present references; new references for the rows
         // that passed theirs by too much and those that see their first tokens.
-        const float most = reduce_rows<HR, true>(x, lane);
-        if (lane < HR) sm.part[warp][r0 + lane] = most;
+        float v[HR];
+#pragma unroll
+        for (int r = 0; r < HR; r += 2) {
+            const float2 a = unpack2(x[r / 2]);
+            v[r] = a.x;
+            v[r + 1] = a.y;
+        }
+        reduce_rows<HR, true>(sm.part + r0, v, lane, warp);
         half_sync(half);
         if ((tid & 127) < 32) {
-            const int r = r0 + (lane & (HR - 1));
-            const float over = fmaxf(fmaxf(sm.part[0][r], sm.part[1][r]), fmaxf(sm.part[2][r], sm.part[3][r]));
-            const float old = sm.row[r].y;
+            const int r = r0 + min(lane, HR - 1);
+            const float4 q = sm.part[r];
+            const float over = fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w));
+            const float old = sm.ref[r];
             const bool none = old == 0.0f;
             float y = old;
             if (over > -INFINITY && (none || over > kUp + kBehind)) {
-                y = old + over - kUp;
+                y = old - over + kUp;
                 if (y == 0.0f) y = 1e-30f;       // 0 stands for none
             }
             __syncwarp();
             if (lane < HR) {
-                sm.grow[r] = none ? 1.0f : ex2_approx(old - y);
-                sm.row[r].y = y;
+                sm.grow[r] = none ? 1.0f : ex2_approx(y - old);
+                sm.ref[r] = y;
             }
             const bool any = __any_sync(0xffffffffu, y == 0.0f);
             if (lane == 0) sm.unseen[half] = any;
         }
         half_sync(half);
-        if (first) continue;
+        if (first) {                             // the present references were 0
+#pragma unroll
+            for (int r = 0; r < HR; r += 4) {
+                    const float4 ref = ref4[r / 4];
+                    x[r / 2] = add2(x[r / 2], pack2(ref.x, ref.y));
+                    x[r / 2 + 1] = add2(x[r / 2 + 1], pack2(ref.z, ref.w));
+                }
+            break;
+        }
         // the tiles before this one have to be in the sums before these are scaled
-        if (it > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done[(it - 1) & 1]),
-                                                         ((it - 1) >> 1) & 1, stalled)))
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done[(it - 1) & 1]), ((it - 1) >> 1) & 1, stalled)))
             return false;
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < HR; c += 4) {
             float o[4], lo[4];
             tc_ld<4>(o_addr + r0 + c, o);
-            tc_ld<4>(o_addr + NR + r0 + c, lo);
+            tc_ld<4>(o_addr + R + r0 + c, lo);
             tc_wait_ld();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -244,106 +298,106 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, const int2* see, int half, f
                 lo[j] *= sm.grow[r0 + c + j];
             }
             tc_st4(o_addr + r0 + c, o);
-            tc_st4(o_addr + NR + r0 + c, lo);
+            tc_st4(o_addr + R + r0 + c, lo);
         }
         tc_wait_st();
 #pragma unroll
-        for (int r = 0; r < HR; ++r) l[r] *= sm.grow[r0 + r];
+        for (int r = 0; r < HR; r += 2)
+            l[r / 2] = mul2(l[r / 2], pack2(sm.grow[r0 + r], sm.grow[r0 + r + 1]));
     }
     // the last tile's products read the weights that these replace
     if (it > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done[(it - 1) & 1]),
                                                      ((it - 1) >> 1) & 1, stalled)))
         return false;
-    uint32_t hi[HR / 4], lo[HR / 4];
-#pragma unroll
-    for (int c = 0; c < HR / 4; ++c) {
-        float* y = x + 4 * c;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            y[j] = ex2_approx(y[j]);
-            l[4 * c + j] = fmaf(y[j], k.n.inv, l[4 * c + j]);
-        }
-        uint32_t h0, h1, l0, l1;
-        split2<true>(y[0], y[1], &h0, &l0);
-        split2<true>(y[2], y[3], &h1, &l1);
-        hi[c] = h0 | (h1 << 16);
-        lo[c] = l0 | (l1 << 16);
-    }
     const int token = tid & 127;
     uint8_t* p = &sm.p[token * kP];
     const int swz = (token >> 1) & 3;            // the 64-byte swizzle: 16-byte chunks
-    uint8_t* ph = p + (((r0 >> 4) ^ swz) << 4) + (r0 & 15);
-    uint8_t* pl = p + ((((NR + r0) >> 4) ^ swz) << 4) + ((NR + r0) & 15);
+    auto place = [&](int byte) -> uint8_t* { return p + (((byte >> 4) ^ swz) << 4) + (byte & 15); };
+    const uint64_t inv2 = pack2(k.n.inv, k.n.inv);
+    uint32_t hi[HR / 4], lo[HR / 4];
+#pragma unroll
+    for (int c = 0; c < HR / 4; ++c)
+        if (4 * c < HR) {
+            float2 a = unpack2(x[2 * c]), b = unpack2(x[2 * c + 1]);
+            a.x = ex2_approx(a.x);
+            a.y = ex2_approx(a.y);
+            b.x = ex2_approx(b.x);
+            b.y = ex2_approx(b.y);
+            l[2 * c] = fma2(pack2(a.x, a.y), inv2, l[2 * c]);
+            l[2 * c + 1] = fma2(pack2(b.x, b.y), inv2, l[2 * c + 1]);
+            uint32_t h0, h1, l0, l1;
+            split2<true>(a.x, a.y, &h0, &l0);
+            split2<true>(b.x, b.y, &h1, &l1);
+            hi[c] = h0 | (h1 << 16);
+            lo[c] = l0 | (l1 << 16);
+        }
     if (HR == 16) {
-        *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(place(r0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(place(R + r0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     } else if (HR == 8) {
-        *reinterpret_cast<uint2*>(ph) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(pl) = make_uint2(lo[0], lo[1]);
+        *reinterpret_cast<uint2*>(place(r0)) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(place(R + r0)) = make_uint2(lo[0], lo[1]);
     } else {
-        *reinterpret_cast<uint32_t*>(ph) = hi[0];
-        *reinterpret_cast<uint32_t*>(pl) = lo[0];
+        *reinterpret_cast<uint32_t*>(place(r0)) = hi[0];
+        *reinterpret_cast<uint32_t*>(place(R + r0)) = lo[0];
     }
     return true;
 }
 
-// A finished piece: sums over the threads, results or a part written. Lane d holds element d.
-template <int D, int HR>
-__device__ __forceinline__ void finish(const AttendCall& A, Smem<D>& sm, const RowInfo* info, int half,
-                                       float* l, uint32_t o_addr, int rows, bool whole, int part,
-                                       const Workspace& ws)
+// A finished piece, after its row sums are in part: results or a part written. Lane d holds
+// element d.
+template <int D, int R>
+__device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R>& sm, int half, uint32_t o_addr, int rows,
+                                       bool whole, int part, const Workspace& ws)
 {
-    constexpr int NR = 2 * HR;
-    const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3;
+    const int tid = threadIdx.x;
+    constexpr int HR = R / 2;
     const int r0 = half * HR;
-    const float mine = reduce_rows<HR, false>(l, lane);
-    if (lane < HR) sm.part[warp][r0 + lane] = mine;
-    half_sync(half);
-    const int r = r0 + (tid & 127);
-    if ((tid & 127) < HR && r < rows) {
-        const float sum = (sm.part[0][r] + sm.part[1][r]) + (sm.part[2][r] + sm.part[3][r]);
-        const float m = sm.row[r].y;             // reference - kUp, as the weights are
-        if (!whole)
-            ws.ml[part * kTile + r] = make_float2(sum == 0.0f ? kNone : m, sum);
-        else if (A.lse != nullptr)
-            A.lse[info[r].lse] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
-        sm.grow[r] = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;    // nothing seen: zeros
-    }
-    half_sync(half);
     const int d = tid & 127;
     uint16_t* out = static_cast<uint16_t*>(A.out) + d;
     float* po = ws.o + static_cast<int64_t>(part) * kTile * D + d;
 #pragma unroll 1
-    for (int c = r0; c < r0 + HR; c += 4) {
-        if (c >= rows) break;
+    for (int c = r0; c < r0 + HR && c < rows; c += 4) {
         float o[4], lo[4];
-        int64_t at[4];
         tc_ld<4>(o_addr + c, o);
-        tc_ld<4>(o_addr + NR + c, lo);
+        tc_ld<4>(o_addr + R + c, lo);
+        int64_t at[4];
+        float g[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) at[j] = info[c + j].out;
-        const float4 g = *reinterpret_cast<const float4*>(sm.grow + c);
+        for (int j = 0; j < 4; ++j) {
+            const float4 q = sm.part[c + j];
+            const float sum = (q.x + q.y) + (q.z + q.w);
+            at[j] = sm.now_info[c + j].out;
+            g[j] = !whole ? 1.0f : sum == 0.0f ? 0.0f : __frcp_rn(sum);      // nothing seen: zeros
+        }
         tc_wait_ld();
-        o[0] = fmaf(lo[0], kLowBack, o[0]) * g.x;
-        o[1] = fmaf(lo[1], kLowBack, o[1]) * g.y;
-        o[2] = fmaf(lo[2], kLowBack, o[2]) * g.z;
-        o[3] = fmaf(lo[3], kLowBack, o[3]) * g.w;
         if (D == 128 || d < D) {                 // D = 64: lanes 64.. repeat the first ones
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (whole && c + j < rows) store1<DSPARK_BF16>(out, at[j], o[j]);
-                if (!whole && c + j < rows) po[(c + j) * D] = o[j];
+                const float y = fmaf(lo[j], kLowBack, o[j]) * g[j];
+                if (whole && c + j < rows) store1<DSPARK_BF16>(out, at[j], y);
+                if (!whole && c + j < rows) po[(c + j) * D] = y;
             }
         }
+    }
+    const int r = r0 + d;
+    if (d < HR && r < rows) {
+        const float4 q = sm.part[r];
+        const float sum = (q.x + q.y) + (q.z + q.w);
+        const float m = -sm.ref[r];              // reference - kUp, as the weights are
+        if (!whole)
+            ws.ml[part * kTile + r] = make_float2(sum == 0.0f ? kNone : m, sum);
+        else if (A.lse != nullptr)
+            A.lse[sm.now_info[r].lse] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
     }
 }
 
 // One pass of 32 lanes over a unit's queries, as two pieces in shared memory: a lane takes 16
 // elements of row `row` (of D / 16 such segments), the row's factor and what the softmax needs to
 // know of it go to slot `slot`. Rows past the unit's are zeros.
-template <int D>
-static __device__ __noinline__ void load_queries(const AttendCall& A, Smem<D>& sm, const Piece& pc, int slot,
-                                                 uint8_t* q, int row, int nr)
+template <int D, int R>
+static __device__ __noinline__ void load_queries(const AttendCall& A, Smem<D, R>& sm, const Piece& pc, int slot,
+                                                 uint8_t* q, int row)
 {
     constexpr int S = D / 16;
     const int seg = threadIdx.x & (S - 1);
@@ -395,7 +449,7 @@ static __device__ __noinline__ void load_queries(const AttendCall& A, Smem<D>& s
     }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-        const int rr = p * nr + row;
+        const int rr = p * R + row;
         const int chunk = seg ^ (D == 128 ? rr & 7 : (rr >> 1) & 3);
         *reinterpret_cast<uint4*>(q + rr * D + chunk * 16) =
             p ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -411,14 +465,15 @@ static __device__ __noinline__ void load_queries(const AttendCall& A, Smem<D>& s
     }
 }
 
-__device__ __forceinline__ void describe(const AttendCall& A, const Walk<kRows>& wk, Piece& p)
+template <int R>
+__device__ __forceinline__ void describe(const AttendCall& A, const Walk<R>& wk, Piece& p)
 {
     p.b = wk.b;
     p.h = wk.h;
     p.len = wk.len;
     p.w = wk.w;
     p.row0 = wk.row0;
-    p.flat0 = wk.qt * kRows;
+    p.flat0 = wk.qt * R;
     p.rows = wk.rows(A);
     p.i0 = p.flat0 == 0 ? 0 : p.flat0 / A.group;
     p.g0 = p.flat0 - p.i0 * A.group;
@@ -429,16 +484,16 @@ __device__ __forceinline__ void describe(const AttendCall& A, const Walk<kRows>&
     p.last = wk.last();
 }
 
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 2)
 attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map)
 {
     extern __shared__ __align__(16) unsigned char raw[];
-    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(
+    Smem<D, R>& sm = *reinterpret_cast<Smem<D, R>*>(
         raw + ((kSmemAlign - (smem_addr(raw) & (kSmemAlign - 1))) & (kSmemAlign - 1)));
-    constexpr int kSlots = Smem<D>::kSlots;
-    constexpr int kNums = Smem<D>::kNums;
+    constexpr int kSlots = Smem<D, R>::kSlots;
+    constexpr int kNums = Smem<D, R>::kNums;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Workspace ws = workspace_of(A.ws);
 
@@ -466,17 +521,17 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
         tc_fence_before();
     }
     pdl_wait_and_trigger();
-    const int run = cut_line<kRows, kThreads>(A, sm.cut);
+    const int run = cut_line<R, kThreads>(A, sm.cut);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
 
     volatile int* stalled = &sm.stalled;
-    if (tid == 0) write_meta<kRows>(A, ws, sm.cut.walk, run);
+    if (tid == 0) write_meta<R>(A, ws, sm.cut.walk, run);
     if (sm.cut.walk.n > 0) {
         if (warp == 10) {
             // ---- the walk: pieces described up to three ahead; queries from the second on ----
-            Walk<kRows> wk = sm.cut.walk;
+            Walk<R> wk = sm.cut.walk;
             int described = 0;
             bool more = true, ok = true;
 #pragma unroll 1
@@ -495,15 +550,14 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                 if (piece == described) break;
                 const Piece& pc = sm.piece[piece & (kPieces - 1)];
                 if (piece > 0) {
-                    const int nr = columns_of(pc.rows);
                     if (piece >= 2)
                         ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.q_empty[piece & 1]),
                                                                ((piece >> 1) & 1) ^ 1, stalled));
                     if (!ok) break;
                     constexpr int S = D / 16;
 #pragma unroll 1
-                    for (int r = lane / S; r < nr; r += 32 / S)
-                        load_queries<D>(A, sm, pc, piece & 3, sm.q[piece & 1], r, nr);
+                    for (int r = lane / S; r < R; r += 32 / S)
+                        load_queries<D, R>(A, sm, pc, piece & 3, sm.q[piece & 1], r);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive(smem_addr(&sm.q_full[piece & 1]));
                     mbar_arrive(smem_addr(&sm.info_full[piece & 3]));
@@ -516,27 +570,30 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
             const int beyond = A.c.n_pages * A.c.heads * A.c.page;     // a row past the tensor: zeros
             int bad = 0, issued = 0, slot = 0, num = 0;
             uint32_t phase = 0;                              // parity of this use of the slot
-            bool ok = true;
+            bool ok = true, ahead = false;
+            int ahead_id = -1;
+            auto id_of = [&](const Piece& p, int j) -> int {        // -1: dead, not there, or not a page
+                if (j >= (p.k0 + p.n) * per_tile || j >= (p.len + p.w + A.c.page - 1) / A.c.page ||
+                    (j + 1) * A.c.page <= p.first_seen) return -1;
+                const int id = j < A.c.width ? A.c.table[static_cast<int64_t>(p.b) * A.c.width + j] : -1;
+                if (id < 0 || id >= A.c.n_pages) { bad = 1; return -1; }
+                return id;
+            };
 #pragma unroll 1
             for (int piece = 0; ok; ++piece) {
                 const Piece& pc = sm.piece[piece & (kPieces - 1)];
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.piece_full[piece & (kPieces - 1)]),
                                                        (piece / kPieces) & 1, stalled));
                 if (!ok) break;
-                const int h = pc.h, n = pc.n, lo = pc.first_seen;
+                const int h = pc.h, n = pc.n;
                 const bool last = pc.last;
-                const int32_t* table = A.c.table + static_cast<int64_t>(pc.b) * A.c.width;
                 const int total_blocks = (pc.len + pc.w + A.c.page - 1) / A.c.page;
-                // 32 blocks at a time, one per lane; the next 32 are fetched while these load
+                // 32 blocks at a time, one per lane; the next 32, or the next piece's first, are
+                // fetched while these load
                 int base = pc.k0 * per_tile;
-                const int end_block = base + n * per_tile;
-                auto id_of = [&](int j) -> int {        // -1: dead, not there, or not a page
-                    if (j >= end_block || j >= total_blocks || (j + 1) * A.c.page <= lo) return -1;
-                    const int id = j < A.c.width ? table[j] : -1;
-                    if (id < 0 || id >= A.c.n_pages) { bad = 1; return -1; }
-                    return id;
-                };
-                int id = -1, next_id = id_of(base + lane), j0 = 32;
+                int id = -1, next_id = ahead_id, j0 = 32;
+                if (!ahead) next_id = id_of(pc, base + lane);
+                ahead = false;
                 float2 sc = make_float2(0.0f, 0.0f);
                 base -= 32;
 #pragma unroll 1
@@ -549,7 +606,14 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                             const int64_t bh = static_cast<int64_t>(id) * A.c.heads + h;
                             sc = make_float2(A.c.k_scale[bh], A.c.v_scale[bh]);
                         }
-                        next_id = id_of(base + 32 + lane);
+                        if (base + 32 < (pc.k0 + n) * per_tile) {
+                            next_id = id_of(pc, base + 32 + lane);
+                        } else if (!last) {
+                            const int s = (piece + 1) & (kPieces - 1);
+                            ahead = __all_sync(0xffffffffu, mbar_try(smem_addr(&sm.piece_full[s]),
+                                                                     ((piece + 1) / kPieces) & 1));
+                            if (ahead) ahead_id = id_of(sm.piece[s], sm.piece[s].k0 * per_tile + lane);
+                        }
                     }
                     const int src = j0 + (lane & (per_tile - 1));
                     const int my_id = __shfl_sync(0xffffffffu, id, src);
@@ -595,18 +659,18 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
         } else if (warp == 9) {
             // ---- products: the warp runs as one, an elected lane issues ----
             const bool leader = elect_one();
-            constexpr uint32_t kIdesc = (1u << 4) | (kTile / 16 << 24);
+            constexpr uint32_t kIdesc = (1u << 4) | (kTile / 16 << 24) | (R / 4 << 17);      // 2 R columns
             // V^T: the head's elements are contiguous, and so are the weights' rows
             constexpr uint32_t kIdescPV = kIdesc | (1u << 15) | (1u << 16);
             const uint32_t tmem = sm.tmem;
             const uint64_t ring0 = operand<D>(smem_addr(sm.ring[0]));
             const uint64_t q_op = operand<D>(smem_addr(sm.q[0]));
             const uint64_t p_op = operand<kP>(smem_addr(sm.p));
-            constexpr uint32_t kStep = Smem<D>::kSlot / 16;
+            constexpr uint32_t kStep = Smem<D, R>::kSlot / 16;
             constexpr uint32_t kQStep = sizeof(sm.q[0]) / 16;
             // the scores run one tile ahead of the sums: their own place in the pieces
             int pa = -1, left_a = 0, it_a = 0, slot_a = 0;
-            uint32_t phase_a = 0, columns_a = 0;
+            uint32_t phase_a = 0;
             bool last_a = false, ready = true, ok = true;
             auto test = [&](uint32_t bar, uint32_t parity, bool wait) -> bool {
                 return __all_sync(0xffffffffu, mbar_try(bar, parity) || (wait && mbar_wait_slow(bar, parity, stalled)));
@@ -621,7 +685,6 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     ready = true;
                     left_a = sm.piece[s].n;
                     last_a = sm.piece[s].last;
-                    columns_a = columns_of(sm.piece[s].rows) >> 2 << 17;
                 }
                 if (!test(smem_addr(&sm.full[slot_a]), phase_a, wait)) return false;
                 tc_fence_after();
@@ -630,7 +693,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     const uint64_t a = ring0 + slot_a * kStep, b = q_op + (pa & 1) * kQStep;
 #pragma unroll
                     for (int s = 0; s < D / 32; ++s)
-                        mma_ss(tmem + 64 * (it_a & 1), a + 2 * s, b + 2 * s, kIdesc | columns_a, s > 0);
+                        mma_ss(tmem + 64 * (it_a & 1), a + 2 * s, b + 2 * s, kIdesc, s > 0);
                     tc_commit(smem_addr(&sm.s_full[it_a & 1]));
                     tc_commit(smem_addr(&sm.empty[slot_a]));
                     if (left_a == 0) tc_commit(smem_addr(&sm.q_empty[pa & 1]));
@@ -642,7 +705,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                 return true;
             };
             int it = 0, piece = -1, left = 0, slot = 1;
-            uint32_t phase = 0, idesc = 0, o_addr = 0;
+            uint32_t phase = 0, o_addr = 0;
             bool last = false, fresh = true;
 #pragma unroll 1
             while (true) {
@@ -657,7 +720,6 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     const Piece& pc = sm.piece[++piece & (kPieces - 1)];
                     left = pc.n;
                     last = pc.last;
-                    idesc = kIdescPV | (columns_of(pc.rows) >> 2 << 17);
                     o_addr = tmem + kSums + 64 * (piece & 1);
                     fresh = true;
                 }
@@ -668,7 +730,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     const uint64_t a = v_operand<D>(ring0 + slot * kStep);
 #pragma unroll
                     for (int s = 0; s < kTile / 32; ++s)
-                        mma_ss(o_addr, a + s * (32 * D / 16), p_op + s * (32 * kP / 16), idesc, !fresh || s > 0);
+                        mma_ss(o_addr, a + s * (32 * D / 16), p_op + s * (32 * kP / 16), kIdescPV, !fresh || s > 0);
                     tc_commit(smem_addr(&sm.pv_done[it & 1]));
                     tc_commit(smem_addr(&sm.empty[slot]));
                 }
@@ -697,9 +759,8 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
             uint32_t phase = 0;
             bool ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.piece_full[0]), 0, stalled));
             if (ok) {                            // the first unit's queries: all eight warps
-                const int nr = columns_of(sm.piece[0].rows);
                 constexpr int S = D / 16;
-                if (warp * 32 / S < nr) load_queries<D>(A, sm, sm.piece[0], 0, sm.q[0], tid / S, nr);
+                if (warp * 32 / S < R) load_queries<D, R>(A, sm, sm.piece[0], 0, sm.q[0], tid / S);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             asm volatile("bar.sync 5, 256;" ::: "memory");
@@ -707,30 +768,28 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                 mbar_arrive(smem_addr(&sm.q_full[0]));
                 mbar_arrive(smem_addr(&sm.info_full[0]));
             }
-            auto run_piece = [&](auto tag) -> bool {
-                constexpr int HR = decltype(tag)::value;
+            auto run_piece = [&]() -> bool {
                 const Piece& pc = sm.piece[piece & (kPieces - 1)];
-                const RowInfo* info = sm.now_info;
-                const int2* see = sm.now_see;
+                constexpr int HR = R / 2;
                 const int n = pc.n, rows = pc.rows;
-                float l[HR];
+                uint64_t l[HR / 2];
 #pragma unroll
-                for (int r = 0; r < HR; ++r) l[r] = 0.0f;
+                for (int r = 0; r < HR / 2; ++r) l[r] = 0;
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.info_full[piece & 3]),
                                                              (piece >> 2) & 1, stalled));
                 // copied: the walk may describe the piece after the next three over these
                 if (token < HR) {
                     const int r = half * HR + token;
-                    sm.row[r] = make_float2(sm.f[piece & 3][r], 0.0f);
+                    sm.now_f[r] = sm.f[piece & 3][r];
+                    sm.ref[r] = 0.0f;
                     sm.now_info[r] = sm.info[piece & 3][r];
                     sm.now_see[r] = sm.see[piece & 3][r];
                 }
-                if (token == 0) sm.unseen[half] = 1;
                 // tiles that every row sees whole need no mask
                 const int first_pos = sm.see[piece & 3][0].x + sm.see[piece & 3][0].y;
                 const int last_lo = sm.see[piece & 3][rows - 1].x;
-                half_sync(half);
                 const int stored = pc.len + pc.w;
+                half_sync(half);
                 const uint32_t o_addr = sm.tmem + lanes + kSums + 64 * (piece & 1);
                 // a warp whose wait gave up goes on to the piece's end, where the warps agree on it:
                 // they share the barriers within
@@ -746,8 +805,8 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     t.n = sm.nums[num][my_block];
                     if (++num == kNums) num = 0;
                     const bool mask = token0 + kTile - 1 > first_pos || token0 < last_lo;
-                    ok = soften<D, HR>(sm, see, half, l, sm.tmem + lanes + 64 * (it & 1), o_addr, t, mask, k == 0,
-                                       it, stalled) && ok;
+                    ok = soften<D, R>(sm, half, l, sm.tmem + lanes + 64 * (it & 1), o_addr, t, mask, k == 0, it,
+                                       stalled) && ok;
                     tc_fence_before();
                     if (t.t >= stored) {         // a slot past the last token: 0 x NaN is NaN
                         uint4* v = reinterpret_cast<uint4*>(&sm.ring[slot][token * D + half * (D / 2)]);
@@ -759,11 +818,19 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     slot += 2;
                     if (slot >= kSlots) { slot -= kSlots; phase ^= 1u; }
                 }
+                float v[HR];
+#pragma unroll
+                for (int r = 0; r < HR; r += 2) {
+                    const float2 a = unpack2(l[r / 2]);
+                    v[r] = a.x;
+                    v[r + 1] = a.y;
+                }
+                reduce_rows<HR, false>(sm.part + half * HR, v, lane, warp & 3);
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done[(it - 1) & 1]),
                                                              ((it - 1) >> 1) & 1, stalled));
                 if (half_any(half, !ok)) return false;
                 tc_fence_after();
-                finish<D, HR>(A, sm, info, half, l, o_addr, rows, pc.whole, blockIdx.x * 2 + (piece > 0), ws);
+                finish<D, R>(A, sm, half, o_addr, rows, pc.whole, blockIdx.x * 2 + (piece > 0), ws);
                 return true;
             };
 #pragma unroll 1
@@ -774,10 +841,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.piece_full[piece & (kPieces - 1)]),
                                                            (piece / kPieces) & 1, stalled));
                 if (half_any(half, !ok)) break;
-                const int nr = columns_of(pc.rows);
-                ok = nr == 8 ? run_piece(std::integral_constant<int, 4>{})
-                   : nr == 16 ? run_piece(std::integral_constant<int, 8>{})
-                              : run_piece(std::integral_constant<int, 16>{});
+                ok = run_piece();
                 if (!ok) break;
                 if (pc.last) break;
             }
@@ -791,13 +855,13 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(sm.tmem));
 }
 
-template <int D>
+template <int D, int R>
 int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 {
-    const size_t smem = sizeof(Smem<D>) + kSmemAlign;
+    const size_t smem = sizeof(Smem<D, R>) + kSmemAlign;
     static bool ready[64] = {};               // opt-in to large shared memory, once per device
     if (!ready[device]) {
-        const cudaError_t e = cudaFuncSetAttribute(attend_narrow_kernel<D>,
+        const cudaError_t e = cudaFuncSetAttribute(attend_narrow_kernel<D, R>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
         if (e != cudaSuccess) {
@@ -806,13 +870,13 @@ int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
         }
         ready[device] = true;
     }
-    if (!places_fit<kRows>(A))
+    if (!places_fit<R>(A))
         return fail(DSPARK_ERR_UNSUPPORTED, "dspark_attend: rows, heads and pages beyond what one call can cut");
     CUtensorMap k_map, v_map;
     int rc = encode_cache(&k_map, A.c.k, A.c);
     if (rc == DSPARK_OK) rc = encode_cache(&v_map, A.c.v, A.c);
     if (rc != DSPARK_OK) return rc;
-    return launch_pdl("attend", attend_narrow_kernel<D>, dim3(ctas), dim3(kThreads), smem, stream, A,
+    return launch_pdl("attend", attend_narrow_kernel<D, R>, dim3(ctas), dim3(kThreads), smem, stream, A,
                       k_map, v_map);
 }
 
@@ -820,7 +884,16 @@ int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 
 int launch_attend_narrow(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 {
-    return A.c.dim == 128 ? launch<128>(A, ctas, device, stream) : launch<64>(A, ctas, device, stream);
+    // Rows per unit by the requests' average: what a call's windows are is known on the device only,
+    // and a longer one is several units.
+    const int64_t rows = static_cast<int64_t>(A.rows) * A.group;
+    if (A.c.dim == 128)
+        return rows <= 8ll * A.B ? launch<128, 8>(A, ctas, device, stream)
+             : rows <= 16ll * A.B ? launch<128, 16>(A, ctas, device, stream)
+                                  : launch<128, 32>(A, ctas, device, stream);
+    return rows <= 8ll * A.B ? launch<64, 8>(A, ctas, device, stream)
+         : rows <= 16ll * A.B ? launch<64, 16>(A, ctas, device, stream)
+                              : launch<64, 32>(A, ctas, device, stream);
 }
 
 }  // namespace dspark
