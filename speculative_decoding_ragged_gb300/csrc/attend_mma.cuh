@@ -103,6 +103,19 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
         : "=r"(done) : "r"(bar), "r"(parity) : "memory");
     return done != 0;
 }
+// The same without waiting at all (try_wait may suspend the thread for some microseconds).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
 // Bounded wait for the phase of this parity. Once any thread of the CTA has given up (about a
 // second), *stalled is set and every wait returns false, so that all roles leave their loops.
 // The loop is out of line: the kernels run each part of their code a few times from a cold
@@ -422,11 +435,10 @@ __device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R>& cut)
     __syncthreads();
     int sums = lane < NT / 32 ? cut.scan[lane] : 0;
 #pragma unroll
-    for (int d = 1; d < 16; d <<= 1) {
+    for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, sums, d);
         if (lane >= d) sums += y;
     }
-    static_assert(NT / 32 <= 16, "the second scan covers 16 warps");
     const int total = __shfl_sync(0xffffffffu, sums, NT / 32 - 1);
     const int before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
     const int from = (warp > 0 ? before : 0) + upto - mine;

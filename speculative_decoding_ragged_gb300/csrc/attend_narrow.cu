@@ -13,22 +13,25 @@
 // only a tile that passes one by kLag, or a unit's first, finds the true maxima. The row sums stay
 // in registers, one partial sum per row and thread, until the unit ends.
 //
-// A CTA: warps 0-7 do the softmax, two threads per token with half of the rows each (two groups
-// of four warps that never meet), warp 8 loads pages with TMA, warp 9 issues the products one tile
-// of scores ahead, warp 10 walks the run's units, describes them to the others and prepares their
+// A CTA: two groups of four warps do the softmax, a thread per token with half of the rows (groups
+// of eight rows, four of them at R = 32, were 10 to 15 % slower); one warp loads pages with TMA, one issues the products one tile of
+// scores ahead, one walks the run's units, describes them to the others and prepares their
 // queries. Scores and sums are double buffered in TMEM (256 columns), the ring holds 2.5 tiles of
 // K and V, two CTAs per SM.
 //
 // Bound by HBM: 2 D bytes per token and cache head. What else showed in clock stamps was cold
 // code (about 16 cycles per instruction the first time), hence one walker, rolled loops where
-// registers allow them, and half the rows per thread.
+// registers allow them.
 #include "attend_mma.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kSoftThreads = 256;
-constexpr int kThreads = 352;
+// Softmax threads: two groups of four warps (a thread per token), half of the rows each.
+constexpr int group_rows(int R) { return R / 2; }
+constexpr int groups(int R) { return R / group_rows(R); }
+constexpr int soft_threads(int R) { return 128 * groups(R); }
+constexpr int all_threads(int R) { return soft_threads(R) + 96; }
 constexpr int kP = 64;                       // bytes of a token's row of weights: two pieces of 32
 constexpr int kPieces = 8;                   // described pieces
 // Weights are 2^(x - m + kUp) where m may lag the true maximum by kBehind: at most 2^8.5 < 448.
@@ -64,7 +67,7 @@ struct Smem {
     uint8_t p[kTile * kP];                               // the weights, a row per token
     BlockNums nums[kNums][kBlocks];
     Piece piece[kPieces];
-    RowInfo info[4][R];                              // four units' rows
+    RowInfo info[4][R];                                  // four units' rows
     int2 see[4][R];                                  // first token seen, and how many past it
     float f[4][R];                                   // score factors: scale log2(e) 2^e
     RowInfo now_info[R];                             // the softmax's own copies of its unit's
@@ -73,12 +76,13 @@ struct Smem {
     __align__(16) float ref[R];                      // kUp - reference (0: nothing seen yet)
     __align__(16) float grow[R];                     // 2^(old reference - new)
     float4 part[R];                                  // the four warps' maxima or sums
-    int unseen[2];                                       // a row of the half has seen nothing yet
+    int unseen[groups(R)];                               // a row of the group has seen nothing yet
     uint64_t full[kSlots], empty[kSlots];
-    uint64_t piece_full[kPieces], info_full[4], q_full[2], q_empty[2];
+    uint64_t piece_full[kPieces], q_full[2];
     uint64_t s_full[2], pv_done[2], p_full;
     Cut<R> cut;
     uint32_t tmem;
+    int softened;        // pieces whose tiles the softmax is done with
     int stalled;         // a wait gave up: every role leaves its loop
 };
 
@@ -144,9 +148,9 @@ __device__ __forceinline__ void tc_st4(uint32_t addr, const float* x)
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};"
                  ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
-// The four warps of a half: a barrier, and a barrier with a vote.
-__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
-__device__ __forceinline__ bool half_any(int half, bool yes)
+// The four warps of a group: a barrier, and a barrier with a vote.
+__device__ __forceinline__ void group_sync(int grp) { asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory"); }
+__device__ __forceinline__ bool group_any(int grp, bool yes)
 {
     uint32_t r;
     asm volatile(
@@ -155,7 +159,7 @@ __device__ __forceinline__ bool half_any(int half, bool yes)
         " setp.ne.u32 p, %1, 0;\n"
         " barrier.cta.red.or.pred q, %2, 128, p;\n"
         " selp.u32 %0, 1, 0, q;\n"
-        "}\n" : "=r"(r) : "r"(static_cast<uint32_t>(yes)), "r"(3 + half) : "memory");
+        "}\n" : "=r"(r) : "r"(static_cast<uint32_t>(yes)), "r"(5 + grp) : "memory");
     return r != 0;
 }
 
@@ -192,15 +196,15 @@ struct Token {
     int t;
 };
 
-// One tile, this thread's token, half of the R rows: scores in TMEM -> weights in shared memory;
+// One tile, this thread's token, one group's rows: scores in TMEM -> weights in shared memory;
 // l += this token's weights.
 template <int D, int R>
-__device__ __forceinline__ bool soften(Smem<D, R>& sm, int half, uint64_t* l, uint32_t s_addr, uint32_t o_addr,
+__device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, uint64_t* l, uint32_t s_addr, uint32_t o_addr,
                                        const Token& k, bool mask, bool first, int it, volatile int* stalled)
 {
-    constexpr int HR = R / 2;
+    constexpr int HR = group_rows(R);
     const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3;
-    const int r0 = half * HR;
+    const int r0 = grp * HR;
     const float4* f4 = reinterpret_cast<const float4*>(sm.now_f + r0);
     const float4* ref4 = reinterpret_cast<const float4*>(sm.ref + r0);
     const uint64_t ks2 = pack2(k.n.ks, k.n.ks), bias2 = pack2(k.n.bias, k.n.bias);
@@ -241,7 +245,7 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int half, uint64_t* l, ui
                 }
         }
         if (pass) break;
-        if (!first && !half_any(half, top > kUp + kBehind || sm.unseen[half])) break;
+        if (!first && !group_any(grp, top > kUp + kBehind || sm.unseen[grp])) break;
         // The rows' maxima, as exponents over the present references; new references for the rows
         // that passed theirs by too much and those that see their first tokens.
         float v[HR];
@@ -252,7 +256,7 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int half, uint64_t* l, ui
             v[r + 1] = a.y;
         }
         reduce_rows<HR, true>(sm.part + r0, v, lane, warp);
-        half_sync(half);
+        group_sync(grp);
         if ((tid & 127) < 32) {
             const int r = r0 + min(lane, HR - 1);
             const float4 q = sm.part[r];
@@ -270,9 +274,9 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int half, uint64_t* l, ui
                 sm.ref[r] = y;
             }
             const bool any = __any_sync(0xffffffffu, y == 0.0f);
-            if (lane == 0) sm.unseen[half] = any;
+            if (lane == 0) sm.unseen[grp] = any;
         }
-        half_sync(half);
+        group_sync(grp);
         if (first) {                             // the present references were 0
 #pragma unroll
             for (int r = 0; r < HR; r += 4) {
@@ -347,12 +351,12 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int half, uint64_t* l, ui
 // A finished piece, after its row sums are in part: results or a part written. Lane d holds
 // element d.
 template <int D, int R>
-__device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R>& sm, int half, uint32_t o_addr, int rows,
+__device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R>& sm, int grp, uint32_t o_addr, int rows,
                                        bool whole, int part, const Workspace& ws)
 {
     const int tid = threadIdx.x;
-    constexpr int HR = R / 2;
-    const int r0 = half * HR;
+    constexpr int HR = group_rows(R);
+    const int r0 = grp * HR;
     const int d = tid & 127;
     uint16_t* out = static_cast<uint16_t*>(A.out) + d;
     float* po = ws.o + static_cast<int64_t>(part) * kTile * D + d;
@@ -368,7 +372,7 @@ __device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R>& sm, int 
             const float4 q = sm.part[c + j];
             const float sum = (q.x + q.y) + (q.z + q.w);
             at[j] = sm.now_info[c + j].out;
-            g[j] = !whole ? 1.0f : sum == 0.0f ? 0.0f : __frcp_rn(sum);      // nothing seen: zeros
+            g[j] = !whole ? 1.0f : sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);      // nothing seen: zeros
         }
         tc_wait_ld();
         if (D == 128 || d < D) {                 // D = 64: lanes 64.. repeat the first ones
@@ -392,44 +396,57 @@ __device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R>& sm, int 
     }
 }
 
-// One pass of 32 lanes over a unit's queries, as two pieces in shared memory: a lane takes 16
-// elements of row `row` (of D / 16 such segments), the row's factor and what the softmax needs to
-// know of it go to slot `slot`. Rows past the unit's are zeros.
-template <int D, int R>
-static __device__ __noinline__ void load_queries(const AttendCall& A, Smem<D, R>& sm, const Piece& pc, int slot,
-                                                 uint8_t* q, int row)
+// A lane's share of a unit's queries: 16 elements of row `row`, one of its D / 16 segments.
+struct QueryAt {
+    int64_t prow;                                // the row's packed row and head
+    int head, pos;
+};
+__device__ __forceinline__ QueryAt query_at(const AttendCall& A, const Piece& pc, int row)
 {
-    constexpr int S = D / 16;
-    const int seg = threadIdx.x & (S - 1);
-    const bool live = row < pc.rows;
-    int i = pc.i0, g = pc.g0 + (live ? row : pc.rows - 1);
+    QueryAt q;
+    int i = pc.i0, g = pc.g0 + min(row, pc.rows - 1);
     if (g >= A.group) {
         const int more = g / A.group;
         i += more;
         g -= more * A.group;
     }
-    const int64_t prow = pc.row0 + i;
-    const int head = pc.h * A.group + g;
-    const uint16_t* at = static_cast<const uint16_t*>(A.q) + prow * A.q_stride + static_cast<int64_t>(head) * D + seg * 16;
-    uint4 v[2];
+    q.prow = pc.row0 + i;
+    q.head = pc.h * A.group + g;
+    q.pos = pc.len + i;
+    return q;
+}
+template <int D>
+__device__ __forceinline__ void fetch_query(const AttendCall& A, const QueryAt& q, uint4* v)
+{
+    const uint16_t* at = static_cast<const uint16_t*>(A.q) + q.prow * A.q_stride +
+                         static_cast<int64_t>(q.head) * D + (threadIdx.x & (D / 16 - 1)) * 16;
     if ((reinterpret_cast<uintptr_t>(at) & 15u) == 0) {
         v[0] = reinterpret_cast<const uint4*>(at)[0];
         v[1] = reinterpret_cast<const uint4*>(at)[1];
     } else {
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < 2; ++j) {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 w[k] = at[8 * j + 2 * k] | (static_cast<uint32_t>(at[8 * j + 2 * k + 1]) << 16);
-            v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            (j ? v[1] : v[0]) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+}
+// The fetched elements as two pieces in shared memory; the row's factor and what the softmax needs
+// to know of it go to slot `slot`. Rows past the unit's are zeros. All 32 lanes.
+template <int D, int R>
+static __device__ __noinline__ void put_query(const AttendCall& A, Smem<D, R>& sm, const Piece& pc, int slot,
+                                              uint8_t* q, int row, uint4 v0, uint4 v1)
+{
+    constexpr int S = D / 16;
+    const int seg = threadIdx.x & (S - 1);
+    uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     uint32_t top = 0;                            // magnitudes' bits order like them, NaN above all
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        if (!live) w[k] = 0;
+        if (row >= pc.rows) w[k] = 0;
         top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
     }
 #pragma unroll
@@ -455,11 +472,11 @@ static __device__ __noinline__ void load_queries(const AttendCall& A, Smem<D, R>
             p ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
     if (seg == 0) {
-        const int pos = pc.len + i;
-        const int first = A.window > 0 && pos >= A.window ? pos - A.window + 1 : 0;
-        sm.info[slot][row].out = prow * A.out_stride + static_cast<int64_t>(head) * D;
-        sm.info[slot][row].lse = prow * A.q_heads + head;
-        sm.see[slot][row] = make_int2(first, pos - first);
+        const QueryAt at = query_at(A, pc, row);
+        const int first = A.window > 0 && at.pos >= A.window ? at.pos - A.window + 1 : 0;
+        sm.info[slot][row].out = at.prow * A.out_stride + static_cast<int64_t>(at.head) * D;
+        sm.info[slot][row].lse = at.prow * A.q_heads + at.head;
+        sm.see[slot][row] = make_int2(first, at.pos - first);
         // a query that is not finite makes its row's factor, hence its results, NaN
         sm.f[slot][row] = fine ? A.scale * kLog2e * exp2i(e) : __int_as_float(0x7fc00000);
     }
@@ -485,7 +502,7 @@ __device__ __forceinline__ void describe(const AttendCall& A, const Walk<R>& wk,
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(all_threads(R), 2)
 attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map)
 {
@@ -494,6 +511,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
         raw + ((kSmemAlign - (smem_addr(raw) & (kSmemAlign - 1))) & (kSmemAlign - 1)));
     constexpr int kSlots = Smem<D, R>::kSlots;
     constexpr int kNums = Smem<D, R>::kNums;
+    constexpr int G = groups(R), kLoader = 4 * G, kIssuer = kLoader + 1, kWalker = kLoader + 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Workspace ws = workspace_of(A.ws);
 
@@ -503,25 +521,23 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
     } else if (tid >= 32 && tid < 32 + kPieces) {
         const int s = tid - 32;
         mbar_init(smem_addr(&sm.piece_full[s]), 1);
-        if (s < 4) mbar_init(smem_addr(&sm.info_full[s]), 32);
         if (s < 2) {
-            mbar_init(smem_addr(&sm.q_full[s]), 32);
-            mbar_init(smem_addr(&sm.q_empty[s]), 1);
+            mbar_init(smem_addr(&sm.q_full[s]), soft_threads(R));
             mbar_init(smem_addr(&sm.s_full[s]), 1);
             mbar_init(smem_addr(&sm.pv_done[s]), 1);
         }
-        if (s == 2) mbar_init(smem_addr(&sm.p_full), kSoftThreads);
-        if (s == 3) sm.stalled = 0;
+        if (s == 2) mbar_init(smem_addr(&sm.p_full), soft_threads(R));
+        if (s == 3) sm.stalled = sm.softened = 0;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (warp == 9) {
+    if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;"
                      ::"r"(smem_addr(&sm.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         tc_fence_before();
     }
     pdl_wait_and_trigger();
-    const int run = cut_line<R, kThreads>(A, sm.cut);
+    const int run = cut_line<R, all_threads(R)>(A, sm.cut);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -529,41 +545,35 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
     volatile int* stalled = &sm.stalled;
     if (tid == 0) write_meta<R>(A, ws, sm.cut.walk, run);
     if (sm.cut.walk.n > 0) {
-        if (warp == 10) {
-            // ---- the walk: pieces described up to three ahead; queries from the second on ----
+        if (warp == kWalker) {
+            // ---- the walk: pieces described to the others, and their queries fetched into L2 ----
             Walk<R> wk = sm.cut.walk;
-            int described = 0;
-            bool more = true, ok = true;
 #pragma unroll 1
-            for (int piece = 0; ok; ++piece) {
-#pragma unroll 1
-                while (more && described <= piece + 2) {
-                    if (lane == 0) {
-                        describe(A, wk, sm.piece[described & (kPieces - 1)]);
-                        mbar_arrive(smem_addr(&sm.piece_full[described & (kPieces - 1)]));
-                    }
-                    __syncwarp();
-                    ++described;
-                    more = !wk.last();
-                    if (more) wk.next(A);
+            for (int d = 0;; ++d) {
+                // the slot's last piece, and the one after it, are behind every role
+                const long long deadline = clock64() + kWaitCycles;
+                while (d >= kPieces - 2 && *reinterpret_cast<volatile int*>(&sm.softened) < d - (kPieces - 2) + 1) {
+                    if (*stalled || clock64() > deadline) { *stalled = 1; break; }
+                    __nanosleep(100);
                 }
-                if (piece == described) break;
-                const Piece& pc = sm.piece[piece & (kPieces - 1)];
-                if (piece > 0) {
-                    if (piece >= 2)
-                        ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.q_empty[piece & 1]),
-                                                               ((piece >> 1) & 1) ^ 1, stalled));
-                    if (!ok) break;
-                    constexpr int S = D / 16;
-#pragma unroll 1
-                    for (int r = lane / S; r < R; r += 32 / S)
-                        load_queries<D, R>(A, sm, pc, piece & 3, sm.q[piece & 1], r);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive(smem_addr(&sm.q_full[piece & 1]));
-                    mbar_arrive(smem_addr(&sm.info_full[piece & 3]));
+                if (__any_sync(0xffffffffu, *stalled)) break;
+                Piece& pc = sm.piece[d & (kPieces - 1)];
+                if (lane == 0) {
+                    describe(A, wk, pc);
+                    mbar_arrive(smem_addr(&sm.piece_full[d & (kPieces - 1)]));
                 }
+                __syncwarp();
+                if (lane < pc.rows) {
+                    const QueryAt at = query_at(A, pc, lane);
+                    const char* q = reinterpret_cast<const char*>(static_cast<const uint16_t*>(A.q) + at.prow * A.q_stride +
+                                                                  static_cast<int64_t>(at.head) * D);
+#pragma unroll
+                    for (int o = 0; o < D * 2; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + o));
+                }
+                if (wk.last()) break;
+                wk.next(A);
             }
-        } else if (warp == 8) {
+        } else if (warp == kLoader) {
             // ---- pages in ----
             const int per_tile = kTile / A.c.page;
             const uint32_t box = static_cast<uint32_t>(A.c.page) * D;
@@ -572,6 +582,12 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
             uint32_t phase = 0;                              // parity of this use of the slot
             bool ok = true, ahead = false;
             int ahead_id = -1;
+            float2 ahead_sc = make_float2(0.0f, 0.0f);
+            auto scales_of = [&](int id, int h) -> float2 {
+                if (id < 0) return make_float2(0.0f, 0.0f);
+                const int64_t bh = static_cast<int64_t>(id) * A.c.heads + h;
+                return make_float2(A.c.k_scale[bh], A.c.v_scale[bh]);
+            };
             auto id_of = [&](const Piece& p, int j) -> int {        // -1: dead, not there, or not a page
                 if (j >= (p.k0 + p.n) * per_tile || j >= (p.len + p.w + A.c.page - 1) / A.c.page ||
                     (j + 1) * A.c.page <= p.first_seen) return -1;
@@ -593,6 +609,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                 int base = pc.k0 * per_tile;
                 int id = -1, next_id = ahead_id, j0 = 32;
                 if (!ahead) next_id = id_of(pc, base + lane);
+                bool have = ahead;               // the first blocks' scales
                 ahead = false;
                 float2 sc = make_float2(0.0f, 0.0f);
                 base -= 32;
@@ -602,16 +619,14 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                         j0 = 0;
                         base += 32;
                         id = next_id;
-                        if (id >= 0) {
-                            const int64_t bh = static_cast<int64_t>(id) * A.c.heads + h;
-                            sc = make_float2(A.c.k_scale[bh], A.c.v_scale[bh]);
-                        }
+                        sc = have ? ahead_sc : scales_of(id, h);
+                        have = false;
                         if (base + 32 < (pc.k0 + n) * per_tile) {
                             next_id = id_of(pc, base + 32 + lane);
                         } else if (!last) {
                             const int s = (piece + 1) & (kPieces - 1);
-                            ahead = __all_sync(0xffffffffu, mbar_try(smem_addr(&sm.piece_full[s]),
-                                                                     ((piece + 1) / kPieces) & 1));
+                            ahead = __all_sync(0xffffffffu, mbar_test(smem_addr(&sm.piece_full[s]),
+                                                                      ((piece + 1) / kPieces) & 1));
                             if (ahead) ahead_id = id_of(sm.piece[s], sm.piece[s].k0 * per_tile + lane);
                         }
                     }
@@ -648,6 +663,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     if (!ok) break;
                     j0 += per_tile;
                 }
+                if (ahead) ahead_sc = scales_of(ahead_id, sm.piece[(piece + 1) & (kPieces - 1)].h);
                 if (last) break;
             }
             if (bad) raise_status(A.status, DSPARK_STATUS_BAD_PAGE);
@@ -656,7 +672,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
 #pragma unroll 1
             for (int s = 0; s < kSlots && s < issued; ++s)
                 drain(smem_addr(&sm.full[s]), ((issued - 1 - s) / kSlots) & 1, stalled);
-        } else if (warp == 9) {
+        } else if (warp == kIssuer) {
             // ---- products: the warp runs as one, an elected lane issues ----
             const bool leader = elect_one();
             constexpr uint32_t kIdesc = (1u << 4) | (kTile / 16 << 24) | (R / 4 << 17);      // 2 R columns
@@ -673,7 +689,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
             uint32_t phase_a = 0;
             bool last_a = false, ready = true, ok = true;
             auto test = [&](uint32_t bar, uint32_t parity, bool wait) -> bool {
-                return __all_sync(0xffffffffu, mbar_try(bar, parity) || (wait && mbar_wait_slow(bar, parity, stalled)));
+                return __all_sync(0xffffffffu, wait ? mbar_wait(bar, parity, stalled) : mbar_test(bar, parity));
             };
             // the scores of tile it_a; unless `wait`, only if everything is there already
             auto scores = [&](bool wait) -> bool {
@@ -696,7 +712,6 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                         mma_ss(tmem + 64 * (it_a & 1), a + 2 * s, b + 2 * s, kIdesc, s > 0);
                     tc_commit(smem_addr(&sm.s_full[it_a & 1]));
                     tc_commit(smem_addr(&sm.empty[slot_a]));
-                    if (left_a == 0) tc_commit(smem_addr(&sm.q_empty[pa & 1]));
                 }
                 __syncwarp();
                 slot_a += 2;
@@ -746,40 +761,49 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                 const int uk = 2 * (it - 1), uv = uk + 1;
                 drain(smem_addr(&sm.empty[uk % kSlots]), (uk / kSlots) & 1, stalled);
                 drain(smem_addr(&sm.empty[uv % kSlots]), (uv / kSlots) & 1, stalled);
-                drain(smem_addr(&sm.q_empty[piece & 1]), (piece >> 1) & 1, stalled);
             }
             __syncwarp();
         } else {
             // ---- softmax ----
-            const int half = warp >> 2;
-            const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+            const int grp = warp >> 2;
+                        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
             const int token = tid & 127;
             const int my_block = token / A.c.page;
             int it = 0, piece = 0, slot = 1, num = 0;
             uint32_t phase = 0;
-            bool ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.piece_full[0]), 0, stalled));
-            if (ok) {                            // the first unit's queries: all eight warps
-                constexpr int S = D / 16;
-                if (warp * 32 / S < R) load_queries<D, R>(A, sm, sm.piece[0], 0, sm.q[0], tid / S);
+            bool ok = true;
+            // Piece `p`'s queries: fetched here, put into shared memory by put() some time later.
+            constexpr int S = D / 16;
+            const bool carries = warp * 32 / S < R;
+            uint4 v[2];
+            auto fetch = [&](int p) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.piece_full[p & (kPieces - 1)]),
+                                                             (p / kPieces) & 1, stalled));
+                if (ok && carries) fetch_query<D>(A, query_at(A, sm.piece[p & (kPieces - 1)], tid / S), v);
+            };
+            auto put = [&](int p) {
+                if (ok && carries)
+                    put_query<D, R>(A, sm, sm.piece[p & (kPieces - 1)], p & 3, sm.q[p & 1], tid / S, v[0], v[1]);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
-            asm volatile("bar.sync 5, 256;" ::: "memory");
-            if (warp == 0) {
-                mbar_arrive(smem_addr(&sm.q_full[0]));
-                mbar_arrive(smem_addr(&sm.info_full[0]));
+                mbar_arrive(smem_addr(&sm.q_full[p & 1]));
+            };
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p) {
+                fetch(p);
+                put(p);
+                if (!ok || sm.piece[p].last) break;
             }
             auto run_piece = [&]() -> bool {
                 const Piece& pc = sm.piece[piece & (kPieces - 1)];
-                constexpr int HR = R / 2;
+                constexpr int HR = group_rows(R);
                 const int n = pc.n, rows = pc.rows;
                 uint64_t l[HR / 2];
 #pragma unroll
                 for (int r = 0; r < HR / 2; ++r) l[r] = 0;
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.info_full[piece & 3]),
-                                                             (piece >> 2) & 1, stalled));
-                // copied: the walk may describe the piece after the next three over these
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.q_full[piece & 1]),
+                                                             (piece >> 1) & 1, stalled));
                 if (token < HR) {
-                    const int r = half * HR + token;
+                    const int r = grp * HR + token;
                     sm.now_f[r] = sm.f[piece & 3][r];
                     sm.ref[r] = 0.0f;
                     sm.now_info[r] = sm.info[piece & 3][r];
@@ -789,7 +813,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                 const int first_pos = sm.see[piece & 3][0].x + sm.see[piece & 3][0].y;
                 const int last_lo = sm.see[piece & 3][rows - 1].x;
                 const int stored = pc.len + pc.w;
-                half_sync(half);
+                group_sync(grp);
                 const uint32_t o_addr = sm.tmem + lanes + kSums + 64 * (piece & 1);
                 // a warp whose wait gave up goes on to the piece's end, where the warps agree on it:
                 // they share the barriers within
@@ -805,42 +829,43 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     t.n = sm.nums[num][my_block];
                     if (++num == kNums) num = 0;
                     const bool mask = token0 + kTile - 1 > first_pos || token0 < last_lo;
-                    ok = soften<D, R>(sm, half, l, sm.tmem + lanes + 64 * (it & 1), o_addr, t, mask, k == 0, it,
+                    ok = soften<D, R>(sm, grp, l, sm.tmem + lanes + 64 * (it & 1), o_addr, t, mask, k == 0, it,
                                        stalled) && ok;
                     tc_fence_before();
                     if (t.t >= stored) {         // a slot past the last token: 0 x NaN is NaN
-                        uint4* v = reinterpret_cast<uint4*>(&sm.ring[slot][token * D + half * (D / 2)]);
+                        uint4* v = reinterpret_cast<uint4*>(&sm.ring[slot][token * D + grp * (D / G)]);
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) v[c] = make_uint4(0, 0, 0, 0);
+                        for (int c = 0; c < D / G / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     if (ok) mbar_arrive(smem_addr(&sm.p_full));
                     slot += 2;
                     if (slot >= kSlots) { slot -= kSlots; phase ^= 1u; }
                 }
-                float v[HR];
+                // the queries of the piece after the next go where this one's were
+                if (tid == 0) *reinterpret_cast<volatile int*>(&sm.softened) = piece + 1;
+                const bool more = !pc.last && !sm.piece[(piece + 1) & (kPieces - 1)].last;
+                if (more) fetch(piece + 2);
+                float sums[HR];
 #pragma unroll
                 for (int r = 0; r < HR; r += 2) {
                     const float2 a = unpack2(l[r / 2]);
-                    v[r] = a.x;
-                    v[r + 1] = a.y;
+                    sums[r] = a.x;
+                    sums[r + 1] = a.y;
                 }
-                reduce_rows<HR, false>(sm.part + half * HR, v, lane, warp & 3);
+                reduce_rows<HR, false>(sm.part + grp * HR, sums, lane, warp & 3);
+                if (more) put(piece + 2);
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done[(it - 1) & 1]),
                                                              ((it - 1) >> 1) & 1, stalled));
-                if (half_any(half, !ok)) return false;
+                if (group_any(grp, !ok)) return false;
                 tc_fence_after();
-                finish<D, R>(A, sm, half, o_addr, rows, pc.whole, blockIdx.x * 2 + (piece > 0), ws);
+                finish<D, R>(A, sm, grp, o_addr, rows, pc.whole, blockIdx.x * 2 + (piece > 0), ws);
                 return true;
             };
 #pragma unroll 1
-            for (; ok; ++piece) {
+            for (;; ++piece) {
                 const Piece& pc = sm.piece[piece & (kPieces - 1)];
-                // the roles before this one have seen the description; so has this thread, by them
-                if (piece > 0)
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.piece_full[piece & (kPieces - 1)]),
-                                                           (piece / kPieces) & 1, stalled));
-                if (half_any(half, !ok)) break;
+                if (group_any(grp, !ok)) break;
                 ok = run_piece();
                 if (!ok) break;
                 if (pc.last) break;
@@ -851,7 +876,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && sm.stalled) raise_status(A.status, DSPARK_STATUS_STALL);
-    if (warp == 9)
+    if (warp == kIssuer)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(sm.tmem));
 }
 
@@ -876,7 +901,7 @@ int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
     int rc = encode_cache(&k_map, A.c.k, A.c);
     if (rc == DSPARK_OK) rc = encode_cache(&v_map, A.c.v, A.c);
     if (rc != DSPARK_OK) return rc;
-    return launch_pdl("attend", attend_narrow_kernel<D, R>, dim3(ctas), dim3(kThreads), smem, stream, A,
+    return launch_pdl("attend", attend_narrow_kernel<D, R>, dim3(ctas), dim3(all_threads(R)), smem, stream, A,
                       k_map, v_map);
 }
 
