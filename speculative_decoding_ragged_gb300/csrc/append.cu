@@ -4,15 +4,14 @@
 // A block is one page's slots of one kv head; its scale is a power of two, so that growing it
 // rescales the codes already there by an exact shift of their exponent (only codes that leave
 // e4m3's normal range round again), and multiplying by it is exact. The step's rows that fall
-// into one block are consecutive packed rows; the first of them leads. One warp owns a block (of
+// into one block are consecutive packed rows; the first of them leads. One warp, or for prompts one CTA, owns a block (of
 // keys or of values): it finds the block's rows, their largest magnitude, hence the scale,
-// requantises the retained codes if the scale grew, and writes the rows' codes. No two warps touch
+// requantises the retained codes if the scale grew, and writes the rows' codes. No two touch
 // one block, so there are no atomics and the result does not depend on any order.
 //
-// A CTA takes one packed row (several where there are many rows) and the blocks of four heads'
-// keys and values that it leads; the rotation's factors of the block's rows are computed once per
-// CTA in shared memory. A window's few rows stay in registers between the maximum and the codes; a
-// prompt's are read again, from L1 or L2, and the factors kept.
+// The rotation's factors of the block's rows are computed once per CTA in shared memory, for four
+// heads' keys at a time in a step. The rows' elements stay in registers between the maximum and the
+// codes where they fit (8 rows of 128 for a warp, 64 for a CTA); else they are read again.
 // Bound by memory for prompts, by the chain of dependent loads (row owner, length, page id,
 // scale, retained codes) for a step.
 #include "cache.cuh"
@@ -21,20 +20,24 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;      // of a step's CTA, and of one that rotates queries
 constexpr int kWarps = kThreads / 32;
+constexpr int kTeam = 16;          // warps that take a prompt's block together
 constexpr int kTable = 4096;       // shared rope factors (32 KB): 64 rows of 64 pairs
-constexpr int kKeep = 4;           // units of a lane that stay in registers
+constexpr int keep_of(int T) { return T > 1 ? 2 : 4; }     // units of a lane that stay in registers
+constexpr int kQueryRows = 4;      // most rows of a CTA that rotates queries
+constexpr int kQueryFactors = 512; // their factors
+constexpr int kHeads = 4;          // heads of a CTA that takes whole blocks, one after the other
 
 struct AppendArgs {
     dspark_cache c;
     Rope rope;
-    RowsIn k, v, q;
-    RowsOut q_out;
+    RowsIn k, v;
+    Turns q;
     const int32_t* row_req;
     const int32_t* row_pos;
     const int32_t* lengths;
-    int rows, B, q_heads;
+    int rows, B;
     int kv_ctas;          // first of the grid: (rows, eight blocks)
     int per_row;          // of them for the same rows
     int chunk;            // rows a kv CTA looks for leaders in
@@ -63,34 +66,53 @@ struct Unit {
     }
 };
 
+// A unit as it was loaded, and its elements in fp32.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load_unit(const void* base, int64_t at, const Unit<VEC>& un, float* x)
-{
-    if (!VEC) {
-        x[0] = load1<DT>(base, at + un.a);
-        x[1] = load1<DT>(base, at + un.b);
-    } else if (DT == DSPARK_BF16) {
-        const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-        const uint2 a = *reinterpret_cast<const uint2*>(p + un.a), b = *reinterpret_cast<const uint2*>(p + un.b);
-        x[0] = bf16_lo(a.x); x[1] = bf16_hi(a.x); x[2] = bf16_lo(a.y); x[3] = bf16_hi(a.y);
-        x[4] = bf16_lo(b.x); x[5] = bf16_hi(b.x); x[6] = bf16_lo(b.y); x[7] = bf16_hi(b.y);
-    } else {
-        const float* p = static_cast<const float*>(base) + at;
-        const float4 a = *reinterpret_cast<const float4*>(p + un.a), b = *reinterpret_cast<const float4*>(p + un.b);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+struct Raw {
+    static constexpr int W = VEC ? (DT == DSPARK_BF16 ? 4 : 8) : 2;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const void* base, int64_t at, const Unit<VEC>& un)
+    {
+        if (!VEC) {
+            w[0] = __float_as_uint(load1<DT>(base, at + un.a));
+            w[1] = __float_as_uint(load1<DT>(base, at + un.b));
+        } else if (DT == DSPARK_BF16) {
+            const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+            const uint2 a = *reinterpret_cast<const uint2*>(p + un.a), b = *reinterpret_cast<const uint2*>(p + un.b);
+            w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+        } else {
+            const uint32_t* p = static_cast<const uint32_t*>(base) + at;
+            const uint4 a = *reinterpret_cast<const uint4*>(p + un.a), b = *reinterpret_cast<const uint4*>(p + un.b);
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+            w[W - 4] = b.x; w[W - 3] = b.y; w[W - 2] = b.z; w[W - 1] = b.w;
+        }
     }
-}
+    __device__ __forceinline__ void get(float* x) const
+    {
+        if (VEC && DT == DSPARK_BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16_lo(w[i]);
+                x[2 * i + 1] = bf16_hi(w[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) x[i] = __uint_as_float(w[i]);
+        }
+    }
+};
 
-// Non-finite elements count as 0; the rotated ones turn. Returns whether anything was not finite.
-template <bool VEC>
+// The rotated elements turn. CHECK: non-finite elements count as 0, before and after; returns
+// whether there were any.
+template <bool VEC, bool CHECK>
 __device__ __forceinline__ bool turn_unit(const Rope& r, const Unit<VEC>& un, const float2* tab, float* x)
 {
     constexpr int N = Unit<VEC>::N;
     bool bad = false;
+    if (CHECK)
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (!finite(x[j])) { x[j] = 0.0f; bad = true; }
+        for (int j = 0; j < N; ++j)
+            if (!finite(x[j])) { x[j] = 0.0f; bad = true; }
     if (un.pair < 0) return bad;
     if (un.split) {
 #pragma unroll
@@ -107,9 +129,10 @@ __device__ __forceinline__ bool turn_unit(const Rope& r, const Unit<VEC>& un, co
             x[2 * j + 1] = t.y;
         }
     }
+    if (CHECK)
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (!finite(x[j])) { x[j] = 0.0f; bad = true; }      // the sum of two products overflowed
+        for (int j = 0; j < N; ++j)
+            if (!finite(x[j])) { x[j] = 0.0f; bad = true; }  // the sum of two products overflowed
     return bad;
 }
 
@@ -117,7 +140,7 @@ template <bool VEC>
 __device__ __forceinline__ float amax_unit(const float* x, float m)
 {
 #pragma unroll
-    for (int j = 0; j < Unit<VEC>::N; ++j) m = fmaxf(m, fabsf(x[j]));
+    for (int j = 0; j < Unit<VEC>::N; ++j) m = max_nan(m, fabsf(x[j]));
     return m;
 }
 
@@ -140,24 +163,40 @@ __device__ __forceinline__ void store_unit(uint8_t* row, const Unit<VEC>& un, co
     }
 }
 
-// A block's scale from its rows' largest magnitude; the retained codes follow it. One warp.
-__device__ __forceinline__ float settle_scale(float amax, float* scale, uint8_t* codes, int retained, int lane)
+// The largest of a team of T warps (1, or the whole CTA), NaN above all; `me` of 32 T threads.
+template <int T>
+__device__ __forceinline__ float team_max(float amax, int me, float* red)
 {
-    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    if (T > 1) {
+        if ((me & 31) == 0) red[me >> 5] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < T; ++w) amax = max_nan(amax, red[w]);
+    }
+    return amax;
+}
+
+// A block's scale from its rows' largest magnitude; the retained codes follow it. `old`: the scale
+// as every thread of the team read it before.
+template <int T>
+__device__ __forceinline__ float settle_scale(float amax, float old, float* scale, uint8_t* codes, int retained,
+                                              int me)
+{
     const float fresh = exp2i(scale_exponent(amax));
+    if (T == 1) __syncwarp();              // every lane has read the old scale
     if (retained == 0) {
-        if (lane == 0) *scale = fresh;
+        if (me == 0) *scale = fresh;
         return fresh;
     }
-    const float old = *scale;
-    __syncwarp();                          // read by all before one writes it
     const float s = fmaxf(old, fresh);
     if (s > old) {
-        if (lane == 0) *scale = s;
+        if (me == 0) *scale = s;
         const float ratio = old / s;
         uint4* kept = reinterpret_cast<uint4*>(codes);
 #pragma unroll 2
-        for (int i = lane; i < retained / 16; i += 32) {
+        for (int i = me; i < retained / 16; i += 32 * T) {
             const uint4 c = kept[i];
             const uint32_t w[4] = {c.x, c.y, c.z, c.w};
             uint32_t o[4];
@@ -187,144 +226,254 @@ __device__ __forceinline__ int row_owner(const AppendArgs& A, int64_t r, int* po
     return b;
 }
 
-// The blocks that packed row r (request b's row i0, at position pos) leads: eight of them from hv0,
-// one per warp. Returns status bits.
-template <int DT, bool VEC>
+// The blocks that packed row r (request b's row i0, at position pos) leads. T = 1: eight of them
+// from hv0 (head, K or V), one per warp; T = kWarps: those of kHeads heads from hv0, by the whole
+// CTA, the next head's rows on their way while one's are worked on. Returns status bits.
+template <int DT, bool VEC, int T>
 __device__ __forceinline__ int append_blocks(const AppendArgs& A, int64_t r, int b, int i0, int pos, int hv0,
-                                             float2* tab)
+                                             float2* tab, float* red)
 {
+    constexpr int kKeep = keep_of(T), kAll = T > 1 ? 32 * T : kThreads;
     const dspark_cache& c = A.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int slot0 = pos & (c.page - 1), block = pos / c.page;
+    const int slot0 = pos & (c.page - 1), block = pos / c.page, most = c.page - slot0;
+    const int me = T > 1 ? threadIdx.x : lane;
+    const int hv = T > 1 ? hv0 : hv0 + warp;
+    const bool works = hv < 2 * c.heads, value = hv & 1;
+    const int h0 = hv >> 1, heads = T > 1 ? min(kHeads, c.heads - h0) : 1;
+    const int half = T > 1 && value ? 0 : A.rope.half;
+    const int units = c.dim / Unit<VEC>::N;
+    // Lanes over units, `step` rows at a time; a head wider than a warp's units (scalar accesses
+    // only) takes several turns over a row.
+    const int wide = units > 32 ? 32 : units, per_warp = 32 / wide, step = per_warp * T;
+    const int in_warp = lane / wide, u0 = lane - in_warp * wide;
+    const int k0 = T > 1 ? in_warp + per_warp * warp : in_warp;
+    const bool has = works && in_warp < per_warp;
+    Rope rope = A.rope;
+    if (value) rope.half = 0;
+    const RowsIn in = value ? A.v : A.k;
+    const int64_t first = r * in.row_stride;
+    const Unit<VEC> un(rope, u0);
+    // the rows that may be the block's, before it is known which are
+    const int may = static_cast<int>(min(static_cast<int64_t>(most), A.rows - r));
+    auto fetch = [&](Raw<DT, VEC>* raw, int h) {
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i)
+            if (has && k0 + i * step < may)
+                raw[i].load(in.base, first + (k0 + i * step) * in.row_stride + static_cast<int64_t>(h) * c.dim, un);
+    };
+    Raw<DT, VEC> raw[kKeep];
+    fetch(raw, h0);
     const int page = block < c.width ? c.table[static_cast<int64_t>(b) * c.width + block] : -1;
-    if (page < 0 || page >= c.n_pages) return DSPARK_STATUS_BAD_PAGE;
     // the block's rows: the packed rows that follow, while they are b's next positions
-    const int most = c.page - slot0;
     int n = 1;
     for (int j0 = 1; j0 < most; j0 += 32) {
         const int j = j0 + lane;
-        const bool mine = j < most && r + j < A.rows && A.row_req[r + j] == b && A.row_pos[r + j] == i0 + j;
+        const bool mine = j < may && A.row_req[r + j] == b && A.row_pos[r + j] == i0 + j;
         const unsigned run = __ballot_sync(0xffffffffu, mine);
         n += run == 0xffffffffu ? 32 : __ffs(~run) - 1;
         if (run != 0xffffffffu) break;
     }
-    const int hv = hv0 + warp;
-    const bool works = hv < 2 * c.heads, value = hv & 1;
-    const int h = hv >> 1;
-    const int half = A.rope.half;
-    const int units = c.dim / Unit<VEC>::N;
-    // Lanes over units, `step` rows at a time; a head wider than a warp's units (scalar accesses
-    // only) takes several turns over a row.
-    const int wide = units > 32 ? 32 : units, step = 32 / wide;
-    const int k0 = lane / wide, u0 = lane - k0 * wide;
-    const bool has = works && k0 < step;
-    Rope rope = A.rope;
-    if (value) rope.half = 0;
-    const RowsIn in = value ? A.v : A.k;
-    const int64_t bh = static_cast<int64_t>(page) * c.heads + h;
-    uint8_t* codes = static_cast<uint8_t*>(value ? c.v : c.k) + bh * c.page * c.dim;
-    float* scale = (value ? c.v_scale : c.k_scale) + bh;
-    const int64_t first = r * in.row_stride + static_cast<int64_t>(h) * c.dim;
-    bool bad = false;
-    float amax = 0.0f;
+    if (page < 0 || page >= c.n_pages) return DSPARK_STATUS_BAD_PAGE;
 
     const int rows_at_once = half > 0 ? kTable / half : n;       // factors for so many rows fit
     auto factors = [&](int from, int m) {
         __syncthreads();
-        for (int i = threadIdx.x; i < m * half; i += kThreads) {
+        for (int i = threadIdx.x; i < m * half; i += kAll) {
             const int k = i / half;
             tab[i] = rope_factor(A.rope, A.rope.turns[i - k * half], pos + from + k);
         }
         __syncthreads();
     };
-    if (n <= kKeep * step && n <= rows_at_once && units <= 32) {
-        // a window: its values stay in registers
-        float x[kKeep][Unit<VEC>::N];
-        const Unit<VEC> un(rope, u0);
+    const bool keep = n <= kKeep * step && n <= rows_at_once && units <= 32;
+    bool bad = false;
+    if (keep && half > 0) factors(0, n);
+#pragma unroll 1
+    for (int h = h0; h < h0 + heads; ++h) {
+        const int64_t bh = static_cast<int64_t>(page) * c.heads + h;
+        uint8_t* codes = static_cast<uint8_t*>(value ? c.v : c.k) + bh * c.page * c.dim;
+        float* scale = (value ? c.v_scale : c.k_scale) + bh;
+        float* parts = red + (T > 1 ? ((h - h0) & 1) * T : 0);
+        float amax = 0.0f;
+        if (keep) {
+            if (!works) return 0;
+            const float old = slot0 > 0 ? *scale : 0.0f;
+            // a CTA's threads keep the turned elements and fetch the next head's; a warp's turn
+            // them again, which leaves registers for more warps
+            float y[T > 1 ? kKeep : 1][Unit<VEC>::N];
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i)
-            if (has && k0 + i * step < n) load_unit<DT, VEC>(in.base, first + (k0 + i * step) * in.row_stride, un, x[i]);
-        if (half > 0) factors(0, n);
-        if (!works) return 0;
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i)
-            if (has && k0 + i * step < n) {
-                bad |= turn_unit<VEC>(rope, un, tab + (k0 + i * step) * half, x[i]);
-                amax = amax_unit<VEC>(x[i], amax);
+            for (int i = 0; i < kKeep; ++i)
+                if (has && k0 + i * step < n) {
+                    float* x = y[T > 1 ? i : 0];
+                    raw[i].get(x);
+                    turn_unit<VEC, false>(rope, un, tab + (k0 + i * step) * half, x);
+                    amax = amax_unit<VEC>(x, amax);
+                }
+            if (T > 1 && h + 1 < h0 + heads) fetch(raw, h + 1);
+            amax = team_max<T>(amax, me, parts);
+            const bool clean = finite(amax);     // the same for the team
+            if (!clean) {                        // rare: the offenders count as 0
+                amax = 0.0f;
+#pragma unroll 1
+                for (int k = k0; has && k < n; k += step) {
+                    Raw<DT, VEC> one;
+                    float x[Unit<VEC>::N];
+                    one.load(in.base, first + k * in.row_stride + static_cast<int64_t>(h) * c.dim, un);
+                    one.get(x);
+                    bad |= turn_unit<VEC, true>(rope, un, tab + k * half, x);
+                    amax = amax_unit<VEC>(x, amax);
+                }
+                if (T > 1) __syncthreads();
+                amax = team_max<T>(amax, me, parts);
             }
-        const float inv = 1.0f / settle_scale(amax, scale, codes, slot0 * c.dim, lane);
+            const float inv = 1.0f / settle_scale<T>(amax, old, scale, codes, slot0 * c.dim, me);
+            uint8_t* to = codes + static_cast<int64_t>(slot0) * c.dim;
+            if (clean) {
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i)
-            if (has && k0 + i * step < n)
-                store_unit<VEC>(codes + static_cast<int64_t>(slot0 + k0 + i * step) * c.dim, un, x[i], inv);
-    } else {
-        float inv = 0.0f;
+                for (int i = 0; i < kKeep; ++i)
+                    if (has && k0 + i * step < n) {
+                        float* x = y[T > 1 ? i : 0];
+                        if (T == 1) {
+                            raw[i].get(x);
+                            turn_unit<VEC, false>(rope, un, tab + (k0 + i * step) * half, x);
+                        }
+                        store_unit<VEC>(to + (k0 + i * step) * c.dim, un, x, inv);
+                    }
+            } else {
+#pragma unroll 1
+                for (int k = k0; has && k < n; k += step) {
+                    Raw<DT, VEC> one;
+                    float x[Unit<VEC>::N];
+                    one.load(in.base, first + k * in.row_stride + static_cast<int64_t>(h) * c.dim, un);
+                    one.get(x);
+                    turn_unit<VEC, true>(rope, un, tab + k * half, x);
+                    store_unit<VEC>(to + k * c.dim, un, x, inv);
+                }
+            }
+            continue;
+        }
+        float inv = 0.0f, x[Unit<VEC>::N];
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
             for (int from = 0; from < n; from += rows_at_once) {
                 const int m = min(rows_at_once, n - from);
-                if (half > 0 && (pass == 0 || rows_at_once < n)) factors(from, m);
+                if (half > 0 && ((pass == 0 && h == h0) || rows_at_once < n)) factors(from, m);
                 if (!has) continue;
 #pragma unroll 1
                 for (int u = u0; u < units; u += wide) {
                     const Unit<VEC> un(rope, u);
-#pragma unroll 4
+#pragma unroll 2
                     for (int k = k0; k < m; k += step) {
-                        float x[Unit<VEC>::N];
-                        load_unit<DT, VEC>(in.base, first + (from + k) * in.row_stride, un, x);
-                        bad |= turn_unit<VEC>(rope, un, tab + k * half, x);
+                        Raw<DT, VEC> one;
+                        one.load(in.base, first + (from + k) * in.row_stride + static_cast<int64_t>(h) * c.dim, un);
+                        one.get(x);
+                        bad |= turn_unit<VEC, true>(rope, un, tab + k * half, x);
                         if (pass == 0) amax = amax_unit<VEC>(x, amax);
                         else store_unit<VEC>(codes + static_cast<int64_t>(slot0 + from + k) * c.dim, un, x, inv);
                     }
                 }
             }
-            if (pass == 0 && works) inv = 1.0f / settle_scale(amax, scale, codes, slot0 * c.dim, lane);
+            if (pass == 0 && works) {
+                const float old = slot0 > 0 ? *scale : 0.0f;
+                if (T == 1) __syncwarp();
+                amax = team_max<T>(amax, me, parts);
+                inv = 1.0f / settle_scale<T>(amax, old, scale, codes, slot0 * c.dim, me);
+            }
         }
     }
     return bad ? DSPARK_STATUS_BAD_VALUE : 0;
 }
 
-template <int DT, bool VEC, bool QVEC>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs A)
+// A CTA's part of the keys and values: the rows [row0, row0 + chunk) and its share of their blocks.
+template <int DT, bool VEC, int T>
+__device__ __forceinline__ int append_rows(const AppendArgs& A, float2* tab, float* red)
 {
-    __shared__ float2 tab[kTable];
-    __shared__ int32_t own[8], at[8];
-    pdl_wait_and_trigger();
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x / A.per_row) * A.chunk;
+    const int share = blockIdx.x % A.per_row;
+    const int hv0 = T > 1 ? 2 * (share >> 1) * kHeads + (share & 1) : share * kWarps;
+    // each warp looks at the rows side by side; those that lead a block are the same for all
+    const int lane = threadIdx.x & 31;
     int bits = 0;
-    if (static_cast<int>(blockIdx.x) >= A.kv_ctas) {              // queries
-        const int64_t row0 = static_cast<int64_t>(blockIdx.x - A.kv_ctas) * A.q_rows;
-        const int n = min(static_cast<int64_t>(A.q_rows), A.rows - row0);
-        if (threadIdx.x < n) own[threadIdx.x] = row_owner(A, row0 + threadIdx.x, &at[threadIdx.x], &bits);
-        __syncthreads();
-        for (int i = threadIdx.x; i < n * A.rope.half; i += kThreads) {
-            const int k = i / A.rope.half;
-            if (own[k] >= 0)
-                tab[i] = rope_factor(A.rope, A.rope.turns[i - k * A.rope.half], at[k]);
-        }
-        __syncthreads();
-        const bool copy = !(A.q.base == A.q_out.base && A.q.row_stride == A.q_out.row_stride);
-        rotate_rows<DT, QVEC>(A.rope, tab, A.q, A.q_out, row0, n, A.q_heads, A.c.dim, copy, own);
-    } else {
-        const int64_t row0 = static_cast<int64_t>(blockIdx.x / A.per_row) * A.chunk;
-        const int hv0 = (blockIdx.x % A.per_row) * kWarps;
-        // each warp looks at the rows side by side; those that lead a block are the same for all
-        const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int from = 0; from < A.chunk; from += 32) {
+        const int64_t r = row0 + from + lane;
         int b = -1, pos = 0, i = 0;
-        if (lane < A.chunk && row0 + lane < A.rows) {
-            b = row_owner(A, row0 + lane, &pos, &bits);
-            if (b >= 0) i = A.row_pos[row0 + lane];
+        if (from + lane < A.chunk && r < A.rows) {
+            b = row_owner(A, r, &pos, &bits);
+            if (b >= 0) i = A.row_pos[r];
         }
         unsigned leads = __ballot_sync(0xffffffffu, b >= 0 && (i == 0 || (pos & (A.c.page - 1)) == 0));
 #pragma unroll 1
         while (leads != 0) {
             const int k = __ffs(leads) - 1;
             leads &= leads - 1;
-            bits |= append_blocks<DT, VEC>(A, row0 + k, __shfl_sync(0xffffffffu, b, k),
-                                           __shfl_sync(0xffffffffu, i, k), __shfl_sync(0xffffffffu, pos, k), hv0, tab);
+            bits |= append_blocks<DT, VEC, T>(A, row0 + from + k, __shfl_sync(0xffffffffu, b, k),
+                                              __shfl_sync(0xffffffffu, i, k), __shfl_sync(0xffffffffu, pos, k),
+                                              hv0, tab, red);
+            if (T > 1) __syncthreads();                  // red and the factors, before the next block's
         }
     }
+    return bits;
+}
+
+// A CTA's part of the queries, `block` of them.
+template <int DT, bool QVEC>
+__device__ __forceinline__ int rotate_queries(const AppendArgs& A, int block, float2* tab, int32_t* own, int32_t* at)
+{
+    int bits = 0;
+    const int64_t row0 = static_cast<int64_t>(block) * A.q_rows;
+    const int n = min(static_cast<int64_t>(A.q_rows), A.rows - row0);
+    rotate_rows<DT, QVEC>(A.q, tab, row0, n, own, [&]() {
+        if (threadIdx.x < n) own[threadIdx.x] = row_owner(A, row0 + threadIdx.x, &at[threadIdx.x], &bits);
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * A.rope.half; i += kThreads) {
+            const int k = i / A.rope.half;
+            if (own[k] >= 0) tab[i] = rope_factor(A.rope, A.rope.turns[i - k * A.rope.half], at[k]);
+        }
+        __syncthreads();
+    });
+    return bits;
+}
+
+// A step: keys and values, and after them queries, in one launch.
+template <int DT, bool VEC, bool QVEC>
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs A)
+{
+    __shared__ __align__(16) float2 tab[kTable];
+    __shared__ int32_t own[kQueryRows], at[kQueryRows];
+    pdl_wait_and_trigger();
+    int bits;
+    if (static_cast<int>(blockIdx.x) >= A.kv_ctas)
+        bits = rotate_queries<DT, QVEC>(A, blockIdx.x - A.kv_ctas, tab, own, at);
+    else
+        bits = append_rows<DT, VEC, 1>(A, tab, nullptr);
     if (bits) raise_status(A.status, bits);
+}
+
+// Prompts: the keys and values.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(32 * kTeam, 2) append_prompt_kernel(AppendArgs A)
+{
+    __shared__ __align__(16) float2 tab[kTable];
+    __shared__ float red[2 * kTeam];
+    pdl_wait_and_trigger();
+    const int bits = append_rows<DT, VEC, kTeam>(A, tab, red);
+    if (bits) raise_status(A.status, bits);
+}
+
+// Prompts: the queries, beside the kernel above. It starts when that one has triggered its
+// dependents, that is after everything before the call is done, touches nothing that one writes,
+// and waits for it at its own end, so that what follows on the stream waits for both.
+template <int DT, bool QVEC>
+__global__ void __launch_bounds__(kThreads) append_query_kernel(AppendArgs A)
+{
+    __shared__ __align__(16) float2 tab[kQueryFactors];
+    __shared__ int32_t own[kQueryRows], at[kQueryRows];
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const int bits = rotate_queries<DT, QVEC>(A, blockIdx.x, tab, own, at);
+    if (bits) raise_status(A.status, bits);
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
 bool vector_rows(const Rope& r, const void* base, int64_t stride, int dim, int elem)
@@ -346,32 +495,40 @@ int launch_append(const dspark_cache& cache, const Rope& rope, const void* k, in
     A.rope = rope;
     A.k = {k, ks};
     A.v = {v, vs};
-    A.q = {q, qs};
-    A.q_out = {q_out, os};
     A.row_req = row_req;
     A.row_pos = row_pos;
     A.lengths = lengths;
     A.rows = rows;
     A.B = B;
-    A.q_heads = q_heads;
     A.status = status;
-    // One row per kv CTA gives a step's windows the shortest chains; of a prompt's rows only one in a
-    // page leads, so a CTA looks at 16.
-    A.chunk = rows <= 4096 ? 1 : 16;
+    // Steps: a warp per block, one row per CTA for the shortest chains in a small one, four in a
+    // large one, where about one row in four leads (256 windows: 16 us with 4, 18 with 1). Prompts: a
+    // CTA for four heads' blocks, so that a page's rows are read once and stay in registers.
+    const bool prompts = rows > 4096;
+    A.chunk = prompts ? cache.page : rows <= 512 ? 1 : 4;
     A.q_rows = rows >= 152 * 8 && rope.half > 0 ? (rope.half <= 64 ? 4 : 2) : 1;
-    A.per_row = static_cast<int>(ceil_div(2 * cache.heads, kWarps));
+    A.per_row = static_cast<int>(prompts ? 2 * ceil_div(cache.heads, kHeads) : ceil_div(2 * cache.heads, kWarps));
     A.kv_ctas = static_cast<int>(ceil_div(rows, A.chunk)) * A.per_row;
     const int q_ctas = q != nullptr ? static_cast<int>(ceil_div(rows, A.q_rows)) : 0;
     const bool bf = dtype == DSPARK_BF16;
     const int e = bf ? 2 : 4;
     const bool qvec = rotate_vec(rope, q, qs, q_out, os, cache.dim, e);
     const bool vec = vector_rows(rope, k, ks, cache.dim, e) && vector_rows(rope, v, vs, cache.dim, e);
+    A.q = turns_of(rope, q, qs, q_out, os, q != nullptr ? q_heads : 1, cache.dim, qvec, A.q_rows);
+    if (prompts) {
+        auto kv = bf ? (vec ? append_prompt_kernel<DSPARK_BF16, true> : append_prompt_kernel<DSPARK_BF16, false>)
+                     : (vec ? append_prompt_kernel<DSPARK_F32, true> : append_prompt_kernel<DSPARK_F32, false>);
+        const int rc = launch_pdl("append", kv, dim3(static_cast<unsigned>(A.kv_ctas)), dim3(32 * kTeam), 0, stream, A);
+        if (rc != DSPARK_OK || q == nullptr) return rc;
+        auto turn = bf ? (qvec ? append_query_kernel<DSPARK_BF16, true> : append_query_kernel<DSPARK_BF16, false>)
+                       : (qvec ? append_query_kernel<DSPARK_F32, true> : append_query_kernel<DSPARK_F32, false>);
+        return launch_pdl("append queries", turn, dim3(static_cast<unsigned>(q_ctas)), dim3(kThreads), 0, stream, A);
+    }
     auto kernel = bf ? (vec ? (qvec ? append_kernel<DSPARK_BF16, true, true> : append_kernel<DSPARK_BF16, true, false>)
                             : (qvec ? append_kernel<DSPARK_BF16, false, true> : append_kernel<DSPARK_BF16, false, false>))
                      : (vec ? (qvec ? append_kernel<DSPARK_F32, true, true> : append_kernel<DSPARK_F32, true, false>)
                             : (qvec ? append_kernel<DSPARK_F32, false, true> : append_kernel<DSPARK_F32, false, false>));
-    return launch_pdl("append", kernel, dim3(static_cast<unsigned>(A.kv_ctas + q_ctas)),
-                      dim3(kThreads), 0, stream, A);
+    return launch_pdl("append", kernel, dim3(static_cast<unsigned>(A.kv_ctas + q_ctas)), dim3(kThreads), 0, stream, A);
 }
 
 }  // namespace dspark

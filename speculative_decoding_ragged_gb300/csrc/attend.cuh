@@ -25,14 +25,6 @@ struct AttendCall {
     int32_t* status;
 };
 
-// The larger, or NaN where either is: a row whose query is not finite answers NaN, not nothing.
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 size_t attend_workspace_bytes(int dim);
 int launch_attend(const AttendCall& A, int dtype, cudaStream_t stream);
 // The tensor-core kernel: whether it serves a call, and its launch.

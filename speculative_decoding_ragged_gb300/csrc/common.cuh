@@ -174,6 +174,14 @@ __device__ __forceinline__ float ex2_approx(float x)
     return y;
 }
 
+// The larger, or NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Logit v of a row as fp32 (exact widening for bf16).
 template <int DT>
 __device__ __forceinline__ float load_logit(const void* row, int64_t v)

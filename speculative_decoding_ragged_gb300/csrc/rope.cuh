@@ -106,77 +106,161 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float x)
 struct RowsIn { const void* base; int64_t row_stride; };
 struct RowsOut { void* base; int64_t row_stride; };
 
-// One CTA's part of a rotation: rows [row0, row0 + n) of `heads` heads of `dim` elements, with
-// the factors of those rows in `tab` (n * half entries of shared memory, row-major).
-// VEC: units of eight pairs (16-byte accesses; dim, half and the strides multiples of 8, bases
-// 16-byte aligned), a unit past the rotated part being 16 copied elements (dim - rot a multiple
-// of 16); else one pair, or two copied elements, at a time.
-// `live` (shared, one flag per row; NULL: all): rows to touch. `copy`: also write the elements
-// past the rotated ones (not needed in place).
-template <int DT, bool VEC>
-__device__ __forceinline__ void rotate_rows(const Rope& r, const float2* tab, RowsIn x, RowsOut y,
-                                            int64_t row0, int n, int heads, int dim, bool copy,
-                                            const int* live)
+// n / d for small n by one multiplication: exact while n * d < 2^32 (the host checks).
+struct Divider {
+    uint32_t d, magic;     // magic 0: divide
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return magic != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), magic))
+                          : static_cast<int>(static_cast<uint32_t>(n) / d);
+    }
+};
+inline Divider divider(int64_t d, int64_t most)
 {
-    constexpr int P = VEC ? 8 : 1;
-    constexpr int E = DT == DSPARK_BF16 ? 2 : 4;
-    const int rot_units = r.half / P;                     // a head's rotated units
-    const int all_units = copy ? (dim + 2 * P - 1) / (2 * P) : rot_units;
-    const int per_row = heads * all_units;
-    for (int u = threadIdx.x; u < n * per_row; u += blockDim.x) {
-        const int k = u / per_row;
-        const int in_row = u - k * per_row;
-        const int h = in_row / all_units;
-        const int o = in_row - h * all_units;
-        if (live != nullptr && live[k] < 0) continue;
-        const int64_t xi = (row0 + k) * x.row_stride + static_cast<int64_t>(h) * dim;
-        const int64_t yi = (row0 + k) * y.row_stride + static_cast<int64_t>(h) * dim;
-        if (VEC) {
-            const char* xp = static_cast<const char*>(x.base) + xi * E;
-            char* yp = static_cast<char*>(y.base) + yi * E;
-            float a[8], b[8];
-            if (o < rot_units) {
-                const int ia = r.interleaved ? o * 16 : o * 8;
-                const int ib = r.interleaved ? o * 16 + 8 : r.half + o * 8;
-                load8<DT>(xp + ia * E, a);
-                load8<DT>(xp + ib * E, b);
-                const float2* f = tab + k * r.half + o * 8;
-                if (r.interleaved) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float2 t = rope_turn(a[2 * q], a[2 * q + 1], f[q]);
-                        const float2 s = rope_turn(b[2 * q], b[2 * q + 1], f[q + 4]);
-                        a[2 * q] = t.x; a[2 * q + 1] = t.y;
-                        b[2 * q] = s.x; b[2 * q + 1] = s.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float2 t = rope_turn(a[q], b[q], f[q]);
-                        a[q] = t.x;
-                        b[q] = t.y;
-                    }
-                }
-                store8<DT>(yp + ia * E, a);
-                store8<DT>(yp + ib * E, b);
-            } else {
-                const int i = 2 * r.half + (o - rot_units) * 16;
-                load8<DT>(xp + i * E, a);
-                load8<DT>(xp + (i + 8) * E, b);
-                store8<DT>(yp + i * E, a);
-                store8<DT>(yp + (i + 8) * E, b);
-            }
-        } else if (o < rot_units) {
-            const int ia = r.interleaved ? 2 * o : o;
-            const int ib = r.interleaved ? 2 * o + 1 : o + r.half;
-            const float2 t = rope_turn(load1<DT>(x.base, xi + ia), load1<DT>(x.base, xi + ib),
-                                       tab[k * r.half + o]);
-            store1<DT>(y.base, yi + ia, t.x);
-            store1<DT>(y.base, yi + ib, t.y);
+    Divider r;
+    r.d = static_cast<uint32_t>(d);
+    r.magic = d > 1 && d * most < (1ll << 32) ? static_cast<uint32_t>(((1ull << 32) + d - 1) / d) : 0;
+    return r;
+}
+
+// How a rotation cuts its rows: units of eight pairs (VEC: 16-byte accesses; dim, half and the
+// strides multiples of 8, bases 16-byte aligned), a unit past the rotated part being 16 copied
+// elements; else one pair, or two copied elements, at a time.
+struct Turns {
+    Rope r;
+    RowsIn x;
+    RowsOut y;
+    int heads, dim;
+    int rot_units;         // of a head
+    Divider units, per_row;    // units of a head, of a row
+};
+inline Turns turns_of(const Rope& r, const void* x, int64_t xs, void* y, int64_t ys, int heads, int dim,
+                      bool vec, int rows_per_cta)
+{
+    const int P = vec ? 8 : 1;
+    const bool copy = !(x == y && xs == ys);       // in place the rest stays where it is
+    Turns t;
+    t.r = r;
+    t.x = {x, xs};
+    t.y = {y, ys};
+    t.heads = heads;
+    t.dim = dim;
+    t.rot_units = r.half / P;
+    const int64_t units = copy ? (dim + 2 * P - 1) / (2 * P) : t.rot_units;
+    t.units = divider(units, units * heads);
+    t.per_row = divider(units * heads, units * heads * rows_per_cta);
+    return t;
+}
+
+// A vector unit: where it is, and its elements as loaded.
+template <int DT>
+struct TurnUnit {
+    static constexpr int Q = DT == DSPARK_BF16 ? 1 : 2;     // 16-byte loads per eight elements
+    uint4 v[2 * Q];
+    int64_t y;
+    int a, b, f;             // offsets of the two eights in the head; first factor, or -1: copied
+    __device__ __forceinline__ void load(const Turns& t, int64_t row0, int u)
+    {
+        constexpr int E = DT == DSPARK_BF16 ? 2 : 4;
+        const int k = t.per_row(u), in_row = u - k * static_cast<int>(t.per_row.d);
+        const int h = t.units(in_row), o = in_row - h * static_cast<int>(t.units.d);
+        const int64_t head = static_cast<int64_t>(h) * t.dim;
+        if (o < t.rot_units) {
+            a = t.r.interleaved ? o * 16 : o * 8;
+            b = t.r.interleaved ? a + 8 : t.r.half + o * 8;
+            f = k * t.r.half + o * 8;
         } else {
-            const int i = 2 * o;
-            store1<DT>(y.base, yi + i, load1<DT>(x.base, xi + i));
-            if (i + 1 < dim) store1<DT>(y.base, yi + i + 1, load1<DT>(x.base, xi + i + 1));
+            a = 2 * t.r.half + (o - t.rot_units) * 16;
+            b = a + 8;
+            f = -1 - k;
+        }
+        y = (row0 + k) * t.y.row_stride + head;
+        const char* x = static_cast<const char*>(t.x.base) + ((row0 + k) * t.x.row_stride + head) * E;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            v[i] = *reinterpret_cast<const uint4*>(x + a * E + i * 16);
+            v[Q + i] = *reinterpret_cast<const uint4*>(x + b * E + i * 16);
+        }
+    }
+    // live: one flag per row (NULL: all), negative: leave the row alone
+    __device__ __forceinline__ void turn(const Turns& t, const float2* tab, const int* live)
+    {
+        constexpr int E = DT == DSPARK_BF16 ? 2 : 4;
+        if (live != nullptr && live[f >= 0 ? f / t.r.half : -1 - f] < 0) return;
+        char* out = static_cast<char*>(t.y.base) + y * E;
+        if (f >= 0) {
+            float p[8], q[8];
+            load8<DT>(v, p);
+            load8<DT>(v + Q, q);
+            const float4* c = reinterpret_cast<const float4*>(tab + f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 g = c[j];               // factors 2j and 2j + 1
+                if (t.r.interleaved) {
+                    float* z = j < 2 ? p + 4 * j : q + 4 * j - 8;
+                    const float2 s = rope_turn(z[0], z[1], make_float2(g.x, g.y));
+                    const float2 w = rope_turn(z[2], z[3], make_float2(g.z, g.w));
+                    z[0] = s.x; z[1] = s.y; z[2] = w.x; z[3] = w.y;
+                } else {
+                    const float2 s = rope_turn(p[2 * j], q[2 * j], make_float2(g.x, g.y));
+                    const float2 w = rope_turn(p[2 * j + 1], q[2 * j + 1], make_float2(g.z, g.w));
+                    p[2 * j] = s.x; q[2 * j] = s.y;
+                    p[2 * j + 1] = w.x; q[2 * j + 1] = w.y;
+                }
+            }
+            store8<DT>(out + a * E, p);
+            store8<DT>(out + b * E, q);
+        } else {
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                *reinterpret_cast<uint4*>(out + a * E + i * 16) = v[i];
+                *reinterpret_cast<uint4*>(out + b * E + i * 16) = v[Q + i];
+            }
+        }
+    }
+};
+
+// One CTA's rows [row0, row0 + n): `table` fills the factors of the rows (n * half entries of
+// shared memory, row-major, 16-byte aligned) and synchronises; it runs after the first loads are
+// on their way.
+template <int DT, bool VEC, class Table>
+__device__ __forceinline__ void rotate_rows(const Turns& t, const float2* tab, int64_t row0, int n,
+                                            const int* live, Table&& table)
+{
+    const int total = n * static_cast<int>(t.per_row.d), step = blockDim.x;
+    if (VEC) {
+        TurnUnit<DT> now;
+        int u = threadIdx.x;
+        if (u < total) now.load(t, row0, u);
+        table();
+#pragma unroll 1
+        for (; u < total; u += step) {
+            TurnUnit<DT> next;
+            if (u + step < total) next.load(t, row0, u + step);
+            now.turn(t, tab, live);
+            now = next;
+        }
+    } else {
+        table();
+#pragma unroll 1
+        for (int u = threadIdx.x; u < total; u += step) {
+            const int k = t.per_row(u), in_row = u - k * static_cast<int>(t.per_row.d);
+            const int h = t.units(in_row), o = in_row - h * static_cast<int>(t.units.d);
+            if (live != nullptr && live[k] < 0) continue;
+            const int64_t xi = (row0 + k) * t.x.row_stride + static_cast<int64_t>(h) * t.dim;
+            const int64_t yi = (row0 + k) * t.y.row_stride + static_cast<int64_t>(h) * t.dim;
+            if (o < t.rot_units) {
+                const int ia = t.r.interleaved ? 2 * o : o;
+                const int ib = t.r.interleaved ? 2 * o + 1 : o + t.r.half;
+                const float2 s = rope_turn(load1<DT>(t.x.base, xi + ia), load1<DT>(t.x.base, xi + ib),
+                                           tab[k * t.r.half + o]);
+                store1<DT>(t.y.base, yi + ia, s.x);
+                store1<DT>(t.y.base, yi + ib, s.y);
+            } else {
+                const int i = 2 * o;
+                store1<DT>(t.y.base, yi + i, load1<DT>(t.x.base, xi + i));
+                if (i + 1 < t.dim) store1<DT>(t.y.base, yi + i + 1, load1<DT>(t.x.base, xi + i + 1));
+            }
         }
     }
 }

@@ -18,19 +18,19 @@ constexpr int kTable = 512;        // shared factors: at least one row's, at mos
 
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-rotate_kernel(Rope r, RowsIn x, RowsOut y, const int32_t* __restrict__ positions, int rows,
-              int heads, int dim, int per_cta, int copy)
+rotate_kernel(Turns t, const int32_t* __restrict__ positions, int rows, int per_cta)
 {
-    __shared__ float2 tab[kTable];
+    __shared__ __align__(16) float2 tab[kTable];
     pdl_wait_and_trigger();
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * per_cta;
     const int n = min(static_cast<int64_t>(per_cta), rows - row0);
-    for (int i = threadIdx.x; i < n * r.half; i += kThreads) {
-        const int k = i / r.half;
-        tab[i] = rope_factor(r, r.turns[i - k * r.half], positions[row0 + k]);
-    }
-    __syncthreads();
-    rotate_rows<DT, VEC>(r, tab, x, y, row0, n, heads, dim, copy, nullptr);
+    rotate_rows<DT, VEC>(t, tab, row0, n, nullptr, [&]() {
+        for (int i = threadIdx.x; i < n * t.r.half; i += kThreads) {
+            const int k = i / t.r.half;
+            tab[i] = rope_factor(t.r, t.r.turns[i - k * t.r.half], positions[row0 + k]);
+        }
+        __syncthreads();
+    });
 }
 
 }  // namespace
@@ -45,14 +45,11 @@ int launch_rotate(const Rope& r, const void* x, int64_t xs, void* y, int64_t ys,
         per_cta = kThreads / r.half;
         per_cta = per_cta < 1 ? 1 : per_cta > 4 ? 4 : per_cta;
     }
-    const RowsIn in = {x, xs};
-    const RowsOut out = {y, ys};
-    const int copy = !(x == y && xs == ys);
+    const Turns t = turns_of(r, x, xs, y, ys, heads, dim, vec, per_cta);
     const dim3 grid(static_cast<unsigned>(ceil_div(rows, per_cta)));
     auto kernel = bf ? (vec ? rotate_kernel<DSPARK_BF16, true> : rotate_kernel<DSPARK_BF16, false>)
                      : (vec ? rotate_kernel<DSPARK_F32, true> : rotate_kernel<DSPARK_F32, false>);
-    return launch_pdl("rotate", kernel, grid, dim3(kThreads), 0, stream, r, in, out, positions,
-                      rows, heads, dim, per_cta, copy);
+    return launch_pdl("rotate", kernel, grid, dim3(kThreads), 0, stream, t, positions, rows, per_cta);
 }
 
 int check_rope(const char* fn, const dspark_rope* rope, int dim)

@@ -136,6 +136,11 @@ CASES = [
     ([129, 2], [127, 128], 1, 4, 128, 128, "bf16"),
     ([0, 3, 0], [5, 5, 0], 2, 2, 256, 16, "bf16"),
     ([2] * 40, list(range(40)), 2, 1, 128, 16, "bf16"),
+    # more than 4096 rows: a CTA per block
+    ([4100, 3], [5, 30], 2, 1, 64, 16, "bf16"),
+    ([200, 4000, 1], [77, 0, 64], 1, 2, 128, 64, "bf16"),
+    ([4097], [100], 1, 1, 128, 128, "f32"),
+    ([2100, 2100], [0, 127], 2, 1, 48, 128, "bf16"),
 ]
 
 
