@@ -4,14 +4,14 @@
 // A block is one page's slots of one kv head; its scale is a power of two, so that growing it
 // rescales the codes already there by an exact shift of their exponent (only codes that leave
 // e4m3's normal range round again), and multiplying by it is exact. The step's rows that fall
-// into one block are consecutive packed rows; the first of them leads. One warp, or for prompts one CTA, owns a block (of
-// keys or of values): it finds the block's rows, their largest magnitude, hence the scale,
+// into one block are consecutive packed rows; the first of them leads. One warp, or for prompts a team of four, owns a block
+// (of keys or of values): it finds the block's rows, their largest magnitude, hence the scale,
 // requantises the retained codes if the scale grew, and writes the rows' codes. No two touch
 // one block, so there are no atomics and the result does not depend on any order.
 //
 // The rotation's factors of the block's rows are computed once per CTA in shared memory, for four
 // heads' keys at a time in a step. The rows' elements stay in registers between the maximum and the
-// codes where they fit (8 rows of 128 for a warp, 64 for a CTA); else they are read again.
+// codes where they fit (8 rows of 128 for a warp, 64 for a prompt's four); else they are read again.
 // Bound by memory for prompts, by the chain of dependent loads (row owner, length, page id,
 // scale, retained codes) for a step.
 #include "cache.cuh"
@@ -22,12 +22,12 @@ namespace {
 
 constexpr int kThreads = 256;      // of a step's CTA, and of one that rotates queries
 constexpr int kWarps = kThreads / 32;
-constexpr int kTeam = 16;          // warps that take a prompt's block together
+constexpr int kTeam = 4;           // warps that take a prompt's block together
+constexpr int kPromptWarps = 16;   // of a CTA: four heads' blocks side by side
 constexpr int kTable = 4096;       // shared rope factors (32 KB): 64 rows of 64 pairs
-constexpr int keep_of(int T) { return T > 1 ? 2 : 4; }     // units of a lane that stay in registers
+constexpr int keep_of(int T) { return T > 1 ? 8 : 4; }     // units of a lane that stay in registers
 constexpr int kQueryRows = 4;      // most rows of a CTA that rotates queries
 constexpr int kQueryFactors = 512; // their factors
-constexpr int kHeads = 4;          // heads of a CTA that takes whole blocks, one after the other
 
 struct AppendArgs {
     dspark_cache c;
@@ -163,18 +163,27 @@ __device__ __forceinline__ void store_unit(uint8_t* row, const Unit<VEC>& un, co
     }
 }
 
-// The largest of a team of T warps (1, or the whole CTA), NaN above all; `me` of 32 T threads.
+// A team: T warps that share a block, 1 or 4.
 template <int T>
-__device__ __forceinline__ float team_max(float amax, int me, float* red)
+__device__ __forceinline__ void team_sync()
+{
+    if (T == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / (32 * T)), "n"(32 * T) : "memory");
+}
+// The team's largest, NaN above all. `red`: T floats of the team's own.
+template <int T>
+__device__ __forceinline__ float team_max(float amax, float* red)
 {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
     if (T > 1) {
-        if ((me & 31) == 0) red[me >> 5] = amax;
-        __syncthreads();
+        team_sync<T>();                    // the last use of red is over
+        if ((threadIdx.x & 31) == 0) red[(threadIdx.x >> 5) & (T - 1)] = amax;
+    }
+    team_sync<T>();
+    if (T > 1)
 #pragma unroll
         for (int w = 0; w < T; ++w) amax = max_nan(amax, red[w]);
-    }
     return amax;
 }
 
@@ -185,7 +194,6 @@ __device__ __forceinline__ float settle_scale(float amax, float old, float* scal
                                               int me)
 {
     const float fresh = exp2i(scale_exponent(amax));
-    if (T == 1) __syncwarp();              // every lane has read the old scale
     if (retained == 0) {
         if (me == 0) *scale = fresh;
         return fresh;
@@ -227,43 +235,44 @@ __device__ __forceinline__ int row_owner(const AppendArgs& A, int64_t r, int* po
 }
 
 // The blocks that packed row r (request b's row i0, at position pos) leads. T = 1: eight of them
-// from hv0 (head, K or V), one per warp; T = kWarps: those of kHeads heads from hv0, by the whole
-// CTA, the next head's rows on their way while one's are worked on. Returns status bits.
+// from hv0 (head, K or V), one per warp; T = 4: the keys' or the values' of four heads from hv0.
+// Returns status bits.
 template <int DT, bool VEC, int T>
 __device__ __forceinline__ int append_blocks(const AppendArgs& A, int64_t r, int b, int i0, int pos, int hv0,
-                                             float2* tab, float* red)
+                                             float2* tab, float* reds)
 {
-    constexpr int kKeep = keep_of(T), kAll = T > 1 ? 32 * T : kThreads;
+    constexpr int kKeep = keep_of(T), kAll = T > 1 ? 32 * kPromptWarps : kThreads;
     const dspark_cache& c = A.c;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / T;
     const int slot0 = pos & (c.page - 1), block = pos / c.page, most = c.page - slot0;
-    const int me = T > 1 ? threadIdx.x : lane;
-    const int hv = T > 1 ? hv0 : hv0 + warp;
+    const int me = threadIdx.x & (32 * T - 1);
+    const int hv = hv0 + (T > 1 ? 2 * team : team);
     const bool works = hv < 2 * c.heads, value = hv & 1;
-    const int h0 = hv >> 1, heads = T > 1 ? min(kHeads, c.heads - h0) : 1;
+    const int h = hv >> 1;
     const int half = T > 1 && value ? 0 : A.rope.half;
     const int units = c.dim / Unit<VEC>::N;
+    float* red = reds + team * T;
     // Lanes over units, `step` rows at a time; a head wider than a warp's units (scalar accesses
     // only) takes several turns over a row.
     const int wide = units > 32 ? 32 : units, per_warp = 32 / wide, step = per_warp * T;
     const int in_warp = lane / wide, u0 = lane - in_warp * wide;
-    const int k0 = T > 1 ? in_warp + per_warp * warp : in_warp;
+    const int k0 = in_warp + per_warp * (warp & (T - 1));
     const bool has = works && in_warp < per_warp;
     Rope rope = A.rope;
     if (value) rope.half = 0;
     const RowsIn in = value ? A.v : A.k;
-    const int64_t first = r * in.row_stride;
     const Unit<VEC> un(rope, u0);
+    constexpr int E = DT == DSPARK_BF16 ? 2 : 4;
+    // this lane's first row, and the bytes from one of its rows to the next
+    const char* mine0 = static_cast<const char*>(in.base) +
+                        ((r + k0) * in.row_stride + static_cast<int64_t>(h) * c.dim) * E;
+    const int64_t hop = step * in.row_stride * E;
     // the rows that may be the block's, before it is known which are
     const int may = static_cast<int>(min(static_cast<int64_t>(most), A.rows - r));
-    auto fetch = [&](Raw<DT, VEC>* raw, int h) {
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i)
-            if (has && k0 + i * step < may)
-                raw[i].load(in.base, first + (k0 + i * step) * in.row_stride + static_cast<int64_t>(h) * c.dim, un);
-    };
     Raw<DT, VEC> raw[kKeep];
-    fetch(raw, h0);
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+        if (has && k0 + i * step < may) raw[i].load(mine0 + i * hop, 0, un);
     const int page = block < c.width ? c.table[static_cast<int64_t>(b) * c.width + block] : -1;
     // the block's rows: the packed rows that follow, while they are b's next positions
     int n = 1;
@@ -286,100 +295,84 @@ __device__ __forceinline__ int append_blocks(const AppendArgs& A, int64_t r, int
         __syncthreads();
     };
     const bool keep = n <= kKeep * step && n <= rows_at_once && units <= 32;
-    bool bad = false;
     if (keep && half > 0) factors(0, n);
+    const int64_t bh = static_cast<int64_t>(page) * c.heads + h;
+    uint8_t* codes = static_cast<uint8_t*>(value ? c.v : c.k) + bh * c.page * c.dim;
+    float* scale = (value ? c.v_scale : c.k_scale) + bh;
+    uint8_t* to = codes + (slot0 + k0) * c.dim;          // within a block: 32 bits
+    float x[Unit<VEC>::N], amax = 0.0f;
+    bool bad = false;
+    if (keep) {
+        if (!works) return 0;
+        const float old = slot0 > 0 ? *scale : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i)
+            if (has && k0 + i * step < n) {
+                raw[i].get(x);
+                turn_unit<VEC, false>(rope, un, tab + (k0 + i * step) * half, x);
+                amax = amax_unit<VEC>(x, amax);
+            }
+        amax = team_max<T>(amax, red);
+        const bool clean = finite(amax);         // the same for the team
+        if (!clean) {                            // rare: the offenders count as 0
+            amax = 0.0f;
 #pragma unroll 1
-    for (int h = h0; h < h0 + heads; ++h) {
-        const int64_t bh = static_cast<int64_t>(page) * c.heads + h;
-        uint8_t* codes = static_cast<uint8_t*>(value ? c.v : c.k) + bh * c.page * c.dim;
-        float* scale = (value ? c.v_scale : c.k_scale) + bh;
-        float* parts = red + (T > 1 ? ((h - h0) & 1) * T : 0);
-        float amax = 0.0f;
-        if (keep) {
-            if (!works) return 0;
-            const float old = slot0 > 0 ? *scale : 0.0f;
-            // a CTA's threads keep the turned elements and fetch the next head's; a warp's turn
-            // them again, which leaves registers for more warps
-            float y[T > 1 ? kKeep : 1][Unit<VEC>::N];
+            for (int k = k0, i = 0; has && k < n; k += step, ++i) {
+                Raw<DT, VEC> one;
+                one.load(mine0 + i * hop, 0, un);
+                one.get(x);
+                bad |= turn_unit<VEC, true>(rope, un, tab + k * half, x);
+                amax = amax_unit<VEC>(x, amax);
+            }
+            amax = team_max<T>(amax, red);
+        }
+        const float inv = 1.0f / settle_scale<T>(amax, old, scale, codes, slot0 * c.dim, me);
+        if (clean) {
 #pragma unroll
             for (int i = 0; i < kKeep; ++i)
                 if (has && k0 + i * step < n) {
-                    float* x = y[T > 1 ? i : 0];
                     raw[i].get(x);
                     turn_unit<VEC, false>(rope, un, tab + (k0 + i * step) * half, x);
-                    amax = amax_unit<VEC>(x, amax);
+                    store_unit<VEC>(to + i * step * c.dim, un, x, inv);
                 }
-            if (T > 1 && h + 1 < h0 + heads) fetch(raw, h + 1);
-            amax = team_max<T>(amax, me, parts);
-            const bool clean = finite(amax);     // the same for the team
-            if (!clean) {                        // rare: the offenders count as 0
-                amax = 0.0f;
+        } else {
 #pragma unroll 1
-                for (int k = k0; has && k < n; k += step) {
-                    Raw<DT, VEC> one;
-                    float x[Unit<VEC>::N];
-                    one.load(in.base, first + k * in.row_stride + static_cast<int64_t>(h) * c.dim, un);
-                    one.get(x);
-                    bad |= turn_unit<VEC, true>(rope, un, tab + k * half, x);
-                    amax = amax_unit<VEC>(x, amax);
-                }
-                if (T > 1) __syncthreads();
-                amax = team_max<T>(amax, me, parts);
+            for (int k = k0, i = 0; has && k < n; k += step, ++i) {
+                Raw<DT, VEC> one;
+                one.load(mine0 + i * hop, 0, un);
+                one.get(x);
+                turn_unit<VEC, true>(rope, un, tab + k * half, x);
+                store_unit<VEC>(to + i * step * c.dim, un, x, inv);
             }
-            const float inv = 1.0f / settle_scale<T>(amax, old, scale, codes, slot0 * c.dim, me);
-            uint8_t* to = codes + static_cast<int64_t>(slot0) * c.dim;
-            if (clean) {
-#pragma unroll
-                for (int i = 0; i < kKeep; ++i)
-                    if (has && k0 + i * step < n) {
-                        float* x = y[T > 1 ? i : 0];
-                        if (T == 1) {
-                            raw[i].get(x);
-                            turn_unit<VEC, false>(rope, un, tab + (k0 + i * step) * half, x);
-                        }
-                        store_unit<VEC>(to + (k0 + i * step) * c.dim, un, x, inv);
-                    }
-            } else {
-#pragma unroll 1
-                for (int k = k0; has && k < n; k += step) {
-                    Raw<DT, VEC> one;
-                    float x[Unit<VEC>::N];
-                    one.load(in.base, first + k * in.row_stride + static_cast<int64_t>(h) * c.dim, un);
-                    one.get(x);
-                    turn_unit<VEC, true>(rope, un, tab + k * half, x);
-                    store_unit<VEC>(to + k * c.dim, un, x, inv);
-                }
-            }
-            continue;
         }
-        float inv = 0.0f, x[Unit<VEC>::N];
+        return bad ? DSPARK_STATUS_BAD_VALUE : 0;
+    }
+    float inv = 0.0f;
 #pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
+    for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
-            for (int from = 0; from < n; from += rows_at_once) {
-                const int m = min(rows_at_once, n - from);
-                if (half > 0 && ((pass == 0 && h == h0) || rows_at_once < n)) factors(from, m);
-                if (!has) continue;
+        for (int from = 0; from < n; from += rows_at_once) {
+            const int m = min(rows_at_once, n - from);
+            if (half > 0 && (pass == 0 || rows_at_once < n)) factors(from, m);
+            if (!has) continue;
 #pragma unroll 1
-                for (int u = u0; u < units; u += wide) {
-                    const Unit<VEC> un(rope, u);
+            for (int u = u0; u < units; u += wide) {
+                const Unit<VEC> at(rope, u);
 #pragma unroll 2
-                    for (int k = k0; k < m; k += step) {
-                        Raw<DT, VEC> one;
-                        one.load(in.base, first + (from + k) * in.row_stride + static_cast<int64_t>(h) * c.dim, un);
-                        one.get(x);
-                        bad |= turn_unit<VEC, true>(rope, un, tab + k * half, x);
-                        if (pass == 0) amax = amax_unit<VEC>(x, amax);
-                        else store_unit<VEC>(codes + static_cast<int64_t>(slot0 + from + k) * c.dim, un, x, inv);
-                    }
+                for (int k = k0; k < m; k += step) {
+                    Raw<DT, VEC> one;
+                    one.load(mine0 + (from + k - k0) * (in.row_stride * E), 0, at);
+                    one.get(x);
+                    bad |= turn_unit<VEC, true>(rope, at, tab + k * half, x);
+                    if (pass == 0) amax = amax_unit<VEC>(x, amax);
+                    else store_unit<VEC>(to + (from + k - k0) * c.dim, at, x, inv);
                 }
             }
-            if (pass == 0 && works) {
-                const float old = slot0 > 0 ? *scale : 0.0f;
-                if (T == 1) __syncwarp();
-                amax = team_max<T>(amax, me, parts);
-                inv = 1.0f / settle_scale<T>(amax, old, scale, codes, slot0 * c.dim, me);
-            }
+        }
+        if (pass == 0 && works) {
+            const float old = slot0 > 0 ? *scale : 0.0f;
+            amax = team_max<T>(amax, red);
+            inv = 1.0f / settle_scale<T>(amax, old, scale, codes, slot0 * c.dim, me);
         }
     }
     return bad ? DSPARK_STATUS_BAD_VALUE : 0;
@@ -391,7 +384,8 @@ __device__ __forceinline__ int append_rows(const AppendArgs& A, float2* tab, flo
 {
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / A.per_row) * A.chunk;
     const int share = blockIdx.x % A.per_row;
-    const int hv0 = T > 1 ? 2 * (share >> 1) * kHeads + (share & 1) : share * kWarps;
+    constexpr int kTeams = kPromptWarps / kTeam;
+    const int hv0 = T > 1 ? 2 * (share >> 1) * kTeams + (share & 1) : share * kWarps;
     // each warp looks at the rows side by side; those that lead a block are the same for all
     const int lane = threadIdx.x & 31;
     int bits = 0;
@@ -411,7 +405,6 @@ __device__ __forceinline__ int append_rows(const AppendArgs& A, float2* tab, flo
             bits |= append_blocks<DT, VEC, T>(A, row0 + from + k, __shfl_sync(0xffffffffu, b, k),
                                               __shfl_sync(0xffffffffu, i, k), __shfl_sync(0xffffffffu, pos, k),
                                               hv0, tab, red);
-            if (T > 1) __syncthreads();                  // red and the factors, before the next block's
         }
     }
     return bits;
@@ -453,10 +446,10 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendArgs A)
 
 // Prompts: the keys and values.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(32 * kTeam, 2) append_prompt_kernel(AppendArgs A)
+__global__ void __launch_bounds__(32 * kPromptWarps, 2) append_prompt_kernel(AppendArgs A)
 {
     __shared__ __align__(16) float2 tab[kTable];
-    __shared__ float red[2 * kTeam];
+    __shared__ float red[kPromptWarps];
     pdl_wait_and_trigger();
     const int bits = append_rows<DT, VEC, kTeam>(A, tab, red);
     if (bits) raise_status(A.status, bits);
@@ -502,12 +495,13 @@ int launch_append(const dspark_cache& cache, const Rope& rope, const void* k, in
     A.B = B;
     A.status = status;
     // Steps: a warp per block, one row per CTA for the shortest chains in a small one, four in a
-    // large one, where about one row in four leads (256 windows: 16 us with 4, 18 with 1). Prompts: a
-    // CTA for four heads' blocks, so that a page's rows are read once and stay in registers.
+    // large one, where about one row in four leads (256 windows: 16 us with 4, 18 with 1). Prompts:
+    // four warps per block, so that a page's rows are read once and stay in registers; with 16 the
+    // work per block's scale, not per element, was most of it (55 us for 12 thousand rows).
     const bool prompts = rows > 4096;
     A.chunk = prompts ? cache.page : rows <= 512 ? 1 : 4;
     A.q_rows = rows >= 152 * 8 && rope.half > 0 ? (rope.half <= 64 ? 4 : 2) : 1;
-    A.per_row = static_cast<int>(prompts ? 2 * ceil_div(cache.heads, kHeads) : ceil_div(2 * cache.heads, kWarps));
+    A.per_row = static_cast<int>(prompts ? 2 * ceil_div(cache.heads, kPromptWarps / kTeam) : ceil_div(2 * cache.heads, kWarps));
     A.kv_ctas = static_cast<int>(ceil_div(rows, A.chunk)) * A.per_row;
     const int q_ctas = q != nullptr ? static_cast<int>(ceil_div(rows, A.q_rows)) : 0;
     const bool bf = dtype == DSPARK_BF16;
@@ -518,7 +512,7 @@ int launch_append(const dspark_cache& cache, const Rope& rope, const void* k, in
     if (prompts) {
         auto kv = bf ? (vec ? append_prompt_kernel<DSPARK_BF16, true> : append_prompt_kernel<DSPARK_BF16, false>)
                      : (vec ? append_prompt_kernel<DSPARK_F32, true> : append_prompt_kernel<DSPARK_F32, false>);
-        const int rc = launch_pdl("append", kv, dim3(static_cast<unsigned>(A.kv_ctas)), dim3(32 * kTeam), 0, stream, A);
+        const int rc = launch_pdl("append", kv, dim3(static_cast<unsigned>(A.kv_ctas)), dim3(32 * kPromptWarps), 0, stream, A);
         if (rc != DSPARK_OK || q == nullptr) return rc;
         auto turn = bf ? (qvec ? append_query_kernel<DSPARK_BF16, true> : append_query_kernel<DSPARK_BF16, false>)
                        : (qvec ? append_query_kernel<DSPARK_F32, true> : append_query_kernel<DSPARK_F32, false>);
