@@ -23,7 +23,7 @@ namespace {
 constexpr int kThreads = 256;      // of a step's CTA, and of one that rotates queries
 constexpr int kWarps = kThreads / 32;
 constexpr int kTeam = 4;           // warps that take a prompt's block together
-constexpr int kPromptWarps = 16;   // of a CTA: four heads' blocks side by side
+constexpr int kPromptWarps = 8;    // of a CTA: two heads' blocks side by side
 constexpr int kTable = 4096;       // shared rope factors (32 KB): 64 rows of 64 pairs
 constexpr int keep_of(int T) { return T > 1 ? 8 : 4; }     // units of a lane that stay in registers
 constexpr int kQueryRows = 4;      // most rows of a CTA that rotates queries
@@ -235,7 +235,7 @@ __device__ __forceinline__ int row_owner(const AppendArgs& A, int64_t r, int* po
 }
 
 // The blocks that packed row r (request b's row i0, at position pos) leads. T = 1: eight of them
-// from hv0 (head, K or V), one per warp; T = 4: the keys' or the values' of four heads from hv0.
+// from hv0 (head, K or V), one per warp; T = 4: the keys' or the values' of two heads from hv0.
 // Returns status bits.
 template <int DT, bool VEC, int T>
 __device__ __forceinline__ int append_blocks(const AppendArgs& A, int64_t r, int b, int i0, int pos, int hv0,
