@@ -1,18 +1,19 @@
 // attend_wide.cu — dspark_attend on the tensor cores for prompts and large groups: units of up to
 // 128 rows, one row per TMEM lane.
 //   S [128 rows, 128 tokens] = (Q_hi + Q_lo) K^T       O [128 rows, D] += (W_hi + W_lo) V
-// the pieces' products adding up in the same columns, W as the operand in TMEM.
+// the pieces' products adding up in the same columns.
 //
 // A CTA: warps 0-7 do the softmax, two threads per row with half of a tile's tokens each, warp 8
 // loads pages with TMA (one box per page and K or V, swizzled), warp 9 issues the products. As in
 // the narrow kernel a row's weights are taken over a reference that may lag its maximum: the
 // scores pass through registers once, and only a tile that passes a reference by kLag, or a
 // unit's first, stops to find the maxima and rescale the sums.
-// The weights overlay the scores in TMEM: 128 + D columns, so two CTAs fit and one's softmax runs
-// under the other's products.
+// The weights go through shared memory, so that a tile's scores leave TMEM as soon as they are read
+// and the next tile's products run under this one's softmax; 128 + D columns, so two CTAs fit and
+// one's softmax runs under the other's.
 //
-// Bound: the products (eight of 101 cycles for the scores, eight of 75 for the sums, a tile) and
-// the softmax's instruction issue, about alike.
+// Bound: the products (sixteen of 101 cycles a tile at D = 128) and the softmax's instruction
+// issue, about alike.
 #include "attend_mma.cuh"
 
 namespace dspark {
@@ -22,6 +23,7 @@ constexpr int kRows = 128;
 constexpr int kSoft = 256;                   // softmax threads
 constexpr int kThreads = kSoft + 64;
 constexpr int kHalf = kTile / 2;             // tokens of a softmax thread
+constexpr int kNums = 4;
 // Weights are 2^(x - m + kUp), m lagging by at most kLag: at most 2^8.5 < 448, and a weight keeps
 // two full pieces down to 2^-12 of the largest.
 constexpr float kUp = 6.0f;
@@ -30,14 +32,19 @@ constexpr float kBehind = 2.5f;
 template <int D>
 struct Smem {
     static constexpr int kSlot = kTile * D;              // one tile's K or V; 1024-byte aligned in order
-    static constexpr int kSlots = D == 128 ? 4 : 8;      // K and V alternate
+    // K and V alternate. One of each suffices at D = 128, where two CTAs leave no room for more: K's
+    // slot is free for a whole softmax, V's until the end of the next one.
+    static constexpr int kSlots = D == 128 ? 2 : 4;
     uint8_t q[2][kTile * D];                             // the queries' two pieces
+    uint8_t w[2][kRows * kTile];                         // the weights'
     uint8_t ring[kSlots][kSlot];
-    BlockNums nums[kSlots / 2][kBlocks];
+    // A tile's numbers are written once K's slot is free, kSlots / 2 tiles ahead at most, and read
+    // until the tile's softmax ends: kNums slots cover kSlots / 2 + 1 tiles and the one being written.
+    BlockNums nums[kNums][kBlocks];
     float f[kRows];                                      // score factors: scale log2(e) 2^e
     float2 pair[kRows];                                  // a row's two threads' maxima or sums
-    uint64_t full[kSlots], empty[kSlots];
-    uint64_t s_full, p_full, pv_done, q_full;
+    uint64_t full[kSlots], empty[kSlots], noted[kNums];
+    uint64_t s_full, s_read, p_full, pv_done, q_full;
     Cut<kRows> cut;
     uint32_t tmem;
     int stalled;       // a wait gave up: every role leaves its loop
@@ -65,16 +72,21 @@ struct Row {
     float l;              // this thread's part of the row's sum
 };
 
-// One tile, this thread's row and 64 of its tokens: scores in TMEM -> weights in TMEM.
+// One tile, this thread's row and 64 of its tokens: scores in TMEM -> weights in shared memory.
+// False once a wait gave up.
 template <int D>
-__device__ __forceinline__ void soften(Smem<D>& sm, Row& r, uint32_t lanes, int row, int half,
-                                       const BlockNums* nums, int shift_page, int token0, bool mask, bool first)
+__device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int row, int half,
+                                       const BlockNums* nums, int shift_page, int token0, bool mask, bool first, int it,
+                                       bool ok, volatile int* stalled)
 {
     const uint32_t s_addr = sm.tmem + lanes;
     float x[kHalf];
     tc_ld32(s_addr + half * kHalf, x);
     tc_ld32(s_addr + half * kHalf + 32, x + 32);
     tc_wait_ld();
+    tc_fence_before();
+    __syncwarp();
+    if (ok && (threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&sm.s_read));
     float top = -INFINITY;
 #pragma unroll
     for (int g = 0; g < kHalf; g += 16) {
@@ -99,9 +111,10 @@ __device__ __forceinline__ void soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
         for (int j = 4; j < kHalf; ++j) m[j & 3] = fmaxf(m[j & 3], x[j]);
         top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     }
-    tc_fence_before();
     const bool stop = soft_any(top > kUp + kBehind || r.ref == 0.0f);
-    tc_fence_after();
+    // the last tile's products read the weights' place and write the sums
+    if (it > 0) ok = ok && mbar_wait(smem_addr(&sm.pv_done), (it - 1) & 1, stalled);
+    ok = __all_sync(0xffffffffu, ok);
     if (stop) {
         // the row's maximum over the present reference, by both its threads
         (half ? sm.pair[row].y : sm.pair[row].x) = top;
@@ -122,7 +135,7 @@ __device__ __forceinline__ void soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) x[j] += shift;
         if (!first && __any_sync(0xffffffffu, g != 1.0f)) {
-            // the last tile's products are done: these scores came after them
+            tc_fence_after();
             const uint32_t o_addr = sm.tmem + lanes + kTile + half * (D / 2);
 #pragma unroll 1
             for (int d = 0; d < D / 2; d += 16) {
@@ -136,34 +149,31 @@ __device__ __forceinline__ void soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
             tc_wait_st();
         }
     }
-    // A group's weights, its part of the sum, and the pieces: chunk c's 8 words of first pieces at
-    // column 16 c, of second ones at 16 c + 8. Every thread of these lanes has read its scores (the
-    // vote was after), so they may be overwritten.
+    // A group's weights, its part of the sum, and the pieces: 16 bytes of each, swizzled.
 #pragma unroll
-    for (int c = 0; c < kHalf; c += 32) {
-        uint32_t p[16];
+    for (int g = 0; g < kHalf; g += 16) {
+        const float inv = nums[(half * kHalf + g) >> shift_page].inv;
+        float* y = x + g;
+        uint32_t p[8];
+        uint64_t s2 = 0;
 #pragma unroll
-        for (int g = 0; g < 32; g += 16) {
-            const float inv = nums[(half * kHalf + c + g) >> shift_page].inv;
-            float* y = x + c + g;
-            uint64_t s2 = 0;
+        for (int j = 0; j < 16; j += 4) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[j + k] = ex2_approx(y[j + k]);
-                s2 = add2(s2, add2(pack2(y[j], y[j + 1]), pack2(y[j + 2], y[j + 3])));
-                uint32_t h0, h1, l0, l1;
-                split2(y[j], y[j + 1], &h0, &l0);
-                split2(y[j + 2], y[j + 3], &h1, &l1);
-                p[(g + j) / 4] = h0 | (h1 << 16);
-                p[8 + (g + j) / 4] = l0 | (l1 << 16);
-            }
-            const float2 s = unpack2(s2);
-            r.l = fmaf(s.x + s.y, inv, r.l);
+            for (int k = 0; k < 4; ++k) y[j + k] = ex2_approx(y[j + k]);
+            s2 = add2(s2, add2(pack2(y[j], y[j + 1]), pack2(y[j + 2], y[j + 3])));
+            uint32_t h0, h1, l0, l1;
+            split2(y[j], y[j + 1], &h0, &l0);
+            split2(y[j + 2], y[j + 3], &h1, &l1);
+            p[j / 4] = h0 | (h1 << 16);
+            p[4 + j / 4] = l0 | (l1 << 16);
         }
-        tc_st16(s_addr + (half * kHalf + c) / 2, p);
+        const float2 s = unpack2(s2);
+        r.l = fmaf(s.x + s.y, inv, r.l);
+        const int at = row * kTile + (((half * kHalf + g) / 16) ^ (row & 7)) * 16;
+        *reinterpret_cast<uint4*>(&sm.w[0][at]) = make_uint4(p[0], p[1], p[2], p[3]);
+        *reinterpret_cast<uint4*>(&sm.w[1][at]) = make_uint4(p[4], p[5], p[6], p[7]);
     }
-    tc_wait_st();
+    return ok;
 }
 
 // A unit's queries as two pieces in shared memory, and their rows' factors: eight (four) lanes per
@@ -289,8 +299,10 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
             mbar_init(smem_addr(&sm.full[s]), 1);
             mbar_init(smem_addr(&sm.empty[s]), 1);
         }
+        for (int s = 0; s < kNums; ++s) mbar_init(smem_addr(&sm.noted[s]), 1);
         mbar_init(smem_addr(&sm.s_full), 1);
-        mbar_init(smem_addr(&sm.p_full), kSoft);
+        mbar_init(smem_addr(&sm.s_read), kSoft / 32);
+        mbar_init(smem_addr(&sm.p_full), kSoft / 32);
         mbar_init(smem_addr(&sm.pv_done), 1);
         mbar_init(smem_addr(&sm.q_full), kSoft);
         sm.stalled = 0;
@@ -369,16 +381,19 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                             ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.empty[s]),
                                                                    ((use / kSlots) & 1) ^ 1, stalled));
                         if (!ok) break;
-                        if (kv == 1 && lane < per_tile) {
+                        if (kv == 0 && lane < per_tile) {
                             BlockNums n;
                             n.ks = my_id < 0 ? 0.0f : ks;
                             n.bias = my_id < 0 ? -INFINITY : log2f(vs);
                             n.inv = my_id < 0 ? 0.0f : 1.0f / vs;
                             n.pad = 0.0f;
-                            sm.nums[it % (kSlots / 2)][lane] = n;
+                            sm.nums[it % kNums][lane] = n;
                         }
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_expect_tx(full, count * box);
+                        if (lane == 0) {
+                            if (kv == 0) mbar_arrive(smem_addr(&sm.noted[it % kNums]));
+                            mbar_arrive_expect_tx(full, count * box);
+                        }
                         __syncwarp();
                         if (there)
                             tma_load(smem_addr(sm.ring[s]) + lane * box, kv ? &v_map : &k_map, row, full);
@@ -405,6 +420,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
             constexpr uint32_t kIdescPV = kIdesc | (D / 8 << 17) | (1u << 16);   // V: dim contiguous
             const uint32_t s_addr = sm.tmem, o_addr = sm.tmem + kTile;
             const uint64_t ring0 = operand<D>(smem_addr(sm.ring[0])), q_op = operand<D>(smem_addr(sm.q[0]));
+            const uint64_t w_op = operand<kTile>(smem_addr(sm.w[0]));
             constexpr uint32_t kStep = Smem<D>::kSlot / 16;
             int it = 0, piece = 0;
             bool ok = true;
@@ -413,41 +429,46 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
             };
             do {
                 ok = wait(sm.q_full, piece & 1);
+                // scores of tile k, then the sums of tile k - 1: it counts the tiles before k
 #pragma unroll 1
-                for (int k = 0; ok && k < wk.n; ++k, ++it) {
-                    const int use = 2 * it;
-                    const int sk = use % kSlots, sv = (use + 1) % kSlots;
-                    const uint32_t round = (use / kSlots) & 1;
-                    // the scores' columns hold the last tile's weights until its products end
-                    ok = wait(sm.full[sk], round) && (it == 0 || wait(sm.pv_done, (it - 1) & 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (leader) {
-                        const uint64_t kb = ring0 + sk * kStep;
-#pragma unroll
-                        for (int p = 0; p < 2; ++p)
-#pragma unroll
-                            for (int s = 0; s < D / 32; ++s)
-                                mma_ss(s_addr, q_op + p * kStep + 2 * s, kb + 2 * s, kIdescQK, p > 0 || s > 0);
-                        tc_commit(smem_addr(&sm.s_full));
-                        tc_commit(smem_addr(&sm.empty[sk]));
-                    }
-                    __syncwarp();
-                    ok = wait(sm.p_full, it & 1) && wait(sm.full[sv], round);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (leader) {
-                        const uint64_t vb = ring0 + sv * kStep;
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
+                for (int k = 0; ok && k <= wk.n; ++k) {
+                    if (k < wk.n) {
+                        const int use = 2 * it, s = use % kSlots;
+                        ok = wait(sm.full[s], (use / kSlots) & 1) && (k == 0 || wait(sm.s_read, (it - 1) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint64_t kb = ring0 + s * kStep;
 #pragma unroll
                             for (int p = 0; p < 2; ++p)
-                                mma_ts(o_addr, s_addr + 16 * s + 8 * p, vb + s * (32 * D / 16), kIdescPV,
-                                       k > 0 || s > 0 || p > 0);
-                        tc_commit(smem_addr(&sm.pv_done));
-                        tc_commit(smem_addr(&sm.empty[sv]));
+#pragma unroll
+                                for (int i = 0; i < D / 32; ++i)
+                                    mma_ss(s_addr, q_op + p * kStep + 2 * i, kb + 2 * i, kIdescQK, p > 0 || i > 0);
+                            tc_commit(smem_addr(&sm.s_full));
+                            tc_commit(smem_addr(&sm.empty[s]));
+                        }
+                        __syncwarp();
+                        ++it;
                     }
-                    __syncwarp();
+                    if (k > 0) {
+                        const int last = k < wk.n ? it - 2 : it - 1;
+                        const int use = 2 * last + 1, s = use % kSlots;
+                        ok = wait(sm.p_full, last & 1) && wait(sm.full[s], (use / kSlots) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint64_t vb = ring0 + s * kStep;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int p = 0; p < 2; ++p)
+                                    mma_ss(o_addr, w_op + p * (kRows * kTile / 16) + 2 * i, vb + i * (32 * D / 16),
+                                           kIdescPV, k > 1 || i > 0 || p > 0);
+                            tc_commit(smem_addr(&sm.pv_done));
+                            tc_commit(smem_addr(&sm.empty[s]));
+                        }
+                        __syncwarp();
+                    }
                 }
                 ++piece;
             } while (ok && next_piece());
@@ -489,24 +510,27 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
 #pragma unroll 1
                 for (int k = 0; k < wk.n; ++k, ++it) {
                     const int token0 = (wk.k0 + k) * kTile;
-                    const int use = 2 * it + 1;
-                    const int s = use % kSlots;
-                    ok = ok && mbar_wait(smem_addr(&sm.full[s]), (use / kSlots) & 1, stalled) &&
+                    ok = ok && mbar_wait(smem_addr(&sm.noted[it % kNums]), (it / kNums) & 1, stalled) &&
                          mbar_wait(smem_addr(&sm.s_full), it & 1, stalled);
                     ok = __all_sync(0xffffffffu, ok);
                     tc_fence_after();
                     const bool mask = token0 + kTile - 1 > p0 || token0 < lo1;
-                    soften<D>(sm, r, lanes, row, half, sm.nums[it % (kSlots / 2)], shift_page, token0, mask, k == 0);
-                    tc_fence_before();
+                    ok = soften<D>(sm, r, lanes, row, half, sm.nums[it % kNums], shift_page, token0, mask, k == 0,
+                                   it, ok, stalled);
                     if (token0 + kTile > stored) {      // slots past the last token: 0 x NaN is NaN
+                        const int use = 2 * it + 1, s = use % kSlots;
+                        ok = ok && mbar_wait(smem_addr(&sm.full[s]), (use / kSlots) & 1, stalled);
+                        ok = __all_sync(0xffffffffu, ok);
                         if (token0 + row >= stored) {
                             uint4* v = reinterpret_cast<uint4*>(&sm.ring[s][row * D + half * (D / 2)]);
 #pragma unroll
                             for (int c = 0; c < D / 32; ++c) v[c] = make_uint4(0, 0, 0, 0);
                         }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
-                    if (ok) mbar_arrive(smem_addr(&sm.p_full));
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    tc_fence_before();
+                    __syncwarp();
+                    if (ok && (tid & 31) == 0) mbar_arrive(smem_addr(&sm.p_full));
                 }
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done), (it - 1) & 1, stalled));
                 if (soft_any(!ok)) break;
