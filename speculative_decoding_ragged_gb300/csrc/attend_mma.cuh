@@ -238,18 +238,21 @@ struct __align__(16) BlockNums {
 // Two weights in two e4m3 pieces each. The weights go through fp16 (11 bits, 2^-12: a sixteenth
 // of what the pieces are off by); the remainder is exact there.
 template <bool LOW = false>      // the second piece times 2^4, where it has a column of its own
-__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo)
+__device__ __forceinline__ void split2(float a, float b, uint16_t* hi, uint16_t* lo)
 {
     uint32_t w, back, rest;
-    uint16_t h, s;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(w));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(*hi) : "r"(w));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(*hi));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(w), "r"(back));
     if (LOW) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(rest), "r"(0x4c004c00u));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(s) : "r"(rest));
-    *hi = h;
-    *lo = s;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(*lo) : "r"(rest));
+}
+__device__ __forceinline__ uint32_t join16(uint16_t a, uint16_t b)
+{
+    uint32_t r;
+    asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(a), "h"(b));
+    return r;
 }
 
 // Packed fp32 pairs: one instruction for two.

@@ -297,11 +297,11 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, uint64_t* l, uin
             b.y = ex2_approx(b.y);
             l[2 * c] = fma2(pack2(a.x, a.y), inv2, l[2 * c]);
             l[2 * c + 1] = fma2(pack2(b.x, b.y), inv2, l[2 * c + 1]);
-            uint32_t h0, h1, l0, l1;
+            uint16_t h0, h1, l0, l1;
             split2<true>(a.x, a.y, &h0, &l0);
             split2<true>(b.x, b.y, &h1, &l1);
-            hi[c] = h0 | (h1 << 16);
-            lo[c] = l0 | (l1 << 16);
+            hi[c] = join16(h0, h1);
+            lo[c] = join16(l0, l1);
         }
     if (HR == 16) {
         *reinterpret_cast<uint4*>(place(r0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);

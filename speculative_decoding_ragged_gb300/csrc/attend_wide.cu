@@ -26,8 +26,8 @@ constexpr int kHalf = kTile / 2;             // tokens of a softmax thread
 constexpr int kNums = 4;
 // Weights are 2^(x - m + kUp), m lagging by at most kLag: at most 2^8.5 < 448, and a weight keeps
 // two full pieces down to 2^-12 of the largest.
-constexpr float kUp = 6.0f;
-constexpr float kBehind = 2.5f;
+constexpr float kUp = 4.0f;
+constexpr float kBehind = 4.5f;
 
 template <int D>
 struct Smem {
@@ -50,20 +50,24 @@ struct Smem {
     int stalled;       // a wait gave up: every role leaves its loop
 };
 
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-// Whether any softmax thread says yes; also a barrier of them.
-__device__ __forceinline__ bool soft_any(bool yes)
+// A barrier of `count` softmax threads, which says whether any of them says yes.
+__device__ __forceinline__ bool any_of(int id, int count, bool yes)
 {
     uint32_t r;
     asm volatile(
         "{\n"
         " .reg .pred p, q;\n"
         " setp.ne.u32 p, %1, 0;\n"
-        " barrier.cta.red.or.pred q, 2, 256, p;\n"
+        " barrier.cta.red.or.pred q, %2, %3, p;\n"
         " selp.u32 %0, 1, 0, q;\n"
-        "}\n" : "=r"(r) : "r"(static_cast<uint32_t>(yes)) : "memory");
+        "}\n" : "=r"(r) : "r"(static_cast<uint32_t>(yes)), "r"(id), "r"(count) : "memory");
     return r != 0;
 }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool yes) { return any_of(1, kSoft, yes); }
+// The two warps that share 32 rows, alone.
+__device__ __forceinline__ void pair_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(2 + q) : "memory"); }
+__device__ __forceinline__ bool pair_any(int q, bool yes) { return any_of(2 + q, 64, yes); }
 
 struct Row {
     float f;              // score factor: scale log2(e) 2^e of the row's pieces
@@ -111,14 +115,15 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
         for (int j = 4; j < kHalf; ++j) m[j & 3] = fmaxf(m[j & 3], x[j]);
         top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     }
-    const bool stop = soft_any(top > kUp + kBehind || r.ref == 0.0f);
+    const int quarter = row / 32;
+    const bool stop = pair_any(quarter, top > kUp + kBehind || r.ref == 0.0f);
     // the last tile's products read the weights' place and write the sums
     if (it > 0) ok = ok && mbar_wait(smem_addr(&sm.pv_done), (it - 1) & 1, stalled);
     ok = __all_sync(0xffffffffu, ok);
     if (stop) {
         // the row's maximum over the present reference, by both its threads
         (half ? sm.pair[row].y : sm.pair[row].x) = top;
-        soft_sync();
+        pair_sync(quarter);
         const float2 both = sm.pair[row];
         const float over = fmaxf(both.x, both.y);
         float shift = 0.0f, g = 1.0f;
@@ -133,7 +138,11 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
             r.ref = ref;
         }
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) x[j] += shift;
+        for (int j = 0; j < kHalf; j += 2) {
+            const float2 y = unpack2(add2(pack2(x[j], x[j + 1]), pack2(shift, shift)));
+            x[j] = y.x;
+            x[j + 1] = y.y;
+        }
         if (!first && __any_sync(0xffffffffu, g != 1.0f)) {
             tc_fence_after();
             const uint32_t o_addr = sm.tmem + lanes + kTile + half * (D / 2);
@@ -161,11 +170,11 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
 #pragma unroll
             for (int k = 0; k < 4; ++k) y[j + k] = ex2_approx(y[j + k]);
             s2 = add2(s2, add2(pack2(y[j], y[j + 1]), pack2(y[j + 2], y[j + 3])));
-            uint32_t h0, h1, l0, l1;
+            uint16_t h0, h1, l0, l1;
             split2(y[j], y[j + 1], &h0, &l0);
             split2(y[j + 2], y[j + 3], &h1, &l1);
-            p[j / 4] = h0 | (h1 << 16);
-            p[4 + j / 4] = l0 | (l1 << 16);
+            p[j / 4] = join16(h0, h1);
+            p[4 + j / 4] = join16(l0, l1);
         }
         const float2 s = unpack2(s2);
         r.l = fmaf(s.x + s.y, inv, r.l);
@@ -240,7 +249,7 @@ __device__ __forceinline__ void finish(const AttendCall& A, Smem<D>& sm, const R
                                        const Workspace& ws)
 {
     (half ? sm.pair[row].y : sm.pair[row].x) = r.l;
-    soft_sync();
+    pair_sync(row / 32);
     const float2 both = sm.pair[row];
     const float l = both.x + both.y, m = -r.ref;             // reference - kUp, as the weights are
     const float g = !whole ? 1.0f : l == 0.0f ? 0.0f : __fdividef(1.0f, l);      // nothing seen: zeros
