@@ -16,9 +16,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendCall
     pdl_wait_and_trigger();
     const Workspace ws = workspace_of(A.ws);
     const RunMeta m = ws.meta[blockIdx.x];
-    if (!m.cut) return;
+    if (m.rows == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = (m.unit + kUnitCost) / m.run;             // the run of the unit's first tile
+    const int c0 = m.first / m.run;                          // the run of the unit's first tile
     const int c1 = (m.end + m.run - 1) / m.run;              // one past the run of its last
     // in the first run an earlier unit's piece may come before
     const int part0 = 2 * c0 + (c0 * m.run < m.unit ? 1 : 0);

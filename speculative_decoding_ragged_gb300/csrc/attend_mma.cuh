@@ -42,10 +42,11 @@ constexpr uint32_t kSmemAlign = 1024;        // the 128-byte swizzle's period
 
 // What the join needs to know of the unit that a run's start cut.
 struct RunMeta {
-    int cut;            // 0: the run starts with a unit's beginning, or holds no tile
     int unit, end;      // the unit's places on the line
+    int first;          // its first tile's
     int run;            // places per run
-    int row0, rows;     // the request's first packed row; the unit's rows (position, head) ...
+    int row0, rows;     // the request's first packed row; the unit's rows (position, head): 0 where
+                        // the run starts with a unit's beginning, or holds no tile ...
     int flat0, head0;   // ... from this flat index on, first query head
 };
 
@@ -292,7 +293,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 // CTA about as much as that many tiles, and runs of equal length should take equal time. Tile k is
 // at place kUnitCost + k of its unit. Run i holds the places [i * run, (i + 1) * run). The host
 // makes sure that a line's length fits an int (places_fit).
-constexpr int kUnitCost = 4;
+template <int R>
+constexpr int kUnitCost = R < kTile ? 4 : 6;
 
 struct Shape {                   // a unit's visible tiles [a, z]
     int a, z;
@@ -331,7 +333,7 @@ __device__ __forceinline__ int head_places(const AttendCall& A, int w, int len)
 #pragma unroll 1
     for (int qt = 0; qt < nq; ++qt) {
         const Shape s = unit_tiles<R>(A, w, len, qt);
-        n += s.z - s.a + 1 + kUnitCost;
+        n += s.z - s.a + 1 + kUnitCost<R>;
     }
     return n;
 }
@@ -340,7 +342,7 @@ template <int R>
 inline bool places_fit(const AttendCall& A)
 {
     const int64_t units = (static_cast<int64_t>(A.rows) * A.q_heads) / R + static_cast<int64_t>(A.B) * A.c.heads;
-    return units * (A.last_tile + 1 + kUnitCost) <= INT32_MAX / 2;
+    return units * (A.last_tile + 1 + kUnitCost<R>) <= INT32_MAX / 2;
 }
 
 // The units of one run in order.
@@ -357,13 +359,13 @@ struct Walk {
         const Shape s = unit_tiles<R>(A, w, len, qt);
         a = s.a;
         z = s.z;
-        const int first = unit + kUnitCost;                          // the place of the first tile
+        const int first = unit + kUnitCost<R>;                          // the place of the first tile
         const int k = from > first ? from - first : 0;
         k0 = a + k;
         n = min(stop - first, z - a + 1) - k;                        // <= 0: nothing of it here
     }
-    __device__ __forceinline__ int end() const { return unit + kUnitCost + z - a + 1; }
-    __device__ __forceinline__ bool last() const { return stop - end() <= kUnitCost; }
+    __device__ __forceinline__ int end() const { return unit + kUnitCost<R> + z - a + 1; }
+    __device__ __forceinline__ bool last() const { return stop - end() <= kUnitCost<R>; }
     // The next unit of the run; only if !last().
     __device__ __forceinline__ void next(const AttendCall& A)
     {
@@ -397,27 +399,53 @@ struct Walk {
     }
 };
 
-// The cut, by a whole CTA of NT threads: each thread counts the places of a stretch of requests, a
-// scan over the threads gives the total and the stretch that holds the run's first place; that
-// thread writes the walk's start (n <= 0: the run holds no tile). The caller synchronises before
-// the walk is read. Returns the places per run.
+// The cut, by a whole CTA of NT threads: a group of threads counts the places of a stretch of
+// requests, a scan over the groups gives the total and the stretch that holds the run's first
+// place; that group finds the walk's start (n <= 0: the run holds no tile). The caller synchronises
+// before the walk is read. Returns the places per run.
+// A group is one thread where units are small: their requests have few units each, and the code is
+// short. Where units are prompts' 128 rows, a few requests can have hundreds each: a group is then
+// up to a warp, whose lanes take a request's units in turn (two prompts of 2000 rows and 32 heads:
+// 66,600 cycles with single threads).
 template <int R>
 struct Cut {
     int scan[32];
     Walk<R> walk;
 };
-// Thread-serial part of the cut: the run [t0, t1) starts `off` places into the requests from b on.
-// `k` holds request b already, and `per_head` its places per head.
+// A group: its lane, size and lanes' mask.
+struct Group {
+    int g, size;
+    uint32_t mask;
+    template <class T>
+    __device__ __forceinline__ T from(T x, int lane_of) const { return __shfl_sync(mask, x, lane_of, size); }
+};
 template <int R>
-__device__ __forceinline__ void find_start(const AttendCall& A, Walk<R>& k, int per_head, int off, int t0, int t1)
+__device__ __forceinline__ int group_places(const AttendCall& A, int w, int len, const Group& gr)
+{
+    if constexpr (R < kTile) return head_places<R>(A, w, len);
+    int n = 0;
+    const int nq = row_tiles<R>(A, w);
+#pragma unroll 1
+    for (int qt = gr.g; qt < nq; qt += gr.size) {
+        const Shape s = unit_tiles<R>(A, w, len, qt);
+        n += s.z - s.a + 1 + kUnitCost<R>;
+    }
+    for (int d = 1; d < gr.size; d <<= 1) n += __shfl_xor_sync(gr.mask, n, d);
+    return n;
+}
+// By one group: the run [t0, t1) starts `off` places into the requests from b on. `k` holds request
+// b already, and `per_head` its places per head.
+template <int R>
+__device__ __forceinline__ void find_start(const AttendCall& A, Walk<R>& k, int per_head, int off, int t0, int t1,
+                                           const Group& gr)
 {
     int bits = 0;
 #pragma unroll 1
-    while (off >= per_head * A.c.heads) {        // only where a thread counts several requests
+    while (off >= per_head * A.c.heads) {        // only where a group counts several requests
         off -= per_head * A.c.heads;
         ++k.b;
         request_rows(A, k.b, &k.row0, &k.w, &k.len, &bits);
-        per_head = head_places<R>(A, k.w, k.len);
+        per_head = group_places<R>(A, k.w, k.len, gr);
     }
     k.h = static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(per_head));
     off -= k.h * per_head;
@@ -425,11 +453,39 @@ __device__ __forceinline__ void find_start(const AttendCall& A, Walk<R>& k, int 
     k.stop = t1;
     k.qt = 0;
     k.unit = t0 - off;
-    k.piece(A, t0);
+    if constexpr (R < kTile) {
+        k.piece(A, t0);
 #pragma unroll 1
-    while (k.end() <= t0) {                      // several units of rows: the one that holds t0
-        ++k.qt;
-        k.unit = k.end();
+        while (k.end() <= t0) {                  // several units of rows: the one that holds t0
+            ++k.qt;
+            k.unit = k.end();
+            k.piece(A, t0);
+        }
+    } else {
+#pragma unroll 1
+        for (;; k.qt += gr.size) {               // the group's units at once: off < per_head ends it
+            const int qt = k.qt + gr.g;
+            int n = 0;
+            if (qt < k.nq) {
+                const Shape s = unit_tiles<R>(A, k.w, k.len, qt);
+                n = s.z - s.a + 1 + kUnitCost<R>;
+            }
+            int upto = n;
+            for (int d = 1; d < gr.size; d <<= 1) {
+                const int y = __shfl_up_sync(gr.mask, upto, d, gr.size);
+                if (gr.g >= d) upto += y;
+            }
+            const uint32_t past = __ballot_sync(gr.mask, off < upto) & gr.mask;
+            if (past || k.qt + gr.size >= k.nq) {
+                const int at = past ? (__ffs(past) - 1) & (gr.size - 1) : 0;
+                k.unit += gr.from(upto - n, at);
+                k.qt += at;
+                break;
+            }
+            const int all = gr.from(upto, gr.size - 1);
+            off -= all;
+            k.unit += all;
+        }
         k.piece(A, t0);
     }
 }
@@ -438,8 +494,15 @@ __device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R>& cut)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int bits = 0;
-    const int per = (A.B + NT - 1) / NT;
-    const int b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
+    Group gr = {0, 1, 1u << lane};
+    if constexpr (R >= kTile) {
+        while (gr.size < 32 && static_cast<int64_t>(2 * gr.size) * A.B <= NT) gr.size *= 2;
+        gr.g = lane & (gr.size - 1);
+        gr.mask = (gr.size == 32 ? 0xffffffffu : (1u << gr.size) - 1) << (lane - gr.g);
+    }
+    const int groups = NT / gr.size;
+    const int per = (A.B + groups - 1) / groups;
+    const int b0 = min(tid / gr.size * per, A.B), b1 = min(b0 + per, A.B);
     int mine = 0, per_head = 1;
     Walk<R> k;
     if (tid == 0) cut.walk.n = 0;
@@ -447,8 +510,8 @@ __device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R>& cut)
     for (int b = b1 - 1; b >= b0; --b) {         // downwards: the walk is left at the first one
         k.b = b;
         request_rows(A, b, &k.row0, &k.w, &k.len, &bits);
-        per_head = head_places<R>(A, k.w, k.len);
-        mine += per_head * A.c.heads;
+        per_head = group_places<R>(A, k.w, k.len, gr);
+        mine += gr.g == 0 ? per_head * A.c.heads : 0;
     }
     int upto = mine;
 #pragma unroll
@@ -466,12 +529,16 @@ __device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R>& cut)
     }
     const int total = __shfl_sync(0xffffffffu, sums, NT / 32 - 1);
     const int before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
-    const int from = (warp > 0 ? before : 0) + upto - mine;
+    int from = (warp > 0 ? before : 0) + upto - mine;
     const int run = static_cast<int>((static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x);
     const int t0 = min(static_cast<int>(blockIdx.x) * run, total), t1 = min(t0 + run, total);
+    if constexpr (R >= kTile) {
+        mine = gr.from(mine, 0);
+        from = gr.from(from, 0);
+    }
     if (t0 < t1 && t0 >= from && t0 < from + mine) {
-        find_start<R>(A, k, per_head, t0 - from, t0, t1);
-        cut.walk = k;
+        find_start<R>(A, k, per_head, t0 - from, t0, t1, gr);
+        if (gr.g == 0) cut.walk = k;
     }
     if (blockIdx.x == 0 && bits) raise_status(A.status, bits);
     return run;
@@ -481,12 +548,12 @@ template <int R>
 __device__ __forceinline__ void write_meta(const AttendCall& A, const Workspace& ws, const Walk<R>& k, int run)
 {
     RunMeta m;
-    m.cut = k.n > 0 && k.k0 > k.a;
     m.unit = k.unit;
     m.end = k.end();
+    m.first = k.unit + kUnitCost<R>;
     m.run = run;
     m.row0 = k.row0;
-    m.rows = k.rows(A);
+    m.rows = k.n > 0 && k.k0 > k.a ? k.rows(A) : 0;
     m.flat0 = k.qt * R;
     m.head0 = k.h * A.group;
     ws.meta[blockIdx.x] = m;

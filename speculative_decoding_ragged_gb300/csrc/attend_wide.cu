@@ -3,8 +3,8 @@
 //   S [128 rows, 128 tokens] = (Q_hi + Q_lo) K^T       O [128 rows, D] += (W_hi + W_lo) V
 // the pieces' products adding up in the same columns.
 //
-// A CTA: warps 0-7 do the softmax, two threads per row with half of a tile's tokens each, warp 8
-// loads pages with TMA (one box per page and K or V, swizzled), warp 9 issues the products. As in
+// A CTA: warps 0-3 do the softmax, a thread per row, warp 4 loads pages with TMA (one box per page
+// and K or V, swizzled), warp 5 issues the products. As in
 // the narrow kernel a row's weights are taken over a reference that may lag its maximum: the
 // scores pass through registers once, and only a tile that passes a reference by kLag, or a
 // unit's first, stops to find the maxima and rescale the sums.
@@ -20,14 +20,13 @@ namespace dspark {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kSoft = 256;                   // softmax threads
+constexpr int kSoft = kRows;                 // softmax threads: one per row
 constexpr int kThreads = kSoft + 64;
-constexpr int kHalf = kTile / 2;             // tokens of a softmax thread
 constexpr int kNums = 4;
 // Weights are 2^(x - m + kUp), m lagging by at most kLag: at most 2^8.5 < 448, and a weight keeps
 // two full pieces down to 2^-12 of the largest.
-constexpr float kUp = 4.0f;
-constexpr float kBehind = 4.5f;
+constexpr float kUp = 6.0f;
+constexpr float kBehind = 2.5f;
 
 template <int D>
 struct Smem {
@@ -42,60 +41,59 @@ struct Smem {
     // until the tile's softmax ends: kNums slots cover kSlots / 2 + 1 tiles and the one being written.
     BlockNums nums[kNums][kBlocks];
     float f[kRows];                                      // score factors: scale log2(e) 2^e
-    float2 pair[kRows];                                  // a row's two threads' maxima or sums
-    uint64_t full[kSlots], empty[kSlots], noted[kNums];
+    uint64_t full[kSlots], empty[kSlots];
     uint64_t s_full, s_read, p_full, pv_done, q_full;
     Cut<kRows> cut;
     uint32_t tmem;
     int stalled;       // a wait gave up: every role leaves its loop
 };
 
-// A barrier of `count` softmax threads, which says whether any of them says yes.
-__device__ __forceinline__ bool any_of(int id, int count, bool yes)
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// A barrier of the softmax threads, which says whether any of them says yes.
+__device__ __forceinline__ bool soft_any(bool yes)
 {
     uint32_t r;
     asm volatile(
         "{\n"
         " .reg .pred p, q;\n"
         " setp.ne.u32 p, %1, 0;\n"
-        " barrier.cta.red.or.pred q, %2, %3, p;\n"
+        " barrier.cta.red.or.pred q, 1, 128, p;\n"
         " selp.u32 %0, 1, 0, q;\n"
-        "}\n" : "=r"(r) : "r"(static_cast<uint32_t>(yes)), "r"(id), "r"(count) : "memory");
+        "}\n" : "=r"(r) : "r"(static_cast<uint32_t>(yes)) : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ bool soft_any(bool yes) { return any_of(1, kSoft, yes); }
-// The two warps that share 32 rows, alone.
-__device__ __forceinline__ void pair_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(2 + q) : "memory"); }
-__device__ __forceinline__ bool pair_any(int q, bool yes) { return any_of(2 + q, 64, yes); }
 
 struct Row {
     float f;              // score factor: scale log2(e) 2^e of the row's pieces
     int lo, span;         // sees tokens [lo, lo + span]
     float ref;            // kUp - reference; 0: nothing seen yet
-    float l;              // this thread's part of the row's sum
+    float l;              // the sum
 };
 
-// One tile, this thread's row and 64 of its tokens: scores in TMEM -> weights in shared memory.
+// One tile of this thread's row: scores in TMEM -> weights in shared memory.
 // False once a wait gave up.
 template <int D>
-__device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int row, int half,
+__device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int row,
                                        const BlockNums* nums, int shift_page, int token0, bool mask, bool first, int it,
                                        bool ok, volatile int* stalled)
 {
     const uint32_t s_addr = sm.tmem + lanes;
-    float x[kHalf];
-    tc_ld32(s_addr + half * kHalf, x);
-    tc_ld32(s_addr + half * kHalf + 32, x + 32);
+    float x[kTile];
+#pragma unroll
+    for (int c = 0; c < kTile; c += 32) tc_ld32(s_addr + c, x + c);
+    float2 num[kBlocks];
+#pragma unroll
+    for (int g = 0; g < kBlocks; ++g)
+        num[g] = *reinterpret_cast<const float2*>(&nums[(g * 16) >> shift_page]);
     tc_wait_ld();
     tc_fence_before();
     __syncwarp();
     if (ok && (threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&sm.s_read));
     float top = -INFINITY;
 #pragma unroll
-    for (int g = 0; g < kHalf; g += 16) {
-        const BlockNums n = nums[(half * kHalf + g) >> shift_page];
-        const uint64_t f2 = pack2(r.f * n.ks, r.f * n.ks), a2 = pack2(n.bias + r.ref, n.bias + r.ref);
+    for (int g = 0; g < kTile; g += 16) {
+        const float f = r.f * num[g / 16].x, add = num[g / 16].y + r.ref;
+        const uint64_t f2 = pack2(f, f), a2 = pack2(add, add);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
             const float2 y = unpack2(fma2(pack2(x[g + j], x[g + j + 1]), f2, a2));
@@ -104,31 +102,25 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
         }
     }
     if (mask) {
-        const uint32_t at = static_cast<uint32_t>(token0 + half * kHalf - r.lo), span = static_cast<uint32_t>(r.span);
+        const uint32_t at = static_cast<uint32_t>(token0 - r.lo), span = static_cast<uint32_t>(r.span);
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j)
+        for (int j = 0; j < kTile; ++j)
             if (at + j > span) x[j] = -INFINITY;
     }
     {
         float m[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int j = 4; j < kHalf; ++j) m[j & 3] = fmaxf(m[j & 3], x[j]);
+        for (int j = 4; j < kTile; ++j) m[j & 3] = fmaxf(m[j & 3], x[j]);
         top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     }
-    const int quarter = row / 32;
-    const bool stop = pair_any(quarter, top > kUp + kBehind || r.ref == 0.0f);
+    const bool stop = __any_sync(0xffffffffu, top > kUp + kBehind || r.ref == 0.0f);
     // the last tile's products read the weights' place and write the sums
     if (it > 0) ok = ok && mbar_wait(smem_addr(&sm.pv_done), (it - 1) & 1, stalled);
     ok = __all_sync(0xffffffffu, ok);
     if (stop) {
-        // the row's maximum over the present reference, by both its threads
-        (half ? sm.pair[row].y : sm.pair[row].x) = top;
-        pair_sync(quarter);
-        const float2 both = sm.pair[row];
-        const float over = fmaxf(both.x, both.y);
         float shift = 0.0f, g = 1.0f;
-        if (over > -INFINITY && (r.ref == 0.0f || over > kUp + kBehind)) {
-            float ref = r.ref - over + kUp;
+        if (top > -INFINITY && (r.ref == 0.0f || top > kUp + kBehind)) {
+            float ref = r.ref - top + kUp;
             if (ref == 0.0f) ref = 1e-30f;       // 0 stands for none
             shift = ref - r.ref;
             if (r.ref != 0.0f) {
@@ -138,16 +130,16 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
             r.ref = ref;
         }
 #pragma unroll
-        for (int j = 0; j < kHalf; j += 2) {
+        for (int j = 0; j < kTile; j += 2) {
             const float2 y = unpack2(add2(pack2(x[j], x[j + 1]), pack2(shift, shift)));
             x[j] = y.x;
             x[j + 1] = y.y;
         }
         if (!first && __any_sync(0xffffffffu, g != 1.0f)) {
             tc_fence_after();
-            const uint32_t o_addr = sm.tmem + lanes + kTile + half * (D / 2);
+            const uint32_t o_addr = sm.tmem + lanes + kTile;
 #pragma unroll 1
-            for (int d = 0; d < D / 2; d += 16) {
+            for (int d = 0; d < D; d += 16) {
                 float o[16];
                 tc_ld16(o_addr + d, o);
                 tc_wait_ld();
@@ -160,8 +152,8 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
     }
     // A group's weights, its part of the sum, and the pieces: 16 bytes of each, swizzled.
 #pragma unroll
-    for (int g = 0; g < kHalf; g += 16) {
-        const float inv = nums[(half * kHalf + g) >> shift_page].inv;
+    for (int g = 0; g < kTile; g += 16) {
+        const float inv = nums[(g) >> shift_page].inv;
         float* y = x + g;
         uint32_t p[8];
         uint64_t s2 = 0;
@@ -178,7 +170,7 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
         }
         const float2 s = unpack2(s2);
         r.l = fmaf(s.x + s.y, inv, r.l);
-        const int at = row * kTile + (((half * kHalf + g) / 16) ^ (row & 7)) * 16;
+        const int at = row * kTile + (((g) / 16) ^ (row & 7)) * 16;
         *reinterpret_cast<uint4*>(&sm.w[0][at]) = make_uint4(p[0], p[1], p[2], p[3]);
         *reinterpret_cast<uint4*>(&sm.w[1][at]) = make_uint4(p[4], p[5], p[6], p[7]);
     }
@@ -186,20 +178,19 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
 }
 
 // A unit's queries as two pieces in shared memory, and their rows' factors: eight (four) lanes per
-// row with 16 elements each, a few rows per pass. Rows past the unit's are zeros.
+// row with 16 elements each. Rows past the unit's are zeros. All loads come first.
 template <int D>
 __device__ __forceinline__ void load_queries(const AttendCall& A, Smem<D>& sm, const Walk<kRows>& wk, int rows)
 {
-    constexpr int S = D / 16;
+    constexpr int S = D / 16, kStep = kSoft / S;             // lanes per row, rows per pass
     const int seg = threadIdx.x & (S - 1);
-#pragma unroll 2
-    for (int row = threadIdx.x / S; row < kRows; row += kSoft / S) {
+    const bool vec = ((reinterpret_cast<uintptr_t>(A.q) | static_cast<uintptr_t>(A.q_stride * 2)) & 15u) == 0;
+    auto fetch = [&](int row, uint4* v) {
         const int flat = wk.qt * kRows + min(row, rows - 1);
         const int i = flat / A.group;
         const uint16_t* at = static_cast<const uint16_t*>(A.q) + (wk.row0 + i) * A.q_stride +
                              static_cast<int64_t>(wk.h * A.group + flat - i * A.group) * D + seg * 16;
-        uint4 v[2];
-        if ((reinterpret_cast<uintptr_t>(at) & 15u) == 0) {
+        if (vec) {
             v[0] = reinterpret_cast<const uint4*>(at)[0];
             v[1] = reinterpret_cast<const uint4*>(at)[1];
         } else {
@@ -212,13 +203,16 @@ __device__ __forceinline__ void load_queries(const AttendCall& A, Smem<D>& sm, c
                 (j ? v[1] : v[0]) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
+    };
+    auto place = [&](int row, const uint4* v) {
         uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-        uint32_t top = 0;                        // magnitudes' bits order like them, NaN above all
+        uint32_t top2 = 0;                       // magnitudes' bits order like them, NaN above all
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             if (row >= rows) w[k] = 0;
-            top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+            top2 = __vmaxu2(top2, w[k] & 0x7fff7fffu);
         }
+        uint32_t top = max(top2 & 0xffffu, top2 >> 16);
 #pragma unroll
         for (int off = 1; off < S; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
         const bool fine = top < 0x7f80u;
@@ -226,50 +220,53 @@ __device__ __forceinline__ void load_queries(const AttendCall& A, Smem<D>& sm, c
         const float inv = exp2i(-e);
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float y[4] = {bf16_lo(w[2 * k]) * inv, bf16_hi(w[2 * k]) * inv,
-                                bf16_lo(w[2 * k + 1]) * inv, bf16_hi(w[2 * k + 1]) * inv};
-            float z[4];
-            hi[k] = e4m3x4(y[0], y[1], y[2], y[3]);
-            e4m3x4_to_f32(hi[k], z);
-            lo[k] = e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
+        for (int k = 0; k < 4; ++k) {            // through fp16: it holds a bf16's 8 bits, down to 2^-24
+            uint16_t h0, h1, l0, l1;
+            split2(bf16_lo(w[2 * k]) * inv, bf16_hi(w[2 * k]) * inv, &h0, &l0);
+            split2(bf16_lo(w[2 * k + 1]) * inv, bf16_hi(w[2 * k + 1]) * inv, &h1, &l1);
+            hi[k] = join16(h0, h1);
+            lo[k] = join16(l0, l1);
         }
         const int chunk = seg ^ (D == 128 ? row & 7 : (row >> 1) & 3);
         *reinterpret_cast<uint4*>(&sm.q[0][row * D + chunk * 16]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(&sm.q[1][row * D + chunk * 16]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         // a query that is not finite makes its row's factor, hence its results, NaN
         if (seg == 0) sm.f[row] = fine ? A.scale * kLog2e * exp2i(e) : __int_as_float(0x7fc00000);
-    }
+    };
+    constexpr int kPasses = kRows / kStep;
+    uint4 v[kPasses][2];
+    const int row = threadIdx.x / S;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) fetch(row + i * kStep, v[i]);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) place(row + i * kStep, v[i]);
 }
 
-// A finished piece: results or a part written, half of a row's elements by each of its threads.
+// A finished piece: results or a part written.
 template <int D>
 __device__ __forceinline__ void finish(const AttendCall& A, Smem<D>& sm, const Row& r, uint32_t lanes, int row,
-                                       int half, const Walk<kRows>& wk, int rows, bool whole, int part,
+                                       const Walk<kRows>& wk, int rows, bool whole, int part,
                                        const Workspace& ws)
 {
-    (half ? sm.pair[row].y : sm.pair[row].x) = r.l;
-    pair_sync(row / 32);
-    const float2 both = sm.pair[row];
-    const float l = both.x + both.y, m = -r.ref;             // reference - kUp, as the weights are
+    const float l = r.l;
+    const float m = -r.ref;             // reference - kUp, as the weights are
     const float g = !whole ? 1.0f : l == 0.0f ? 0.0f : __fdividef(1.0f, l);      // nothing seen: zeros
     const bool live = row < rows;
     const int flat = wk.qt * kRows + min(row, rows - 1);
     const int64_t prow = wk.row0 + flat / A.group;
     const int head = wk.h * A.group + flat % A.group;
-    if (live && half == 0) {
+    if (live) {
         if (!whole)
             ws.ml[part * kTile + row] = make_float2(l == 0.0f ? kNone : m, l);
         else if (A.lse != nullptr)
             A.lse[prow * A.q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
-    const int d0 = half * (D / 2);
-    uint16_t* out = static_cast<uint16_t*>(A.out) + prow * A.out_stride + static_cast<int64_t>(head) * D + d0;
-    float* po = ws.o + (static_cast<int64_t>(part) * kTile + row) * D + d0;
+    uint16_t* out = static_cast<uint16_t*>(A.out) + prow * A.out_stride + static_cast<int64_t>(head) * D;
+    float* po = ws.o + (static_cast<int64_t>(part) * kTile + row) * D;
     const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-    const uint32_t o_addr = sm.tmem + lanes + kTile + d0;
+    const uint32_t o_addr = sm.tmem + lanes + kTile;
 #pragma unroll 1
-    for (int d = 0; d < D / 2; d += 16) {
+    for (int d = 0; d < D; d += 16) {
         float o[16];
         tc_ld16(o_addr + d, o);
         tc_wait_ld();
@@ -308,8 +305,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
             mbar_init(smem_addr(&sm.full[s]), 1);
             mbar_init(smem_addr(&sm.empty[s]), 1);
         }
-        for (int s = 0; s < kNums; ++s) mbar_init(smem_addr(&sm.noted[s]), 1);
-        mbar_init(smem_addr(&sm.s_full), 1);
+        mbar_init(smem_addr(&sm.s_full), 2);
         mbar_init(smem_addr(&sm.s_read), kSoft / 32);
         mbar_init(smem_addr(&sm.p_full), kSoft / 32);
         mbar_init(smem_addr(&sm.pv_done), 1);
@@ -399,10 +395,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                             sm.nums[it % kNums][lane] = n;
                         }
                         __syncwarp();
-                        if (lane == 0) {
-                            if (kv == 0) mbar_arrive(smem_addr(&sm.noted[it % kNums]));
-                            mbar_arrive_expect_tx(full, count * box);
-                        }
+                        if (lane == 0) mbar_arrive_expect_tx(full, count * box);
                         __syncwarp();
                         if (there)
                             tma_load(smem_addr(sm.ring[s]) + lane * box, kv ? &v_map : &k_map, row, full);
@@ -454,6 +447,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                                 for (int i = 0; i < D / 32; ++i)
                                     mma_ss(s_addr, q_op + p * kStep + 2 * i, kb + 2 * i, kIdescQK, p > 0 || i > 0);
                             tc_commit(smem_addr(&sm.s_full));
+                            mbar_arrive(smem_addr(&sm.s_full));      // hands on the tile's numbers too
                             tc_commit(smem_addr(&sm.empty[s]));
                         }
                         __syncwarp();
@@ -491,7 +485,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
         } else {
             // ---- softmax ----
             const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-            const int row = tid & (kRows - 1), half = tid / kRows;
+            const int row = tid;
             const int shift_page = __ffs(A.c.page) - 1;      // a power of two
             int it = 0, piece = 0;
             bool ok = true;
@@ -519,21 +513,20 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
 #pragma unroll 1
                 for (int k = 0; k < wk.n; ++k, ++it) {
                     const int token0 = (wk.k0 + k) * kTile;
-                    ok = ok && mbar_wait(smem_addr(&sm.noted[it % kNums]), (it / kNums) & 1, stalled) &&
-                         mbar_wait(smem_addr(&sm.s_full), it & 1, stalled);
+                    ok = ok && mbar_wait(smem_addr(&sm.s_full), it & 1, stalled);
                     ok = __all_sync(0xffffffffu, ok);
                     tc_fence_after();
                     const bool mask = token0 + kTile - 1 > p0 || token0 < lo1;
-                    ok = soften<D>(sm, r, lanes, row, half, sm.nums[it % kNums], shift_page, token0, mask, k == 0,
+                    ok = soften<D>(sm, r, lanes, row, sm.nums[it % kNums], shift_page, token0, mask, k == 0,
                                    it, ok, stalled);
                     if (token0 + kTile > stored) {      // slots past the last token: 0 x NaN is NaN
                         const int use = 2 * it + 1, s = use % kSlots;
                         ok = ok && mbar_wait(smem_addr(&sm.full[s]), (use / kSlots) & 1, stalled);
                         ok = __all_sync(0xffffffffu, ok);
                         if (token0 + row >= stored) {
-                            uint4* v = reinterpret_cast<uint4*>(&sm.ring[s][row * D + half * (D / 2)]);
+                            uint4* v = reinterpret_cast<uint4*>(&sm.ring[s][row * D]);
 #pragma unroll
-                            for (int c = 0; c < D / 32; ++c) v[c] = make_uint4(0, 0, 0, 0);
+                            for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
                         }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -544,7 +537,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done), (it - 1) & 1, stalled));
                 if (soft_any(!ok)) break;
                 tc_fence_after();
-                finish<D>(A, sm, r, lanes, row, half, wk, rows, wk.whole(), blockIdx.x * 2 + (piece > 0), ws);
+                finish<D>(A, sm, r, lanes, row, wk, rows, wk.whole(), blockIdx.x * 2 + (piece > 0), ws);
                 tc_fence_before();
                 ++piece;
             } while (next_piece());
