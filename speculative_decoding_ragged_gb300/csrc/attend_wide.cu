@@ -44,6 +44,14 @@ struct Smem {
     uint64_t full[kSlots], empty[kSlots];
     uint64_t s_full, s_read, p_full, pv_done, q_full;
     Cut<kRows> cut;
+    // The softmax threads' piece: here rather than in registers, which the scores need.
+    Walk<kRows> soft;
+    struct {
+        int k0, n;         // its tiles
+        int lo, hi;        // tokens from lo to hi are seen by all its rows
+    } span;
+    int stored;            // the request's tokens
+    int2 sees[kRows];      // a row sees tokens [x, x + y]
     uint32_t tmem;
     int stalled;       // a wait gave up: every role leaves its loop
 };
@@ -65,7 +73,6 @@ __device__ __forceinline__ bool soft_any(bool yes)
 
 struct Row {
     float f;              // score factor: scale log2(e) 2^e of the row's pieces
-    int lo, span;         // sees tokens [lo, lo + span]
     float ref;            // kUp - reference; 0: nothing seen yet
     float l;              // the sum
 };
@@ -74,8 +81,8 @@ struct Row {
 // False once a wait gave up.
 template <int D>
 __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int row,
-                                       const BlockNums* nums, int shift_page, int token0, bool mask, bool first, int it,
-                                       bool ok, volatile int* stalled)
+                                       const BlockNums* nums, int shift_page, int k, int it, bool ok,
+                                        volatile int* stalled)
 {
     const uint32_t s_addr = sm.tmem + lanes;
     float x[kTile];
@@ -101,8 +108,10 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
             x[g + j + 1] = y.y;
         }
     }
-    if (mask) {
-        const uint32_t at = static_cast<uint32_t>(token0 - r.lo), span = static_cast<uint32_t>(r.span);
+    const int token0 = (sm.span.k0 + k) * kTile;
+    if (token0 + kTile - 1 > sm.span.hi || token0 < sm.span.lo) {
+        const int2 sees = sm.sees[row];
+        const uint32_t at = static_cast<uint32_t>(token0 - sees.x), span = static_cast<uint32_t>(sees.y);
 #pragma unroll
         for (int j = 0; j < kTile; ++j)
             if (at + j > span) x[j] = -INFINITY;
@@ -135,7 +144,7 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
             x[j] = y.x;
             x[j + 1] = y.y;
         }
-        if (!first && __any_sync(0xffffffffu, g != 1.0f)) {
+        if (k > 0 && __any_sync(0xffffffffu, g != 1.0f)) {
             tc_fence_after();
             const uint32_t o_addr = sm.tmem + lanes + kTile;
 #pragma unroll 1
@@ -244,10 +253,11 @@ __device__ __forceinline__ void load_queries(const AttendCall& A, Smem<D>& sm, c
 
 // A finished piece: results or a part written.
 template <int D>
-__device__ __forceinline__ void finish(const AttendCall& A, Smem<D>& sm, const Row& r, uint32_t lanes, int row,
-                                       const Walk<kRows>& wk, int rows, bool whole, int part,
-                                       const Workspace& ws)
+__device__ __forceinline__ void finish(const AttendCall& A, const Row& r, uint32_t o_addr, int row,
+                                       const Walk<kRows>& wk, int part, const Workspace& ws)
 {
+    const int rows = wk.rows(A);
+    const bool whole = wk.whole();
     const float l = r.l;
     const float m = -r.ref;             // reference - kUp, as the weights are
     const float g = !whole ? 1.0f : l == 0.0f ? 0.0f : __fdividef(1.0f, l);      // nothing seen: zeros
@@ -264,7 +274,6 @@ __device__ __forceinline__ void finish(const AttendCall& A, Smem<D>& sm, const R
     uint16_t* out = static_cast<uint16_t*>(A.out) + prow * A.out_stride + static_cast<int64_t>(head) * D;
     float* po = ws.o + (static_cast<int64_t>(part) * kTile + row) * D;
     const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-    const uint32_t o_addr = sm.tmem + lanes + kTile;
 #pragma unroll 1
     for (int d = 0; d < D; d += 16) {
         float o[16];
@@ -488,42 +497,45 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
             const int row = tid;
             const int shift_page = __ffs(A.c.page) - 1;      // a power of two
             int it = 0, piece = 0;
-            bool ok = true;
-            do {
-                const int rows = wk.rows(A);
-                load_queries<D>(A, sm, wk, rows);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(smem_addr(&sm.q_full));
+            bool ok = true, more = true;
+            if (tid == 0) sm.soft = wk;
+            while (more) {
                 soft_sync();
-                const int i = (wk.qt * kRows + min(row, rows - 1)) / A.group;
-                const int pos = wk.len + i;
-                Row r;
-                r.f = sm.f[row];
-                r.lo = A.window > 0 && pos >= A.window ? pos - A.window + 1 : 0;
-                r.span = pos - r.lo;
-                r.ref = 0.0f;
-                r.l = 0.0f;
-                // tiles that every row sees whole need no mask: those within [hi lo, lo pos]
-                const int p0 = wk.len + wk.qt * kRows / A.group;
-                const int p1 = wk.len + (wk.qt * kRows + rows - 1) / A.group;
-                const int lo1 = A.window > 0 && p1 >= A.window ? p1 - A.window + 1 : 0;
-                const int stored = wk.len + wk.w;
+                {
+                    const Walk<kRows> now = sm.soft;
+                    const int rows = now.rows(A);
+                    load_queries<D>(A, sm, now, rows);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(smem_addr(&sm.q_full));
+                    const int pos = now.len + (now.qt * kRows + min(row, rows - 1)) / A.group;
+                    const int lo = A.window > 0 && pos >= A.window ? pos - A.window + 1 : 0;
+                    sm.sees[row] = make_int2(lo, pos - lo);
+                    // tiles that every row sees whole need no mask: those within [hi lo, lo pos]
+                    if (tid == 0) {
+                        const int p0 = now.len + now.qt * kRows / A.group;
+                        const int p1 = now.len + (now.qt * kRows + rows - 1) / A.group;
+                        const int lo1 = A.window > 0 && p1 >= A.window ? p1 - A.window + 1 : 0;
+                        sm.span = {now.k0, now.n, lo1, p0};
+                        sm.stored = now.len + now.w;
+                    }
+                }
+                soft_sync();
+                Row r = {sm.f[row], 0.0f, 0.0f};
+                const int n = sm.span.n;
                 // a warp whose wait gave up goes on to the piece's end, where the warps agree on it:
                 // they share the barriers within
 #pragma unroll 1
-                for (int k = 0; k < wk.n; ++k, ++it) {
-                    const int token0 = (wk.k0 + k) * kTile;
+                for (int k = 0; k < n; ++k, ++it) {
                     ok = ok && mbar_wait(smem_addr(&sm.s_full), it & 1, stalled);
                     ok = __all_sync(0xffffffffu, ok);
                     tc_fence_after();
-                    const bool mask = token0 + kTile - 1 > p0 || token0 < lo1;
-                    ok = soften<D>(sm, r, lanes, row, sm.nums[it % kNums], shift_page, token0, mask, k == 0,
-                                   it, ok, stalled);
-                    if (token0 + kTile > stored) {      // slots past the last token: 0 x NaN is NaN
+                    ok = soften<D>(sm, r, lanes, row, sm.nums[it % kNums], shift_page, k, it, ok, stalled);
+                    const int token0 = (sm.span.k0 + k) * kTile;
+                    if (token0 + kTile > sm.stored) {   // slots past the last token: 0 x NaN is NaN
                         const int use = 2 * it + 1, s = use % kSlots;
                         ok = ok && mbar_wait(smem_addr(&sm.full[s]), (use / kSlots) & 1, stalled);
                         ok = __all_sync(0xffffffffu, ok);
-                        if (token0 + row >= stored) {
+                        if (token0 + row >= sm.stored) {
                             uint4* v = reinterpret_cast<uint4*>(&sm.ring[s][row * D]);
 #pragma unroll
                             for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
@@ -535,12 +547,19 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                     if (ok && (tid & 31) == 0) mbar_arrive(smem_addr(&sm.p_full));
                 }
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done), (it - 1) & 1, stalled));
+                const Walk<kRows> now = sm.soft;
+                more = !now.last();
                 if (soft_any(!ok)) break;
+                if (tid == 0 && more) {
+                    Walk<kRows> next = now;
+                    next.next(A);
+                    sm.soft = next;
+                }
                 tc_fence_after();
-                finish<D>(A, sm, r, lanes, row, wk, rows, wk.whole(), blockIdx.x * 2 + (piece > 0), ws);
+                finish<D>(A, r, sm.tmem + lanes + kTile, row, now, blockIdx.x * 2 + (piece > 0), ws);
                 tc_fence_before();
                 ++piece;
-            } while (next_piece());
+            }
         }
     }
     tc_fence_before();
