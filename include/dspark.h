@@ -51,7 +51,8 @@
  *     the documented clamp and carries on. The caller zeroes `status` when it wants a fresh
  *     report and reads it whenever convenient.
  *   - No kernel waits on another kernel or a peer. The only waits are inside one CTA (the
- *     bulk-copy verify kernel's shared-memory stages); each is bounded, and one that gives up
+ *     shared-memory stages of the bulk-copy verify kernel and of dspark_attend); each is
+ *     bounded, and one that gives up
  *     sets DSPARK_STATUS_STALL instead of hanging.
  */
 #ifndef DSPARK_H_
@@ -488,7 +489,8 @@ int dspark_rotate(const void* x, int64_t x_stride, void* y, int64_t y_stride, ds
  * A request or position out of range (row_req >= B, row_pos < 0) flags DSPARK_STATUS_BAD_ROWS, a
  * length that is negative or passes int32 DSPARK_STATUS_BAD_LENGTH, a page id outside
  * [0, n_pages) or a block >= width DSPARK_STATUS_BAD_PAGE; those rows are not stored.
- * One kernel; a block belongs to one CTA: no atomics, the same bits every time.
+ * One kernel, or (more than 4096 rows, with queries) two side by side; a block belongs to one team
+ * of warps: no atomics, the same bits every time.
  * ------------------------------------------------------------------------------------- */
 typedef struct {
     void*          k;
@@ -528,6 +530,8 @@ int dspark_append(const dspark_cache* cache, const dspark_rope* rope, const void
  * lse [rows, q_heads] fp32 or NULL; status as everywhere. q_heads is a multiple of heads.
  * workspace: at least dspark_attend_workspace_bytes(heads, dim) bytes of device scratch, 16-byte
  * aligned, no clearing needed, rewritten by every call; calls that share it must not overlap.
+ * Where (rows * q_heads / 8 + B * heads) * (width * page / 128 + 10) passes 2^30 a call may be
+ * refused with DSPARK_ERR_UNSUPPORTED: split its rows.
  *
  * Precision: bf16 with dim 64 or 128 runs on the tensor cores, q as two e4m3 pieces (its eight
  * mantissa bits exactly, down to 2^-17 of a row's largest element), the softmax weights as two
