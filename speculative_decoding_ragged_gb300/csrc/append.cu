@@ -508,7 +508,7 @@ int launch_append(const dspark_cache& cache, const Rope& rope, const void* k, in
     const int e = bf ? 2 : 4;
     const bool qvec = rotate_vec(rope, q, qs, q_out, os, cache.dim, e);
     const bool vec = vector_rows(rope, k, ks, cache.dim, e) && vector_rows(rope, v, vs, cache.dim, e);
-    A.q = turns_of(rope, q, qs, q_out, os, q != nullptr ? q_heads : 1, cache.dim, qvec, A.q_rows);
+    A.q = turns_of(rope, q, qs, q_out, os, q != nullptr ? q_heads : 1, cache.dim, qvec, e, A.q_rows);
     if (prompts) {
         auto kv = bf ? (vec ? append_prompt_kernel<DSPARK_BF16, true> : append_prompt_kernel<DSPARK_BF16, false>)
                      : (vec ? append_prompt_kernel<DSPARK_F32, true> : append_prompt_kernel<DSPARK_F32, false>);

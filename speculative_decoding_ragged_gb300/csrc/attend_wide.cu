@@ -287,8 +287,8 @@ __device__ __forceinline__ void finish(const AttendCall& A, const Row& r, uint32
             for (int j = 0; j < 16; j += 4)
                 *reinterpret_cast<float4*>(po + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         } else if (vec) {
-            store8<DSPARK_BF16>(out + d, o);
-            store8<DSPARK_BF16>(out + d + 8, o + 8);
+            *reinterpret_cast<uint4*>(out + d) = store16<DSPARK_BF16>(o);
+            *reinterpret_cast<uint4*>(out + d + 8) = store16<DSPARK_BF16>(o + 8);
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) store1<DSPARK_BF16>(out, d + j, o[j]);

@@ -49,21 +49,6 @@ __device__ __forceinline__ float2 rope_turn(float a, float b, float2 f)
     return make_float2(a * f.x - b * f.y, b * f.x + a * f.y);
 }
 
-// Eight elements of type DT at p (16-byte aligned) as fp32, and back.
-template <int DT>
-__device__ __forceinline__ void load8(const void* p, float* x)
-{
-    if (DT == DSPARK_BF16) {
-        const uint4 v = *static_cast<const uint4*>(p);
-        x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
-        x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
-    } else {
-        const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
-}
-
 // Two fp32 as packed bf16, rounded to nearest even; `lo` in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
@@ -72,16 +57,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
+// 16 bytes: eight bf16 or four fp32.
 template <int DT>
-__device__ __forceinline__ void store8(void* p, const float* x)
+__device__ __forceinline__ void load16(const uint4& v, float* x)
 {
     if (DT == DSPARK_BF16) {
-        *static_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                             pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
+        x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
     } else {
-        static_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        static_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
     }
+}
+template <int DT>
+__device__ __forceinline__ uint4 store16(const float* x)
+{
+    if (DT == DSPARK_BF16)
+        return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
 template <int DT>
@@ -123,9 +116,10 @@ inline Divider divider(int64_t d, int64_t most)
     return r;
 }
 
-// How a rotation cuts its rows: units of eight pairs (VEC: 16-byte accesses; dim, half and the
-// strides multiples of 8, bases 16-byte aligned), a unit past the rotated part being 16 copied
-// elements; else one pair, or two copied elements, at a time.
+// How a rotation cuts its rows: units of two 16-byte accesses (VEC: eight pairs of bf16, four of
+// fp32, so that a warp's accesses lie side by side; with eight of fp32 the gradient of 4999 rows
+// took 22.0 us; dim, half and the strides multiples of 8, bases 16-byte aligned), a unit past the
+// rotated part being as many copied elements; else one pair, or two copied elements, at a time.
 struct Turns {
     Rope r;
     RowsIn x;
@@ -135,9 +129,9 @@ struct Turns {
     Divider units, per_row;    // units of a head, of a row
 };
 inline Turns turns_of(const Rope& r, const void* x, int64_t xs, void* y, int64_t ys, int heads, int dim,
-                      bool vec, int rows_per_cta)
+                      bool vec, int elem, int rows_per_cta)
 {
-    const int P = vec ? 8 : 1;
+    const int P = vec ? 16 / elem : 1;
     const bool copy = !(x == y && xs == ys);       // in place the rest stays where it is
     Turns t;
     t.r = r;
@@ -155,68 +149,59 @@ inline Turns turns_of(const Rope& r, const void* x, int64_t xs, void* y, int64_t
 // A vector unit: where it is, and its elements as loaded.
 template <int DT>
 struct TurnUnit {
-    static constexpr int Q = DT == DSPARK_BF16 ? 1 : 2;     // 16-byte loads per eight elements
-    uint4 v[2 * Q];
+    static constexpr int E = DT == DSPARK_BF16 ? 2 : 4, N = 16 / E;     // elements of an access
+    uint4 v[2];
     int64_t y;
-    int a, b, f;             // offsets of the two eights in the head; first factor, or -1: copied
+    int a, b, f;             // offsets of the two accesses in the head; first factor, or -1: copied
     __device__ __forceinline__ void load(const Turns& t, int64_t row0, int u)
     {
-        constexpr int E = DT == DSPARK_BF16 ? 2 : 4;
         const int k = t.per_row(u), in_row = u - k * static_cast<int>(t.per_row.d);
         const int h = t.units(in_row), o = in_row - h * static_cast<int>(t.units.d);
         const int64_t head = static_cast<int64_t>(h) * t.dim;
         if (o < t.rot_units) {
-            a = t.r.interleaved ? o * 16 : o * 8;
-            b = t.r.interleaved ? a + 8 : t.r.half + o * 8;
-            f = k * t.r.half + o * 8;
+            a = t.r.interleaved ? o * 2 * N : o * N;
+            b = t.r.interleaved ? a + N : t.r.half + o * N;
+            f = k * t.r.half + o * N;
         } else {
-            a = 2 * t.r.half + (o - t.rot_units) * 16;
-            b = a + 8;
+            a = 2 * t.r.half + (o - t.rot_units) * 2 * N;
+            b = a + N;
             f = -1 - k;
         }
         y = (row0 + k) * t.y.row_stride + head;
         const char* x = static_cast<const char*>(t.x.base) + ((row0 + k) * t.x.row_stride + head) * E;
-#pragma unroll
-        for (int i = 0; i < Q; ++i) {
-            v[i] = *reinterpret_cast<const uint4*>(x + a * E + i * 16);
-            v[Q + i] = *reinterpret_cast<const uint4*>(x + b * E + i * 16);
-        }
+        v[0] = *reinterpret_cast<const uint4*>(x + a * E);
+        v[1] = *reinterpret_cast<const uint4*>(x + b * E);
     }
     // live: one flag per row (NULL: all), negative: leave the row alone
     __device__ __forceinline__ void turn(const Turns& t, const float2* tab, const int* live)
     {
-        constexpr int E = DT == DSPARK_BF16 ? 2 : 4;
         if (live != nullptr && live[f >= 0 ? f / t.r.half : -1 - f] < 0) return;
         char* out = static_cast<char*>(t.y.base) + y * E;
         if (f >= 0) {
-            float p[8], q[8];
-            load8<DT>(v, p);
-            load8<DT>(v + Q, q);
+            float x[2 * N];
+            load16<DT>(v[0], x);
+            load16<DT>(v[1], x + N);
             const float4* c = reinterpret_cast<const float4*>(tab + f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 g = c[j];               // factors 2j and 2j + 1
+            for (int j = 0; j < N; j += 2) {
+                const float4 g = c[j / 2];           // factors j and j + 1
                 if (t.r.interleaved) {
-                    float* z = j < 2 ? p + 4 * j : q + 4 * j - 8;
+                    float* z = x + 2 * j;
                     const float2 s = rope_turn(z[0], z[1], make_float2(g.x, g.y));
                     const float2 w = rope_turn(z[2], z[3], make_float2(g.z, g.w));
                     z[0] = s.x; z[1] = s.y; z[2] = w.x; z[3] = w.y;
                 } else {
-                    const float2 s = rope_turn(p[2 * j], q[2 * j], make_float2(g.x, g.y));
-                    const float2 w = rope_turn(p[2 * j + 1], q[2 * j + 1], make_float2(g.z, g.w));
-                    p[2 * j] = s.x; q[2 * j] = s.y;
-                    p[2 * j + 1] = w.x; q[2 * j + 1] = w.y;
+                    const float2 s = rope_turn(x[j], x[N + j], make_float2(g.x, g.y));
+                    const float2 w = rope_turn(x[j + 1], x[N + j + 1], make_float2(g.z, g.w));
+                    x[j] = s.x; x[N + j] = s.y;
+                    x[j + 1] = w.x; x[N + j + 1] = w.y;
                 }
             }
-            store8<DT>(out + a * E, p);
-            store8<DT>(out + b * E, q);
-        } else {
-#pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                *reinterpret_cast<uint4*>(out + a * E + i * 16) = v[i];
-                *reinterpret_cast<uint4*>(out + b * E + i * 16) = v[Q + i];
-            }
+            v[0] = store16<DT>(x);
+            v[1] = store16<DT>(x + N);
         }
+        *reinterpret_cast<uint4*>(out + a * E) = v[0];
+        *reinterpret_cast<uint4*>(out + b * E) = v[1];
     }
 };
 

@@ -5,7 +5,7 @@
 // a rotation's transpose is the rotation back. Bound by memory: 2 e bytes and 3 flops per
 // element. A CTA takes a few rows, computes their factors once in shared memory (one sincospif
 // per pair and row, shared by all heads: 40 heads would otherwise spend 40 of them) and then
-// streams the rows' heads in units of eight pairs (16-byte accesses).
+// streams the rows' heads, two 16-byte accesses a thread at a time.
 #include <cmath>
 
 #include "rope.cuh"
@@ -13,7 +13,7 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;   // 8192 rows of 40 heads: 31.3 us; 32.6 with 256, 37.9 with 512 and more rows each
 constexpr int kTable = 512;        // shared factors: at least one row's, at most kTable entries
 
 template <int DT, bool VEC>
@@ -45,7 +45,7 @@ int launch_rotate(const Rope& r, const void* x, int64_t xs, void* y, int64_t ys,
         per_cta = kThreads / r.half;
         per_cta = per_cta < 1 ? 1 : per_cta > 4 ? 4 : per_cta;
     }
-    const Turns t = turns_of(r, x, xs, y, ys, heads, dim, vec, per_cta);
+    const Turns t = turns_of(r, x, xs, y, ys, heads, dim, vec, bf ? 2 : 4, per_cta);
     const dim3 grid(static_cast<unsigned>(ceil_div(rows, per_cta)));
     auto kernel = bf ? (vec ? rotate_kernel<DSPARK_BF16, true> : rotate_kernel<DSPARK_BF16, false>)
                      : (vec ? rotate_kernel<DSPARK_F32, true> : rotate_kernel<DSPARK_F32, false>);
