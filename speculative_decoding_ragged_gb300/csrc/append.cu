@@ -20,13 +20,15 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 256;      // of a step's CTA, and of one that rotates queries
+constexpr int kThreads = 256;      // of a step's CTA
 constexpr int kWarps = kThreads / 32;
 constexpr int kTeam = 4;           // warps that take a prompt's block together
 constexpr int kPromptWarps = 8;    // of a CTA: two heads' blocks side by side
+constexpr int kGroups = 2;         // heads of keys that a prompt's team takes in turn
 constexpr int kTable = 4096;       // shared rope factors (32 KB): 64 rows of 64 pairs
 constexpr int keep_of(int T) { return T > 1 ? 8 : 4; }     // units of a lane that stay in registers
 constexpr int kQueryRows = 4;      // most rows of a CTA that rotates queries
+constexpr int kQueryThreads = 128; // of a prompts' CTA that rotates queries
 constexpr int kQueryFactors = 512; // their factors
 
 struct AppendArgs {
@@ -40,6 +42,7 @@ struct AppendArgs {
     int rows, B;
     int kv_ctas;          // first of the grid: (rows, eight blocks)
     int per_row;          // of them for the same rows
+    int key_shares;       // of a prompt's: those with keys
     int chunk;            // rows a kv CTA looks for leaders in
     int q_rows;           // rows a query CTA rotates
     int32_t* status;
@@ -236,10 +239,10 @@ __device__ __forceinline__ int row_owner(const AppendArgs& A, int64_t r, int* po
 
 // The blocks that packed row r (request b's row i0, at position pos) leads. T = 1: eight of them
 // from hv0 (head, K or V), one per warp; T = 4: the keys' or the values' of two heads from hv0.
-// Returns status bits.
+// again: the factors are those of the call before. Returns status bits.
 template <int DT, bool VEC, int T>
 __device__ __forceinline__ int append_blocks(const AppendArgs& A, int64_t r, int b, int i0, int pos, int hv0,
-                                             float2* tab, float* reds)
+                                             bool again, float2* tab, float* reds)
 {
     constexpr int kKeep = keep_of(T), kAll = T > 1 ? 32 * kPromptWarps : kThreads;
     const dspark_cache& c = A.c;
@@ -295,7 +298,7 @@ __device__ __forceinline__ int append_blocks(const AppendArgs& A, int64_t r, int
         __syncthreads();
     };
     const bool keep = n <= kKeep * step && n <= rows_at_once && units <= 32;
-    if (keep && half > 0) factors(0, n);
+    if (keep && half > 0 && !again) factors(0, n);
     const int64_t bh = static_cast<int64_t>(page) * c.heads + h;
     uint8_t* codes = static_cast<uint8_t*>(value ? c.v : c.k) + bh * c.page * c.dim;
     float* scale = (value ? c.v_scale : c.k_scale) + bh;
@@ -385,7 +388,10 @@ __device__ __forceinline__ int append_rows(const AppendArgs& A, float2* tab, flo
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / A.per_row) * A.chunk;
     const int share = blockIdx.x % A.per_row;
     constexpr int kTeams = kPromptWarps / kTeam;
-    const int hv0 = T > 1 ? 2 * (share >> 1) * kTeams + (share & 1) : share * kWarps;
+    // a prompt's CTA of keys takes kGroups times its teams' heads, one after the other: the factors
+    // are theirs all; the values have none
+    const bool value = share >= A.key_shares;
+    const int head0 = value ? (share - A.key_shares) * kTeams : share * kTeams * kGroups;
     // each warp looks at the rows side by side; those that lead a block are the same for all
     const int lane = threadIdx.x & 31;
     int bits = 0;
@@ -402,9 +408,17 @@ __device__ __forceinline__ int append_rows(const AppendArgs& A, float2* tab, flo
         while (leads != 0) {
             const int k = __ffs(leads) - 1;
             leads &= leads - 1;
-            bits |= append_blocks<DT, VEC, T>(A, row0 + from + k, __shfl_sync(0xffffffffu, b, k),
-                                              __shfl_sync(0xffffffffu, i, k), __shfl_sync(0xffffffffu, pos, k),
-                                              hv0, tab, red);
+            const int bk = __shfl_sync(0xffffffffu, b, k), ik = __shfl_sync(0xffffffffu, i, k);
+            const int pk = __shfl_sync(0xffffffffu, pos, k);
+            if (T == 1) {
+                bits |= append_blocks<DT, VEC, T>(A, row0 + from + k, bk, ik, pk, share * kWarps, false, tab, red);
+                continue;
+            }
+#pragma unroll 1
+            for (int g = 0; g < (value ? 1 : kGroups); ++g)
+                if (head0 + g * kTeams < A.c.heads)
+                    bits |= append_blocks<DT, VEC, T>(A, row0 + from + k, bk, ik, pk,
+                                                      2 * (head0 + g * kTeams) + value, g > 0, tab, red);
         }
     }
     return bits;
@@ -420,7 +434,7 @@ __device__ __forceinline__ int rotate_queries(const AppendArgs& A, int block, fl
     rotate_rows<DT, QVEC>(A.q, tab, row0, n, own, [&]() {
         if (threadIdx.x < n) own[threadIdx.x] = row_owner(A, row0 + threadIdx.x, &at[threadIdx.x], &bits);
         __syncthreads();
-        for (int i = threadIdx.x; i < n * A.rope.half; i += kThreads) {
+        for (int i = threadIdx.x; i < n * A.rope.half; i += blockDim.x) {
             const int k = i / A.rope.half;
             if (own[k] >= 0) tab[i] = rope_factor(A.rope, A.rope.turns[i - k * A.rope.half], at[k]);
         }
@@ -459,7 +473,7 @@ __global__ void __launch_bounds__(32 * kPromptWarps, 2) append_prompt_kernel(App
 // dependents, that is after everything before the call is done, touches nothing that one writes,
 // and waits for it at its own end, so that what follows on the stream waits for both.
 template <int DT, bool QVEC>
-__global__ void __launch_bounds__(kThreads) append_query_kernel(AppendArgs A)
+__global__ void __launch_bounds__(kQueryThreads) append_query_kernel(AppendArgs A)
 {
     __shared__ __align__(16) float2 tab[kQueryFactors];
     __shared__ int32_t own[kQueryRows], at[kQueryRows];
@@ -501,7 +515,9 @@ int launch_append(const dspark_cache& cache, const Rope& rope, const void* k, in
     const bool prompts = rows > 4096;
     A.chunk = prompts ? cache.page : rows <= 512 ? 1 : 4;
     A.q_rows = rows >= 152 * 8 && rope.half > 0 ? (rope.half <= 64 ? 4 : 2) : 1;
-    A.per_row = static_cast<int>(prompts ? 2 * ceil_div(cache.heads, kPromptWarps / kTeam) : ceil_div(2 * cache.heads, kWarps));
+    A.key_shares = static_cast<int>(ceil_div(cache.heads, kPromptWarps / kTeam * kGroups));
+    A.per_row = static_cast<int>(prompts ? A.key_shares + ceil_div(cache.heads, kPromptWarps / kTeam)
+                                         : ceil_div(2 * cache.heads, kWarps));
     A.kv_ctas = static_cast<int>(ceil_div(rows, A.chunk)) * A.per_row;
     const int q_ctas = q != nullptr ? static_cast<int>(ceil_div(rows, A.q_rows)) : 0;
     const bool bf = dtype == DSPARK_BF16;
@@ -516,7 +532,7 @@ int launch_append(const dspark_cache& cache, const Rope& rope, const void* k, in
         if (rc != DSPARK_OK || q == nullptr) return rc;
         auto turn = bf ? (qvec ? append_query_kernel<DSPARK_BF16, true> : append_query_kernel<DSPARK_BF16, false>)
                        : (qvec ? append_query_kernel<DSPARK_F32, true> : append_query_kernel<DSPARK_F32, false>);
-        return launch_pdl("append queries", turn, dim3(static_cast<unsigned>(q_ctas)), dim3(kThreads), 0, stream, A);
+        return launch_pdl("append queries", turn, dim3(static_cast<unsigned>(q_ctas)), dim3(kQueryThreads), 0, stream, A);
     }
     auto kernel = bf ? (vec ? (qvec ? append_kernel<DSPARK_BF16, true, true> : append_kernel<DSPARK_BF16, true, false>)
                             : (qvec ? append_kernel<DSPARK_BF16, false, true> : append_kernel<DSPARK_BF16, false, false>))
