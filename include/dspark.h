@@ -489,7 +489,7 @@ int dspark_rotate(const void* x, int64_t x_stride, void* y, int64_t y_stride, ds
  * A request or position out of range (row_req >= B, row_pos < 0) flags DSPARK_STATUS_BAD_ROWS, a
  * length that is negative or passes int32 DSPARK_STATUS_BAD_LENGTH, a page id outside
  * [0, n_pages) or a block >= width DSPARK_STATUS_BAD_PAGE; those rows are not stored.
- * One kernel, or (more than 4096 rows, with queries) two side by side; a block belongs to one team
+ * One kernel, or (prompts, with queries) two side by side; a block belongs to one team
  * of warps: no atomics, the same bits every time.
  * ------------------------------------------------------------------------------------- */
 typedef struct {

@@ -4,16 +4,22 @@
 // A block is one page's slots of one kv head; its scale is a power of two, so that growing it
 // rescales the codes already there by an exact shift of their exponent (only codes that leave
 // e4m3's normal range round again), and multiplying by it is exact. The step's rows that fall
-// into one block are consecutive packed rows; the first of them leads. One warp, or for prompts a team of four, owns a block
-// (of keys or of values): it finds the block's rows, their largest magnitude, hence the scale,
-// requantises the retained codes if the scale grew, and writes the rows' codes. No two touch
-// one block, so there are no atomics and the result does not depend on any order.
+// into one block are consecutive packed rows; the first of them leads. One warp, or for prompts a
+// team of four, owns a block (of keys or of values): it finds the block's rows, their largest
+// magnitude, hence the scale, requantises the retained codes if the scale grew, and writes the
+// rows' codes. No two touch one block, so there are no atomics and the result does not depend on
+// any order.
 //
 // The rotation's factors of the block's rows are computed once per CTA in shared memory, for four
-// heads' keys at a time in a step. The rows' elements stay in registers between the maximum and the
-// codes where they fit (8 rows of 128 for a warp, 64 for a prompt's four); else they are read again.
-// Bound by memory for prompts, by the chain of dependent loads (row owner, length, page id,
-// scale, retained codes) for a step.
+// heads' keys (a prompt's: two teams, each two heads in turn). The rows' elements stay in registers
+// between the maximum and the codes where they fit (8 rows of 128 for a warp, 64 for a prompt's
+// four); else they are read again.
+// Bound for a step by the chain of dependent loads (row owner, length, page id, scale, retained
+// codes): one window of 4 rows, 8 heads of 128 and 32 query heads, 4.4 us, 256 windows 12.9 us (3.9 at
+// the copy rate). For prompts by bandwidth in the queries (36 us of 200 MB), which start when the
+// keys' and values' CTAs are all running, and by the chain and the factors in those (40 us of 74 MB):
+// three prompts, 12 thousand rows in all, 75.7 us. Both kinds of CTAs mixed in one launch took 90 us:
+// the queries need more warps than the others leave.
 #include "cache.cuh"
 #include "rope.cuh"
 
@@ -390,8 +396,8 @@ __device__ __forceinline__ int append_rows(const AppendArgs& A, float2* tab, flo
     constexpr int kTeams = kPromptWarps / kTeam;
     // a prompt's CTA of keys takes kGroups times its teams' heads, one after the other: the factors
     // are theirs all; the values have none
-    const bool value = share >= A.key_shares;
-    const int head0 = value ? (share - A.key_shares) * kTeams : share * kTeams * kGroups;
+    [[maybe_unused]] const bool value = share >= A.key_shares;
+    [[maybe_unused]] const int head0 = value ? (share - A.key_shares) * kTeams : share * kTeams * kGroups;
     // each warp looks at the rows side by side; those that lead a block are the same for all
     const int lane = threadIdx.x & 31;
     int bits = 0;
@@ -410,15 +416,15 @@ __device__ __forceinline__ int append_rows(const AppendArgs& A, float2* tab, flo
             leads &= leads - 1;
             const int bk = __shfl_sync(0xffffffffu, b, k), ik = __shfl_sync(0xffffffffu, i, k);
             const int pk = __shfl_sync(0xffffffffu, pos, k);
-            if (T == 1) {
+            if constexpr (T == 1) {
                 bits |= append_blocks<DT, VEC, T>(A, row0 + from + k, bk, ik, pk, share * kWarps, false, tab, red);
-                continue;
-            }
+            } else {
 #pragma unroll 1
-            for (int g = 0; g < (value ? 1 : kGroups); ++g)
-                if (head0 + g * kTeams < A.c.heads)
-                    bits |= append_blocks<DT, VEC, T>(A, row0 + from + k, bk, ik, pk,
-                                                      2 * (head0 + g * kTeams) + value, g > 0, tab, red);
+                for (int g = 0; g < (value ? 1 : kGroups); ++g)
+                    if (head0 + g * kTeams < A.c.heads)
+                        bits |= append_blocks<DT, VEC, T>(A, row0 + from + k, bk, ik, pk,
+                                                          2 * (head0 + g * kTeams) + value, g > 0, tab, red);
+            }
         }
     }
     return bits;
@@ -508,12 +514,14 @@ int launch_append(const dspark_cache& cache, const Rope& rope, const void* k, in
     A.rows = rows;
     A.B = B;
     A.status = status;
-    // Steps: a warp per block, one row per CTA for the shortest chains in a small one, four in a
-    // large one, where about one row in four leads (256 windows: 16 us with 4, 18 with 1). Prompts:
-    // four warps per block, so that a page's rows are read once and stay in registers; with 16 the
-    // work per block's scale, not per element, was most of it (55 us for 12 thousand rows).
-    const bool prompts = rows > 4096;
-    A.chunk = prompts ? cache.page : rows <= 512 ? 1 : 4;
+    // Steps: a warp per block, one row per CTA for the shortest chains in a small one (4 rows: 4.42 us
+    // and 4.51 with four), four in a larger one, where about one row in four leads (2048 rows in 256
+    // windows: 25 us, 33 with one). Prompts: four warps per block, so that a page's rows are read once
+    // and stay in registers; by the rows that a block gets, which the page and the requests' average
+    // bound. Pages of 64: one prompt of 64 rows 23 us, 40 the other way, 2048 rows 25 and 54; 64 windows
+    // of 32 27 and 27, 256 of 8 53 and 25. One prompt of 2048 rows in pages of 32: 27 and 35, of 16: 33 and 25.
+    const bool prompts = rows > 32ll * B && cache.page >= 32;
+    A.chunk = prompts ? cache.page : rows <= 128 ? 1 : 4;
     A.q_rows = rows >= 152 * 8 && rope.half > 0 ? (rope.half <= 64 ? 4 : 2) : 1;
     A.key_shares = static_cast<int>(ceil_div(cache.heads, kPromptWarps / kTeam * kGroups));
     A.per_row = static_cast<int>(prompts ? A.key_shares + ceil_div(cache.heads, kPromptWarps / kTeam)

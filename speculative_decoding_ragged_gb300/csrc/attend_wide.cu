@@ -4,16 +4,22 @@
 // the pieces' products adding up in the same columns.
 //
 // A CTA: warps 0-3 do the softmax, a thread per row, warp 4 loads pages with TMA (one box per page
-// and K or V, swizzled), warp 5 issues the products. As in
-// the narrow kernel a row's weights are taken over a reference that may lag its maximum: the
-// scores pass through registers once, and only a tile that passes a reference by kLag, or a
-// unit's first, stops to find the maxima and rescale the sums.
+// and K or V, swizzled), warp 5 issues the products. As in the narrow kernel a row's weights are
+// taken over a reference that may lag its maximum: the scores pass through registers once, and
+// only a tile in which some row of a warp passes its reference by kBehind, or a unit's first, stops
+// to find the maxima and rescale the sums. Two or four threads per row were slower (617 and 677 us
+// for 570 below): what a warp does once per tile, waits, votes, numbers, costs it as much as its
+// elements, and one row's threads have to agree on a reference.
 // The weights go through shared memory, so that a tile's scores leave TMEM as soon as they are read
-// and the next tile's products run under this one's softmax; 128 + D columns, so two CTAs fit and
-// one's softmax runs under the other's.
+// and the next tile's products run under this one's softmax (as an operand in TMEM they overlaid
+// the scores: 705 us for 641); 128 + D columns, so two CTAs fit and one's softmax runs under the
+// other's. What a piece needs to be known by lives in shared memory: a thread holds 128 scores.
 //
-// Bound: the products (sixteen of 101 cycles a tile at D = 128) and the softmax's instruction
-// issue, about alike.
+// Bound: sixteen products of 101 cycles a tile at D = 128, 1616 cycles a tile and SM, and the
+// softmax, which takes a CTA about 4250 cycles a tile, 2100 with two of them. Two prompts' pieces of
+// about 2000 rows, 32 query heads of 128 over 8 heads, after 4 to 8 thousand tokens: 521 us, 0.91
+// PFLOP/s of the plain form's 16-bit products. Its registers are tight: ptxas places the same
+// source's scores well or badly (640 us with the queries loaded in two halves).
 #include "attend_mma.cuh"
 
 namespace dspark {
@@ -23,8 +29,9 @@ constexpr int kRows = 128;
 constexpr int kSoft = kRows;                 // softmax threads: one per row
 constexpr int kThreads = kSoft + 64;
 constexpr int kNums = 4;
-// Weights are 2^(x - m + kUp), m lagging by at most kLag: at most 2^8.5 < 448, and a weight keeps
-// two full pieces down to 2^-12 of the largest.
+// Weights are 2^(x - m + kUp), m lagging by at most kBehind: at most 2^8.5 < 448, and a weight
+// is within 2^-8 of itself or 2^-16 of the largest. Room for a longer lag (2.5 -> 6.5) would give 2 %
+// and cost the small weights four bits.
 constexpr float kUp = 6.0f;
 constexpr float kBehind = 2.5f;
 
@@ -515,7 +522,10 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                         const int p0 = now.len + now.qt * kRows / A.group;
                         const int p1 = now.len + (now.qt * kRows + rows - 1) / A.group;
                         const int lo1 = A.window > 0 && p1 >= A.window ? p1 - A.window + 1 : 0;
-                        sm.span = {now.k0, now.n, lo1, p0};
+                        sm.span.k0 = now.k0;
+                        sm.span.n = now.n;
+                        sm.span.lo = lo1;
+                        sm.span.hi = p0;
                         sm.stored = now.len + now.w;
                     }
                 }

@@ -136,7 +136,11 @@ CASES = [
     ([129, 2], [127, 128], 1, 4, 128, 128, "bf16"),
     ([0, 3, 0], [5, 5, 0], 2, 2, 256, 16, "bf16"),
     ([2] * 40, list(range(40)), 2, 1, 128, 16, "bf16"),
-    # more than 4096 rows: a CTA per block
+    # prompts: many rows in a block, teams of warps; heads that fill no team, or half of one
+    ([40], [70], 3, 2, 128, 32, "bf16"),
+    ([33, 34, 64], [0, 61, 63], 5, 1, 64, 64, "f32"),
+    ([70, 0, 60], [9, 9, 100], 4, 2, 96, 64, "bf16"),
+    # thousands of rows
     ([4100, 3], [5, 30], 2, 1, 64, 16, "bf16"),
     ([200, 4000, 1], [77, 0, 64], 1, 2, 128, 64, "bf16"),
     ([4097], [100], 1, 1, 128, 128, "f32"),
