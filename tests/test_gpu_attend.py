@@ -168,6 +168,45 @@ def test_attend(lib, case, dtype):
     Case(sum(case[0]) + case[4], *case).check(dtype)
 
 
+PROMPTS = [
+    # w, lengths, heads, group, dim, page, window: requests of many units of 128 rows, and the
+    # threads that count them from 32 for one request down to one for two requests
+    ([1100, 0, 5], [3, 9, 200], 1, 4, 64, 16, 0),
+    ([1100], [0], 1, 4, 128, 64, 100),
+    ([40, 61, 300, 1, 0, 90, 33], [0, 127, 5, 600, 7, 64, 1], 2, 3, 64, 32, 0),
+    ([13] * 60, [7 * i for i in range(60)], 1, 4, 64, 16, 0),
+    ([12] * 200, [i % 90 for i in range(200)], 1, 4, 64, 16, 0),
+    ([129, 257], [1000, 3], 3, 1, 128, 32, 40),
+    ([90], [2900], 1, 16, 128, 128, 0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", PROMPTS)
+def test_prompts(lib, case):
+    c = Case(sum(case[0]) + case[6], *case[:6])
+    c.check(torch.bfloat16, case[6])
+    c.q *= 5.0                               # one token takes nearly all: maxima rise from tile to tile
+    c.check(torch.bfloat16, case[6])
+
+
+@gpu
+def test_prompts_with_bad_pages_and_queries(lib):
+    c = Case(21, [70, 50], [300, 0], 2, 4, 128, 16)
+    c.table[0, 3] = -1
+    c.table[1, 0] = c.n                      # request 1's first rows see nothing
+    out, lse = c.check(torch.bfloat16, status=bd.STATUS_BAD_PAGE)
+    assert np.isneginf(lse[c.cu[1]:c.cu[1] + 16]).all()
+    q = c.q.copy()
+    c.q[33, 5, 7], c.q[100, 0, 0] = np.nan, -np.inf
+    _, bad, _, _ = c.run(torch.bfloat16)
+    c.q = q
+    hit = np.zeros(out.shape[:2], bool)
+    hit[33, 5] = hit[100, 0] = True
+    assert np.isnan(bad[hit]).all()
+    np.testing.assert_array_equal(bad[~hit], out[~hit])
+
+
 @gpu
 @pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("window", [1, 2, 16, 100, 129, 1000])
