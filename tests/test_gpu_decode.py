@@ -190,3 +190,33 @@ def test_rotate_gradient_by_differences(dev, dtype):
     bound = eps * size * (((plus.abs() + minus.abs()).double().amax((1, 2)) * w.double().abs().sum((1, 2))) +
                           step.abs().sum((1, 2)) * w.double().abs().amax((1, 2)) * 1.0)
     assert ((lhs - rhs).abs() <= bound).all(), (lhs - rhs, bound)
+
+
+@pytest.mark.parametrize("rows,dim,dtype", [(29, 128, torch.bfloat16), (400, 128, torch.bfloat16),
+                                            (29, 128, torch.float32)])
+def test_cache_past_32_bits(dev, rows, dim, dtype):
+    """Pages whose codes lie more than 2^32 bytes into the cache: the same bits as in a small one."""
+    small, packed, lengths = case(dev, 4, rows=rows, dim=dim, page=64)
+    heads, page = 2, 64
+    per = heads * page * dim
+    pages = small.cache.n_pages
+    n = (2 ** 32 + per - 1) // per + pages + 1
+    assert (n - pages) * per > 2 ** 32
+    big = CachedAttention(small.out.shape[0], small.out.shape[1], heads, dim,
+                          small.cache.table + (n - pages), 1, page, small.rope, dtype=dtype)
+    k, v = (torch.empty(n, heads, page, dim, dtype=torch.uint8, device=dev) for _ in range(2))
+    ks, vs = (torch.ones(n, heads, device=dev) for _ in range(2))
+    other = CachedAttention(small.out.shape[0], small.out.shape[1], heads, dim, small.cache.table,
+                            pages, page, small.rope, dtype=dtype)
+    for name, t in (("k", k), ("v", v), ("k_scale", ks), ("v_scale", vs)):
+        src = getattr(small.cache, name)
+        t[n - pages:].view(torch.uint8).copy_(src.view(torch.uint8))
+        getattr(other.cache, name).view(torch.uint8).copy_(src.view(torch.uint8))
+    big.cache = bd.PagedCache(k, v, ks, vs, big.cache.table)
+    args = [t.to(dtype) for t in packed[:3]] + packed[3:] + [lengths]
+    a, b = other.run(*args), big.run(*args)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and bool(a.float().abs().sum() > 0)
+    assert torch.equal(other.cache.k.view(torch.uint8), k[n - pages:])
+    assert torch.equal(other.cache.v.view(torch.uint8), v[n - pages:])
+    assert int(big.status.item()) == 0
