@@ -116,10 +116,11 @@ def test_repeats_bit_for_bit(dev):
     assert same(first, state(att))
 
 
-def test_graph_replays_eager_steps(dev):
-    att, rows, lengths = case(dev, 2)
+@pytest.mark.parametrize("size", [dict(), dict(rows=400, page=64)])      # windows; prompts
+def test_graph_replays_eager_steps(dev, size):
+    att, rows, lengths = case(dev, 2, **size)
     side = torch.cuda.Stream(device=dev)
-    other, orows, olen = case(dev, 2)         # the same case, run eagerly
+    other, orows, olen = case(dev, 2, **size)  # the same case, run eagerly
     assert same(state(att), state(other))
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
@@ -133,7 +134,7 @@ def test_graph_replays_eager_steps(dev):
     replay = graph.prepare_launch()
     for step in range(4):
         # new inputs into the same tensors: other lengths, another split of the rows
-        att2, fresh, flen = case(dev, 10 + step)
+        att2, fresh, flen = case(dev, 10 + step, **size)
         for dst, odst, src in zip([*rows, lengths], [*orows, olen], [*fresh, flen]):
             dst.copy_(src)
             odst.copy_(src)
@@ -149,10 +150,11 @@ def test_graph_replays_eager_steps(dev):
         assert (err <= tol).all()
 
 
-def test_another_stream(dev):
+@pytest.mark.parametrize("size", [dict(), dict(rows=400, page=64)])
+def test_another_stream(dev, size):
     """Calls follow the stream they are given, not the stream their tensors came from."""
-    att, rows, lengths = case(dev, 3)
-    want, wrows, wlen = case(dev, 3)
+    att, rows, lengths = case(dev, 3, **size)
+    want, wrows, wlen = case(dev, 3, **size)
     want.run(*wrows, wlen)
     late = rows[0].clone()
     rows[0].zero_()
