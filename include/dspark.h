@@ -534,9 +534,12 @@ int dspark_append(const dspark_cache* cache, const dspark_rope* rope, const void
  * refused with DSPARK_ERR_UNSUPPORTED: split its rows.
  *
  * Precision: bf16 with dim 64 or 128 runs on the tensor cores, q as two e4m3 pieces (its eight
- * mantissa bits exactly, down to 2^-17 of a row's largest element), the softmax weights as two
- * pieces (relative error below 2^-8, 6e-4 rms: under bf16's own), sums in fp32. fp32, and other
- * dims, run in fp32 throughout.
+ * mantissa bits exactly, down to 2^-17 of a row's largest element), sums in fp32. A softmax weight,
+ * its value's scale included, is within 2^-8 of itself (4e-4 rms, under bf16's own rounding) from
+ * 2^-17 of the row's largest so far up, and within 2^-26 of that largest below. A stretch of tokens
+ * that all lie 2^-9 or more under the largest, the tail behind an attention sink, is measured against
+ * its own largest instead, from 16 * 128 tokens after its start at the latest, down to 2^-32. fp32, and
+ * other dims, run in fp32 throughout.
  * ------------------------------------------------------------------------------------- */
 int dspark_attend(const dspark_cache* cache, const void* q, int64_t q_stride, void* out,
                   int64_t out_stride, int q_heads, dspark_dtype dtype, int rows,

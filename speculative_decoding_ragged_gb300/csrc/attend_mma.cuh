@@ -5,16 +5,17 @@
 //   x_t = log2(e) scale q.K_t + log2 vs_t,   w_t = 2^(x_t - m),   O = sum_t w_t Vcode_t,
 //   l = sum_t w_t / vs_t,   out = O / l,     lse = ln 2 (m + log2 l).
 // Putting the value's scale into the exponent makes every product of the value side a plain
-// product of codes, keeps w_t <= 1 whatever the blocks' scales, and costs nothing: it is the
+// product of codes, bounds w_t whatever the blocks' scales, and costs nothing: it is the
 // addend of the multiply-add that scales the score.
 //
-// The cache stays in its 8 bits all the way into the tensor cores (kind::f8f6f4). What is not
-// 8-bit is split into e4m3 pieces whose products add up in fp32: a bf16 query element has 8
-// significant bits, an e4m3 piece 4, so two pieces (over a power of two per row) hold it exactly
-// down to 2^-17 of the row's largest; a weight in two pieces is within 2^-8 (6e-4 rms, below the
-// rounding of the bf16 result). Compared with widening K and V to 16 bits in shared memory this
-// needs no conversion of the cache and moves half the shared-memory bytes; the second piece
-// doubles the 8-bit products, which run at twice the 16-bit rate.
+// K stays in its 8 bits all the way into the tensor cores (kind::f8f6f4), and so does V where the rows
+// are few. What is not 8-bit is split into pieces of 8 bits whose products add up in fp32. A bf16 query
+// element has 8 significant bits, an e4m3 piece 4, so two pieces (over a power of two per row) hold it
+// exactly down to 2^-17 of the row's largest. What counts for a weight is range, since one dominant
+// token over a long context leaves the others small weights and much of the mass: it is three e5m2
+// pieces (see split3) or, where there are rows enough to pay for widening V, one fp16 number. Compared
+// with widening K too this moves half the shared-memory bytes; 8-bit products run at twice the 16-bit
+// rate.
 //
 // Work. A unit is (request, cache head, up to R of its rows); its visible tokens come in tiles of
 // 128. All tiles of all units form one line, which the persistent grid (two CTAs per SM) cuts
@@ -37,8 +38,23 @@ constexpr int kBlocks = kTile / 16;          // most blocks in a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;              // a row's reference before it has seen a token
+// Weights are 2^(x - m + kUp), where the reference m may lag the row's true maximum by kBehind: at
+// most 2^15.75, under fp16's largest and e5m2's. Less room for the lag rescales more often: 2.75 took
+// 129 us where 6.5 took 115 (256 windows of 1 to 8 over 128 to 2048), 515 and 505 (two prompts' pieces).
+constexpr float kUp = 9.25f;
+constexpr float kBehind = 6.5f;
+// What a weight may be off by is absolute under 2^-8 (see split3; fp16: under 2^-17), 2^-17 of the
+// largest. So that a long tail of small weights after a dominant token keeps its bits, the reference
+// also goes down, to a tile whose maximum lies kBelow under it: looked at after a tile that makes that
+// likely, and every kLook tiles. The sums grow then: by at most 2^kDown in all over what the largest
+// reference made them. It costs 2 us of 117 and 3 us of 509 in the two cases above.
+constexpr float kBelow = 9.0f;
+constexpr float kDown = 32.0f;
+constexpr int kLook = 16;
+__device__ __forceinline__ bool look_down(int k) { return k > 0 && (k & (kLook - 1)) == 0; }
 constexpr long long kWaitCycles = 1ll << 31;
 constexpr uint32_t kSmemAlign = 1024;        // the 128-byte swizzle's period
+constexpr size_t kSmemTwo = 115712;          // of an SM's 228 KB, 1 KB reserved per CTA, for each of two CTAs
 
 // What the join needs to know of the unit that a run's start cut.
 struct RunMeta {
@@ -137,6 +153,20 @@ static __device__ __noinline__ void drain(uint32_t bar, uint32_t parity, volatil
     while (!mbar_try(bar, parity))
         if (clock64() > deadline) { *stalled = 1; return; }
 }
+// The tiles' swizzle needs shared memory that starts at its period, which the declaration asks for.
+// Were it not so, the call would report a stall and write nothing.
+__device__ __forceinline__ bool smem_aligned(const AttendCall& A, const Workspace& ws, const void* raw)
+{
+    const bool yes = (smem_addr(raw) & (kSmemAlign - 1)) == 0;
+    if (!yes) {
+        pdl_wait_and_trigger();
+        if (threadIdx.x == 0) {
+            ws.meta[blockIdx.x].rows = 0;        // nothing for the join
+            raise_status(A.status, DSPARK_STATUS_STALL);
+        }
+    }
+    return yes;
+}
 // True in one lane of the warp, which runs converged here.
 __device__ __forceinline__ bool elect_one()
 {
@@ -167,7 +197,7 @@ __device__ __forceinline__ void tc_commit(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                  ::"r"(bar) : "memory");
 }
-// D[tmem] (+)= A[smem] B[smem]
+// D[tmem] (+)= A[smem] B[smem], 8-bit types; and fp16 by fp16
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
@@ -175,6 +205,15 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
         " .reg .pred p;\n"
         " setp.ne.u32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ss_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
         "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 __device__ __forceinline__ void tc_ld16(uint32_t addr, float* x)
@@ -212,11 +251,11 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r)
         "r"(r[15]) : "memory");
 }
 
-// K-major and MN-major operands share the TMA swizzle: rows of BYTES (128 or 64), groups of 8 rows.
+// K-major and MN-major operands share the TMA swizzle: rows of BYTES (128, 64 or 32), groups of 8 rows.
 template <int BYTES>
 __device__ __forceinline__ uint64_t operand(uint32_t addr)
 {
-    constexpr uint64_t swizzle = BYTES == 128 ? 2 : 4;   // 128- or 64-byte
+    constexpr uint64_t swizzle = BYTES == 128 ? 2 : BYTES == 64 ? 4 : 6;   // 128-, 64- or 32-byte
     return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (1ull << 16) |
            (static_cast<uint64_t>(8 * BYTES / 16) << 32) | (1ull << 46) | (swizzle << 61);
 }
@@ -226,18 +265,41 @@ struct __align__(16) BlockNums {
     float ks, bias, inv, pad;
 };
 
-// Two weights in two e4m3 pieces each. The weights go through fp16 (11 bits, 2^-12: a sixteenth
-// of what the pieces are off by); the remainder is exact there.
-template <bool LOW = false>      // the second piece times 2^4, where it has a column of its own
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two query elements (under 448 in magnitude) in two e4m3 pieces each, through fp16, which holds a
+// bf16's 8 bits down to 2^-17; the remainder is exact there.
 __device__ __forceinline__ void split2(float a, float b, uint16_t* hi, uint16_t* lo)
 {
-    uint32_t w, back, rest;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    const uint32_t w = pack_f16(a, b);
+    uint32_t back, rest;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(*hi) : "r"(w));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(*hi));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(w), "r"(back));
-    if (LOW) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(rest), "r"(0x4c004c00u));
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(*lo) : "r"(rest));
+}
+// Four weights in three e5m2 pieces each: p[i] holds the i-th pieces of a, b, c, d in order of bytes.
+// An e5m2 number is the upper byte of an fp16 one. So the weight goes through fp16; the first piece is
+// its upper byte, the second and third are those of what remains, rounded to nearest by adding half of
+// the last place kept. Remainders are exact in fp16, of either sign after the second piece. From 2^-8
+// up the three are within 2^-8.6 of the weight (3.7e-4 rms); below it the third piece ends at e5m2's
+// smallest step, and they are off by 2^-16.8 at most. NaN stays NaN (first piece).
+__device__ __forceinline__ void split3(float a, float b, float c, float d, uint32_t* p)
+{
+    uint32_t w0 = pack_f16(a, b), w1 = pack_f16(c, d), r0, r1;
+    p[0] = __byte_perm(w0, w1, 0x7531);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(w0), "r"(w0 & 0xff00ff00u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(w1), "r"(w1 & 0xff00ff00u));
+    w0 = r0 + 0x00800080u;
+    w1 = r1 + 0x00800080u;
+    p[1] = __byte_perm(w0, w1, 0x7531);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(r0), "r"(w0 & 0xff00ff00u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(r1), "r"(w1 & 0xff00ff00u));
+    p[2] = __byte_perm(r0 + 0x00800080u, r1 + 0x00800080u, 0x7531);
 }
 __device__ __forceinline__ uint32_t join16(uint16_t a, uint16_t b)
 {

@@ -3,15 +3,17 @@
 //
 // With few rows the products are turned round: the tile's 128 tokens (for the scores) and the
 // head's elements (for the sums) fill the 128 lanes of the instruction, the rows are its columns:
-//   S^T [128 tokens, 2 R] = K [128, D] (Q_hi, Q_lo)^T       O^T [D, 2 R] += V^T [D, 128] (W_hi, W_lo)
-// so the products cost what the rows need (about 600 cycles a tile at R = 32, where 128 row lanes
-// cost 1400) and K and V are read from shared memory once.
-// The two pieces are separate columns and are added when they are read.
+//   S^T [128 tokens, 2 R] = K [128, D] (Q_1, Q_2)^T       O^T [D, 3 R] += V^T [D, 128] (W_1, W_2, W_3)
+// so the products cost what the rows need, where 128 row lanes cost 1600 cycles a tile, and K and V
+// are read from shared memory once. The pieces are separate columns and are added when they are read;
+// at R = 32, where TMEM has no room for three sets of columns twice, the weights' are three products
+// into one set. The weights' pieces are e5m2 for its range; in two e4m3 pieces, which end at 2^-16 of
+// the largest, the batch below took 109 us, and a dominant token over 8192 others lost up to all of them.
 // A thread's lane is a token: block scales are per-thread scalars, the rows' factors and
 // references broadcast reads. The softmax needs no reduction over lanes in the common case: every
 // thread checks its own exponents against the rows' references (one barrier with a vote), and
-// only a tile that passes one by kBehind, or a unit's first, finds the true maxima. The row sums stay
-// in registers, one partial sum per row and thread, until the unit ends.
+// only a tile that passes one by kBehind, a unit's first, or one that may lie far below finds the
+// true maxima. The row sums stay in registers, one partial sum per row and thread, until the unit ends.
 //
 // A CTA: two groups of four warps do the softmax, a thread per token with half of the rows (groups
 // of eight rows, four of them at R = 32, were 10 to 15 % slower) and prepare the queries of the
@@ -23,7 +25,7 @@
 // Bound by HBM: 2 D bytes per token and cache head. What else showed in clock stamps was cold
 // code (about 16 cycles per instruction the first time), hence one walker, rolled loops where
 // registers allow them. 192 single tokens over 1 to 8 thousand, 8 heads of 128: 6.5 TB/s, 97 % of a
-// copy. 256 windows of 1 to 8 over 128 to 2048: 109 us, 3.5 TB/s: a unit has about nine tiles, of 2400
+// copy. 256 windows of 1 to 8 over 128 to 2048: 117 us, 3.3 TB/s: a unit has about nine tiles, of 2500
 // cycles each, and changing units costs 9000, the start 15 to 25 thousand.
 #include "attend_mma.cuh"
 
@@ -35,14 +37,13 @@ constexpr int group_rows(int R) { return R / 2; }
 constexpr int groups(int R) { return R / group_rows(R); }
 constexpr int soft_threads(int R) { return 128 * groups(R); }
 constexpr int all_threads(int R) { return soft_threads(R) + 96; }
-constexpr int kP = 64;                       // bytes of a token's row of weights: two pieces of 32
 constexpr int kPieces = 8;                   // described pieces
-// Weights are 2^(x - m + kUp) where m may lag the true maximum by kBehind: at most 2^8.5 < 448.
-// The second piece has columns of its own and is scaled by 2^4 more, so a weight is within 2^-8 of
-// itself or 2^-16 of the largest. A wide margin for m makes rescaling rare.
-constexpr float kUp = 2.0f;
-constexpr float kBehind = 6.5f;
-constexpr float kLowBack = 0.0625f;
+// The weights' products: sets of R columns of sums, one for each of the three pieces or (R = 32) one
+// for all; products for each 32 tokens; their columns, a multiple of 16; bytes of a token's row of weights.
+constexpr int sum_sets(int R) { return R == 32 ? 1 : 3; }
+constexpr int weight_products(int R) { return R == 32 ? 3 : 1; }
+constexpr int weight_cols(int R) { return (sum_sets(R) * R + 15) / 16 * 16; }
+constexpr int weight_row(int R) { return R == 32 ? 32 : 64; }
 
 // A run's part of one unit.
 struct Piece {
@@ -56,8 +57,7 @@ struct Piece {
     int i0, g0;          // position and head of the unit's first row
 };
 struct RowInfo {
-    int64_t out;         // element offset of the row's results
-    int64_t lse;
+    int prow, head;      // the row's packed row and query head
 };
 
 template <int D, int R>
@@ -67,19 +67,18 @@ struct Smem {
     static constexpr int kNums = kSlots / 2 + 2;         // tiles whose numbers may still be read
     uint8_t ring[kSlots][kSlot];
     uint8_t q[2][2 * R * D];                         // two units' queries: hi rows, lo rows
-    uint8_t p[kTile * kP];                               // the weights, a row per token
+    uint8_t p[weight_products(R)][kTile * weight_row(R)];    // the weights, a row per token
     BlockNums nums[kNums][kBlocks];
     Piece piece[kPieces];
     RowInfo info[4][R];                                  // four units' rows
-    int2 see[4][R];                                  // first token seen, and how many past it
-    float f[4][R];                                   // score factors: scale log2(e) 2^e
-    RowInfo now_info[R];                             // the softmax's own copies of its unit's
-    __align__(16) int2 now_see[R];
-    __align__(16) float now_f[R];
+    __align__(16) int2 see[4][R];                    // first token seen, and how many past it
+    __align__(16) float f[4][R];                     // score factors: scale log2(e) 2^e
     __align__(16) float ref[R];                      // kUp - reference (0: nothing seen yet)
     __align__(16) float grow[R];                     // 2^(old reference - new)
+    float peak[R];                                   // kUp - the largest reference so far
     float4 part[R];                                  // the four warps' maxima or sums
-    int unseen[groups(R)];                               // a row of the group has seen nothing yet
+    int look[groups(R)];                                 // the next tile that finds the maxima in any case
+    int changed[groups(R)];                              // the last one that did changed a reference
     uint64_t full[kSlots], empty[kSlots];
     uint64_t piece_full[kPieces], q_full[2];
     uint64_t s_full[2], pv_done[2], p_full;
@@ -170,13 +169,14 @@ struct Token {
 // One tile, this thread's token, one group's rows: scores in TMEM -> weights in shared memory;
 // l += this token's weights.
 template <int D, int R>
-__device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, uint64_t* l, uint32_t s_addr, uint32_t o_addr,
-                                       const Token& k, bool mask, bool first, int it, volatile int* stalled)
+__device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, int slot, uint64_t* l, uint32_t s_addr,
+                                       uint32_t o_addr, const Token& k, bool mask, int tile, int it,
+                                       volatile int* stalled)
 {
     constexpr int HR = group_rows(R);
     const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3;
     const int r0 = grp * HR;
-    const float4* f4 = reinterpret_cast<const float4*>(sm.now_f + r0);
+    const float4* f4 = reinterpret_cast<const float4*>(sm.f[slot] + r0);
     const float4* ref4 = reinterpret_cast<const float4*>(sm.ref + r0);
     const uint64_t ks2 = pack2(k.n.ks, k.n.ks), bias2 = pack2(k.n.bias, k.n.bias);
     uint64_t x[HR / 2];                       // pairs of rows
@@ -204,7 +204,7 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, uint64_t* l, uin
             }
         if (mask) {
             top = -INFINITY;
-            const int4* see2 = reinterpret_cast<const int4*>(sm.now_see + r0);
+            const int4* see2 = reinterpret_cast<const int4*>(sm.see[slot] + r0);
 #pragma unroll
             for (int r = 0; r < HR; r += 2) {
                     const int4 s = see2[r / 2];
@@ -216,9 +216,10 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, uint64_t* l, uin
                 }
         }
         if (pass) break;
-        if (!first && !group_any(grp, top > kUp + kBehind || sm.unseen[grp])) break;
+        const bool first = tile == 0;
+        if (!first && !group_any(grp, top > kUp + kBehind || tile == sm.look[grp])) break;
         // The rows' maxima, as exponents over the present references; new references for the rows
-        // that passed theirs by too much and those that see their first tokens.
+        // that passed theirs by too much or lie far below, and those that see their first tokens.
         float v[HR];
 #pragma unroll
         for (int r = 0; r < HR; r += 2) {
@@ -234,18 +235,28 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, uint64_t* l, uin
             const float over = fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w));
             const float old = sm.ref[r];
             const bool none = old == 0.0f;
+            const float peak = sm.peak[r];
             float y = old;
-            if (over > -INFINITY && (none || over > kUp + kBehind)) {
+            if (over > -INFINITY && (none || over > kUp + kBehind || over < kUp - kBelow)) {
                 y = old - over + kUp;
+                if (!none) y = fminf(y, peak + kDown);
                 if (y == 0.0f) y = 1e-30f;       // 0 stands for none
             }
             __syncwarp();
             if (lane < HR) {
                 sm.grow[r] = none ? 1.0f : ex2_approx(y - old);
                 sm.ref[r] = y;
+                sm.peak[r] = none ? y : fminf(peak, y);
             }
-            const bool any = __any_sync(0xffffffffu, y == 0.0f);
-            if (lane == 0) sm.unseen[grp] = any;
+            // the next tile finds the maxima too where a row has seen nothing yet, or where a quarter of
+            // this one lies far below another
+            const float least = fminf(fminf(q.x, q.y), fminf(q.z, q.w));
+            const bool next = __any_sync(0xffffffffu, y == 0.0f || over - least > kBelow);
+            const bool changed = __any_sync(0xffffffffu, y != old);
+            if (lane == 0) {
+                sm.look[grp] = next ? tile + 1 : (tile | (kLook - 1)) + 1;
+                sm.changed[grp] = changed;
+            }
         }
         group_sync(grp);
         if (first) {                             // the present references were 0
@@ -257,23 +268,23 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, uint64_t* l, uin
                 }
             break;
         }
+        if (!sm.changed[grp]) break;
         // the tiles before this one have to be in the sums before these are scaled
         if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done[(it - 1) & 1]), ((it - 1) >> 1) & 1, stalled)))
             return false;
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < HR; c += 4) {
-            float o[4], lo[4];
-            tc_ld<4>(o_addr + r0 + c, o);
-            tc_ld<4>(o_addr + R + r0 + c, lo);
+            float o[sum_sets(R)][4];
+#pragma unroll
+            for (int i = 0; i < sum_sets(R); ++i) tc_ld<4>(o_addr + i * R + r0 + c, o[i]);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                o[j] *= sm.grow[r0 + c + j];
-                lo[j] *= sm.grow[r0 + c + j];
+            for (int i = 0; i < sum_sets(R); ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][j] *= sm.grow[r0 + c + j];
+                tc_st4(o_addr + i * R + r0 + c, o[i]);
             }
-            tc_st4(o_addr + r0 + c, o);
-            tc_st4(o_addr + R + r0 + c, lo);
         }
         tc_wait_st();
 #pragma unroll
@@ -285,11 +296,15 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, uint64_t* l, uin
                                                      ((it - 1) >> 1) & 1, stalled)))
         return false;
     const int token = tid & 127;
-    uint8_t* p = &sm.p[token * kP];
-    const int swz = (token >> 1) & 3;            // the 64-byte swizzle: 16-byte chunks
-    auto place = [&](int byte) -> uint8_t* { return p + (((byte >> 4) ^ swz) << 4) + (byte & 15); };
+    // piece i of the rows from r0 on: the 64- or 32-byte swizzle of 16-byte chunks
+    auto place = [&](int i) -> uint8_t* {
+        if (weight_products(R) == 3)
+            return &sm.p[i % weight_products(R)][token * 32 + (((r0 >> 4) ^ ((token >> 2) & 1)) << 4)];
+        const int byte = i * R + r0;
+        return &sm.p[0][token * 64 + (((byte >> 4) ^ ((token >> 1) & 3)) << 4) + (byte & 15)];
+    };
     const uint64_t inv2 = pack2(k.n.inv, k.n.inv);
-    uint32_t hi[HR / 4], lo[HR / 4];
+    uint32_t w[HR / 4][3];
 #pragma unroll
     for (int c = 0; c < HR / 4; ++c)
         if (4 * c < HR) {
@@ -300,21 +315,16 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, uint64_t* l, uin
             b.y = ex2_approx(b.y);
             l[2 * c] = fma2(pack2(a.x, a.y), inv2, l[2 * c]);
             l[2 * c + 1] = fma2(pack2(b.x, b.y), inv2, l[2 * c + 1]);
-            uint16_t h0, h1, l0, l1;
-            split2<true>(a.x, a.y, &h0, &l0);
-            split2<true>(b.x, b.y, &h1, &l1);
-            hi[c] = join16(h0, h1);
-            lo[c] = join16(l0, l1);
+            split3(a.x, a.y, b.x, b.y, w[c]);
         }
-    if (HR == 16) {
-        *reinterpret_cast<uint4*>(place(r0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(place(R + r0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    } else if (HR == 8) {
-        *reinterpret_cast<uint2*>(place(r0)) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(place(R + r0)) = make_uint2(lo[0], lo[1]);
-    } else {
-        *reinterpret_cast<uint32_t*>(place(r0)) = hi[0];
-        *reinterpret_cast<uint32_t*>(place(R + r0)) = lo[0];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        if (HR == 16)
+            *reinterpret_cast<uint4*>(place(i)) = make_uint4(w[0][i], w[HR / 16][i], w[HR / 8][i], w[HR / 4 - 1][i]);
+        else if (HR == 8)
+            *reinterpret_cast<uint2*>(place(i)) = make_uint2(w[0][i], w[HR / 4 - 1][i]);
+        else
+            *reinterpret_cast<uint32_t*>(place(i)) = w[0][i];
     }
     return true;
 }
@@ -322,8 +332,8 @@ __device__ __forceinline__ bool soften(Smem<D, R>& sm, int grp, uint64_t* l, uin
 // A finished piece, after its row sums are in part: results or a part written. Lane d holds
 // element d.
 template <int D, int R>
-__device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R>& sm, int grp, uint32_t o_addr, int rows,
-                                       bool whole, int part, const Workspace& ws)
+__device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R>& sm, int grp, int slot, uint32_t o_addr,
+                                       int rows, bool whole, int part, const Workspace& ws)
 {
     const int tid = threadIdx.x;
     constexpr int HR = group_rows(R);
@@ -333,23 +343,27 @@ __device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R>& sm, int 
     float* po = ws.o + static_cast<int64_t>(part) * kTile * D + d;
 #pragma unroll 1
     for (int c = r0; c < r0 + HR && c < rows; c += 4) {
-        float o[4], lo[4];
-        tc_ld<4>(o_addr + c, o);
-        tc_ld<4>(o_addr + R + c, lo);
+        float o[sum_sets(R)][4];
+#pragma unroll
+        for (int i = 0; i < sum_sets(R); ++i) tc_ld<4>(o_addr + i * R + c, o[i]);
         int64_t at[4];
         float g[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float4 q = sm.part[c + j];
             const float sum = (q.x + q.y) + (q.z + q.w);
-            at[j] = sm.now_info[c + j].out;
+            const RowInfo in = sm.info[slot][c + j];
+            at[j] = in.prow * A.out_stride + static_cast<int64_t>(in.head) * D;
             g[j] = !whole ? 1.0f : sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);      // nothing seen: zeros
         }
         tc_wait_ld();
         if (D == 128 || d < D) {                 // D = 64: lanes 64.. repeat the first ones
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float y = fmaf(lo[j], kLowBack, o[j]) * g[j];
+                float y = o[sum_sets(R) - 1][j];
+#pragma unroll
+                for (int i = sum_sets(R) - 2; i >= 0; --i) y += o[i][j];
+                y *= g[j];
                 if (whole && c + j < rows) store1<DSPARK_BF16>(out, at[j], y);
                 if (!whole && c + j < rows) po[(c + j) * D] = y;
             }
@@ -363,7 +377,7 @@ __device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R>& sm, int 
         if (!whole)
             ws.ml[part * kTile + r] = make_float2(sum == 0.0f ? kNone : m, sum);
         else if (A.lse != nullptr)
-            A.lse[sm.now_info[r].lse] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+            A.lse[static_cast<int64_t>(sm.info[slot][r].prow) * A.q_heads + sm.info[slot][r].head] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
     }
 }
 
@@ -445,8 +459,7 @@ static __device__ __noinline__ void put_query(const AttendCall& A, Smem<D, R>& s
     if (seg == 0) {
         const QueryAt at = query_at(A, pc, row);
         const int first = A.window > 0 && at.pos >= A.window ? at.pos - A.window + 1 : 0;
-        sm.info[slot][row].out = at.prow * A.out_stride + static_cast<int64_t>(at.head) * D;
-        sm.info[slot][row].lse = at.prow * A.q_heads + at.head;
+        sm.info[slot][row] = {static_cast<int>(at.prow), at.head};
         sm.see[slot][row] = make_int2(first, at.pos - first);
         // a query that is not finite makes its row's factor, hence its results, NaN
         sm.f[slot][row] = fine ? A.scale * kLog2e * exp2i(e) : __int_as_float(0x7fc00000);
@@ -477,14 +490,15 @@ __global__ void __launch_bounds__(all_threads(R), 2)
 attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
-    Smem<D, R>& sm = *reinterpret_cast<Smem<D, R>*>(
-        raw + ((kSmemAlign - (smem_addr(raw) & (kSmemAlign - 1))) & (kSmemAlign - 1)));
+    extern __shared__ __align__(kSmemAlign) unsigned char raw[];
+    Smem<D, R>& sm = *reinterpret_cast<Smem<D, R>*>(raw);
+    static_assert(sizeof(Smem<D, R>) <= kSmemTwo, "two CTAs per SM");
     constexpr int kSlots = Smem<D, R>::kSlots;
     constexpr int kNums = Smem<D, R>::kNums;
     constexpr int G = groups(R), kLoader = 4 * G, kIssuer = kLoader + 1, kWalker = kLoader + 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Workspace ws = workspace_of(A.ws);
+    if (!smem_aligned(A, ws, raw)) return;
 
     if (tid < kSlots) {
         mbar_init(smem_addr(&sm.full[tid]), 1);
@@ -648,10 +662,13 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
             const bool leader = elect_one();
             constexpr uint32_t kIdesc = (1u << 4) | (kTile / 16 << 24) | (R / 4 << 17);      // 2 R columns
             // V^T: the head's elements are contiguous, and so are the weights' rows
-            constexpr uint32_t kIdescPV = kIdesc | (1u << 15) | (1u << 16);
+            // by e5m2
+            constexpr uint32_t kIdescPV = (1u << 4) | (1u << 10) | (1u << 15) | (1u << 16) |
+                                          (weight_cols(R) / 8 << 17) | (kTile / 16 << 24);
             const uint32_t tmem = sm.tmem;
             const uint64_t ring0 = operand<D>(smem_addr(sm.ring[0]));
             const uint64_t q_op = operand<D>(smem_addr(sm.q[0]));
+            constexpr int kP = weight_row(R);
             const uint64_t p_op = operand<kP>(smem_addr(sm.p));
             constexpr uint32_t kStep = Smem<D, R>::kSlot / 16;
             constexpr uint32_t kQStep = sizeof(sm.q[0]) / 16;
@@ -716,7 +733,10 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     const uint64_t a = v_operand<D>(ring0 + slot * kStep);
 #pragma unroll
                     for (int s = 0; s < kTile / 32; ++s)
-                        mma_ss(o_addr, a + s * (32 * D / 16), p_op + s * (32 * kP / 16), kIdescPV, !fresh || s > 0);
+#pragma unroll
+                        for (int i = 0; i < weight_products(R); ++i)
+                            mma_ss(o_addr, a + s * (32 * D / 16), p_op + i * (kTile * kP / 16) + s * (32 * kP / 16),
+                                   kIdescPV, !fresh || s > 0 || i > 0);
                     tc_commit(smem_addr(&sm.pv_done[it & 1]));
                     tc_commit(smem_addr(&sm.empty[slot]));
                 }
@@ -773,13 +793,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                 for (int r = 0; r < HR / 2; ++r) l[r] = 0;
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.q_full[piece & 1]),
                                                              (piece >> 1) & 1, stalled));
-                if (token < HR) {
-                    const int r = grp * HR + token;
-                    sm.now_f[r] = sm.f[piece & 3][r];
-                    sm.ref[r] = 0.0f;
-                    sm.now_info[r] = sm.info[piece & 3][r];
-                    sm.now_see[r] = sm.see[piece & 3][r];
-                }
+                if (token < HR) sm.ref[grp * HR + token] = 0.0f;
                 // tiles that every row sees whole need no mask
                 const int first_pos = sm.see[piece & 3][0].x + sm.see[piece & 3][0].y;
                 const int last_lo = sm.see[piece & 3][rows - 1].x;
@@ -800,7 +814,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     t.n = sm.nums[num][my_block];
                     if (++num == kNums) num = 0;
                     const bool mask = token0 + kTile - 1 > first_pos || token0 < last_lo;
-                    ok = soften<D, R>(sm, grp, l, sm.tmem + lanes + 64 * (it & 1), o_addr, t, mask, k == 0, it,
+                    ok = soften<D, R>(sm, grp, piece & 3, l, sm.tmem + lanes + 64 * (it & 1), o_addr, t, mask, k, it,
                                        stalled) && ok;
                     tc_fence_before();
                     if (t.t >= stored) {         // a slot past the last token: 0 x NaN is NaN
@@ -830,7 +844,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                                                              ((it - 1) >> 1) & 1, stalled));
                 if (group_any(grp, !ok)) return false;
                 tc_fence_after();
-                finish<D, R>(A, sm, grp, o_addr, rows, pc.whole, blockIdx.x * 2 + (piece > 0), ws);
+                finish<D, R>(A, sm, grp, piece & 3, o_addr, rows, pc.whole, blockIdx.x * 2 + (piece > 0), ws);
                 return true;
             };
 #pragma unroll 1
@@ -854,7 +868,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
 template <int D, int R>
 int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 {
-    const size_t smem = sizeof(Smem<D, R>) + kSmemAlign;
+    const size_t smem = sizeof(Smem<D, R>);
     static bool ready[64] = {};               // opt-in to large shared memory, once per device
     if (!ready[device]) {
         const cudaError_t e = cudaFuncSetAttribute(attend_narrow_kernel<D, R>,

@@ -1,23 +1,27 @@
 // attend_wide.cu — dspark_attend on the tensor cores for prompts and large groups: units of up to
 // 128 rows, one row per TMEM lane.
-//   S [128 rows, 128 tokens] = (Q_hi + Q_lo) K^T       O [128 rows, D] += (W_hi + W_lo) V
-// the pieces' products adding up in the same columns.
+//   S [128 rows, 128 tokens] = (Q_1 + Q_2) K^T       O [128 rows, D] += W V
+// the queries' pieces adding up in the same columns, the weights in fp16.
 //
 // A CTA: warps 0-3 do the softmax, a thread per row, warp 4 loads pages with TMA (one box per page
 // and K or V, swizzled), warp 5 issues the products. As in the narrow kernel a row's weights are
 // taken over a reference that may lag its maximum: the scores pass through registers once, and
-// only a tile in which some row of a warp passes its reference by kBehind, or a unit's first, stops
-// to find the maxima and rescale the sums. Two or four threads per row were slower (617 and 677 us
-// for 570 below): what a warp does once per tile, waits, votes, numbers, costs it as much as its
-// elements, and one row's threads have to agree on a reference.
+// only a tile in which some row of a warp passes its reference by kBehind or, where that is looked
+// at, lies far below it, or a unit's first, stops to change references and rescale the sums. Two or
+// four threads per row were slower (617 and 677 us, where one took 570): what a warp does once per
+// tile, waits, votes, numbers, costs it as much as its elements, and one row's threads have to agree
+// on a reference.
+// The values are widened to fp16 in shared memory (exact), a token by each softmax thread, while the
+// weights are one fp16 number each. Here the rows are many: for 128 of them three e5m2 pieces per
+// weight cost 610 us for 509 (splitting them), and two e4m3 pieces, 508, end at 2^-16 of the largest.
 // The weights go through shared memory, so that a tile's scores leave TMEM as soon as they are read
 // and the next tile's products run under this one's softmax (as an operand in TMEM they overlaid
 // the scores: 705 us for 641); 128 + D columns, so two CTAs fit and one's softmax runs under the
 // other's. What a piece needs to be known by lives in shared memory: a thread holds 128 scores.
 //
-// Bound: sixteen products of 101 cycles a tile at D = 128, 1616 cycles a tile and SM, and the
+// Bound: sixteen products of about 101 cycles a tile at D = 128, 1616 cycles a tile and SM, and the
 // softmax, which takes a CTA about 4250 cycles a tile, 2100 with two of them. Two prompts' pieces of
-// about 2000 rows, 32 query heads of 128 over 8 heads, after 4 to 8 thousand tokens: 508 us, 0.93
+// about 2000 rows, 32 query heads of 128 over 8 heads, after 4 to 8 thousand tokens: 509 us, 0.93
 // PFLOP/s of the plain form's 16-bit products. Its registers are tight: ptxas places the same
 // source's scores well or badly (640 us with the queries loaded in two halves).
 #include "attend_mma.cuh"
@@ -28,12 +32,6 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kSoft = kRows;                 // softmax threads: one per row
 constexpr int kThreads = kSoft + 64;
-constexpr int kNums = 4;
-// Weights are 2^(x - m + kUp), m lagging by at most kBehind: at most 2^8.5 < 448, and a weight
-// is within 2^-8 of itself or 2^-16 of the largest. Room for a longer lag (2.5 -> 6.5) would give 2 %
-// and cost the small weights four bits.
-constexpr float kUp = 6.0f;
-constexpr float kBehind = 2.5f;
 
 template <int D>
 struct Smem {
@@ -42,26 +40,32 @@ struct Smem {
     // slot is free for a whole softmax, V's until the end of the next one.
     static constexpr int kSlots = D == 128 ? 2 : 4;
     uint8_t q[2][kTile * D];                             // the queries' two pieces
-    uint8_t w[2][kRows * kTile];                         // the weights'
+    uint8_t w[2][kRows * kTile];                         // the weights in fp16, 64 tokens each
     uint8_t ring[kSlots][kSlot];
+    // The tile's values in fp16, 64 elements each. At D = 128 the first 64 take the place of V's codes in
+    // the ring: a thread widens the 128 bytes of its own token, there and here.
+    uint8_t wide[kTile * 128];
     // A tile's numbers are written once K's slot is free, kSlots / 2 tiles ahead at most, and read
     // until the tile's softmax ends: kNums slots cover kSlots / 2 + 1 tiles and the one being written.
+    static constexpr int kNums = kSlots / 2 + 2;
     BlockNums nums[kNums][kBlocks];
-    float f[kRows];                                      // score factors: scale log2(e) 2^e
+    int8_t e[kRows];                                     // the rows' exponents; kNotFine: a query that is not finite
+    uint8_t after[kRows];                                // their positions after the unit's first
     uint64_t full[kSlots], empty[kSlots];
     uint64_t s_full, s_read, p_full, pv_done, q_full;
-    Cut<kRows> cut;
+    Cut<kRows> cut;        // its scan: afterwards how far the rows' references went down
     // The softmax threads' piece: here rather than in registers, which the scores need.
     Walk<kRows> soft;
     struct {
         int k0, n;         // its tiles
-        int lo, hi;        // tokens from lo to hi are seen by all its rows
+        int lo, hi;        // tokens from lo to hi are seen by all its rows; hi is the first row's position
     } span;
     int stored;            // the request's tokens
-    int2 sees[kRows];      // a row sees tokens [x, x + y]
     uint32_t tmem;
     int stalled;       // a wait gave up: every role leaves its loop
 };
+
+constexpr int kNotFine = 127;
 
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // A barrier of the softmax threads, which says whether any of them says yes.
@@ -82,14 +86,15 @@ struct Row {
     float f;              // score factor: scale log2(e) 2^e of the row's pieces
     float ref;            // kUp - reference; 0: nothing seen yet
     float l;              // the sum
+    bool watch;           // a reference of the warp changed in the last tile
 };
 
 // One tile of this thread's row: scores in TMEM -> weights in shared memory.
 // False once a wait gave up.
 template <int D>
 __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int row,
-                                       const BlockNums* nums, int shift_page, int k, int it, bool ok,
-                                        volatile int* stalled)
+                                       const BlockNums* nums, int shift_page, int window, int k, int it, bool ok,
+                                       volatile int* stalled)
 {
     const uint32_t s_addr = sm.tmem + lanes;
     float x[kTile];
@@ -117,8 +122,9 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
     }
     const int token0 = (sm.span.k0 + k) * kTile;
     if (token0 + kTile - 1 > sm.span.hi || token0 < sm.span.lo) {
-        const int2 sees = sm.sees[row];
-        const uint32_t at = static_cast<uint32_t>(token0 - sees.x), span = static_cast<uint32_t>(sees.y);
+        const int pos = sm.span.hi + sm.after[row];
+        const int first = window > 0 && pos >= window ? pos - window + 1 : 0;
+        const uint32_t at = static_cast<uint32_t>(token0 - first), span = static_cast<uint32_t>(pos - first);
 #pragma unroll
         for (int j = 0; j < kTile; ++j)
             if (at + j > span) x[j] = -INFINITY;
@@ -129,14 +135,25 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
         for (int j = 4; j < kTile; ++j) m[j & 3] = fmaxf(m[j & 3], x[j]);
         top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     }
-    const bool stop = __any_sync(0xffffffffu, top > kUp + kBehind || r.ref == 0.0f);
+    const bool down = r.watch || look_down(k);
+    const bool stop = __any_sync(0xffffffffu, top > kUp + kBehind || r.ref == 0.0f || (down && top < kUp - kBelow));
+    r.watch = false;
     // the last tile's products read the weights' place and write the sums
     if (it > 0) ok = ok && mbar_wait(smem_addr(&sm.pv_done), (it - 1) & 1, stalled);
     ok = __all_sync(0xffffffffu, ok);
     if (stop) {
         float shift = 0.0f, g = 1.0f;
-        if (top > -INFINITY && (r.ref == 0.0f || top > kUp + kBehind)) {
-            float ref = r.ref - top + kUp;
+        if (top > -INFINITY && (r.ref == 0.0f || top > kUp + kBehind || top < kUp - kBelow)) {
+            // how far the reference lies under the row's largest, in whole steps, at most kDown
+            uint8_t& lowered = reinterpret_cast<uint8_t*>(sm.cut.scan)[row];
+            shift = kUp - top;
+            if (r.ref == 0.0f) {
+                lowered = 0;
+            } else {
+                if (shift > 0.0f) shift = floorf(fminf(shift, kDown - lowered));
+                lowered = static_cast<uint8_t>(max(0, lowered + static_cast<int>(ceilf(shift))));
+            }
+            float ref = r.ref + shift;
             if (ref == 0.0f) ref = 1e-30f;       // 0 stands for none
             shift = ref - r.ref;
             if (r.ref != 0.0f) {
@@ -145,6 +162,7 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
             }
             r.ref = ref;
         }
+        r.watch = __any_sync(0xffffffffu, shift != 0.0f);
 #pragma unroll
         for (int j = 0; j < kTile; j += 2) {
             const float2 y = unpack2(add2(pack2(x[j], x[j + 1]), pack2(shift, shift)));
@@ -180,23 +198,52 @@ __device__ __forceinline__ bool soften(Smem<D>& sm, Row& r, uint32_t lanes, int 
 #pragma unroll
             for (int k = 0; k < 4; ++k) y[j + k] = ex2_approx(y[j + k]);
             s2 = add2(s2, add2(pack2(y[j], y[j + 1]), pack2(y[j + 2], y[j + 3])));
-            uint16_t h0, h1, l0, l1;
-            split2(y[j], y[j + 1], &h0, &l0);
-            split2(y[j + 2], y[j + 3], &h1, &l1);
-            p[j / 4] = join16(h0, h1);
-            p[4 + j / 4] = join16(l0, l1);
+            p[j / 2] = pack_f16(y[j], y[j + 1]);
+            p[j / 2 + 1] = pack_f16(y[j + 2], y[j + 3]);
         }
         const float2 s = unpack2(s2);
         sum = fmaf(s.x + s.y, inv, sum);
-        const int at = row * kTile + (((g) / 16) ^ (row & 7)) * 16;
-        *reinterpret_cast<uint4*>(&sm.w[0][at]) = make_uint4(p[0], p[1], p[2], p[3]);
-        *reinterpret_cast<uint4*>(&sm.w[1][at]) = make_uint4(p[4], p[5], p[6], p[7]);
+        uint8_t* to = &sm.w[g / 64][row * kTile];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<uint4*>(to + (((g % 64) / 8 + i) ^ (row & 7)) * 16) =
+                make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
     }
     r.l += sum;
     return ok;
 }
 
-// A unit's queries as two pieces in shared memory, and their rows' factors: eight (four) lanes per
+// This thread's token of V's tile as fp16 (exact). Slots past the last token become zeros, whatever they
+// hold: 0 x NaN is NaN.
+template <int D>
+__device__ __forceinline__ void widen(Smem<D>& sm, uint8_t* slot, int token, bool live)
+{
+    uint4 c[D / 16];
+    const uint8_t* raw = slot + token * D;
+    const int swz = D == 128 ? token & 7 : (token >> 1) & 3;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        c[i] = *reinterpret_cast<const uint4*>(raw + ((i ^ swz) << 4));
+        if (!live) c[i] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        const uint32_t in[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[2 * k]) : "h"(static_cast<uint16_t>(in[k] & 0xffffu)));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[2 * k + 1]) : "h"(static_cast<uint16_t>(in[k] >> 16)));
+        }
+        uint8_t* to = (D == 128 && i < 4 ? slot : sm.wide) + token * 128;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<uint4*>(to + (((2 * i + k) ^ token) & 7) * 16) =
+                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+    }
+}
+
+// A unit's queries as two pieces in shared memory, and their rows' exponents: eight (four) lanes per
 // row with 16 elements each. Rows past the unit's are zeros. All loads come first.
 template <int D>
 __device__ __forceinline__ void load_queries(const AttendCall& A, Smem<D>& sm, const Walk<kRows>& wk, int rows)
@@ -249,8 +296,7 @@ __device__ __forceinline__ void load_queries(const AttendCall& A, Smem<D>& sm, c
         const int chunk = seg ^ (D == 128 ? row & 7 : (row >> 1) & 3);
         *reinterpret_cast<uint4*>(&sm.q[0][row * D + chunk * 16]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(&sm.q[1][row * D + chunk * 16]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        // a query that is not finite makes its row's factor, hence its results, NaN
-        if (seg == 0) sm.f[row] = fine ? A.scale * kLog2e * exp2i(e) : __int_as_float(0x7fc00000);
+        if (seg == 0) sm.e[row] = static_cast<int8_t>(fine ? e : kNotFine);
     };
     constexpr int kPasses = kRows / kStep;
     uint4 v[kPasses][2];
@@ -312,13 +358,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__ CUtensorMap k_map,
                    const __grid_constant__ CUtensorMap v_map)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
-    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(
-        raw + ((kSmemAlign - (smem_addr(raw) & (kSmemAlign - 1))) & (kSmemAlign - 1)));
-    constexpr int kSlots = Smem<D>::kSlots;
+    extern __shared__ __align__(kSmemAlign) unsigned char raw[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
+    static_assert(sizeof(Smem<D>) <= kSmemTwo, "two CTAs per SM");
+    constexpr int kSlots = Smem<D>::kSlots, kNums = Smem<D>::kNums;
     constexpr int kLoader = kSoft / 32, kIssuer = kLoader + 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Workspace ws = workspace_of(A.ws);
+    if (!smem_aligned(A, ws, raw)) return;
 
     if (tid == 0) {
         for (int s = 0; s < kSlots; ++s) {
@@ -439,10 +486,14 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
             const bool leader = elect_one();
             constexpr uint32_t kIdesc = (1u << 4) | (kTile / 16 << 24);
             constexpr uint32_t kIdescQK = kIdesc | (kTile / 8 << 17);
-            constexpr uint32_t kIdescPV = kIdesc | (D / 8 << 17) | (1u << 16);   // V: dim contiguous
+            constexpr uint32_t kIdescPV = kIdesc | (D / 8 << 17) | (1u << 16);   // fp16; V: dim contiguous
             const uint32_t s_addr = sm.tmem, o_addr = sm.tmem + kTile;
             const uint64_t ring0 = operand<D>(smem_addr(sm.ring[0])), q_op = operand<D>(smem_addr(sm.q[0]));
             const uint64_t w_op = operand<kTile>(smem_addr(sm.w[0]));
+            // V in fp16: 64 elements at the ring's slot, the next 64 one slot on, which is `wide`
+            static_assert(D == 64 || (Smem<D>::kSlots == 2 && Smem<D>::kSlot == kTile * 128), "V's slot is the last");
+            const uint64_t v_op = operand<128>(smem_addr(D == 128 ? sm.ring[kSlots - 1] : sm.wide)) &
+                                  ~(0x3fffull << 16) | (static_cast<uint64_t>(kTile * 128 / 16) << 16);
             constexpr uint32_t kStep = Smem<D>::kSlot / 16;
             int it = 0, piece = 0;
             bool ok = true;
@@ -480,13 +531,10 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                         if (!ok) break;
                         tc_fence_after();
                         if (leader) {
-                            const uint64_t vb = ring0 + s * kStep;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int p = 0; p < 2; ++p)
-                                    mma_ss(o_addr, w_op + p * (kRows * kTile / 16) + 2 * i, vb + i * (32 * D / 16),
-                                           kIdescPV, k > 1 || i > 0 || p > 0);
+                            for (int i = 0; i < kTile / 16; ++i)
+                                mma_ss_f16(o_addr, w_op + i / 4 * (kRows * kTile / 16) + i % 4 * 2,
+                                           v_op + i * (16 * 128 / 16), kIdescPV, k > 1 || i > 0);
                             tc_commit(smem_addr(&sm.pv_done));
                             tc_commit(smem_addr(&sm.empty[s]));
                         }
@@ -518,12 +566,11 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                     load_queries<D>(A, sm, now, rows);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive(smem_addr(&sm.q_full));
-                    const int pos = now.len + (now.qt * kRows + min(row, rows - 1)) / A.group;
-                    const int lo = A.window > 0 && pos >= A.window ? pos - A.window + 1 : 0;
-                    sm.sees[row] = make_int2(lo, pos - lo);
+                    const int i0 = now.qt * kRows / A.group;
+                    sm.after[row] = static_cast<uint8_t>((now.qt * kRows + min(row, rows - 1)) / A.group - i0);
                     // tiles that every row sees whole need no mask: those within [hi lo, lo pos]
                     if (tid == 0) {
-                        const int p0 = now.len + now.qt * kRows / A.group;
+                        const int p0 = now.len + i0;
                         const int p1 = now.len + (now.qt * kRows + rows - 1) / A.group;
                         const int lo1 = A.window > 0 && p1 >= A.window ? p1 - A.window + 1 : 0;
                         sm.span.k0 = now.k0;
@@ -534,7 +581,10 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                     }
                 }
                 soft_sync();
-                Row r = {sm.f[row], 0.0f, 0.0f};
+                // a query that is not finite makes its row's factor, hence its results, NaN
+                const int e = sm.e[row];
+                Row r = {e == kNotFine ? __int_as_float(0x7fc00000) : A.scale * kLog2e * exp2i(e), 0.0f, 0.0f,
+                         false};
                 const int n = sm.span.n;
                 // a warp whose wait gave up goes on to the piece's end, where the warps agree on it:
                 // they share the barriers within
@@ -543,18 +593,12 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                     ok = ok && mbar_wait(smem_addr(&sm.s_full), it & 1, stalled);
                     ok = __all_sync(0xffffffffu, ok);
                     tc_fence_after();
-                    ok = soften<D>(sm, r, lanes, row, sm.nums[it % kNums], shift_page, k, it, ok, stalled);
-                    const int token0 = (sm.span.k0 + k) * kTile;
-                    if (token0 + kTile > sm.stored) {   // slots past the last token: 0 x NaN is NaN
-                        const int use = 2 * it + 1, s = use % kSlots;
-                        ok = ok && mbar_wait(smem_addr(&sm.full[s]), (use / kSlots) & 1, stalled);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (token0 + row >= sm.stored) {
-                            uint4* v = reinterpret_cast<uint4*>(&sm.ring[s][row * D]);
-#pragma unroll
-                            for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
-                        }
-                    }
+                    ok = soften<D>(sm, r, lanes, row, sm.nums[it % kNums], shift_page, A.window, k, it, ok,
+                                   stalled);
+                    const int use = 2 * it + 1, s = use % kSlots;
+                    ok = ok && mbar_wait(smem_addr(&sm.full[s]), (use / kSlots) & 1, stalled);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok) widen<D>(sm, sm.ring[s], row, (sm.span.k0 + k) * kTile + row < sm.stored);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     tc_fence_before();
                     __syncwarp();
@@ -587,7 +631,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
 template <int D>
 int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 {
-    const size_t smem = sizeof(Smem<D>) + kSmemAlign;
+    const size_t smem = sizeof(Smem<D>);
     static bool ready[64] = {};               // opt-in to large shared memory, once per device
     if (!ready[device]) {
         const cudaError_t e = cudaFuncSetAttribute(attend_wide_kernel<D>,

@@ -116,3 +116,43 @@ class Sink:
 def test_log_sum_of_many_equal_weights(lib, w, at):
     """Equal addends round the same way every time: one fp32 sum over all tokens would drift."""
     Sink(131072, 0.95, w, 128, 4, True, at=at).check(out_too=False)
+
+
+WINDOWS = [1, 4, 8, 40]                      # 4, 16, 32 and 160 (position, head) rows of a cache head
+
+
+@gpu
+@pytest.mark.parametrize("flat", [True, False])
+@pytest.mark.parametrize("share", [0.5, 0.9, 0.95, 0.999])
+@pytest.mark.parametrize("w", WINDOWS)
+@pytest.mark.parametrize("context", [8192, 32768, 131072])
+def test_sink_and_long_tail(lib, context, w, share, flat):
+    top = Sink(context, share, w, 128, 4, flat).check()
+    assert 0.2 < float(top.mean()) < 0.9999
+
+
+@gpu
+@pytest.mark.parametrize("flat", [True, False])
+@pytest.mark.parametrize("w", WINDOWS)
+@pytest.mark.parametrize("at", [700, 100001, (0, 130), (0, 1, 2, 3), (5, 3000)])
+def test_sinks_elsewhere_and_several(lib, at, w, flat):
+    Sink(131072, 0.95, w, 128, 4, flat, at=at).check()
+
+
+@gpu
+@pytest.mark.parametrize("share", [0.5, 0.9])
+@pytest.mark.parametrize("w", WINDOWS)
+@pytest.mark.parametrize("at", [0, 1000])
+def test_sink_in_64_wide_heads(lib, at, w, share):
+    Sink(20000, share, w, 64, 4, True, at=at, page=16).check()
+    Sink(20000, share, w, 64, 4, False, at=at, page=128).check()
+
+
+@gpu
+@pytest.mark.parametrize("context", [60, 127, 300, 2000])
+@pytest.mark.parametrize("w", WINDOWS)
+def test_sink_over_short_contexts(lib, w, context):
+    """The tail shares the dominant token's tile."""
+    for share in (0.9, 0.95, 0.99, 0.999):
+        for flat in (True, False):
+            Sink(context, share, w, 128, 4, flat, page=32).check()
