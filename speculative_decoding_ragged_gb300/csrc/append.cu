@@ -1,7 +1,7 @@
 // append.cu — dspark_append: a step's keys and values, rotated, quantised and written to the
 // paged 8-bit cache, its queries rotated on the way.
 //
-// A block is one page's slots of one kv head; its scale is a power of two, so that growing it
+// A block is one page's slots of one kv head; the scale given to it is a power of two, so that growing it
 // rescales the codes already there by an exact shift of their exponent (only codes that leave
 // e4m3's normal range round again), and multiplying by it is exact. The step's rows that fall
 // into one block are consecutive packed rows; the first of them leads. One warp, or for prompts a
@@ -53,6 +53,25 @@ struct AppendArgs {
     int q_rows;           // rows a query CTA rotates
     int32_t* status;
 };
+
+// Scales are powers of two unless the cache was filled elsewhere: products and quotients are then
+// exact in fp32. Else these give an fp32 number on the exact value's side of every border between two
+// codes (which have five bits at most), so that its code is the exact value's.
+__device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
+// x s: cut off, the last bit set where that lost anything.
+__device__ __forceinline__ float sided_product(float x, float s)
+{
+    const float p = __fmul_rz(x, s);
+    return fmaf(x, s, -p) != 0.0f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
+}
+// x / s, inv = 1 / s: the product, off by a few last places, goes to the nearest multiple of 64 of
+// them, then one step towards what the exact remainder says.
+__device__ __forceinline__ float sided_quotient(float x, float s, float inv)
+{
+    const uint32_t near = (__float_as_uint(x * inv) + 32u) & ~63u;
+    const float rest = fmaf(-__uint_as_float(near), s, x);
+    return __uint_as_float(rest == 0.0f ? near : (rest < 0.0f) == (x < 0.0f) ? near + 1u : near - 1u);
+}
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
@@ -172,6 +191,19 @@ __device__ __forceinline__ void store_unit(uint8_t* row, const Unit<VEC>& un, co
     }
 }
 
+// The same for any scale.
+template <bool VEC>
+__device__ __forceinline__ void store_exact(uint8_t* row, const Unit<VEC>& un, float* x, float scale)
+{
+    float inv = 1.0f / scale;
+    if (!power_of_two(scale)) {
+#pragma unroll
+        for (int j = 0; j < Unit<VEC>::N; ++j) x[j] = sided_quotient(x[j], scale, inv);
+        inv = 1.0f;
+    }
+    store_unit<VEC>(row, un, x, inv);
+}
+
 // A team: T warps that share a block, 1 or 4.
 template <int T>
 __device__ __forceinline__ void team_sync()
@@ -221,7 +253,8 @@ __device__ __forceinline__ float settle_scale(float amax, float old, float* scal
             for (int k = 0; k < 4; ++k) {
                 float f[4];
                 e4m3x4_to_f32(w[k], f);
-                o[k] = e4m3x4(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+                o[k] = e4m3x4(sided_product(f[0], ratio), sided_product(f[1], ratio),
+                              sided_product(f[2], ratio), sided_product(f[3], ratio));
             }
             kept[i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -335,8 +368,8 @@ __device__ __forceinline__ int append_blocks(const AppendArgs& A, int64_t r, int
             }
             amax = team_max<T>(amax, red);
         }
-        const float inv = 1.0f / settle_scale<T>(amax, old, scale, codes, slot0 * c.dim, me);
-        if (clean) {
+        const float s = settle_scale<T>(amax, old, scale, codes, slot0 * c.dim, me), inv = 1.0f / s;
+        if (clean && power_of_two(s)) {
 #pragma unroll
             for (int i = 0; i < kKeep; ++i)
                 if (has && k0 + i * step < n) {
@@ -351,12 +384,12 @@ __device__ __forceinline__ int append_blocks(const AppendArgs& A, int64_t r, int
                 one.load(mine0 + i * hop, 0, un);
                 one.get(x);
                 turn_unit<VEC, true>(rope, un, tab + k * half, x);
-                store_unit<VEC>(to + i * step * c.dim, un, x, inv);
+                store_exact<VEC>(to + i * step * c.dim, un, x, s);
             }
         }
         return bad ? DSPARK_STATUS_BAD_VALUE : 0;
     }
-    float inv = 0.0f;
+    float s = 1.0f;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
@@ -374,14 +407,14 @@ __device__ __forceinline__ int append_blocks(const AppendArgs& A, int64_t r, int
                     one.get(x);
                     bad |= turn_unit<VEC, true>(rope, at, tab + k * half, x);
                     if (pass == 0) amax = amax_unit<VEC>(x, amax);
-                    else store_unit<VEC>(to + (from + k - k0) * c.dim, at, x, inv);
+                    else store_exact<VEC>(to + (from + k - k0) * c.dim, at, x, s);
                 }
             }
         }
         if (pass == 0 && works) {
             const float old = slot0 > 0 ? *scale : 0.0f;
             amax = team_max<T>(amax, red);
-            inv = 1.0f / settle_scale<T>(amax, old, scale, codes, slot0 * c.dim, me);
+            s = settle_scale<T>(amax, old, scale, codes, slot0 * c.dim, me);
         }
     }
     return bad ? DSPARK_STATUS_BAD_VALUE : 0;
