@@ -486,7 +486,8 @@ int dspark_rotate(const void* x, int64_t x_stride, void* y, int64_t y_stride, ds
  * must not be shared with another request.
  * k, v [rows, heads, dim], bf16 or fp32 (dtype), row strides in elements as in dspark_rotate;
  * row_req, row_pos [rows] int32; lengths [B] int32, tokens in the cache before this call's rows.
- * A request or position out of range (row_req >= B, row_pos < 0) flags DSPARK_STATUS_BAD_ROWS, a
+ * A request or position out of range (row_req >= B, row_pos < 0), or a row that is neither its
+ * request's first, nor the first of a page, nor after the row before it, flags DSPARK_STATUS_BAD_ROWS, a
  * length that is negative or passes int32 DSPARK_STATUS_BAD_LENGTH, a page id outside
  * [0, n_pages) or a block >= width DSPARK_STATUS_BAD_PAGE; those rows are not stored.
  * One kernel, or (prompts, with queries) two side by side; a block belongs to one team

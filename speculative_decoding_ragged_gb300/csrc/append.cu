@@ -437,12 +437,19 @@ __device__ __forceinline__ int append_rows(const AppendArgs& A, float2* tab, flo
 #pragma unroll 1
     for (int from = 0; from < A.chunk; from += 32) {
         const int64_t r = row0 + from + lane;
-        int b = -1, pos = 0, i = 0;
+        int b = -1, pos = 0, i = 0, before_b = -1, before_i = 0;
         if (from + lane < A.chunk && r < A.rows) {
+            if (share == 0 && r > 0) {
+                before_b = A.row_req[r - 1];
+                before_i = A.row_pos[r - 1];
+            }
             b = row_owner(A, r, &pos, &bits);
             if (b >= 0) i = A.row_pos[r];
         }
-        unsigned leads = __ballot_sync(0xffffffffu, b >= 0 && (i == 0 || (pos & (A.c.page - 1)) == 0));
+        const bool lead = b >= 0 && (i == 0 || (pos & (A.c.page - 1)) == 0);
+        // a row that neither leads nor follows its request's last one is nobody's: not stored
+        if (share == 0 && b >= 0 && !lead && (before_b != b || before_i != i - 1)) bits |= DSPARK_STATUS_BAD_ROWS;
+        unsigned leads = __ballot_sync(0xffffffffu, lead);
 #pragma unroll 1
         while (leads != 0) {
             const int k = __ffs(leads) - 1;
