@@ -869,8 +869,9 @@ template <int D, int R>
 int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 {
     const size_t smem = sizeof(Smem<D, R>);
-    static bool ready[64] = {};               // opt-in to large shared memory, once per device
-    if (!ready[device]) {
+    // opt-in to large shared memory, once per device and host thread: threads share no state
+    static thread_local int ready_device = -1;
+    if (ready_device != device) {
         const cudaError_t e = cudaFuncSetAttribute(attend_narrow_kernel<D, R>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
@@ -878,7 +879,7 @@ int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
             cudaGetLastError();
             return fail(DSPARK_ERR_CUDA, "dspark attend: %s", cudaGetErrorString(e));
         }
-        ready[device] = true;
+        ready_device = device;
     }
     if (!places_fit<R>(A))
         return fail(DSPARK_ERR_UNSUPPORTED, "dspark_attend: rows, heads and pages beyond what one call can cut");
