@@ -482,8 +482,9 @@ int dspark_rotate(const void* x, int64_t x_stride, void* y, int64_t y_stride, ds
  * request are left as they are.
  *
  * Rows are as dspark_pack writes them: a request's rows consecutive, row_pos 0, 1, 2, ...;
- * row_req -1 is padding. No two requests of a call may write one page, and a page that is written
- * must not be shared with another request.
+ * row_req -1 is padding. dspark_pack leaves the rows past its tier as they were: a call over more
+ * rows than the tier needs row_req -1 in them. No two requests of a call, and no two runs of rows of
+ * one request, may write one page, and a page that is written must not be shared with another request.
  * k, v [rows, heads, dim], bf16 or fp32 (dtype), row strides in elements as in dspark_rotate;
  * row_req, row_pos [rows] int32; lengths [B] int32, tokens in the cache before this call's rows.
  * A request or position out of range (row_req >= B, row_pos < 0), or a row that is neither its

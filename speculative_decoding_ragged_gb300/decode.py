@@ -22,8 +22,19 @@ from . import _binding as bd
 from .step import DSparkStep
 
 
+def packed_owners(row_req, cu_seqlens):
+    """row_req with -1 in the rows at or past cu_seqlens[B]: dspark_pack leaves those past its tier as
+    they were, which is an earlier step's owners."""
+    index = torch.arange(row_req.numel(), dtype=torch.int32, device=row_req.device)
+    return torch.where(index < cu_seqlens[-1], row_req, -1).to(torch.int32)
+
+
 class CachedAttention:
-    """One layer's cache and the buffers its calls need; `rows` is the most rows of a call."""
+    """One layer's cache and the buffers its calls need; `rows` is the most rows of a call.
+
+    Rows at or past cu_seqlens[B] are padding, whatever row_req says of them (dspark_pack leaves
+    those past its tier as they were): two small kernels before the calls see to it. Where many
+    layers share the rows, `owned=True` spares them: row_req is then packed_owners' already."""
 
     def __init__(self, rows: int, q_heads: int, kv_heads: int, dim: int, table: torch.Tensor,
                  n_pages: int, page: int, rope: Optional[bd.Rope] = None, *, window: int = 0,
@@ -34,22 +45,36 @@ class CachedAttention:
         self.turned = torch.zeros(rows, q_heads, dim, dtype=dtype, device=dev)
         self.out = torch.zeros(rows, q_heads, dim, dtype=dtype, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.owners = torch.full((rows,), -1, dtype=torch.int32, device=dev)
+        self.index = torch.arange(rows, dtype=torch.int32, device=dev)
+        self.live = torch.zeros(rows, dtype=torch.bool, device=dev)
+        self.nobody = torch.tensor(-1, dtype=torch.int32, device=dev)
         need = bd.dspark_attend_workspace_bytes(kv_heads, dim)
         self.workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
 
-    def prepare(self, q, k, v, row_req, row_pos, cu_seqlens, lengths):
-        """The two calls for these tensors (which stay alive and in place), checked once."""
+    def prepare(self, q, k, v, row_req, row_pos, cu_seqlens, lengths, *, owned=False):
+        """The calls for these tensors (which stay alive and in place), checked once."""
         rows = q.shape[0]
         turned, out = self.turned[:rows], self.out[:rows]
-        return [bd.dspark_append(self.cache, k, v, row_req, row_pos, lengths, rope=self.rope, q=q,
-                                 q_out=turned, status=self.status, prepare=True),
-                bd.dspark_attend(self.cache, turned, out, cu_seqlens, lengths, self.workspace,
-                                 window=self.window, status=self.status, prepare=True)]
+        calls = []
+        if not owned:
+            given, last = row_req[:rows], cu_seqlens[-1:]
+            row_req, index, live = self.owners[:rows], self.index[:rows], self.live[:rows]
 
-    def run(self, q, k, v, row_req, row_pos, cu_seqlens, lengths):
+            def owners():
+                torch.lt(index, last, out=live)
+                torch.where(live, given, self.nobody, out=row_req)
+            calls.append(owners)
+        return calls + [
+            bd.dspark_append(self.cache, k, v, row_req, row_pos, lengths, rope=self.rope, q=q,
+                             q_out=turned, status=self.status, prepare=True),
+            bd.dspark_attend(self.cache, turned, out, cu_seqlens, lengths, self.workspace,
+                             window=self.window, status=self.status, prepare=True)]
+
+    def run(self, q, k, v, row_req, row_pos, cu_seqlens, lengths, *, owned=False):
         """Packed rows in, attention out ([rows, q_heads, dim], overwritten by the next call);
         lengths: tokens in the cache before these rows."""
-        for call in self.prepare(q, k, v, row_req, row_pos, cu_seqlens, lengths):
+        for call in self.prepare(q, k, v, row_req, row_pos, cu_seqlens, lengths, owned=owned):
             call()
         return self.out[:q.shape[0]]
 
