@@ -435,7 +435,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                 for (int k = 0; ok && k < wk.n; ++k, ++it) {
                     const int j0 = first_block + k * per_tile - base;   // this tile's first lane
                     if (j0 == 0 && base + 32 + lane < end_block) next_id = id_of(base + 32 + lane);
-                    if (j0 == per_tile || (per_tile == 32 && j0 == 0)) next_sc = nums_of(next_id);
+                    if (j0 == per_tile) next_sc = nums_of(next_id);
                     const int src = j0 + (lane & (per_tile - 1));
                     const int my_id = __shfl_sync(0xffffffffu, id, src);
                     const float ks = __shfl_sync(0xffffffffu, sc.x, src);
