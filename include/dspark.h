@@ -37,10 +37,12 @@
  *     kernel of this library is writing at that moment: confidences, cost tables, block
  *     tokens, logits and, in a verify call's second kernel, windows, cu_seqlens and the
  *     history lengths out_len (that kernel starts early only after the call's first kernel,
- *     which writes none of them, has itself waited for everything before it). Tiers and every
- *     output wait for the previous kernel. A kernel of the caller's that precedes a call on
- *     the stream and triggers its dependents early (griddepcontrol.launch_dependents) must
- *     have written those inputs before it triggers; kernels launched without that trigger
+ *     which writes none of them, has itself waited for everything before it). So does the second
+ *     kernel of dspark_append over prompts with its inputs, and it writes q_out: it starts only
+ *     after the call's first kernel, which touches none of these rows' queries, has waited. Tiers
+ *     and every other output wait for the previous kernel. A kernel of the caller's that precedes
+ *     a call on the stream and triggers its dependents early (griddepcontrol.launch_dependents)
+ *     must have written those inputs before it triggers; kernels launched without that trigger
  *     need nothing.
  *   - Return value: DSPARK_OK, or a negative DSPARK_ERR_* code when the host-side argument check
  *     or the kernel launch failed. On error nothing was enqueued (argument errors) or the launch
@@ -81,8 +83,8 @@ extern "C" {
 #define DSPARK_STATUS_BAD_ROWS       0x20 /* a request's rows lie outside the verified rows      */
 #define DSPARK_STATUS_BAD_TOKEN      0x40 /* a draft id outside [0,V): treated as rejected       */
 #define DSPARK_STATUS_BAD_LENGTH     0x80 /* accept_len / out_len outside range: clamped         */
-#define DSPARK_STATUS_STALL         0x100 /* a bounded in-kernel wait gave up: this call's verify
-                                             results are invalid (not expected in operation)   */
+#define DSPARK_STATUS_STALL         0x100 /* a bounded in-kernel wait gave up: the verify or attend
+                                             call's results are invalid (not expected)         */
 #define DSPARK_STATUS_BAD_PAGE      0x200 /* a page id or block outside the cache: not stored, or
                                              its tokens not attended to                        */
 #define DSPARK_STATUS_BAD_VALUE     0x400 /* a non-finite key or value: stored as 0              */
