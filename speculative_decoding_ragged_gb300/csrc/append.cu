@@ -15,10 +15,10 @@
 // between the maximum and the codes where they fit (8 rows of 128 for a warp, 64 for a prompt's
 // four); else they are read again.
 // Bound for a step by the chain of dependent loads (row owner, length, page id, scale, retained
-// codes): one window of 4 rows, 8 heads of 128 and 32 query heads, 4.4 us, 256 windows 12.9 us (3.9 at
+// codes): one window of 4 rows, 8 heads of 128 and 32 query heads, 4.4 us, 256 windows 12.8 us (3.9 at
 // the copy rate). For prompts by bandwidth in the queries (36 us of 200 MB), which start when the
 // keys' and values' CTAs are all running, and by the chain and the factors in those (40 us of 74 MB):
-// three prompts, 12 thousand rows in all, 75.7 us. Both kinds of CTAs mixed in one launch took 90 us:
+// three prompts, 12 thousand rows in all, 73.9 us. Both kinds of CTAs mixed in one launch took 90 us:
 // the queries need more warps than the others leave.
 #include "cache.cuh"
 #include "rope.cuh"

@@ -149,9 +149,9 @@ int launch_attend_mma(const AttendCall& A, cudaStream_t stream)
     if (rc != DSPARK_OK) return rc;
     const int ctas = dev.sm_count * 2 < kMaxCtas ? dev.sm_count * 2 : kMaxCtas;
     // By the requests' average of (position, head) rows: up to 32 the narrow kernel (64 requests over
-    // 2048 tokens, 8 heads of 128: at 16 rows 73 us, wide 124; at 32 84 and 130), where it takes one
-    // unit per request and head. From 33 to 64, two units, the two are within 5 % of each other
-    // (48 rows: 132 and 134; 256 requests over 512: 192 and 179), then wide (128 rows: 235 and 160).
+    // 2048 tokens, 8 heads of 128: at 16 rows 74 us, wide 120; at 32 87 and 126), where it takes one
+    // unit per request and head. From 33 on, two units and more, wide (48 rows: 138 and 131; 256 requests
+    // over 512: 206 and 175; 128 rows: 248 and 155).
     const bool narrow = static_cast<int64_t>(A.rows) * A.group <= 32ll * A.B;
     rc = narrow ? launch_attend_narrow(A, ctas, dev.device, stream)
                 : launch_attend_wide(A, ctas, dev.device, stream);

@@ -47,7 +47,7 @@ constexpr float kBehind = 6.5f;
 // largest. So that a long tail of small weights after a dominant token keeps its bits, the reference
 // also goes down, to a tile whose maximum lies kBelow under it: looked at after a tile that makes that
 // likely, and every kLook tiles. The sums grow then: by at most 2^kDown in all over what the largest
-// reference made them. It costs 2 us of 117 and 3 us of 509 in the two cases above.
+// reference made them. It costs 2 us of 116 and 3 us of 507 in the two cases above.
 constexpr float kBelow = 9.0f;
 constexpr float kDown = 32.0f;
 constexpr int kLook = 16;

@@ -13,7 +13,7 @@
 // on a reference.
 // The values are widened to fp16 in shared memory (exact), a token by each softmax thread, while the
 // weights are one fp16 number each. Here the rows are many: for 128 of them three e5m2 pieces per
-// weight cost 610 us for 509 (splitting them), and two e4m3 pieces, 508, end at 2^-16 of the largest.
+// weight cost 610 us for 507 (splitting them), and two e4m3 pieces, 508, end at 2^-16 of the largest.
 // The weights go through shared memory, so that a tile's scores leave TMEM as soon as they are read
 // and the next tile's products run under this one's softmax (as an operand in TMEM they overlaid
 // the scores: 705 us for 641); 128 + D columns, so two CTAs fit and one's softmax runs under the
@@ -21,7 +21,7 @@
 //
 // Bound: sixteen products of about 101 cycles a tile at D = 128, 1616 cycles a tile and SM, and the
 // softmax, which takes a CTA about 4250 cycles a tile, 2100 with two of them. Two prompts' pieces of
-// about 2000 rows, 32 query heads of 128 over 8 heads, after 4 to 8 thousand tokens: 509 us, 0.93
+// about 2000 rows, 32 query heads of 128 over 8 heads, after 4 to 8 thousand tokens: 507 us, 0.93
 // PFLOP/s of the plain form's 16-bit products. Its registers are tight: ptxas places the same
 // source's scores well or badly (640 us with the queries loaded in two halves).
 #include "attend_mma.cuh"
