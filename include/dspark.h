@@ -19,6 +19,10 @@
  *   dspark_attend    the rows' queries -> attention over that cache
  *   dspark_rotate    rotary positions over rows of heads, and their inverse
  *
+ * and, between its logits and dspark_verify,
+ *
+ *   dspark_adjust    penalties for repeated tokens, biases and grammar masks on the rows' logits
+ *
  * Source of the method: "DSpark in SGLang: Speculative Decoding with Confidence-Driven,
  * Variable-Length Verification" (LMSYS blog, as summarised by papercache.org), sections
  * "A2 method details" (confidence scheduler, verify modes, ragged verify over full CUDA graphs,
@@ -87,13 +91,17 @@ extern "C" {
                                              call's results are invalid (not expected)         */
 #define DSPARK_STATUS_BAD_PAGE      0x200 /* a page id or block outside the cache: not stored, or
                                              its tokens not attended to                        */
-#define DSPARK_STATUS_BAD_VALUE     0x400 /* a non-finite key or value: stored as 0              */
+#define DSPARK_STATUS_BAD_VALUE     0x400 /* a non-finite key or value: stored as 0; a penalty or
+                                             bias that is none: left out                         */
+#define DSPARK_STATUS_NO_TOKEN      0x800 /* a mask that allows no token: its row is all -inf    */
 
 /* ---- limits of the library ----------------------------------------------------------- */
 #define DSPARK_MAX_GAMMA        32     /* block width                                         */
 #define DSPARK_MAX_CANDIDATES   16384  /* B*(gamma-1): the scheduler sorts them in one CTA    */
 #define DSPARK_MAX_BATCH        8192   /* B for schedule and pack (single-CTA scans)          */
 #define DSPARK_MAX_TIERS        1024
+#define DSPARK_MAX_HISTORY      1048000 /* tokens of a request that dspark_adjust counts      */
+#define DSPARK_MAX_BIAS         2047   /* biases of a request                                 */
 #define DSPARK_MAX_HEAD         1024   /* head size of dspark_rotate                          */
 #define DSPARK_MAX_CACHE_HEAD   256    /* head size of a cache, a multiple of 16              */
 
@@ -554,6 +562,65 @@ int dspark_attend(const dspark_cache* cache, const void* q, int64_t q_stride, vo
 /* Bytes of device workspace dspark_attend needs; a value that depends on the sizes only. Returns
  * 0 and sets dspark_last_error on invalid sizes. */
 size_t dspark_attend_workspace_bytes(int heads, int dim);
+
+/* ---------------------------------------------------------------------------------------
+ * dspark_adjust — the packed rows' logits, adjusted before dspark_verify: penalties for tokens that
+ * the request has used, biases, and grammar masks. Row cu_seqlens[b] + i (cu_seqlens NULL: row
+ * b * gamma + i) of request b predicts the token after history[b, 0 .. history_len[b]), whose last
+ * is the block's anchor block_tokens[b, 0], and the drafts block_tokens[b, 1 .. i]. With
+ *   c(v)    uses of token v in history[b, prompt_len[b] ..] and among those drafts
+ *   seen(v) v is in history[b, ..] or c(v) > 0
+ * out = logits, for each token v of the row in fp32 and in this order:
+ *   seen(v):     x = x / repetition[b] where x > 0, else x * repetition[b]
+ *   c(v) > 0:    x = x - (frequency[b] * c(v) + presence[b])
+ *   a bias:      x = x + bias_values[b, j], j the last of the request's biases for v
+ *   not allowed: x = -inf, whatever it was (NaN too)
+ * and one rounding to the type of out. Logits that nothing applies to keep their bits. Each part is
+ * left out where its arrays are NULL (repetition NULL: 1; presence, frequency NULL: 0; prompt_len
+ * NULL: 0; history NULL: the drafts alone). A request with neutral penalties has its history not read.
+ *   history [B, history_cap] int32, history_len [B], prompt_len [B] int32: histories as
+ *       dspark_scatter keeps them (the prompt's tokens first)
+ *   repetition, presence, frequency [B] fp32
+ *   bias_tokens [B, bias_cap] int32, bias_values [B, bias_cap] fp32, bias_len [B] int32; -inf bans
+ *   mask [mask_rows, mask_stride] 32-bit words, bit v % 32 of word v / 32: token v is allowed
+ *       (bits past V do not matter); row r goes by mask row mask_row[r] (-1: none), or by mask row r
+ *       where mask_row is NULL. Rows may share mask rows.
+ * A mask that allows no token makes its row -inf throughout and flags DSPARK_STATUS_NO_TOKEN: verify
+ * has no token to choose there. A mask row outside [-1, mask_rows): the row is not masked,
+ * DSPARK_STATUS_BAD_ROWS.
+ * Tokens outside [0, V) are left out (DSPARK_STATUS_BAD_TOKEN); lengths outside their range are
+ * clamped into it (DSPARK_STATUS_BAD_LENGTH); a penalty that is not finite, or a repetition that is not
+ * positive, counts as neutral, and a bias that is NaN or +inf as none (DSPARK_STATUS_BAD_VALUE). A
+ * request whose rows lie outside [0, rows), run backwards or are more than gamma gets nothing written
+ * (DSPARK_STATUS_BAD_ROWS). Rows of no request are not written. cu_seqlens is non-decreasing.
+ *
+ * logits, out [rows, V] bf16 or fp32 (dtype), row strides in elements; out may be logits (same
+ * stride: in place, only what changes is written), otherwise the two must not overlap. block_tokens
+ * [B, gamma] int32 (NULL without penalties). The struct is read during the call only. One kernel, no
+ * workspace, the same bits every time. Limits: B <= DSPARK_MAX_BATCH, gamma <= DSPARK_MAX_GAMMA,
+ * history_cap <= DSPARK_MAX_HISTORY, bias_cap <= DSPARK_MAX_BIAS.
+ * ------------------------------------------------------------------------------------- */
+typedef struct {
+    const int32_t*  history;
+    const int32_t*  history_len;
+    const int32_t*  prompt_len;
+    int32_t         history_cap;
+    int32_t         bias_cap;
+    const float*    repetition;
+    const float*    presence;
+    const float*    frequency;
+    const int32_t*  bias_tokens;
+    const float*    bias_values;
+    const int32_t*  bias_len;
+    const uint32_t* mask;
+    const int32_t*  mask_row;
+    int64_t         mask_stride;
+    int32_t         mask_rows;
+} dspark_adjustments;
+int dspark_adjust(const void* logits, int64_t stride, void* out, int64_t out_stride,
+                  dspark_dtype dtype, int rows, int V, const int32_t* cu_seqlens,
+                  const int32_t* block_tokens, int B, int gamma, const dspark_adjustments* how,
+                  int32_t* status, cudaStream_t stream);
 
 /* Message of the last failed call on this host thread ("" if none). Never NULL. */
 const char* dspark_last_error(void);

@@ -30,6 +30,7 @@ STATUS_BAD_LENGTH = 0x80
 STATUS_STALL = 0x100
 STATUS_BAD_PAGE = 0x200
 STATUS_BAD_VALUE = 0x400
+STATUS_NO_TOKEN = 0x800
 
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BY_PARTS = 0, 1, 2
 ROPE_SCALINGS = {"none": ROPE_PLAIN, "linear": ROPE_LINEAR, "by_parts": ROPE_BY_PARTS}
@@ -39,6 +40,8 @@ STREAM_AUTO, STREAM_REGISTER, STREAM_BULK = 0, 1, 2
 MAX_GAMMA = 32
 MAX_CANDIDATES = 16384
 MAX_BATCH = 8192
+MAX_HISTORY = 1048000
+MAX_BIAS = 2047
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdspark.so")
 _LOCK = threading.Lock()
@@ -74,6 +77,17 @@ class _Cache(ctypes.Structure):
                 ("dim", ctypes.c_int32), ("width", ctypes.c_int32)]
 
 
+class _Adjustments(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("history_len", ctypes.c_void_p),
+                ("prompt_len", ctypes.c_void_p), ("history_cap", ctypes.c_int32),
+                ("bias_cap", ctypes.c_int32), ("repetition", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("bias_tokens", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("bias_len", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("mask_row", ctypes.c_void_p), ("mask_stride", ctypes.c_int64),
+                ("mask_rows", ctypes.c_int32)]
+
+
 SYMBOLS = {
     "dspark_schedule": ([_p, _i, _i, ctypes.POINTER(_Cost), _p, _p, _p, _p], _i),
     "dspark_pack": ([_p, _p, _i, _i, _p, _i, _p, _p, _p, _p, _i, _p, _p, _p], _i),
@@ -96,6 +110,8 @@ SYMBOLS = {
     "dspark_attend": ([ctypes.POINTER(_Cache), _p, _i64, _p, _i64, _i, _i, _i, _p, _p, _i,
                        ctypes.c_float, _i, _p, _p, ctypes.c_size_t, _p, _p], _i),
     "dspark_attend_workspace_bytes": ([_i, _i], ctypes.c_size_t),
+    "dspark_adjust": ([_p, _i64, _p, _i64, _i, _i, _i, _p, _p, _i, _i,
+                       ctypes.POINTER(_Adjustments), _p, _p], _i),
     "dspark_graph_begin": ([_p], _i),
     "dspark_graph_end": ([_p, ctypes.POINTER(_p)], _i),
     "dspark_graph_launch": ([_p, _p], _i),
@@ -609,6 +625,110 @@ def dspark_attend(cache: PagedCache, q: torch.Tensor, out: torch.Tensor, cu_seql
             _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
             _ptr(status, "status", torch.int32, min_numel=1, required=False), _stream(stream))
     return _call("dspark_attend", args, prepare)
+
+
+# ---- the logits between the target forward and verify ---------------------------------------
+class Adjustments:
+    """What dspark_adjust applies to a step's logits (dspark_adjustments), over the caller's CUDA
+    tensors; what is None is left out. For B requests: history [B, cap] int32 with history_len and
+    prompt_len [B] int32; repetition, presence, frequency [B] float32; bias_tokens [B, n] int32,
+    bias_values [B, n] float32, bias_len [B] int32; mask [mask rows, >= V / 32 words] int32 (or
+    uint32), its rows dense, and mask_row, int32, the mask row of each logits row (-1: none)."""
+
+    def __init__(self, *, history=None, history_len=None, prompt_len=None, repetition=None,
+                 presence=None, frequency=None, bias_tokens=None, bias_values=None, bias_len=None,
+                 mask=None, mask_row=None):
+        self.history, self.history_len, self.prompt_len = history, history_len, prompt_len
+        self.repetition, self.presence, self.frequency = repetition, presence, frequency
+        self.bias_tokens, self.bias_values, self.bias_len = bias_tokens, bias_values, bias_len
+        self.mask, self.mask_row = mask, mask_row
+        self.B = None                        # requests, by the first array given
+
+        def rows(name, t, dtype, dims, like=None):
+            if t is None:
+                return None
+            if t.dim() != dims:
+                raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+            if self.B is None:
+                self.B = t.shape[0]
+            if t.shape[0] != self.B:
+                raise ValueError(f"{name} must be for {self.B} requests, got {t.shape[0]}")
+            if like is not None and t.shape != like.shape:
+                raise ValueError(f"{name} must be {tuple(like.shape)}, got {tuple(t.shape)}")
+            return _ptr(t, name, dtype)
+
+        if (history is None) != (history_len is None) or (history is None and prompt_len is not None):
+            raise ValueError("history and history_len go together, prompt_len with them")
+        if not (bias_tokens is None) == (bias_values is None) == (bias_len is None):
+            raise ValueError("bias_tokens, bias_values and bias_len go together")
+        if mask is None and mask_row is not None:
+            raise ValueError("mask_row needs a mask")
+        c = _Adjustments()
+        c.history = rows("history", history, torch.int32, 2)
+        c.history_len = rows("history_len", history_len, torch.int32, 1)
+        c.prompt_len = rows("prompt_len", prompt_len, torch.int32, 1)
+        c.history_cap = 0 if history is None else history.shape[1]
+        c.repetition = rows("repetition", repetition, torch.float32, 1)
+        c.presence = rows("presence", presence, torch.float32, 1)
+        c.frequency = rows("frequency", frequency, torch.float32, 1)
+        c.bias_tokens = rows("bias_tokens", bias_tokens, torch.int32, 2)
+        c.bias_values = rows("bias_values", bias_values, torch.float32, 2, bias_tokens)
+        c.bias_len = rows("bias_len", bias_len, torch.int32, 1)
+        c.bias_cap = 0 if bias_tokens is None else bias_tokens.shape[1]
+        if mask is not None:
+            if mask.dim() != 2 or mask.dtype not in (torch.int32, torch.uint32):
+                raise ValueError("mask must be [mask rows, words] int32 or uint32")
+            if not mask.is_cuda:
+                raise ValueError("mask must be a CUDA tensor")
+            if mask.shape[1] > 1 and mask.stride(1) != 1:
+                raise ValueError("mask: the words of a row must be dense")
+            c.mask = ctypes.c_void_p(mask.data_ptr())
+            c.mask_rows = mask.shape[0]
+            c.mask_stride = mask.stride(0) if mask.shape[0] > 1 else mask.shape[1]
+            c.mask_row = _ptr(mask_row, "mask_row", torch.int32, required=False)
+        self._c = c
+
+    @property
+    def c(self):
+        return self._c
+
+
+def _rows_of(t: torch.Tensor, name: str):
+    """(pointer, row stride) of [rows, V], a row's elements dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, V]")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be dense")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def dspark_adjust(logits: torch.Tensor, out: torch.Tensor, block_tokens: torch.Tensor,
+                  how: Adjustments, *, cu_seqlens: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """out = the rows' logits with penalties, biases and masks applied (out may be logits);
+    cu_seqlens None: row b * gamma + i is request b's, as in the static verify mode."""
+    xp, xs = _rows_of(logits, "logits")
+    yp, ys = _rows_of(out, "out")
+    if out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out must have the shape and type of logits")
+    rows, V = logits.shape
+    B, gamma = block_tokens.shape
+    if how.B is not None and how.B != B:
+        raise ValueError(f"the adjustments are for {how.B} requests, the block tokens for {B}")
+    if how.mask is not None and how.mask.shape[1] * 32 < V:
+        raise ValueError(f"a mask row must have {-(-V // 32)} words, got {how.mask.shape[1]}")
+    if how.mask_row is not None and how.mask_row.numel() < rows:
+        raise ValueError(f"mask_row must have {rows} elements, got {how.mask_row.numel()}")
+    args = (xp, xs, yp, ys, _dtype_code(logits), rows, V,
+            _ptr(cu_seqlens, "cu_seqlens", torch.int32, min_numel=B + 1, required=False),
+            _ptr(block_tokens, "block_tokens", torch.int32, required=B > 0), B, gamma,
+            ctypes.byref(how.c), _ptr(status, "status", torch.int32, min_numel=1, required=False),
+            _stream(stream))
+    return _call("dspark_adjust", args, prepare)
 
 
 NOALLOC_SCRATCH_BYTES = 4 << 20
