@@ -100,7 +100,7 @@ extern "C" {
 #define DSPARK_MAX_CANDIDATES   16384  /* B*(gamma-1): the scheduler sorts them in one CTA    */
 #define DSPARK_MAX_BATCH        8192   /* B for schedule and pack (single-CTA scans)          */
 #define DSPARK_MAX_TIERS        1024
-#define DSPARK_MAX_HISTORY      1048000 /* tokens of a request that dspark_adjust counts      */
+#define DSPARK_MAX_HISTORY      524000 /* tokens of a request that dspark_adjust counts       */
 #define DSPARK_MAX_BIAS         2047   /* biases of a request                                 */
 #define DSPARK_MAX_HEAD         1024   /* head size of dspark_rotate                          */
 #define DSPARK_MAX_CACHE_HEAD   256    /* head size of a cache, a multiple of 16              */

@@ -40,7 +40,7 @@ STREAM_AUTO, STREAM_REGISTER, STREAM_BULK = 0, 1, 2
 MAX_GAMMA = 32
 MAX_CANDIDATES = 16384
 MAX_BATCH = 8192
-MAX_HISTORY = 1048000
+MAX_HISTORY = 524000
 MAX_BIAS = 2047
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdspark.so")

@@ -2,12 +2,12 @@
 // rows' logits, between the target forward and verify.
 //
 // A row's adjustment differs from the next row's of its request by one draft, so a CTA takes one
-// request and one slice of the vocabulary: it counts the request's tokens that fall into the slice
-// once, in shared memory, a word per token (its uses, whether the prompt has it, its bias), and
-// streams the slice of every row. A bit per token says which words are not zero, so that untouched
-// logits are copied without looking at words; the drafts before a row are counted where a touched
-// token is met. No sort, no hash, no order that matters: counts are integers, and of several
-// biases for one token the last one counts.
+// request and one slice of the vocabulary. It counts the request's tokens that fall into the slice
+// once, in shared memory: a word per token (its uses, whether the prompt has it, its bias) and lists of
+// the tokens met, one for each part of the slice. Its warps stream the slice of every row part by part,
+// masked on the way, and a warp that has written a part then adjusts its listed tokens, a lane each.
+// No sort, no hash, no order that matters: counts are integers, and of several biases for one token the
+// last one counts.
 //
 #include <cmath>
 
@@ -18,14 +18,19 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;                      // 16-byte units a thread has in flight
-constexpr int kMaxSlice = 4096, kMinSlice = 1024;
-// A token's word: uses in the answer, whether the prompt has it, 1 + the index of its bias.
-constexpr uint32_t kUses = (1u << 20) - 1;
-constexpr uint32_t kPrompt = 1u << 20;
+constexpr int kMaxSlice = 7168, kMinSlice = 1024;
+static_assert(kMinSlice % (32 * kUnits * 8) == 0 && kMaxSlice % kMinSlice == 0, "slices of whole parts");
+// A token's word: uses in the answer, whether the prompt has it, whether it is a draft, 1 + the index of
+// its bias.
+constexpr uint32_t kUses = (1u << 19) - 1;
+constexpr uint32_t kPrompt = 1u << 19;
+constexpr uint32_t kDraft = 1u << 20;
 constexpr int kBiasShift = 21;
 static_assert(DSPARK_MAX_HISTORY + DSPARK_MAX_GAMMA <= static_cast<int>(kUses), "uses fit their bits");
-static_assert((kMaxSlice + kMaxSlice / 32 + 4) * sizeof(uint32_t) <= 48 * 1024, "no opt-in to large shared memory");
 static_assert(DSPARK_MAX_BIAS < (1 << (32 - kBiasShift)), "biases fit their bits");
+// A word and a place in a list for each token of a slice.
+constexpr size_t slice_bytes(int slice) { return slice * 6; }
+static_assert(slice_bytes(kMaxSlice) <= 48 * 1024, "no opt-in to large shared memory");
 
 struct AdjustCall {
     const void* x;
@@ -59,14 +64,6 @@ __device__ __forceinline__ int clamped(int x, int hi, int* bits)
     *bits |= DSPARK_STATUS_BAD_LENGTH;
     return x < 0 ? 0 : hi;
 }
-// A bias that counts: -inf bans a token.
-__device__ __forceinline__ bool bias_counts(float v) { return v < INFINITY; }
-
-// Bits t .. t + 31 of a bit array in shared memory (one word past its end may be read).
-__device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int t)
-{
-    return __funnelshift_r(words[t >> 5], words[(t >> 5) + 1], t & 31);
-}
 // N bits from v on of a mask row, which ends with bit V - 1's word.
 template <int N>
 __device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int v)
@@ -75,23 +72,21 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int v)
     return (v & 31) + N > 32 ? lo | __ldg(row + (v >> 5) + 1) << (32 - (v & 31)) : lo;
 }
 
-// What a CTA knows of its request.
-struct Request {
-    float rep, presence, frequency;
-    const float* bias;
-    const uint32_t* word;
-    const int* draft;                          // slice-relative tokens of the drafts 1 .. i
+// Four tokens of a history at a 16-byte boundary, those outside [0, cap) left out.
+struct Four {
+    int v[4];
 };
-__device__ __forceinline__ float adjusted(float x, int t, int i, const Request& q)
+__device__ __forceinline__ Four four_of(const int32_t* history, int j, int cap)
 {
-    const uint32_t word = q.word[t];
-    uint32_t uses = word & kUses;
-    for (int j = 1; j <= i; ++j) uses += q.draft[j] == t;
-    if ((word & kPrompt) | uses) x = x > 0.0f ? x / q.rep : x * q.rep;
-    if (uses) x -= fmaf(q.frequency, static_cast<float>(uses), q.presence);
-    const uint32_t entry = word >> kBiasShift;
-    if (entry) x += q.bias[entry - 1];
-    return x;
+    Four f;
+    if (j >= 0 && j <= cap - 4) {
+        const int4 x = *reinterpret_cast<const int4*>(history + j);
+        f.v[0] = x.x, f.v[1] = x.y, f.v[2] = x.z, f.v[3] = x.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.v[e] = static_cast<uint32_t>(j + e) < static_cast<uint32_t>(cap) ? history[j + e] : -1;
+    }
+    return f;
 }
 
 template <int DT>
@@ -127,25 +122,8 @@ struct Element<DSPARK_F32> {
         return allow >> k & 1 ? x : kLowest;
     }
 };
-// Element j of a unit of 16 bytes, which stays in registers, replaced.
 template <int DT>
-__device__ __forceinline__ void replace(uint4& q, int j, int t, int i, const Request& rq)
-{
-    typedef Element<DT> E;
-    constexpr int kIn = E::kPer / 4;           // elements of a word
-    const int k = j / kIn, shift = j % kIn * 16;
-    const uint32_t w = k < 2 ? (k == 0 ? q.x : q.y) : (k == 2 ? q.z : q.w);
-    const uint32_t y = E::down(adjusted(E::up(static_cast<typename E::type>(w >> shift)), t, i, rq));
-    const uint32_t field = kIn == 1 ? 0xffffffffu : 0xffffu << shift;
-    const uint32_t z = (w & ~field) | (y << shift & field);
-    if (k == 0) q.x = z;
-    if (k == 1) q.y = z;
-    if (k == 2) q.z = z;
-    if (k == 3) q.w = z;
-}
-
-template <int DT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place)
 {
     typedef Element<DT> E;
@@ -154,16 +132,23 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
     constexpr uint32_t kAll = (1u << N) - 1;
     constexpr int kPart = 32 * kUnits * N;     // a warp's tokens at a time
     extern __shared__ __align__(16) uint32_t sm[];
-    __shared__ int draft[DSPARK_MAX_GAMMA];
+    __shared__ int draft[DSPARK_MAX_GAMMA];    // the drafts' places in the slice
+    __shared__ int listed[kMaxSlice / kPart];  // tokens met in each part of the slice
     const int tid = threadIdx.x, lane = tid & 31;
     const int b = blockIdx.x / A.slices, slice = blockIdx.x - b * A.slices;
     const int v0 = slice * A.slice, nv = min(A.slice, A.V - v0);
-    uint32_t* word = sm;                       // both only where something counts
-    uint32_t* touched = word + A.slice;        // tokens whose word is not zero, or that are drafts
+    uint32_t* word = sm;                       // these only where something counts
+    uint16_t* list = reinterpret_cast<uint16_t*>(word + A.slice);
+    if (counting) {
+        for (int i = tid; i < A.slice / 4; i += kThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
+        if (tid < kMaxSlice / kPart) listed[tid] = 0;
+        __syncthreads();
+    }
     pdl_wait_and_trigger();
 
     const dspark_adjustments& h = A.h;
     int bits = 0;
+    // Everything the call says of the request, in one round of loads: the first of its history too.
     int r0 = static_cast<int64_t>(b) * A.gamma, w = A.gamma;
     if (A.cu != nullptr) {
         r0 = A.cu[b];
@@ -171,59 +156,66 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
         w = r1 - r0;
         if (r0 < 0 || r1 < r0 || r1 > A.rows || w > A.gamma) { w = 0; bits |= DSPARK_STATUS_BAD_ROWS; }
     }
-    Request q;
-    q.word = word;
-    q.draft = draft;
-    bool counts = false;
+    float rep = 1.0f, presence = 0.0f, frequency = 0.0f;
+    int n = 0, n_prompt = 0, n_bias = 0, shift = 0, my_draft = -1;
+    const int32_t* history = nullptr;
+    const float* bias = h.bias_values + static_cast<int64_t>(b) * h.bias_cap;
+    Four first;
     if (counting) {
-        q.rep = penalty_of(h.repetition, b, 1.0f, true, &bits);
-        q.presence = penalty_of(h.presence, b, 0.0f, false, &bits);
-        q.frequency = penalty_of(h.frequency, b, 0.0f, false, &bits);
-        const bool penalties = q.rep != 1.0f || q.presence != 0.0f || q.frequency != 0.0f;
-        int n = 0, n_prompt = 0, n_bias = 0;
-        if (penalties && h.history != nullptr) {
+        rep = penalty_of(h.repetition, b, 1.0f, true, &bits);
+        presence = penalty_of(h.presence, b, 0.0f, false, &bits);
+        frequency = penalty_of(h.frequency, b, 0.0f, false, &bits);
+        if (A.tokens != nullptr && tid > 0 && tid < A.gamma) my_draft = A.tokens[static_cast<int64_t>(b) * A.gamma + tid];
+        if (h.history != nullptr) {
+            history = h.history + static_cast<int64_t>(b) * h.history_cap;
+            shift = static_cast<int>(reinterpret_cast<uintptr_t>(history) / 4 & 3);
+            first = four_of(history, 4 * tid - shift, h.history_cap);
             n = clamped(h.history_len[b], h.history_cap, &bits);
             if (h.prompt_len != nullptr) n_prompt = clamped(h.prompt_len[b], n, &bits);
         }
         if (h.bias_tokens != nullptr) n_bias = clamped(h.bias_len[b], h.bias_cap, &bits);
-        q.bias = h.bias_values + static_cast<int64_t>(b) * h.bias_cap;
-        counts = w > 0 && (penalties || n_bias > 0);
-        // where token v of this request has its word: -1 outside the slice
-        auto place = [&](int v) -> int {
-            if (static_cast<uint32_t>(v) >= static_cast<uint32_t>(A.V)) { bits |= DSPARK_STATUS_BAD_TOKEN; return -1; }
-            return static_cast<uint32_t>(v - v0) < static_cast<uint32_t>(nv) ? v - v0 : -1;
-        };
-        auto touch = [&](int t) { atomicOr(&touched[t >> 5], 1u << (t & 31)); };
-        if (counts) {
-            for (int i = tid; i < (A.slice + A.slice / 32 + 4) / 4; i += kThreads)
-                reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
-            __syncthreads();
-            const int32_t* ids = h.bias_tokens + static_cast<int64_t>(b) * h.bias_cap;
-            for (int j = tid; j < n_bias; j += kThreads) {
-                const int t = place(ids[j]);
-                if (t < 0) continue;
-                if (!bias_counts(q.bias[j])) { bits |= DSPARK_STATUS_BAD_VALUE; continue; }
-                atomicMax(&word[t], static_cast<uint32_t>(j + 1) << kBiasShift);
-                touch(t);
-            }
-            if (n_bias > 0) __syncthreads();   // the maximum is over biases alone
-            if (tid < w) {
-                const int t = penalties && tid > 0 ? place(A.tokens[static_cast<int64_t>(b) * A.gamma + tid]) : -1;
-                draft[tid] = t;
-                if (t >= 0) touch(t);
-            }
-            const int32_t* history = h.history + static_cast<int64_t>(b) * h.history_cap;
-#pragma unroll 4
-            for (int j = tid; j < n; j += kThreads) {
-                const int t = place(history[j]);
-                if (t < 0) continue;
-                if (j < n_prompt) atomicOr(&word[t], kPrompt);
-                else atomicAdd(&word[t], 1u);
-                touch(t);
-            }
-            __syncthreads();
-        }
     }
+    const bool penalties = rep != 1.0f || presence != 0.0f || frequency != 0.0f;
+    const bool counts = w > 0 && (penalties || n_bias > 0);
+
+    auto count = [&]() {
+        // the place of token v in the slice, or -1
+        auto place = [&](int v) -> int {
+            if (static_cast<uint32_t>(v - v0) < static_cast<uint32_t>(nv)) return v - v0;
+            if (static_cast<uint32_t>(v) >= static_cast<uint32_t>(A.V)) bits |= DSPARK_STATUS_BAD_TOKEN;
+            return -1;
+        };
+        // the one that finds a word empty lists its token
+        auto meet = [&](int t, uint32_t before) {
+            if (before == 0) list[t / kPart * kPart + atomicAdd(&listed[t / kPart], 1)] = static_cast<uint16_t>(t);
+        };
+        const int32_t* ids = h.bias_tokens + static_cast<int64_t>(b) * h.bias_cap;
+        for (int j = tid; j < n_bias; j += kThreads) {
+            const int t = place(ids[j]);
+            if (t < 0) continue;
+            if (!(bias[j] < INFINITY)) { bits |= DSPARK_STATUS_BAD_VALUE; continue; }      // -inf bans a token
+            meet(t, atomicMax(&word[t], static_cast<uint32_t>(j + 1) << kBiasShift));
+        }
+        if (n_bias > 0) __syncthreads();       // the maximum is over biases alone
+        if (tid < w) {
+            const int t = penalties && tid > 0 ? place(my_draft) : -1;
+            draft[tid] = t;
+            if (t >= 0) meet(t, atomicOr(&word[t], kDraft));
+        }
+        Four now = first;
+#pragma unroll 1
+        for (int j = 4 * tid - shift; penalties && j < n; j += 4 * kThreads) {
+            const Four next = four_of(history, j + 4 * kThreads, h.history_cap);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (static_cast<uint32_t>(j + e) >= static_cast<uint32_t>(n)) continue;
+                const int t = place(now.v[e]);
+                if (t >= 0) meet(t, j + e < n_prompt ? atomicOr(&word[t], kPrompt) : atomicAdd(&word[t], 1u));
+            }
+            now = next;
+        }
+        __syncthreads();
+    };
     // The mask row of packed row r, or none.
     auto mask_of = [&](int r) -> const uint32_t* {
         if (h.mask == nullptr) return nullptr;
@@ -232,58 +224,82 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
         if (m != -1) bits |= DSPARK_STATUS_BAD_ROWS;
         return nullptr;
     };
-    // A warp takes kPart tokens of a row at a time.
-    const int parts = (nv + kPart - 1) / kPart;
+    // A warp takes kPart tokens of a row at a time; its part of the mask row is fetched one part ahead,
+    // and the counting runs under its first loads.
+    const int parts = in_place && h.mask == nullptr && !counts ? 0 : (nv + kPart - 1) / kPart;
     int i = 0, part = tid >> 5;
-    while (part >= parts) { part -= parts; ++i; }
+    const uint32_t* mask = nullptr;
+    uint32_t ahead = 0;
+    auto settle = [&]() {
+        if (parts == 0) i = w;
+        while (i < w && part >= parts) { part -= parts; ++i; }
+        if (i >= w || h.mask == nullptr) return;
+        mask = mask_of(r0 + i);
+        const int v = part * kPart + lane * 32;
+        ahead = mask != nullptr && v < min(nv, (part + 1) * kPart) ? __ldg(mask + (v0 + v) / 32) : 0;
+    };
+    settle();
+    bool to_count = counts;
 #pragma unroll 1
-    while (i < w) {
-        const int r = r0 + i;
-        const uint32_t* mask = mask_of(r);
+    while (i < w || to_count) {
+        const bool some = i < w;
+        const int r = r0 + i, p0 = part * kPart, now_i = i, now_part = part;
+        const uint32_t* row_mask = mask;
+        const uint32_t mine = ahead;           // word `lane` of the part's mask
         const T* x = static_cast<const T*>(A.x) + r * A.xs + v0;
         T* y = static_cast<T*>(A.y) + r * A.ys + v0;
-        // elements before the first 16-byte boundary and after the last one go one at a time, and so
-        // do all where rows and results lie differently to the boundaries
         const uintptr_t ax = reinterpret_cast<uintptr_t>(x), ay = reinterpret_cast<uintptr_t>(y);
-        const bool alike = ((ax ^ ay) & 15) == 0;
-        const int head = alike ? min(nv, static_cast<int>(((16 - (ay & 15)) & 15) / sizeof(T))) : 0;
-        const int units = alike ? (nv - head) / N : 0, tail = head + units * N;
-        auto single = [&](int t) {
-            const bool allowed = mask == nullptr || (mask_bits<1>(mask, v0 + t) & 1);
-            if (!allowed) y[t] = E::kLowest;
-            else if (counts && (touched[t >> 5] >> (t & 31) & 1)) y[t] = E::down(adjusted(E::up(x[t]), t, i, q));
-            else if (!in_place) y[t] = x[t];
-        };
-        if (!alike) {
-            const int end = min(nv, (part + 1) * kPart);
-            for (int t = part * kPart + lane; t < end; t += 32) single(t);
-        } else if (part == 0 && lane < nv - units * N) {
-            single(lane < head ? lane : tail + lane - head);
-        }
-        const int u0 = part * (32 * kUnits) + lane;
+        // the common case: a whole part on 16-byte boundaries
+        const bool plain = some && ((ax | ay) & 15) == 0 && p0 + kPart <= nv;
+        uint32_t allow[kUnits];
         uint4 e[kUnits];
-        uint32_t allow[kUnits], touch[kUnits];
+        if (plain) {
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            const int u = u0 + k * 32;
-            allow[k] = u < units && mask != nullptr ? mask_bits<N>(mask, v0 + head + u * N) & kAll : kAll;
-        }
-#pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            const int u = u0 + k * 32, t = head + u * N;
-            touch[k] = counts && u < units ? bits_at(touched, t) & allow[k] : 0;
-            if (u < units && allow[k] != 0 && !(in_place && allow[k] == kAll && touch[k] == 0))
-                e[k] = in_place ? *reinterpret_cast<const uint4*>(x + t) : ld_stream16(x + t);
-        }
-#pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            const int u = u0 + k * 32, t = head + u * N;
-            if (u >= units || (in_place && allow[k] == kAll && touch[k] == 0)) continue;
-#pragma unroll 1
-            for (uint32_t m = touch[k]; m != 0; m &= m - 1) {
-                const int j = __ffs(m) - 1;
-                replace<DT>(e[k], j, t + j, i, q);
+            for (int k = 0; k < kUnits; ++k) {
+                allow[k] = kAll;
+                if (row_mask != nullptr)
+                    allow[k] = __shfl_sync(0xffffffffu, mine, (k * 32 + lane) * N / 32) >> (lane * N & 31) & kAll;
             }
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k)
+                if (allow[k] != 0 && !(in_place && allow[k] == kAll))
+                    e[k] = *(reinterpret_cast<const uint4*>(x + p0) + k * 32 + lane);
+        }
+        if (to_count) {
+            count();
+            to_count = false;
+        }
+        if (!some) continue;
+        part += kThreads / 32;
+        settle();
+
+        // Elements before the first 16-byte boundary and after the last one go one at a time, and so
+        // do all where rows and results lie differently to the boundaries.
+        int head = p0, tail = p0 + kPart;
+        if (!plain) {
+            const int end = min(nv, tail);
+            const bool alike = ((ax ^ ay) & 15) == 0;
+            head = alike ? min(end, p0 + static_cast<int>(((16 - (ay & 15)) & 15) / sizeof(T))) : end;
+            tail = head + (end - head) / N * N;
+            auto single = [&](int t) {
+                const bool allowed = row_mask == nullptr || (mask_bits<1>(row_mask, v0 + t) & 1);
+                if (!allowed) y[t] = E::kLowest;
+                else if (!in_place) y[t] = x[t];
+            };
+            for (int t = p0 + lane; t < head; t += 32) single(t);
+            if (tail + lane < end) single(tail + lane);
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) {
+                const int t = head + (k * 32 + lane) * N;
+                allow[k] = t >= tail || row_mask == nullptr ? kAll : mask_bits<N>(row_mask, v0 + t) & kAll;
+                if (t < tail && allow[k] != 0 && !(in_place && allow[k] == kAll))
+                    e[k] = *reinterpret_cast<const uint4*>(x + t);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            const int t = head + (k * 32 + lane) * N;
+            if (t >= tail || (in_place && allow[k] == kAll)) continue;
             if (allow[k] != kAll) {
                 e[k].x = E::blend(e[k].x, allow[k], 0);
                 e[k].y = E::blend(e[k].y, allow[k], 1);
@@ -292,8 +308,25 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
             }
             *reinterpret_cast<uint4*>(y + t) = e[k];
         }
-        part += kThreads / 32;
-        while (part >= parts) { part -= parts; ++i; }
+        if (!counts) continue;
+        // the part's listed tokens, over what the warp wrote
+        const int m = listed[now_part];
+        __syncwarp();
+#pragma unroll 1
+        for (int k = lane; k < m; k += 32) {
+            const int t = list[p0 + k];
+            const uint32_t its = word[t] & ~kDraft, entry = its >> kBiasShift;
+            uint32_t uses = its & kUses;
+            for (int j = 1; j <= now_i; ++j) uses += draft[j] == t;
+            // a later row's draft; a token that is not allowed
+            if ((its | uses) == 0 || (row_mask != nullptr && !(mask_bits<1>(row_mask, v0 + t) & 1))) continue;
+            float z = E::up(x[t]);
+            const float add = entry ? bias[entry - 1] : 0.0f;
+            if ((its & kPrompt) | uses) z = z > 0.0f ? z / rep : z * rep;
+            if (uses) z -= fmaf(frequency, static_cast<float>(uses), presence);
+            if (entry) z += add;
+            y[t] = E::down(z);
+        }
     }
     // Masks that allow nothing: row i's is looked at by slice i % slices.
     if (h.mask != nullptr) {
@@ -319,13 +352,14 @@ int launch_adjust(AdjustCall& A, int dtype, cudaStream_t stream)
     if (rc != DSPARK_OK) return rc;
     const bool counting = A.h.repetition != nullptr || A.h.presence != nullptr || A.h.frequency != nullptr ||
                           A.h.bias_tokens != nullptr;
-    A.slice = kMaxSlice;
-    while (A.slice > kMinSlice && A.B * ceil_div(A.V, A.slice) < 2ll * dev.sm_count) A.slice /= 2;
-    A.slices = static_cast<int>(ceil_div(A.V, A.slice));
-    const size_t smem = counting ? (A.slice + A.slice / 32 + 4) * sizeof(uint32_t) : 0;
+    // Slices of one size, in steps of kMinSlice: as few as kMaxSlice allows, or (few requests) so many
+    // that there are two CTAs for each SM.
+    const int64_t least = ceil_div(A.V, kMaxSlice), wanted = ceil_div(2ll * dev.sm_count, A.B);
+    A.slice = static_cast<int>(ceil_div(ceil_div(A.V, least > wanted ? least : wanted), kMinSlice) * kMinSlice);
+    A.slices = static_cast<int>(ceil_div(A.V, A.slice));           // each holds a token
     auto kernel = dtype == DSPARK_BF16 ? adjust_kernel<DSPARK_BF16> : adjust_kernel<DSPARK_F32>;
-    return launch_pdl("adjust", kernel, dim3(static_cast<unsigned>(A.B) * A.slices), dim3(kThreads), smem, stream,
-                      A, counting, A.x == A.y);
+    return launch_pdl("adjust", kernel, dim3(static_cast<unsigned>(A.B) * A.slices), dim3(kThreads),
+                      counting ? slice_bytes(A.slice) : 0, stream, A, counting, A.x == A.y);
 }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }

@@ -43,7 +43,7 @@ def test_refuses_on_the_host(lib):
             (-1, dict(gamma=33), "gamma=33"), (-2, dict(B=8193), "B = 8193"),
             (-1, dict(xs=99), "row strides"), (-1, dict(ys=99), "row strides"),
             (-1, dict(y=4096, ys=101), "in place"), (-1, dict(cu=None, rows=5), "cu_seqlens"),
-            (-1, dict(history_cap=-1), "history_cap"), (-2, dict(history_cap=1048001), "history_cap"),
+            (-1, dict(history_cap=-1), "history_cap"), (-2, dict(history_cap=524001), "history_cap"),
             (-1, dict(history=4096), "history_len"),
             (-1, dict(bias_tokens=4096), "bias"), (-2, dict(bias_tokens=4096, bias_cap=2048), "bias_cap"),
             (-1, dict(mask=4096, mask_stride=3, mask_rows=6), "mask"),
