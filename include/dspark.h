@@ -17,6 +17,9 @@
  *
  *   dspark_append    the rows' keys and values -> rotated, quantised, into a paged 8-bit cache
  *   dspark_attend    the rows' queries -> attention over that cache
+ *   dspark_attend_sinks, dspark_attend_shared
+ *                    the same with a window and first tokens that stay visible; for requests that
+ *                    share a prefix, read once for all of them
  *   dspark_rotate    rotary positions over rows of heads, and their inverse
  *
  * and, between its logits and dspark_verify,
@@ -562,6 +565,48 @@ int dspark_attend(const dspark_cache* cache, const void* q, int64_t q_stride, vo
 /* Bytes of device workspace dspark_attend needs; a value that depends on the sizes only. Returns
  * 0 and sets dspark_last_error on invalid sizes. */
 size_t dspark_attend_workspace_bytes(int heads, int dim);
+
+/* ---------------------------------------------------------------------------------------
+ * dspark_attend_sinks — dspark_attend where, beside the last `window` tokens up to its own, a row also
+ * sees the first `sinks` tokens of its request: the row at position p sees the tokens t <= p with
+ * t > p - window or t < sinks. Without a window (window 0) or without sinks it is dspark_attend. Pages
+ * that lie wholly between the sinks and every row's window are not looked at: their entries may be
+ * stale, and their pages in use elsewhere. Everything else is as there, workspace and precision too.
+ * ------------------------------------------------------------------------------------- */
+int dspark_attend_sinks(const dspark_cache* cache, const void* q, int64_t q_stride, void* out,
+                        int64_t out_stride, int q_heads, dspark_dtype dtype, int rows,
+                        const int32_t* cu_seqlens, const int32_t* lengths, int B, float scale,
+                        int window, int sinks, float* lse, void* workspace, size_t workspace_bytes,
+                        int32_t* status, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * dspark_attend_shared — dspark_attend for requests that share a prefix, whose keys and values are then
+ * read once for all rows of its requests instead of once for each. Group g is the requests
+ * group_cu[g] .. group_cu[g + 1] - 1; the first prefix[g] tokens of each are the same tokens in the
+ * same pages: their table entries are alike, and the call may read any of them. prefix is taken in whole
+ * pages (a page that is appended to is not shared). Results are dspark_attend's over the same cache
+ * without a window: a row sees every token up to its own. Requests in no group, or in a group of
+ * one, those with fewer tokens in the cache than the prefix, and groups whose numbers make no sense
+ * (a prefix that passes the page table or is negative, requests outside [0, B)) attend alone.
+ *
+ * group_cu [groups + 1] int32, non-decreasing; prefix [groups] int32 (both may be NULL where groups is 0);
+ * the rest as in dspark_attend. workspace: at least dspark_attend_shared_workspace_bytes(rows, q_heads,
+ * heads, dim, B) bytes, 16-byte aligned, no clearing needed, rewritten by every call; calls that share
+ * it must not overlap. Four kernels: the prefixes and their join, the requests' own tokens and theirs.
+ * fp32, and dims other than 64 and 128, attend request by request.
+ *
+ * Precision: as dspark_attend for each of a row's two parts, whose quotients are kept in fp32.
+ * ------------------------------------------------------------------------------------- */
+int dspark_attend_shared(const dspark_cache* cache, const void* q, int64_t q_stride, void* out,
+                         int64_t out_stride, int q_heads, dspark_dtype dtype, int rows,
+                         const int32_t* cu_seqlens, const int32_t* lengths, int B,
+                         const int32_t* group_cu, const int32_t* prefix, int groups, float scale,
+                         float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                         cudaStream_t stream);
+
+/* Bytes of device workspace dspark_attend_shared needs; a value that depends on the sizes only. Returns
+ * 0 and sets dspark_last_error on invalid sizes. */
+size_t dspark_attend_shared_workspace_bytes(int rows, int q_heads, int heads, int dim, int B);
 
 /* ---------------------------------------------------------------------------------------
  * dspark_adjust — the packed rows' logits, adjusted before dspark_verify: penalties for tokens that

@@ -110,6 +110,11 @@ SYMBOLS = {
     "dspark_attend": ([ctypes.POINTER(_Cache), _p, _i64, _p, _i64, _i, _i, _i, _p, _p, _i,
                        ctypes.c_float, _i, _p, _p, ctypes.c_size_t, _p, _p], _i),
     "dspark_attend_workspace_bytes": ([_i, _i], ctypes.c_size_t),
+    "dspark_attend_sinks": ([ctypes.POINTER(_Cache), _p, _i64, _p, _i64, _i, _i, _i, _p, _p, _i,
+                             ctypes.c_float, _i, _i, _p, _p, ctypes.c_size_t, _p, _p], _i),
+    "dspark_attend_shared": ([ctypes.POINTER(_Cache), _p, _i64, _p, _i64, _i, _i, _i, _p, _p, _i,
+                              _p, _p, _i, ctypes.c_float, _p, _p, ctypes.c_size_t, _p, _p], _i),
+    "dspark_attend_shared_workspace_bytes": ([_i, _i, _i, _i, _i], ctypes.c_size_t),
     "dspark_adjust": ([_p, _i64, _p, _i64, _i, _i, _i, _p, _p, _i, _i,
                        ctypes.POINTER(_Adjustments), _p, _p], _i),
     "dspark_graph_begin": ([_p], _i),
@@ -605,6 +610,24 @@ def dspark_attend_workspace_bytes(heads: int, dim: int) -> int:
     return int(lib().dspark_attend_workspace_bytes(int(heads), int(dim)))
 
 
+def _attend_args(cache, q, out, cu_seqlens, lengths, scale):
+    qp, qs = _heads(q, "q", None, None, None, cache.dim)
+    rows, hq, dim = q.shape
+    op, os_ = _heads(out, "out", q.dtype, rows, hq, dim)
+    if lengths.numel() != cache.B:
+        raise ValueError(f"lengths must have {cache.B} elements, got {lengths.numel()}")
+    return ((ctypes.byref(cache.c), qp, qs, op, os_, hq, _dtype_code(q, "q"), rows,
+             _ptr(cu_seqlens, "cu_seqlens", torch.int32, min_numel=cache.B + 1),
+             _ptr(lengths, "lengths", torch.int32), cache.B),
+            float(dim) ** -0.5 if scale is None else float(scale))
+
+
+def _attend_tail(q, lse, workspace, status, stream):
+    return (_ptr(lse, "lse", torch.float32, min_numel=q.shape[0] * q.shape[1], required=False),
+            _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+            _ptr(status, "status", torch.int32, min_numel=1, required=False), _stream(stream))
+
+
 def dspark_attend(cache: PagedCache, q: torch.Tensor, out: torch.Tensor, cu_seqlens: torch.Tensor,
                   lengths: torch.Tensor, workspace: torch.Tensor, *,
                   scale: Optional[float] = None, window: int = 0,
@@ -612,19 +635,39 @@ def dspark_attend(cache: PagedCache, q: torch.Tensor, out: torch.Tensor, cu_seql
                   stream=None, prepare: bool = False):
     """Attention of the packed rows over the cache; scale None: 1 / sqrt(dim); window 0: every
     token up to the row's own."""
-    qp, qs = _heads(q, "q", None, None, None, cache.dim)
-    rows, hq, dim = q.shape
-    op, os_ = _heads(out, "out", q.dtype, rows, hq, dim)
-    if lengths.numel() != cache.B:
-        raise ValueError(f"lengths must have {cache.B} elements, got {lengths.numel()}")
-    args = (ctypes.byref(cache.c), qp, qs, op, os_, hq, _dtype_code(q, "q"), rows,
-            _ptr(cu_seqlens, "cu_seqlens", torch.int32, min_numel=cache.B + 1),
-            _ptr(lengths, "lengths", torch.int32), cache.B,
-            float(dim) ** -0.5 if scale is None else float(scale), int(window),
-            _ptr(lse, "lse", torch.float32, min_numel=rows * hq, required=False),
-            _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-            _ptr(status, "status", torch.int32, min_numel=1, required=False), _stream(stream))
+    args, scale = _attend_args(cache, q, out, cu_seqlens, lengths, scale)
+    args += (scale, int(window)) + _attend_tail(q, lse, workspace, status, stream)
     return _call("dspark_attend", args, prepare)
+
+
+def dspark_attend_sinks(cache: PagedCache, q: torch.Tensor, out: torch.Tensor,
+                        cu_seqlens: torch.Tensor, lengths: torch.Tensor, workspace: torch.Tensor, *,
+                        window: int, sinks: int, scale: Optional[float] = None,
+                        lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                        stream=None, prepare: bool = False):
+    """dspark_attend over the last `window` tokens and the first `sinks` tokens of each request."""
+    args, scale = _attend_args(cache, q, out, cu_seqlens, lengths, scale)
+    args += (scale, int(window), int(sinks)) + _attend_tail(q, lse, workspace, status, stream)
+    return _call("dspark_attend_sinks", args, prepare)
+
+
+def dspark_attend_shared_workspace_bytes(rows: int, q_heads: int, heads: int, dim: int, B: int) -> int:
+    return int(lib().dspark_attend_shared_workspace_bytes(int(rows), int(q_heads), int(heads), int(dim), int(B)))
+
+
+def dspark_attend_shared(cache: PagedCache, q: torch.Tensor, out: torch.Tensor,
+                         cu_seqlens: torch.Tensor, lengths: torch.Tensor, group_cu: torch.Tensor,
+                         prefix: torch.Tensor, workspace: torch.Tensor, *,
+                         scale: Optional[float] = None, lse: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """dspark_attend where the first prefix[g] tokens of the requests group_cu[g] .. group_cu[g + 1] - 1
+    are the same tokens in the same pages: read once for the group."""
+    args, scale = _attend_args(cache, q, out, cu_seqlens, lengths, scale)
+    groups = prefix.numel()
+    args += (_ptr(group_cu, "group_cu", torch.int32, min_numel=groups + 1, required=groups > 0),
+             _ptr(prefix, "prefix", torch.int32), groups, scale)
+    args += _attend_tail(q, lse, workspace, status, stream)
+    return _call("dspark_attend_shared", args, prepare)
 
 
 # ---- the logits between the target forward and verify ---------------------------------------

@@ -1,9 +1,17 @@
-// attend.cuh — what the two attention kernels share: the call's arguments and a request's rows.
+// attend.cuh — what the attention kernels share: the call's arguments, what a row sees, a request's rows.
 #pragma once
 
 #include "cache.cuh"
 
 namespace dspark {
+
+// What the rows of a call see, a template argument of the tensor-core kernels:
+//   kAll     every token up to the row's own, or the last `window` of them
+//   kSinks   the last `window` tokens, and of those before them the first `sinks`
+//   kPrefix  the rows of a whole group of requests see its shared tokens, all of them: a "request" is
+//            a group, its length the prefix. Results are partial ones, for
+//   kSuffix  a request's own tokens, those behind its group's prefix, joined with the partial results
+enum See { kAll = 0, kSinks = 1, kPrefix = 2, kSuffix = 3 };
 
 struct AttendCall {
     dspark_cache c;
@@ -23,13 +31,25 @@ struct AttendCall {
     int last_tile;             // the last 128-token tile of them
     void* ws;
     int32_t* status;
+    int sinks;                 // kSinks
+    // kPrefix, kSuffix. In a kPrefix call B is the number of groups.
+    int requests;
+    const int32_t* group_cu;   // a group's requests: group_cu[g] .. group_cu[g + 1] - 1
+    const int32_t* prefix;     // its shared tokens
+    int32_t* from;             // [requests] a request's first token that is its own; 0: all are
+    float* part_lse;           // [rows * q_heads] what the prefix gives each row: log2 of the sum,
+    float* part;               // [rows * q_heads, dim] and the quotient
 };
 
 size_t attend_workspace_bytes(int dim);
-int launch_attend(const AttendCall& A, int dtype, cudaStream_t stream);
+size_t attend_shared_workspace_bytes(int rows, int q_heads, int dim, int B);
+// kAll or kSinks.
+int launch_attend(const AttendCall& A, See see, int dtype, cudaStream_t stream);
+int launch_attend_shared(const AttendCall& A, const int32_t* group_cu, const int32_t* prefix, int groups, int dtype,
+                         cudaStream_t stream);
 // The tensor-core kernel: whether it serves a call, and its launch.
 bool attend_mma_serves(const AttendCall& A, int dtype);
-int launch_attend_mma(const AttendCall& A, cudaStream_t stream);
+int launch_attend_mma(const AttendCall& A, See see, cudaStream_t stream);
 
 // Request b's packed rows [row0, row0 + w) and its length, checked: w = 0 for one whose rows are
 // not within the buffer. *bits collects what was wrong, tokens past the page table included.
@@ -45,6 +65,50 @@ __device__ __forceinline__ void request_rows(const AttendCall& A, int b, int* ro
     if (r0 < 0 || r1 < r0 || r1 > A.rows) { *w = 0; *bits |= DSPARK_STATUS_BAD_ROWS; }
     else if (n > INT32_MAX - 256 - *w) { *w = 0; *bits |= DSPARK_STATUS_BAD_LENGTH; }
     else if (*w > 0 && n + *w > A.reach) *bits |= DSPARK_STATUS_BAD_PAGE;
+}
+
+// A group's rows [row0, row0 + w) and its shared tokens in whole pages; w = 0 where they are not to be
+// computed apart: a group of one, no whole page, rows or requests that are none.
+__device__ __forceinline__ void group_rows(const AttendCall& A, int g, int* row0, int* w, int* len)
+{
+    const int b0 = A.group_cu[g], b1 = A.group_cu[g + 1];
+    const int n = A.prefix[g] / A.c.page * A.c.page;
+    *row0 = *w = 0;
+    *len = n;
+    if (b0 < 0 || b1 > A.requests || b1 - b0 < 2 || n <= 0 || n > A.reach) return;
+    const int r0 = A.cu[b0], r1 = A.cu[b1];
+    if (r0 < 0 || r1 < r0 || r1 > A.rows) return;
+    *row0 = r0;
+    *w = r1 - r0;
+}
+// What a call takes as its requests; *from: the first token that is seen at all (kSuffix).
+template <int SEE>
+__device__ __forceinline__ void rows_of(const AttendCall& A, int b, int* row0, int* w, int* len, int* from, int* bits)
+{
+    if constexpr (SEE == kPrefix) {
+        group_rows(A, b, row0, w, len);
+    } else {
+        request_rows(A, b, row0, w, len, bits);
+        if constexpr (SEE == kSuffix) *from = A.from[b];
+    }
+}
+// The tokens of a "request" that are in the cache, its table's row, a row's position.
+template <int SEE>
+__device__ __forceinline__ int stored_tokens(int len, int w) { return SEE == kPrefix ? len : len + w; }
+template <int SEE>
+__device__ __forceinline__ const int32_t* table_row(const AttendCall& A, int b)
+{
+    return A.c.table + static_cast<int64_t>(SEE == kPrefix ? A.group_cu[b] : b) * A.c.width;
+}
+template <int SEE>
+__device__ __forceinline__ int position(int len, int i) { return SEE == kPrefix ? len - 1 : len + i; }
+// The first token that a row at this position sees, sinks apart.
+template <int SEE>
+__device__ __forceinline__ int first_seen_at(const AttendCall& A, int pos, int from)
+{
+    if constexpr (SEE == kPrefix) return 0;
+    if constexpr (SEE == kSuffix) return from;
+    return A.window > 0 && pos >= A.window ? pos - A.window + 1 : 0;
 }
 
 }  // namespace dspark

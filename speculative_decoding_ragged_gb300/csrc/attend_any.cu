@@ -1,4 +1,5 @@
-// attend_any.cu — dspark_attend in fp32 on the ordinary cores: any supported head size and type.
+// attend_any.cu — dspark_attend and dspark_attend_sinks in fp32 on the ordinary cores: any supported
+// head size and type.
 //
 // One CTA takes one packed row and one cache head, up to four of its query heads at a time; its
 // warps take 32-token pieces of the row's visible tokens in turn, each with its own running
@@ -20,7 +21,7 @@ constexpr int kMaxDim = DSPARK_MAX_CACHE_HEAD;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int DT>
+template <int DT, int SEE>
 __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(AttendCall A)
 {
     __shared__ __align__(16) float qs[kHeads][kMaxDim];
@@ -72,10 +73,13 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(AttendCall A)
             for (int j = 0; j < kMaxDim / 32; ++j) acc[g][j] = 0.0f;
         }
         int bits = 0;
-        for (int64_t t0 = (first / 32) * 32 + static_cast<int64_t>(warp) * 32; t0 <= pos;
+        // kSinks: the pieces from the sinks' last to the window's first are left out
+        const int sink_pieces = SEE == kSinks ? (min(A.sinks, first) + 31) / 32 : 0;
+        const int64_t skip = SEE == kSinks ? max(0, first / 32 - sink_pieces) * 32 : 0;
+        for (int64_t t0 = (SEE == kSinks ? 0 : (first / 32) * 32) + static_cast<int64_t>(warp) * 32; t0 + skip <= pos || t0 < sink_pieces * 32;
              t0 += kWarps * 32) {
-            const int64_t t = t0 + lane;
-            bool see = t >= first && t <= pos;
+            const int64_t t = t0 + lane + (t0 < sink_pieces * 32 ? 0 : skip);
+            bool see = (t >= first || (SEE == kSinks && t < A.sinks)) && t <= pos;
             const int block = static_cast<int>(t / page), slot = static_cast<int>(t % page);
             int64_t base = 0;
             float ks = 0.0f, vs = 0.0f;
@@ -186,10 +190,13 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(AttendCall A)
 
 }  // namespace
 
-int launch_attend(const AttendCall& A, int dtype, cudaStream_t stream)
+int launch_attend(const AttendCall& A, See see, int dtype, cudaStream_t stream)
 {
-    if (attend_mma_serves(A, dtype)) return launch_attend_mma(A, stream);
-    auto kernel = dtype == DSPARK_BF16 ? attend_any_kernel<DSPARK_BF16> : attend_any_kernel<DSPARK_F32>;
+    if (attend_mma_serves(A, dtype)) return launch_attend_mma(A, see, stream);
+    const bool bf = dtype == DSPARK_BF16;
+    auto kernel = see == kSinks
+                      ? (bf ? attend_any_kernel<DSPARK_BF16, kSinks> : attend_any_kernel<DSPARK_F32, kSinks>)
+                      : (bf ? attend_any_kernel<DSPARK_BF16, kAll> : attend_any_kernel<DSPARK_F32, kAll>);
     return launch_pdl("attend", kernel, dim3(static_cast<unsigned>(A.rows), static_cast<unsigned>(A.c.heads)),
                       dim3(kWarps * 32), 0, stream, A);
 }

@@ -10,13 +10,15 @@ namespace {
 // lanes first read the parts' references and sums, then dim / 4 lanes add up the parts, 16 loads
 // in flight.
 constexpr int kJoinWarps = 16;
-template <int D>
+template <int D, int SEE>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendCall A)
 {
     pdl_wait_and_trigger();
     const Workspace ws = workspace_of(A.ws);
-    const RunMeta m = ws.meta[blockIdx.x];
+    RunMeta m = ws.meta[blockIdx.x];
     if (m.rows == 0) return;
+    const bool joins = SEE == kSuffix && (m.rows & kHasPrefix) != 0;
+    if constexpr (SEE == kSuffix) m.rows &= ~kHasPrefix;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = m.first / m.run;                          // the run of the unit's first tile
     const int c1 = (m.end + m.run - 1) / m.run;              // one past the run of its last
@@ -67,10 +69,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendCall
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         const int flat = m.flat0 + row;
         const int64_t prow = m.row0 + flat / A.group;
         const int head = m.head0 + flat % A.group;
+        float lse = sum == 0.0f ? -INFINITY : top + log2f(sum);
+        if constexpr (SEE == kPrefix || SEE == kSuffix) {
+            const int64_t at = prow * A.q_heads + head;
+            float4* prefix = reinterpret_cast<float4*>(A.part + at * D + lane * 4);
+            if constexpr (SEE == kPrefix) {
+                if (lane * 4 < D) *prefix = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+                if (lane == 0) A.part_lse[at] = lse;
+                continue;
+            }
+            if (joins) {
+                const Shares sh = shares_of(lse, A.part_lse[at]);
+                inv *= sh.s;
+                lse = sh.lse;
+                const float4 p = lane * 4 < D ? *prefix : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                acc = make_float4(fmaf(acc.x, inv, sh.p * p.x), fmaf(acc.y, inv, sh.p * p.y),
+                                  fmaf(acc.z, inv, sh.p * p.z), fmaf(acc.w, inv, sh.p * p.w));
+                inv = 1.0f;
+            }
+        }
         if (lane * 4 < D) {
             uint16_t* out = static_cast<uint16_t*>(A.out) + prow * A.out_stride +
                             static_cast<int64_t>(head) * D + lane * 4;
@@ -81,7 +102,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendCall
             out[3] = static_cast<uint16_t>(b >> 16);
         }
         if (lane == 0 && A.lse != nullptr)
-            A.lse[prow * A.q_heads + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            A.lse[prow * A.q_heads + head] = lse * kLn2;
     }
 }
 
@@ -125,12 +146,6 @@ int encode_cache(CUtensorMap* map, void* codes, const dspark_cache& c)
     return DSPARK_OK;
 }
 
-int launch_attend_join(const AttendCall& A, int ctas, cudaStream_t stream)
-{
-    return launch_pdl("attend join", A.c.dim == 128 ? attend_join_kernel<128> : attend_join_kernel<64>,
-                      dim3(ctas), dim3(kJoinWarps * 32), 0, stream, A);
-}
-
 bool attend_mma_serves(const AttendCall& A, int dtype)
 {
     return dtype == DSPARK_BF16 && (A.c.dim == 64 || A.c.dim == 128) && A.c.n_pages > 0;
@@ -142,20 +157,62 @@ size_t attend_workspace_bytes(int dim)
     return kMaxCtas * (sizeof(RunMeta) + 2 * kTile * (sizeof(float2) + dim * sizeof(float)));
 }
 
-int launch_attend_mma(const AttendCall& A, cudaStream_t stream)
+// After the parts: each row's share of its group's prefix, and the requests' first own tokens.
+size_t attend_shared_workspace_bytes(int rows, int q_heads, int dim, int B)
 {
-    DeviceInfo dev;
-    int rc = current_device(&dev);
-    if (rc != DSPARK_OK) return rc;
-    const int ctas = dev.sm_count * 2 < kMaxCtas ? dev.sm_count * 2 : kMaxCtas;
+    const size_t parts = attend_workspace_bytes(dim);
+    if (dim != 64 && dim != 128) return parts;
+    return parts + static_cast<size_t>(rows) * q_heads * (dim + 1) * sizeof(float) + static_cast<size_t>(B) * sizeof(int32_t);
+}
+
+namespace {
+template <int SEE>
+int launch_both(const AttendCall& A, int ctas, int device, cudaStream_t stream)
+{
     // By the requests' average of (position, head) rows: up to 32 the narrow kernel (64 requests over
     // 2048 tokens, 8 heads of 128: at 16 rows 74 us, wide 120; at 32 87 and 126), where it takes one
     // unit per request and head. From 33 on, two units and more, wide (48 rows: 138 and 131; 256 requests
     // over 512: 206 and 175; 128 rows: 248 and 155).
     const bool narrow = static_cast<int64_t>(A.rows) * A.group <= 32ll * A.B;
-    rc = narrow ? launch_attend_narrow(A, ctas, dev.device, stream)
-                : launch_attend_wide(A, ctas, dev.device, stream);
-    return rc == DSPARK_OK ? launch_attend_join(A, ctas, stream) : rc;
+    const int rc = narrow ? launch_attend_narrow<SEE>(A, ctas, device, stream)
+                          : launch_attend_wide<SEE>(A, ctas, device, stream);
+    if (rc != DSPARK_OK) return rc;
+    return launch_pdl("attend join", A.c.dim == 128 ? attend_join_kernel<128, SEE> : attend_join_kernel<64, SEE>,
+                      dim3(ctas), dim3(kJoinWarps * 32), 0, stream, A);
+}
+}  // namespace
+
+int launch_attend_mma(const AttendCall& A, See see, cudaStream_t stream)
+{
+    DeviceInfo dev;
+    const int rc = current_device(&dev);
+    if (rc != DSPARK_OK) return rc;
+    const int ctas = dev.sm_count * 2 < kMaxCtas ? dev.sm_count * 2 : kMaxCtas;
+    switch (see) {
+    case kSinks: return launch_both<kSinks>(A, ctas, dev.device, stream);
+    case kPrefix: return launch_both<kPrefix>(A, ctas, dev.device, stream);
+    case kSuffix: return launch_both<kSuffix>(A, ctas, dev.device, stream);
+    default: return launch_both<kAll>(A, ctas, dev.device, stream);
+    }
+}
+
+// The prefixes as a call over groups, then the own tokens. Head sizes and types of the fp32 kernel have no
+// such form: it attends over the whole contexts.
+int launch_attend_shared(const AttendCall& A, const int32_t* group_cu, const int32_t* prefix, int groups, int dtype,
+                         cudaStream_t stream)
+{
+    if (groups == 0 || !attend_mma_serves(A, dtype)) return launch_attend(A, kAll, dtype, stream);
+    AttendCall own = A;
+    own.requests = A.B;
+    own.group_cu = group_cu;
+    own.prefix = prefix;
+    own.part = reinterpret_cast<float*>(static_cast<char*>(A.ws) + attend_workspace_bytes(A.c.dim));
+    own.part_lse = own.part + static_cast<int64_t>(A.rows) * A.q_heads * A.c.dim;
+    own.from = reinterpret_cast<int32_t*>(own.part_lse + static_cast<int64_t>(A.rows) * A.q_heads);
+    AttendCall shared = own;
+    shared.B = groups;
+    const int rc = launch_attend_mma(shared, kPrefix, stream);
+    return rc == DSPARK_OK ? launch_attend_mma(own, kSuffix, stream) : rc;
 }
 
 }  // namespace dspark

@@ -62,9 +62,12 @@ struct RunMeta {
     int first;          // its first tile's
     int run;            // places per run
     int row0, rows;     // the request's first packed row; the unit's rows (position, head): 0 where
-                        // the run starts with a unit's beginning, or holds no tile ...
+                        // the run starts with a unit's beginning, or holds no tile ... (kSuffix: and
+                        // kHasPrefix where the request has one)
     int flat0, head0;   // ... from this flat index on, first query head
 };
+
+constexpr int kHasPrefix = 1 << 16;
 
 struct Workspace {
     RunMeta* meta;      // [kMaxCtas]
@@ -82,8 +85,9 @@ __host__ __device__ inline Workspace workspace_of(void* ws)
 }
 
 int encode_cache(CUtensorMap* map, void* codes, const dspark_cache& c);
-int launch_attend_join(const AttendCall& A, int ctas, cudaStream_t stream);
+template <int SEE>
 int launch_attend_narrow(const AttendCall& A, int ctas, int device, cudaStream_t stream);
+template <int SEE>
 int launch_attend_wide(const AttendCall& A, int ctas, int device, cudaStream_t stream);
 
 // ---- PTX -----------------------------------------------------------------------------------
@@ -348,28 +352,43 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 template <int R>
 constexpr int kUnitCost = R < kTile ? 4 : 6;
 
-struct Shape {                   // a unit's visible tiles [a, z]
-    int a, z;
+struct Shape {                   // a unit's visible tiles [a, z]; kSinks: with `skip` tiles left out after
+    int a, z, skip;              // the sinks', which the numbers leave out too
 };
+__device__ __forceinline__ int sink_tiles(const AttendCall& A) { return (A.sinks + kTile - 1) / kTile; }
+// The tile of the cache that is number k.
+template <int SEE>
+__device__ __forceinline__ int real_tile(const AttendCall& A, int k, int skip)
+{
+    return SEE == kSinks && k >= sink_tiles(A) ? k + skip : k;
+}
+template <int SEE>
+__device__ __forceinline__ Shape shape_of(const AttendCall& A, int lo, int last)
+{
+    const int a = min(lo / kTile, A.last_tile), z = min(last / kTile, A.last_tile);
+    if constexpr (SEE == kSinks) {
+        const int skip = max(0, a - sink_tiles(A));
+        return {0, z - skip, skip};
+    }
+    return {a, z, 0};
+}
 // The tiles that some row of a request's qt-th R rows sees and the page table reaches (one tile at
 // least). The divisions by the group are spared where the unit holds the request's first or last
 // rows: for decode and verify, always.
-template <int R>
-static __device__ __noinline__ Shape some_unit_tiles(const AttendCall& A, int w, int len, int qt)
+template <int R, int SEE>
+static __device__ __noinline__ Shape some_unit_tiles(const AttendCall& A, int w, int len, int from, int qt)
 {
     const int i0 = qt == 0 ? 0 : qt * R / A.group;
     const int i1 = static_cast<int64_t>(qt + 1) * R >= static_cast<int64_t>(w) * A.group
                        ? w - 1 : ((qt + 1) * R - 1) / A.group;
-    const int p0 = len + i0;
-    const int lo = A.window > 0 && p0 >= A.window ? p0 - A.window + 1 : 0;
-    return {min(lo / kTile, A.last_tile), min((len + i1) / kTile, A.last_tile)};
+    return shape_of<SEE>(A, first_seen_at<SEE>(A, len + i0, from), len + i1);
 }
-template <int R>
-__device__ __forceinline__ Shape unit_tiles(const AttendCall& A, int w, int len, int qt)
+template <int R, int SEE>
+__device__ __forceinline__ Shape unit_tiles(const AttendCall& A, int w, int len, int from, int qt)
 {
-    if (static_cast<int64_t>(w) * A.group > R) return some_unit_tiles<R>(A, w, len, qt);
-    const int lo = A.window > 0 && len >= A.window ? len - A.window + 1 : 0;      // the only unit
-    return {min(lo / kTile, A.last_tile), min((len + w - 1) / kTile, A.last_tile)};
+    if constexpr (SEE == kPrefix) return shape_of<SEE>(A, 0, len - 1);
+    if (static_cast<int64_t>(w) * A.group > R) return some_unit_tiles<R, SEE>(A, w, len, from, qt);
+    return shape_of<SEE>(A, first_seen_at<SEE>(A, len, from), len + w - 1);      // the only unit
 }
 template <int R>
 __device__ __forceinline__ int row_tiles(const AttendCall& A, int w)
@@ -377,14 +396,14 @@ __device__ __forceinline__ int row_tiles(const AttendCall& A, int w)
     return static_cast<int>((static_cast<int64_t>(w) * A.group + R - 1) / R);
 }
 // The places that one head of a request takes on the line.
-template <int R>
-__device__ __forceinline__ int head_places(const AttendCall& A, int w, int len)
+template <int R, int SEE>
+__device__ __forceinline__ int head_places(const AttendCall& A, int w, int len, int from)
 {
     int n = 0;
     const int nq = row_tiles<R>(A, w);
 #pragma unroll 1
     for (int qt = 0; qt < nq; ++qt) {
-        const Shape s = unit_tiles<R>(A, w, len, qt);
+        const Shape s = unit_tiles<R, SEE>(A, w, len, from, qt);
         n += s.z - s.a + 1 + kUnitCost<R>;
     }
     return n;
@@ -398,21 +417,23 @@ inline bool places_fit(const AttendCall& A)
 }
 
 // The units of one run in order.
-template <int R>
+template <int R, int SEE>
 struct Walk {
     int b, h, qt, nq;
     int row0, w, len;
+    int from;                    // kSuffix: the first own token; kSinks: the unit's skipped tiles
     int a, z, k0, n;             // the unit's tiles [a, z]; this piece: n tiles from k0
     int unit;                    // the unit's first place on the line
     int stop;                    // the run's end on the line
 
-    __device__ __forceinline__ void piece(const AttendCall& A, int from)
+    __device__ __forceinline__ void piece(const AttendCall& A, int place)
     {
-        const Shape s = unit_tiles<R>(A, w, len, qt);
+        const Shape s = unit_tiles<R, SEE>(A, w, len, from, qt);
         a = s.a;
         z = s.z;
+        if constexpr (SEE == kSinks) from = s.skip;
         const int first = unit + kUnitCost<R>;                          // the place of the first tile
-        const int k = from > first ? from - first : 0;
+        const int k = place > first ? place - first : 0;
         k0 = a + k;
         n = min(stop - first, z - a + 1) - k;                        // <= 0: nothing of it here
     }
@@ -430,7 +451,7 @@ struct Walk {
 #pragma unroll 1
                 do {             // there is one with rows before the run's end
                     ++b;
-                    request_rows(A, b, &row0, &w, &len, &bits);
+                    rows_of<SEE>(A, b, &row0, &w, &len, &from, &bits);
                 } while (w <= 0 && b + 1 < A.B);
                 nq = row_tiles<R>(A, w);
             }
@@ -446,8 +467,7 @@ struct Walk {
     // The first token that some row of the unit sees.
     __device__ __forceinline__ int first_seen(const AttendCall& A) const
     {
-        const int p0 = len + (qt == 0 ? 0 : qt * R / A.group);
-        return A.window > 0 && p0 >= A.window ? p0 - A.window + 1 : 0;
+        return first_seen_at<SEE>(A, len + (qt == 0 ? 0 : qt * R / A.group), from);
     }
 };
 
@@ -459,10 +479,10 @@ struct Walk {
 // short. Where units are prompts' 128 rows, a few requests can have hundreds each: a group is then
 // up to a warp, whose lanes take a request's units in turn (two prompts of 2000 rows and 32 heads:
 // 66,600 cycles with single threads).
-template <int R>
+template <int R, int SEE>
 struct Cut {
     int scan[32];
-    Walk<R> walk;
+    Walk<R, SEE> walk;
 };
 // A group: its lane, size and lanes' mask.
 struct Group {
@@ -471,15 +491,15 @@ struct Group {
     template <class T>
     __device__ __forceinline__ T from(T x, int lane_of) const { return __shfl_sync(mask, x, lane_of, size); }
 };
-template <int R>
-__device__ __forceinline__ int group_places(const AttendCall& A, int w, int len, const Group& gr)
+template <int R, int SEE>
+__device__ __forceinline__ int group_places(const AttendCall& A, int w, int len, int from, const Group& gr)
 {
-    if constexpr (R < kTile) return head_places<R>(A, w, len);
+    if constexpr (R < kTile) return head_places<R, SEE>(A, w, len, from);
     int n = 0;
     const int nq = row_tiles<R>(A, w);
 #pragma unroll 1
     for (int qt = gr.g; qt < nq; qt += gr.size) {
-        const Shape s = unit_tiles<R>(A, w, len, qt);
+        const Shape s = unit_tiles<R, SEE>(A, w, len, from, qt);
         n += s.z - s.a + 1 + kUnitCost<R>;
     }
     for (int d = 1; d < gr.size; d <<= 1) n += __shfl_xor_sync(gr.mask, n, d);
@@ -487,8 +507,8 @@ __device__ __forceinline__ int group_places(const AttendCall& A, int w, int len,
 }
 // By one group: the run [t0, t1) starts `off` places into the requests from b on. `k` holds request
 // b already, and `per_head` its places per head.
-template <int R>
-__device__ __forceinline__ void find_start(const AttendCall& A, Walk<R>& k, int per_head, int off, int t0, int t1,
+template <int R, int SEE>
+__device__ __forceinline__ void find_start(const AttendCall& A, Walk<R, SEE>& k, int per_head, int off, int t0, int t1,
                                            const Group& gr)
 {
     int bits = 0;
@@ -496,8 +516,8 @@ __device__ __forceinline__ void find_start(const AttendCall& A, Walk<R>& k, int 
     while (off >= per_head * A.c.heads) {        // only where a group counts several requests
         off -= per_head * A.c.heads;
         ++k.b;
-        request_rows(A, k.b, &k.row0, &k.w, &k.len, &bits);
-        per_head = group_places<R>(A, k.w, k.len, gr);
+        rows_of<SEE>(A, k.b, &k.row0, &k.w, &k.len, &k.from, &bits);
+        per_head = group_places<R, SEE>(A, k.w, k.len, k.from, gr);
     }
     k.h = static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(per_head));
     off -= k.h * per_head;
@@ -519,7 +539,7 @@ __device__ __forceinline__ void find_start(const AttendCall& A, Walk<R>& k, int 
             const int qt = k.qt + gr.g;
             int n = 0;
             if (qt < k.nq) {
-                const Shape s = unit_tiles<R>(A, k.w, k.len, qt);
+                const Shape s = unit_tiles<R, SEE>(A, k.w, k.len, k.from, qt);
                 n = s.z - s.a + 1 + kUnitCost<R>;
             }
             int upto = n;
@@ -541,8 +561,8 @@ __device__ __forceinline__ void find_start(const AttendCall& A, Walk<R>& k, int 
         k.piece(A, t0);
     }
 }
-template <int R, int NT>
-__device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R>& cut)
+template <int R, int SEE, int NT>
+__device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R, SEE>& cut)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int bits = 0;
@@ -556,13 +576,13 @@ __device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R>& cut)
     const int per = (A.B + groups - 1) / groups;
     const int b0 = min(tid / gr.size * per, A.B), b1 = min(b0 + per, A.B);
     int mine = 0, per_head = 1;
-    Walk<R> k;
+    Walk<R, SEE> k;
     if (tid == 0) cut.walk.n = 0;
 #pragma unroll 1
     for (int b = b1 - 1; b >= b0; --b) {         // downwards: the walk is left at the first one
         k.b = b;
-        request_rows(A, b, &k.row0, &k.w, &k.len, &bits);
-        per_head = group_places<R>(A, k.w, k.len, gr);
+        rows_of<SEE>(A, b, &k.row0, &k.w, &k.len, &k.from, &bits);
+        per_head = group_places<R, SEE>(A, k.w, k.len, k.from, gr);
         mine += gr.g == 0 ? per_head * A.c.heads : 0;
     }
     int upto = mine;
@@ -589,15 +609,47 @@ __device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R>& cut)
         from = gr.from(from, 0);
     }
     if (t0 < t1 && t0 >= from && t0 < from + mine) {
-        find_start<R>(A, k, per_head, t0 - from, t0, t1, gr);
+        find_start<R, SEE>(A, k, per_head, t0 - from, t0, t1, gr);
         if (gr.g == 0) cut.walk = k;
     }
     if (blockIdx.x == 0 && bits) raise_status(A.status, bits);
     return run;
 }
+// ---- results of a prefix, joined with those of the own tokens --------------------------------
+// Of two parts' log2 sums s and p: the shares of their quotients in the whole, and its log2 sum.
+struct Shares {
+    float s, p, lse;
+};
+__device__ __forceinline__ Shares shares_of(float s, float p)
+{
+    if (s == -INFINITY && p == -INFINITY) return {0.0f, 0.0f, -INFINITY};
+    const float top = fmaxf(s, p);
+    const float ws = exp2f(s - top), wp = exp2f(p - top), inv = 1.0f / (ws + wp);
+    return {ws * inv, wp * inv, top + log2f(ws + wp)};
+}
+// Every request's first own token, by a whole grid: its group's prefix, if the group is computed
+// apart, its rows are the request's too and all of it lies before the request's rows; else 0.
+__device__ __forceinline__ void write_from(const AttendCall& A)
+{
+    for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < A.requests; b += gridDim.x * blockDim.x) {
+        int lo = 0, hi = A.B;                    // the last group that starts at or before b
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (A.group_cu[mid] <= b) lo = mid; else hi = mid;
+        }
+        int from = 0;
+        if (A.group_cu[lo] <= b && b < A.group_cu[lo + 1]) {
+            int r0, w, n;
+            group_rows(A, lo, &r0, &w, &n);
+            if (w > 0 && A.cu[b] >= r0 && A.cu[b] <= A.cu[b + 1] && A.cu[b + 1] <= r0 + w && A.lengths[b] >= n) from = n;
+        }
+        A.from[b] = from;
+    }
+}
+
 // The run's entry for the join, by one thread.
-template <int R>
-__device__ __forceinline__ void write_meta(const AttendCall& A, const Workspace& ws, const Walk<R>& k, int run)
+template <int R, int SEE>
+__device__ __forceinline__ void write_meta(const AttendCall& A, const Workspace& ws, const Walk<R, SEE>& k, int run)
 {
     RunMeta m;
     m.unit = k.unit;
@@ -606,6 +658,8 @@ __device__ __forceinline__ void write_meta(const AttendCall& A, const Workspace&
     m.run = run;
     m.row0 = k.row0;
     m.rows = k.n > 0 && k.k0 > k.a ? k.rows(A) : 0;
+    if constexpr (SEE == kSuffix)
+        if (m.rows > 0 && k.from > 0) m.rows |= kHasPrefix;
     m.flat0 = k.qt * R;
     m.head0 = k.h * A.group;
     ws.meta[blockIdx.x] = m;

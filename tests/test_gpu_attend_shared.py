@@ -1,0 +1,262 @@
+"""dspark_attend_shared against 64 bits over every request's whole context: one group and several, few
+rows and many on either side of the prefix, prefixes of one page to many tiles and ends inside a tile;
+groups that make no sense attend alone; pages out of range, queries that are no numbers, strides,
+graphs, two calls in a row; the refusals."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import forms_ref
+from speculative_decoding_ragged_gb300 import _binding as bd
+from test_gpu_attend import BOTH, Case
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from speculative_decoding_ragged_gb300 import build
+    build.build()
+    return bd.lib()
+
+
+def test_refuses_on_the_host(lib):
+    P = ctypes.c_void_p
+    c = bd._Cache(4096, 4096, 4096, 4096, 4096, 8, 2, 16, 64, 4)
+
+    def call(q=4096, hq=4, rows=3, B=2, gcu=4096, prefix=4096, groups=1, ws=4096, wb=1 << 30, scale=0.1):
+        rc = lib.dspark_attend_shared(ctypes.byref(c), P(q), 256, P(4096), 256, hq, 0, rows, P(4096), P(4096), B,
+                                      P(gcu), P(prefix), groups, scale, P(None), P(ws), wb, None, None)
+        return rc, bd.last_error()
+
+    need = bd.dspark_attend_shared_workspace_bytes(3, 4, 2, 64, 2)
+    assert need == bd.dspark_attend_workspace_bytes(2, 64) + 3 * 4 * 65 * 4 + 8
+    for code, kw, word in [(-1, dict(groups=-1), "groups"), (-1, dict(gcu=None), "group_cu"),
+                           (-1, dict(prefix=None), "prefix"), (-1, dict(gcu=4097), "group_cu"),
+                           (-1, dict(wb=need - 1), "workspace"), (-1, dict(ws=4104), "workspace"),
+                           (-1, dict(ws=None), "workspace"), (-1, dict(hq=3), "q_heads"),
+                           (-1, dict(q=None), "required"), (-1, dict(scale=float("inf")), "scale")]:
+        rc, msg = call(**kw)
+        assert rc == code and msg.startswith("dspark_attend_shared") and word in msg, (kw, rc, msg)
+    assert call(rows=0, q=None)[0] == 0 and call(B=0)[0] == 0
+    for bad in ((-1, 4, 2, 64, 2), (3, 3, 2, 64, 2), (3, 4, 2, 24, 2), (3, 4, 2, 64, -1), (3, 0, 1, 64, 2)):
+        assert bd.dspark_attend_shared_workspace_bytes(*bad) == 0 and "bad sizes" in bd.last_error()
+
+
+class Shared(Case):
+    """groups: (requests, prefix) of consecutive groups from request 0 on; own: tokens of each request
+    after its prefix."""
+
+    def __init__(self, seed, w, own, groups, heads, group, dim, page, **kw):
+        front = np.zeros(len(w), np.int64)
+        b = 0
+        for n, p in groups:
+            front[b:b + n] = p
+            b += n
+        super().__init__(seed, w, front + np.asarray(own), heads, group, dim, page, **kw)
+        b = 0
+        for n, p in groups:
+            self.table[b:b + n, :p // page] = self.table[b, :p // page]
+            b += n
+        self.group_cu = np.cumsum([0] + [n for n, _ in groups]).astype(np.int32)
+        self.prefix = np.asarray([p for _, p in groups], np.int32)
+
+    def go(self, dtype, *, strides=False, prepare=False, lse=True, fill=0xAA):
+        dev = torch.device("cuda:0")
+        t = lambda a: torch.as_tensor(np.ascontiguousarray(a)).to(dev)     # noqa: E731
+        cache = bd.PagedCache(t(self.codes["k"]), t(self.codes["v"]), t(self.scale["k"]), t(self.scale["v"]),
+                              t(self.table))
+        q = torch.as_tensor(self.q).to(dtype).to(dev)
+        if strides:
+            q = torch.cat([q, torch.full_like(q, float("nan"))], 1)[:, :self.hq]
+        out = torch.full((self.rows, self.hq + (2 if strides else 0), self.dim), 5.0, dtype=dtype, device=dev)
+        out = out[:, :self.hq]
+        ls = torch.full((self.rows, self.hq), 5.0, device=dev) if lse else None
+        st = torch.zeros(1, dtype=torch.int32, device=dev)
+        size = bd.dspark_attend_shared_workspace_bytes(self.rows, self.hq, self.heads, self.dim, len(self.lengths))
+        ws = torch.full((size,), fill, dtype=torch.uint8, device=dev)
+        cu, lengths, gcu, prefix = t(self.cu), t(self.lengths), t(self.group_cu), t(self.prefix)
+        call = bd.dspark_attend_shared(cache, q, out, cu, lengths, gcu, prefix, ws, lse=ls, status=st, prepare=True)
+        if prepare:
+            return call, q, out, ls, (cache, ws, cu, lengths, gcu, prefix, st)
+        call()
+        call()                               # the second call finds the first's workspace
+        torch.cuda.synchronize()
+        return q.double().cpu().numpy(), out.double().cpu().numpy(), \
+            ls.double().cpu().numpy() if lse else None, int(st.item())
+
+    def hold(self, dtype=torch.bfloat16, status=0, **kw):
+        q, out, lse, st = self.go(dtype, **kw)
+        assert st == status
+        forms_ref.check(self, dtype, q, out, lse, lambda b, pos: np.arange(pos + 1), joined=True)
+        return out, lse
+
+
+# w, own tokens, groups, heads, group, dim, page: the prefix's rows are few (the narrow kernel) or many
+# (the wide one), the own tokens' too; prefixes that end inside a tile and at its end; cut over many CTAs
+SHAPES = [
+    ([1, 1], [0, 0], [(2, 16)], 1, 1, 64, 16),
+    ([1, 1, 1], [0, 5, 130], [(3, 128)], 2, 4, 128, 128),
+    ([4, 4, 4, 4], [20, 33, 60, 0], [(4, 992)], 2, 4, 128, 16),
+    ([1] * 40, list(range(0, 400, 10)), [(40, 1024)], 2, 4, 128, 32),
+    ([3, 1, 7, 2, 5], [1, 300, 0, 129, 15], [(2, 48), (3, 640)], 2, 3, 64, 16),
+    ([2, 0, 3, 1, 0], [9, 50, 0, 700, 3], [(5, 5008)], 1, 8, 64, 16),
+    ([1, 8] * 12, [7 * i for i in range(24)], [(6, 96), (10, 2048), (8, 320)], 1, 4, 128, 32),
+    ([90, 60], [100, 3], [(2, 256)], 1, 4, 64, 64),
+    ([40, 1, 70], [0, 900, 200], [(3, 3008)], 2, 2, 128, 64),
+    ([16, 16], [2500, 1], [(2, 64)], 2, 2, 128, 64),
+    ([1] * 4, [1] * 4, [(4, 9984)], 2, 2, 128, 128),
+]
+
+
+@gpu
+@pytest.mark.parametrize("shape", SHAPES)
+def test_shared(lib, shape):
+    c = Shared(len(shape[0]) + shape[6], *shape)
+    c.hold()
+    c.q *= 5.0                               # one token takes nearly all, before or behind the prefix's end
+    c.hold()
+
+
+@gpu
+@pytest.mark.parametrize("shape", [SHAPES[2], SHAPES[4]])
+def test_fp32_attends_alone(lib, shape):
+    Shared(1, *shape).hold(torch.float32)
+
+
+@gpu
+@pytest.mark.parametrize("dim", [16, 96, 256])
+def test_other_head_sizes(lib, dim):
+    for dtype in BOTH:
+        Shared(dim, [3, 1], [40, 7], [(2, 64)], 2, 3, dim, 16).hold(dtype)
+
+
+def base(seed=2):
+    return Shared(seed, [2, 3, 1, 4, 2], [30, 5, 200, 64, 0], [(3, 160), (2, 320)], 2, 4, 128, 16)
+
+
+@gpu
+def test_a_prefix_counts_in_whole_pages(lib):
+    c = base()
+    want = c.go(torch.bfloat16)
+    c.prefix += 15
+    got = c.hold()
+    np.testing.assert_array_equal(got[0], want[1])
+
+
+@gpu
+@pytest.mark.parametrize("what", ["one", "none", "short", "negative", "long", "gap", "outside", "backwards", "rows",
+                                  "empty"])
+def test_groups_that_attend_alone(lib, what):
+    """Whatever the groups say, a row sees its request's tokens."""
+    c = base(3)
+    status = 0
+    if what == "one":                        # groups of one request
+        c.group_cu, c.prefix = np.arange(6, dtype=np.int32), np.full(5, 160, np.int32)
+    elif what == "none":
+        c.prefix[:] = 0
+    elif what == "short":                    # a request with fewer tokens than the prefix
+        c.lengths[1] = 100
+    elif what == "negative":
+        c.prefix[:] = [-16, -(1 << 31)]
+    elif what == "long":                     # past the page table
+        c.prefix[:] = [1 << 30, 2 ** 31 - 1]
+    elif what == "gap":                      # requests before, between and behind the groups
+        c.group_cu, c.prefix = np.asarray([1, 3, 3], np.int32), np.asarray([160, 64], np.int32)
+    elif what == "outside":                  # requests that are none
+        c.group_cu = np.asarray([0, 3, 9], np.int32)
+    elif what == "backwards":
+        c.group_cu = np.asarray([3, 0, 5], np.int32)
+        c.prefix[:] = [160, 64]
+        c.table[3:, :4] = c.table[0, :4]     # requests 0 to 4 now share 64 tokens
+    elif what == "rows":                     # packed rows of a group that end behind the buffer
+        c.cu[5] = c.rows + 3
+        status = bd.STATUS_BAD_ROWS
+        q, out, lse, st = c.go(torch.bfloat16)
+        assert st == status
+        c.cu[5] = 10                         # request 4 got nothing written
+        forms_ref.check(c, torch.bfloat16, q, out, lse, lambda b, pos: np.arange(pos + 1), joined=True)
+        return
+    elif what == "empty":                    # no rows in the first group, no groups at all
+        c = Shared(4, [0, 0, 2, 3], [30, 5, 200, 64], [(2, 160), (2, 320)], 2, 4, 64, 16)
+        c.hold()
+        c.group_cu, c.prefix = np.zeros(1, np.int32), np.zeros(0, np.int32)
+    c.hold(status=status)
+
+
+@gpu
+def test_bad_pages(lib):
+    c = base(5)
+    c.table[:3, 4] = c.n                     # in the first prefix
+    c.table[3:, 0] = -1
+    c.table[2, 17] = 10 ** 6                 # one of request 2's own
+    c.hold(status=bd.STATUS_BAD_PAGE)
+    c = Shared(6, [2, 1, 70], [0, 0, 20], [(3, 64)], 1, 4, 64, 64)
+    c.table[:, 0] = -1                       # nothing of the prefix: the own tokens alone
+    out, lse = c.hold(status=bd.STATUS_BAD_PAGE)
+    c.table[:] = -1                          # nothing at all
+    _, lse = c.hold(status=bd.STATUS_BAD_PAGE)
+    assert np.isneginf(lse[:73]).all()
+
+
+@gpu
+def test_queries_that_are_no_numbers(lib):
+    c = base(7)
+    _, clean, _, _ = c.go(torch.bfloat16)
+    c.q[2, 1, 5], c.q[7, 2, 0] = np.nan, np.inf
+    _, out, _, _ = c.go(torch.bfloat16)
+    hit = np.zeros(out.shape[:2], bool)
+    hit[2, 1] = hit[7, 2] = True
+    assert np.isnan(out[hit]).all()
+    np.testing.assert_array_equal(out[~hit], clean[~hit])
+
+
+@gpu
+@pytest.mark.parametrize("shape", [SHAPES[3], SHAPES[8]])
+def test_strides_no_lse_and_the_same_bits(lib, shape):
+    c = Shared(8, *shape)
+    out, _ = c.hold()
+    for kw in (dict(strides=True), dict(lse=False), dict(fill=0xFF)):
+        np.testing.assert_array_equal(c.go(torch.bfloat16, **kw)[1], out)
+
+
+@gpu
+@pytest.mark.parametrize("shape", [SHAPES[2], SHAPES[8]])
+def test_graph_on_another_stream(lib, shape):
+    """Replays with other groups in the same buffers too."""
+    c = Shared(9, *shape)
+    want = c.go(torch.bfloat16)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        call, q, out, lse, keep = c.go(torch.bfloat16, prepare=True)
+        graph = bd.StepGraph(stream)
+        call()
+        graph.end()
+    stream.synchronize()
+    assert (out == 5).all()
+    for _ in range(2):
+        graph.launch()
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(out.double().cpu().numpy(), want[1])
+    np.testing.assert_array_equal(lse.double().cpu().numpy(), want[2])
+    keep[5].fill_(c.page)                    # a prefix of one page
+    graph.launch()
+    torch.cuda.synchronize()
+    forms_ref.check(c, torch.bfloat16, q.double().cpu().numpy(), out.double().cpu().numpy(),
+                    lse.double().cpu().numpy(), lambda b, pos: np.arange(pos + 1), joined=True)
+
+
+@gpu
+@pytest.mark.parametrize("seed", range(10))
+def test_random_shapes(lib, seed):
+    rng = np.random.default_rng(500 + seed)
+    G = int(rng.integers(1, 5))
+    page = int(rng.choice([16, 32, 64, 128]))
+    groups = [(int(rng.integers(1, 7)), int(rng.integers(0, 900)) // page * page) for _ in range(G)]
+    B = sum(n for n, _ in groups)
+    w = rng.integers(0, 9, B) if seed % 3 else rng.integers(0, 60, B)
+    w[0] = max(w[0], 1)
+    Shared(seed, w, rng.integers(0, 500, B), groups, int(rng.integers(1, 4)), int(rng.integers(1, 9)),
+           int(rng.choice([64, 128])), page, spread=2.0).hold()
