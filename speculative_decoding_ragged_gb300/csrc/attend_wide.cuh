@@ -352,6 +352,12 @@ static __device__ __noinline__ void finish(const AttendCall& A, const Row& r, ui
     uint16_t* out = static_cast<uint16_t*>(A.out) + prow * A.out_stride + static_cast<int64_t>(head) * D;
     float* po = ws.o + (static_cast<int64_t>(part) * kTile + row) * D;
     const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+    float4 next[4];                     // the prefix's elements, sixteen ahead
+    auto fetch = [&](int d) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) next[j] = *reinterpret_cast<const float4*>(prefix + d + 4 * j);
+    };
+    if (SEE == kSuffix && joins) fetch(0);
 #pragma unroll 1
     for (int d = 0; d < D; d += 16) {
         float o[16];
@@ -359,6 +365,17 @@ static __device__ __noinline__ void finish(const AttendCall& A, const Row& r, ui
         tc_wait_ld();
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[j] *= g;
+        if constexpr (SEE == kSuffix)
+            if (joins) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    o[4 * j] = fmaf(gp, next[j].x, o[4 * j]);
+                    o[4 * j + 1] = fmaf(gp, next[j].y, o[4 * j + 1]);
+                    o[4 * j + 2] = fmaf(gp, next[j].z, o[4 * j + 2]);
+                    o[4 * j + 3] = fmaf(gp, next[j].w, o[4 * j + 3]);
+                }
+                if (d + 16 < D) fetch(d + 16);
+            }
         if (!live) continue;
         if (!whole) {
 #pragma unroll
@@ -372,17 +389,6 @@ static __device__ __noinline__ void finish(const AttendCall& A, const Row& r, ui
                 *reinterpret_cast<float4*>(prefix + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
             continue;
         }
-        if constexpr (SEE == kSuffix)
-            if (joins) {
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 p = *reinterpret_cast<const float4*>(prefix + d + j);
-                    o[j] = fmaf(gp, p.x, o[j]);
-                    o[j + 1] = fmaf(gp, p.y, o[j + 1]);
-                    o[j + 2] = fmaf(gp, p.z, o[j + 2]);
-                    o[j + 3] = fmaf(gp, p.w, o[j + 3]);
-                }
-            }
         if (vec) {
             *reinterpret_cast<uint4*>(out + d) = store16<DSPARK_BF16>(o);
             *reinterpret_cast<uint4*>(out + d + 8) = store16<DSPARK_BF16>(o + 8);
