@@ -592,8 +592,9 @@ int dspark_attend_sinks(const dspark_cache* cache, const void* q, int64_t q_stri
  * group_cu [groups + 1] int32, non-decreasing; prefix [groups] int32 (both may be NULL where groups is 0);
  * the rest as in dspark_attend. workspace: at least dspark_attend_shared_workspace_bytes(rows, q_heads,
  * heads, dim, B) bytes, 16-byte aligned, no clearing needed, rewritten by every call; calls that share
- * it must not overlap. Four kernels: the prefixes and their join, the requests' own tokens and theirs.
- * fp32, and dims other than 64 and 128, attend request by request.
+ * it must not overlap. Five kernels: a plan, the requests' own tokens and their join, the prefixes and
+ * theirs; where the prefixes are too short, or too few requests share them, to be worth that, each
+ * request attends alone. So do fp32 and dims other than 64 and 128.
  *
  * Precision: as dspark_attend for each of a row's two parts, whose quotients are kept in fp32.
  * ------------------------------------------------------------------------------------- */

@@ -8,9 +8,10 @@ namespace dspark {
 // What the rows of a call see, a template argument of the tensor-core kernels:
 //   kAll     every token up to the row's own, or the last `window` of them
 //   kSinks   the last `window` tokens, and of those before them the first `sinks`
+//   kSuffix  a request's own tokens, those behind its group's prefix; results of a request that has
+//            one are partial, for
 //   kPrefix  the rows of a whole group of requests see its shared tokens, all of them: a "request" is
-//            a group, its length the prefix. Results are partial ones, for
-//   kSuffix  a request's own tokens, those behind its group's prefix, joined with the partial results
+//            a group, its length the prefix. Results are joined with the partial ones.
 enum See { kAll = 0, kSinks = 1, kPrefix = 2, kSuffix = 3 };
 
 struct AttendCall {
@@ -36,8 +37,9 @@ struct AttendCall {
     int requests;
     const int32_t* group_cu;   // a group's requests: group_cu[g] .. group_cu[g + 1] - 1
     const int32_t* prefix;     // its shared tokens
-    int32_t* from;             // [requests] a request's first token that is its own; 0: all are
-    float* part_lse;           // [rows * q_heads] what the prefix gives each row: log2 of the sum,
+    int32_t* from;             // [requests + 1] a request's first token that is its own; 0: all are.
+                               // The last: whether prefixes are computed apart at all
+    float* part_lse;           // [rows * q_heads] what the own tokens give each row: log2 of the sum
     float* part;               // [rows * q_heads, dim] and the quotient
 };
 
@@ -67,9 +69,9 @@ __device__ __forceinline__ void request_rows(const AttendCall& A, int b, int* ro
     else if (*w > 0 && n + *w > A.reach) *bits |= DSPARK_STATUS_BAD_PAGE;
 }
 
-// A group's rows [row0, row0 + w) and its shared tokens in whole pages; w = 0 where they are not to be
+// A group's rows [row0, row0 + w) and its shared tokens in whole pages; w = 0 where they cannot be
 // computed apart: a group of one, no whole page, rows or requests that are none.
-__device__ __forceinline__ void group_rows(const AttendCall& A, int g, int* row0, int* w, int* len)
+__device__ __forceinline__ void group_shape(const AttendCall& A, int g, int* row0, int* w, int* len)
 {
     const int b0 = A.group_cu[g], b1 = A.group_cu[g + 1];
     const int n = A.prefix[g] / A.c.page * A.c.page;
@@ -80,6 +82,12 @@ __device__ __forceinline__ void group_rows(const AttendCall& A, int g, int* row0
     if (r0 < 0 || r1 < r0 || r1 > A.rows) return;
     *row0 = r0;
     *w = r1 - r0;
+}
+// The same of a call's groups, none where it does not pay.
+__device__ __forceinline__ void group_rows(const AttendCall& A, int g, int* row0, int* w, int* len)
+{
+    group_shape(A, g, row0, w, len);
+    if (A.from[A.requests] == 0) *w = 0;
 }
 // What a call takes as its requests; *from: the first token that is seen at all (kSuffix).
 template <int SEE>

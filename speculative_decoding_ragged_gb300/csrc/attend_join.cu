@@ -14,48 +14,49 @@ namespace {
 constexpr int kJoinWarps = 8;
 constexpr int kFewParts = 4, kFewRows = 4;
 
-// A unit's row: where its result goes, and what its group's prefix gives it (kSuffix).
+// A unit's row: where its result goes, and (kPrefix) what it is joined with.
 struct JoinRow {
     int64_t prow, at;
     int head;
-    float prefix_lse;
-    float4 prefix;
+    float own_lse;
+    float4 own;
 };
 template <int D, int SEE>
-__device__ __forceinline__ JoinRow join_row(const AttendCall& A, const RunMeta& m, int row, bool joins, int lane)
+__device__ __forceinline__ JoinRow join_row(const AttendCall& A, const RunMeta& m, int row, int lane)
 {
     JoinRow r;
     const int flat = m.flat0 + row;
     r.prow = m.row0 + flat / A.group;
     r.head = m.head0 + flat % A.group;
     r.at = r.prow * A.q_heads + r.head;
-    if (SEE == kSuffix && joins) {
-        r.prefix_lse = A.part_lse[r.at];
-        r.prefix = lane * 4 < D ? *reinterpret_cast<const float4*>(A.part + r.at * D + lane * 4)
-                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if constexpr (SEE == kPrefix) {
+        r.own_lse = A.part_lse[r.at];
+        r.own = lane * 4 < D ? *reinterpret_cast<const float4*>(A.part + r.at * D + lane * 4)
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     return r;
 }
 // Its parts added up: written out.
 template <int D, int SEE>
-__device__ __forceinline__ void put_row(const AttendCall& A, const JoinRow& r, bool joins, int lane, float top,
+__device__ __forceinline__ void put_row(const AttendCall& A, const JoinRow& r, bool partial, int lane, float top,
                                         float sum, float4 acc)
 {
     float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     float lse = sum == 0.0f ? -INFINITY : top + log2f(sum);
-    if constexpr (SEE == kPrefix) {
+    if (SEE == kSuffix && partial) {
         if (lane * 4 < D)
             *reinterpret_cast<float4*>(A.part + r.at * D + lane * 4) =
                 make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if (lane == 0) A.part_lse[r.at] = lse;
         return;
     }
-    if (SEE == kSuffix && joins) {
-        const Shares sh = shares_of(lse, r.prefix_lse);
+    if constexpr (SEE == kPrefix) {
+        if (!is_part(r.own_lse)) return;                 // none of this call's rows
+        const Shares sh = shares_of(lse, r.own_lse);
         inv *= sh.s;
         lse = sh.lse;
-        acc = make_float4(fmaf(acc.x, inv, sh.p * r.prefix.x), fmaf(acc.y, inv, sh.p * r.prefix.y),
-                          fmaf(acc.z, inv, sh.p * r.prefix.z), fmaf(acc.w, inv, sh.p * r.prefix.w));
+        acc = make_float4(fmaf(acc.x, inv, sh.p * r.own.x), fmaf(acc.y, inv, sh.p * r.own.y),
+                          fmaf(acc.z, inv, sh.p * r.own.z), fmaf(acc.w, inv, sh.p * r.own.w));
         inv = 1.0f;
     }
     if (lane * 4 < D) {
@@ -84,8 +85,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) attend_join_kernel(AttendC
     const Workspace ws = workspace_of(A.ws);
     RunMeta m = ws.meta[blockIdx.x];
     if (m.rows == 0) return;
-    const bool joins = SEE == kSuffix && (m.rows & kHasPrefix) != 0;
-    if constexpr (SEE == kSuffix) m.rows &= ~kHasPrefix;
+    const bool partial = SEE == kSuffix && (m.rows & kPartial) != 0;
+    if constexpr (SEE == kSuffix) m.rows &= ~kPartial;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = m.first / m.run;                          // the run of the unit's first tile
     const int c1 = (m.end + m.run - 1) / m.run;              // one past the run of its last
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) attend_join_kernel(AttendC
 #pragma unroll
             for (int j = 0; j < kFewRows; ++j) {
                 const int row = min(row0 + j * step, m.rows - 1);
-                r[j] = join_row<D, SEE>(A, m, row, joins, lane);
+                r[j] = join_row<D, SEE>(A, m, row, lane);
 #pragma unroll
                 for (int k = 0; k < kFewParts; ++k)
                     o[j][k] = c0 + k < c1 && lane * 4 < D
@@ -128,14 +129,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) attend_join_kernel(AttendC
                 for (int k = 0; k < kFewParts; ++k) add_part(acc, __shfl_sync(0xffffffffu, f, kLanes * j + k), o[j][k]);
                 const float its_top = __shfl_sync(0xffffffffu, top, kLanes * j);
                 const float its_sum = __shfl_sync(0xffffffffu, sum, kLanes * j);
-                if (row0 + j * step < m.rows) put_row<D, SEE>(A, r[j], joins, lane, its_top, its_sum, acc);
+                if (row0 + j * step < m.rows) put_row<D, SEE>(A, r[j], partial, lane, its_top, its_sum, acc);
             }
         }
         return;
     }
 #pragma unroll 1
     for (int row = share * kJoinWarps + warp; row < m.rows; row += step) {
-        const JoinRow r = join_row<D, SEE>(A, m, row, joins, lane);
+        const JoinRow r = join_row<D, SEE>(A, m, row, lane);
         float top = kNone, sum = 0.0f;
 #pragma unroll 1
         for (int c = c0 + lane; c < c1; c += 32) top = fmaxf(top, ws.ml[slot(c, row)].x);
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) attend_join_kernel(AttendC
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        put_row<D, SEE>(A, r, joins, lane, top, sum, acc);
+        put_row<D, SEE>(A, r, partial, lane, top, sum, acc);
     }
 }
 
@@ -222,14 +223,6 @@ size_t attend_workspace_bytes(int dim)
     return kMaxCtas * (sizeof(RunMeta) + 2 * kTile * (sizeof(float2) + dim * sizeof(float)));
 }
 
-// After the parts: each row's share of its group's prefix, and the requests' first own tokens.
-size_t attend_shared_workspace_bytes(int rows, int q_heads, int dim, int B)
-{
-    const size_t parts = attend_workspace_bytes(dim);
-    if (dim != 64 && dim != 128) return parts;
-    return parts + static_cast<size_t>(rows) * q_heads * (dim + 1) * sizeof(float) + static_cast<size_t>(B) * sizeof(int32_t);
-}
-
 namespace {
 template <int SEE>
 int launch_both(const AttendCall& A, int ctas, int device, cudaStream_t stream)
@@ -259,25 +252,6 @@ int launch_attend_mma(const AttendCall& A, See see, cudaStream_t stream)
     case kSuffix: return launch_both<kSuffix>(A, ctas, dev.device, stream);
     default: return launch_both<kAll>(A, ctas, dev.device, stream);
     }
-}
-
-// The prefixes as a call over groups, then the own tokens. Head sizes and types of the fp32 kernel have no
-// such form: it attends over the whole contexts.
-int launch_attend_shared(const AttendCall& A, const int32_t* group_cu, const int32_t* prefix, int groups, int dtype,
-                         cudaStream_t stream)
-{
-    if (groups == 0 || !attend_mma_serves(A, dtype)) return launch_attend(A, kAll, dtype, stream);
-    AttendCall own = A;
-    own.requests = A.B;
-    own.group_cu = group_cu;
-    own.prefix = prefix;
-    own.part = reinterpret_cast<float*>(static_cast<char*>(A.ws) + attend_workspace_bytes(A.c.dim));
-    own.part_lse = own.part + static_cast<int64_t>(A.rows) * A.q_heads * A.c.dim;
-    own.from = reinterpret_cast<int32_t*>(own.part_lse + static_cast<int64_t>(A.rows) * A.q_heads);
-    AttendCall shared = own;
-    shared.B = groups;
-    const int rc = launch_attend_mma(shared, kPrefix, stream);
-    return rc == DSPARK_OK ? launch_attend_mma(own, kSuffix, stream) : rc;
 }
 
 }  // namespace dspark

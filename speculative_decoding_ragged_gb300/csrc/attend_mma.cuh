@@ -63,11 +63,11 @@ struct RunMeta {
     int run;            // places per run
     int row0, rows;     // the request's first packed row; the unit's rows (position, head): 0 where
                         // the run starts with a unit's beginning, or holds no tile ... (kSuffix: and
-                        // kHasPrefix where the request has one)
+                        // kPartial where the request has a prefix)
     int flat0, head0;   // ... from this flat index on, first query head
 };
 
-constexpr int kHasPrefix = 1 << 16;
+constexpr int kPartial = 1 << 16;
 
 struct Workspace {
     RunMeta* meta;      // [kMaxCtas]
@@ -627,25 +627,9 @@ __device__ __forceinline__ Shares shares_of(float s, float p)
     const float ws = exp2f(s - top), wp = exp2f(p - top), inv = 1.0f / (ws + wp);
     return {ws * inv, wp * inv, top + log2f(ws + wp)};
 }
-// Every request's first own token, by a whole grid: its group's prefix, if the group is computed
-// apart, its rows are the request's too and all of it lies before the request's rows; else 0.
-__device__ __forceinline__ void write_from(const AttendCall& A)
-{
-    for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < A.requests; b += gridDim.x * blockDim.x) {
-        int lo = 0, hi = A.B;                    // the last group that starts at or before b
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (A.group_cu[mid] <= b) lo = mid; else hi = mid;
-        }
-        int from = 0;
-        if (A.group_cu[lo] <= b && b < A.group_cu[lo + 1]) {
-            int r0, w, n;
-            group_rows(A, lo, &r0, &w, &n);
-            if (w > 0 && A.cu[b] >= r0 && A.cu[b] <= A.cu[b + 1] && A.cu[b + 1] <= r0 + w && A.lengths[b] >= n) from = n;
-        }
-        A.from[b] = from;
-    }
-}
+// The log2 sum of a row that has no part to be joined with: no arithmetic makes this NaN.
+constexpr uint32_t kNoPart = 0xffffdeadu;
+__device__ __forceinline__ bool is_part(float lse) { return __float_as_uint(lse) != kNoPart; }
 
 // The run's entry for the join, by one thread.
 template <int R, int SEE>
@@ -659,7 +643,7 @@ __device__ __forceinline__ void write_meta(const AttendCall& A, const Workspace&
     m.row0 = k.row0;
     m.rows = k.n > 0 && k.k0 > k.a ? k.rows(A) : 0;
     if constexpr (SEE == kSuffix)
-        if (m.rows > 0 && k.from > 0) m.rows |= kHasPrefix;
+        if (m.rows > 0 && k.from > 0) m.rows |= kPartial;
     m.flat0 = k.qt * R;
     m.head0 = k.h * A.group;
     ws.meta[blockIdx.x] = m;

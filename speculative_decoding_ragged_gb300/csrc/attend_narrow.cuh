@@ -338,69 +338,55 @@ __device__ __forceinline__ bool soften(Smem<D, R, SEE>& sm, int grp, int slot, u
     return true;
 }
 
-// What a prefix gives this thread's element of a group's rows, and (thread d < the rows) its row's log2
-// sum: fetched before the piece's last products are waited for.
-template <int HR>
-struct FromPrefix {
-    float o[HR], lse;
-};
-template <int D, int R, int SEE>
-__device__ __forceinline__ void fetch_prefix(const AttendCall& A, const Smem<D, R, SEE>& sm, int grp, int slot, int rows,
-                                             FromPrefix<group_rows(R)>& p)
-{
-    constexpr int HR = group_rows(R);
-    const int r0 = grp * HR, d = threadIdx.x & 127;
-    auto at = [&](int r) -> int64_t {
-        return static_cast<int64_t>(sm.info[slot][r].prow) * A.q_heads + sm.info[slot][r].head;
-    };
-#pragma unroll
-    for (int r = 0; r < HR; ++r)
-        p.o[r] = r0 + r < rows && (D == 128 || d < D) ? A.part[at(r0 + r) * D + d] : 0.0f;
-    if (d < HR && r0 + d < rows) p.lse = A.part_lse[at(r0 + d)];
-}
-
 // A finished piece, after its row sums are in part: results or a part written. Lane d holds
-// element d. `joins`: the prefix's results are joined with these.
+// element d. `partial` (kSuffix): the row has a prefix, whose kernel joins them.
 template <int D, int R, int SEE>
 __device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R, SEE>& sm, int grp, int slot, uint32_t o_addr,
-                                       int rows, bool whole, bool joins, const FromPrefix<group_rows(R)>& prefix,
-                                       int part, const Workspace& ws)
+                                       int rows, bool whole, bool partial, int part, const Workspace& ws)
 {
     const int tid = threadIdx.x;
     constexpr int HR = group_rows(R);
     const int r0 = grp * HR;
     const int d = tid & 127;
-    if constexpr (SEE == kSuffix) {
-        if (joins) {                             // the shares of every row to all its threads
+    if constexpr (SEE == kPrefix) {
+        if (whole) {                             // the shares of every row to all its threads
             if (d < HR && r0 + d < rows) {
+                const int64_t at = static_cast<int64_t>(sm.info[slot][r0 + d].prow) * A.q_heads + sm.info[slot][r0 + d].head;
                 const float4 q = sm.part[r0 + d];
-                const float sum = (q.x + q.y) + (q.z + q.w);
-                const Shares sh = shares_of(sum == 0.0f ? -INFINITY : log2f(sum) - sm.ref[r0 + d], prefix.lse);
-                sm.grow[r0 + d] = sh.s;
-                sm.peak[r0 + d] = sh.p;
-                if (A.lse != nullptr)
-                    A.lse[static_cast<int64_t>(sm.info[slot][r0 + d].prow) * A.q_heads + sm.info[slot][r0 + d].head] = sh.lse * kLn2;
+                const float sum = (q.x + q.y) + (q.z + q.w), own = A.part_lse[at];
+                const Shares sh = shares_of(sum == 0.0f ? -INFINITY : log2f(sum) - sm.ref[r0 + d], own);
+                sm.grow[r0 + d] = sum == 0.0f ? 0.0f : __fdividef(sh.s, sum);
+                sm.peak[r0 + d] = is_part(own) ? sh.p : own;
+                if (A.lse != nullptr && is_part(own)) A.lse[at] = sh.lse * kLn2;
             }
             group_sync(grp);
         }
     }
     uint16_t* out = static_cast<uint16_t*>(A.out) + d;
     float* po = ws.o + static_cast<int64_t>(part) * kTile * D + d;
-    // rows c .. c + 3, whose elements of the prefix are prefix.o[p ..]
-    auto four = [&](int c, int p) {
+#pragma unroll 1
+    for (int c = r0; c < r0 + HR && c < rows; c += 4) {
         float o[sum_sets(R)][4];
 #pragma unroll
         for (int i = 0; i < sum_sets(R); ++i) tc_ld<4>(o_addr + i * R + c, o[i]);
         int64_t at[4];
-        float g[4];
+        float g[4], gp[4];                       // kPrefix: the own tokens' share
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float4 q = sm.part[c + j];
             const float sum = (q.x + q.y) + (q.z + q.w);
             const RowInfo in = sm.info[slot][c + j];
-            at[j] = SEE == kPrefix ? (static_cast<int64_t>(in.prow) * A.q_heads + in.head) * D
-                                   : in.prow * A.out_stride + static_cast<int64_t>(in.head) * D;
+            at[j] = in.prow * A.out_stride + static_cast<int64_t>(in.head) * D;
             g[j] = !whole ? 1.0f : sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);      // nothing seen: zeros
+            if (SEE == kSuffix && partial) at[j] = (static_cast<int64_t>(in.prow) * A.q_heads + in.head) * D + d;
+            if constexpr (SEE == kPrefix) {
+                gp[j] = sm.peak[c + j];
+                if (whole) {
+                    g[j] = sm.grow[c + j];
+                    if (c + j < rows && is_part(gp[j]) && (D == 128 || d < D))
+                        gp[j] *= A.part[(static_cast<int64_t>(in.prow) * A.q_heads + in.head) * D + d];
+                }
+            }
         }
         tc_wait_ld();
         if (D == 128 || d < D) {                 // D = 64: lanes 64.. repeat the first ones
@@ -410,22 +396,14 @@ __device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R, SEE>& sm,
 #pragma unroll
                 for (int i = sum_sets(R) - 2; i >= 0; --i) y += o[i][j];
                 y *= g[j];
-                if constexpr (SEE == kSuffix)
-                    if (joins) y = fmaf(sm.peak[c + j], prefix.o[p + j], sm.grow[c + j] * y);
-                if constexpr (SEE == kPrefix) {
-                    if (whole && c + j < rows) A.part[at[j] + d] = y;
+                if (SEE == kPrefix) {
+                    if (whole && c + j < rows && is_part(sm.peak[c + j])) store1<DSPARK_BF16>(out, at[j], y + gp[j]);
+                } else if (SEE == kSuffix && partial) {
+                    if (whole && c + j < rows) A.part[at[j]] = y;
                 } else if (whole && c + j < rows) store1<DSPARK_BF16>(out, at[j], y);
                 if (!whole && c + j < rows) po[(c + j) * D] = y;
             }
         }
-    };
-    if constexpr (SEE == kSuffix) {              // unrolled: the prefix's elements are in registers
-#pragma unroll
-        for (int p = 0; p < HR; p += 4)
-            if (r0 + p < rows) four(r0 + p, p);
-    } else {
-#pragma unroll 1
-        for (int c = r0; c < r0 + HR && c < rows; c += 4) four(c, 0);
     }
     const int r = r0 + d;
     if (d < HR && r < rows) {
@@ -435,9 +413,9 @@ __device__ __forceinline__ void finish(const AttendCall& A, Smem<D, R, SEE>& sm,
         const int64_t at = static_cast<int64_t>(sm.info[slot][r].prow) * A.q_heads + sm.info[slot][r].head;
         if (!whole)
             ws.ml[part * kTile + r] = make_float2(sum == 0.0f ? kNone : m, sum);
-        else if constexpr (SEE == kPrefix)
+        else if (SEE == kSuffix && partial)
             A.part_lse[at] = sum == 0.0f ? -INFINITY : m + log2f(sum);
-        else if (A.lse != nullptr && !(SEE == kSuffix && joins))
+        else if (A.lse != nullptr && SEE != kPrefix)
             A.lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
     }
 }
@@ -563,6 +541,13 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Workspace ws = workspace_of(A.ws);
     if (!smem_aligned(A, ws, raw)) return;
+    if constexpr (SEE == kPrefix) {              // a call that computes no prefix apart ends here
+        pdl_wait_and_trigger();
+        if (A.from[A.requests] == 0) {
+            if (threadIdx.x == 0) ws.meta[blockIdx.x].rows = 0;
+            return;
+        }
+    }
 
     if (tid < kSlots) {
         mbar_init(smem_addr(&sm.full[tid]), 1);
@@ -586,7 +571,6 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
         tc_fence_before();
     }
     pdl_wait_and_trigger();
-    if constexpr (SEE == kPrefix) write_from(A);
     const int run = cut_line<R, SEE, all_threads(R)>(A, sm.cut);
     tc_fence_before();
     __syncthreads();
@@ -911,17 +895,13 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     sums[r] = a.x;
                     sums[r + 1] = a.y;
                 }
-                const bool joins = SEE == kSuffix && pc.whole && pc.from > 0;
-                FromPrefix<HR> prefix;
-                if constexpr (SEE == kSuffix)
-                    if (joins) fetch_prefix<D, R, SEE>(A, sm, grp, piece & 3, rows, prefix);
                 reduce_rows<HR, false>(sm.part + grp * HR, sums, lane, warp & 3);
                 if (more) put(piece + 2);
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_addr(&sm.pv_done[(it - 1) & 1]),
                                                              ((it - 1) >> 1) & 1, stalled));
                 if (group_any(grp, !ok)) return false;
                 tc_fence_after();
-                finish<D, R, SEE>(A, sm, grp, piece & 3, o_addr, rows, pc.whole, joins, prefix,
+                finish<D, R, SEE>(A, sm, grp, piece & 3, o_addr, rows, pc.whole, SEE == kSuffix && pc.from > 0,
                                   blockIdx.x * 2 + (piece > 0), ws);
                 return true;
             };

@@ -1,0 +1,98 @@
+// attend_shared.cu — dspark_attend_shared: what is computed apart, and the calls of the attention kernels.
+//
+// With own tokens o and a prefix p, a row's result is (2^(lse_o - t) O_o + 2^(lse_p - t) O_p) / (2^(lse_o - t)
+// + 2^(lse_p - t)), t the larger log2 sum. The own tokens go first, request by request in units of few
+// rows, and leave each row's quotient and log2 sum in the workspace; the prefixes follow, group by group
+// in units of up to 128 rows of any of its requests, and join. So the join is paid by the kernel with
+// few, long units, whose parts are joined from the workspace anyway: with the own tokens last, each of
+// their many short units waited for 16 KB of the prefix's results (256 windows of 1 to 8 rows: 136 us
+// for 72).
+#include "attend_mma.cuh"
+
+namespace dspark {
+namespace {
+
+// A prefix computed apart costs a kernel's start and its join, about 25 us; a tile of 128 tokens and a
+// head that is not read again saves about 4 ns (2500 cycles on 304 CTAs). 84 answers in 12 groups behind
+// 300 to 5000 tokens, 3800 tiles saved: 40 us alone, 47 apart; 192 single tokens behind 16384, 195 thousand
+// tiles: 573 and 130.
+constexpr int64_t kWorth = 6000;
+
+// Whether the groups' prefixes are worth it; every request's first own token; no row has a part yet.
+constexpr int kPlanThreads = 256;
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttendCall A)
+{
+    __shared__ int64_t saved[kPlanThreads / 32];
+    pdl_wait_and_trigger();
+    const int tid = threadIdx.x;
+    const int at = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
+    for (int i = at; i < A.rows * A.q_heads; i += step) A.part_lse[i] = __uint_as_float(kNoPart);
+    int64_t tiles = 0;                           // each CTA adds them up for itself
+    for (int g = tid; g < A.B; g += kPlanThreads) {
+        const int64_t n = static_cast<int64_t>(A.group_cu[g + 1]) - A.group_cu[g];
+        if (n > 1 && n <= A.requests && A.prefix[g] > 0 && A.prefix[g] <= A.reach)
+            tiles += (n - 1) * ((A.prefix[g] + kTile - 1) / kTile);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, off);
+    if ((tid & 31) == 0) saved[tid >> 5] = tiles;
+    __syncthreads();
+    tiles = 0;
+    for (int i = 0; i < kPlanThreads / 32; ++i) tiles += saved[i];
+    const bool worth = tiles * A.c.heads >= kWorth;
+    if (at == 0) A.from[A.requests] = worth;
+    for (int b = at; b < A.requests; b += step) {
+        int lo = 0, hi = A.B;                    // the last group that starts at or before b
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (A.group_cu[mid] <= b) lo = mid; else hi = mid;
+        }
+        // its prefix, if the group is computed apart, its rows are the request's too and all of the
+        // prefix lies before the request's rows
+        int from = 0;
+        if (worth && A.group_cu[lo] <= b && b < A.group_cu[lo + 1]) {
+            int r0, w, n;
+            group_shape(A, lo, &r0, &w, &n);
+            if (w > 0 && A.cu[b] >= r0 && A.cu[b] <= A.cu[b + 1] && A.cu[b + 1] <= r0 + w && A.lengths[b] >= n) from = n;
+        }
+        A.from[b] = from;
+    }
+}
+
+}  // namespace
+
+// After the parts: each row's own tokens' quotient and log2 sum, the requests' first own tokens.
+size_t attend_shared_workspace_bytes(int rows, int q_heads, int dim, int B)
+{
+    const size_t parts = attend_workspace_bytes(dim);
+    if (dim != 64 && dim != 128) return parts;
+    return parts + static_cast<size_t>(rows) * q_heads * (dim + 1) * sizeof(float) +
+           (static_cast<size_t>(B) + 1) * sizeof(int32_t);
+}
+
+// Types and head sizes of the fp32 kernel have no such form: it attends over the whole contexts. So do
+// calls whose page tables are too small for any prefix to be worth computing apart (4 windows of 4 rows
+// behind 1000 tokens: 14 us alone, 33 apart, 21 with a plan that says so).
+int launch_attend_shared(const AttendCall& A, const int32_t* group_cu, const int32_t* prefix, int groups, int dtype,
+                         cudaStream_t stream)
+{
+    const int64_t most = (A.B - 1ll) * ((A.reach + kTile - 1ll) / kTile) * A.c.heads;
+    if (groups == 0 || most < kWorth || !attend_mma_serves(A, dtype)) return launch_attend(A, kAll, dtype, stream);
+    AttendCall own = A;
+    own.requests = A.B;
+    own.group_cu = group_cu;
+    own.prefix = prefix;
+    own.part = reinterpret_cast<float*>(static_cast<char*>(A.ws) + attend_workspace_bytes(A.c.dim));
+    own.part_lse = own.part + static_cast<int64_t>(A.rows) * A.q_heads * A.c.dim;
+    own.from = reinterpret_cast<int32_t*>(own.part_lse + static_cast<int64_t>(A.rows) * A.q_heads);
+    AttendCall shared = own;
+    shared.B = groups;
+    const int64_t items = static_cast<int64_t>(A.rows) * A.q_heads > A.B ? static_cast<int64_t>(A.rows) * A.q_heads : A.B;
+    const int64_t ctas = ceil_div(items, kPlanThreads);
+    int rc = launch_pdl("attend plan", plan_kernel, dim3(static_cast<unsigned>(ctas < 64 ? ctas : 64)),
+                        dim3(kPlanThreads), 0, stream, shared);
+    if (rc == DSPARK_OK) rc = launch_attend_mma(own, kSuffix, stream);
+    return rc == DSPARK_OK ? launch_attend_mma(shared, kPrefix, stream) : rc;
+}
+
+}  // namespace dspark

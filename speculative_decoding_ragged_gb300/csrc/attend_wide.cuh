@@ -327,37 +327,38 @@ static __device__ __noinline__ void finish(const AttendCall& A, const Row& r, ui
     const int flat = wk.qt * kRows + min(row, rows - 1);
     const int64_t prow = wk.row0 + flat / A.group;
     const int head = wk.h * A.group + flat % A.group;
-    // kPrefix, kSuffix: what the prefix gives the row, and its share
-    const bool joins = SEE == kSuffix && whole && wk.from > 0;
-    float* prefix = SEE == kPrefix || SEE == kSuffix ? A.part + (prow * A.q_heads + head) * D : nullptr;
+    // kSuffix: the row's results are partial, for its prefix's kernel to join. kPrefix: what they are
+    // joined with, and its share; rows without are none of this call's.
+    const bool partial = SEE == kSuffix && wk.from > 0;
+    const int64_t at = prow * A.q_heads + head;
+    float* other = SEE == kPrefix || SEE == kSuffix ? A.part + at * D : nullptr;
     float gp = 0.0f;
+    bool joins = false;
     if (live) {
         if (!whole) {
             ws.ml[part * kTile + row] = make_float2(l == 0.0f ? kNone : m, l);
         } else if constexpr (SEE == kPrefix) {
-            A.part_lse[prow * A.q_heads + head] = l == 0.0f ? -INFINITY : m + log2f(l);
-        } else if constexpr (SEE == kSuffix) {
-            float lse = l == 0.0f ? -INFINITY : m + log2f(l);
-            if (joins) {
-                const Shares sh = shares_of(lse, A.part_lse[prow * A.q_heads + head]);
-                g *= sh.s;
-                gp = sh.p;
-                lse = sh.lse;
-            }
-            if (A.lse != nullptr) A.lse[prow * A.q_heads + head] = lse * kLn2;
+            const float own = A.part_lse[at];
+            const Shares sh = shares_of(l == 0.0f ? -INFINITY : m + log2f(l), own);
+            joins = is_part(own);
+            g *= sh.s;
+            gp = sh.p;
+            if (A.lse != nullptr && joins) A.lse[at] = sh.lse * kLn2;
+        } else if (partial) {
+            A.part_lse[at] = l == 0.0f ? -INFINITY : m + log2f(l);
         } else if (A.lse != nullptr) {
-            A.lse[prow * A.q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            A.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
     }
     uint16_t* out = static_cast<uint16_t*>(A.out) + prow * A.out_stride + static_cast<int64_t>(head) * D;
     float* po = ws.o + (static_cast<int64_t>(part) * kTile + row) * D;
     const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-    float4 next[4];                     // the prefix's elements, sixteen ahead
+    float4 next[4];                     // the own tokens' elements, sixteen ahead
     auto fetch = [&](int d) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) next[j] = *reinterpret_cast<const float4*>(prefix + d + 4 * j);
+        for (int j = 0; j < 4; ++j) next[j] = *reinterpret_cast<const float4*>(other + d + 4 * j);
     };
-    if (SEE == kSuffix && joins) fetch(0);
+    if (SEE == kPrefix && joins) fetch(0);
 #pragma unroll 1
     for (int d = 0; d < D; d += 16) {
         float o[16];
@@ -365,7 +366,7 @@ static __device__ __noinline__ void finish(const AttendCall& A, const Row& r, ui
         tc_wait_ld();
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[j] *= g;
-        if constexpr (SEE == kSuffix)
+        if constexpr (SEE == kPrefix)
             if (joins) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -383,10 +384,11 @@ static __device__ __noinline__ void finish(const AttendCall& A, const Row& r, ui
                 *reinterpret_cast<float4*>(po + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
             continue;
         }
-        if constexpr (SEE == kPrefix) {
+        if (SEE == kPrefix && !joins) continue;
+        if (SEE == kSuffix && partial) {
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
-                *reinterpret_cast<float4*>(prefix + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                *reinterpret_cast<float4*>(other + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
             continue;
         }
         if (vec) {
@@ -413,6 +415,13 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Workspace ws = workspace_of(A.ws);
     if (!smem_aligned(A, ws, raw)) return;
+    if constexpr (SEE == kPrefix) {              // a call that computes no prefix apart ends here
+        pdl_wait_and_trigger();
+        if (A.from[A.requests] == 0) {
+            if (threadIdx.x == 0) ws.meta[blockIdx.x].rows = 0;
+            return;
+        }
+    }
 
     if (tid == 0) {
         for (int s = 0; s < kSlots; ++s) {
@@ -434,7 +443,6 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
         tc_fence_before();
     }
     pdl_wait_and_trigger();
-    if constexpr (SEE == kPrefix) write_from(A);
     const int run = cut_line<kRows, SEE, kThreads>(A, sm.cut);
     tc_fence_before();
     __syncthreads();

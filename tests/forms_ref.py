@@ -3,44 +3,56 @@ tests of dspark_attend_sinks and dspark_attend_shared hold results to."""
 import numpy as np
 import torch
 
-import cache_ref as ref
-
 
 def attend(case, q, scale, seen):
     """q [rows, q_heads, dim] float64; seen(b, pos) -> token numbers. Returns out, lse and, for the
     tolerances, sum p |v| / l, the largest scale * sum |q k|, and what the softmax weights' pieces may
-    be off by (2^-8 of a weight or 2^-16 of the largest, no more than the weight itself)."""
+    be off by (2^-8 of a weight or 2^-16 of the largest, no more than the weight itself). Request by
+    request, on the GPU's 64-bit units."""
+    dev = torch.device("cuda:0")
+    put = lambda a: torch.as_tensor(np.ascontiguousarray(a)).to(dev)       # noqa: E731
     rows, hq, D = q.shape
     n, heads, page = case.n, case.heads, case.page
     group = hq // heads
-    out, lse = np.zeros((rows, hq, D)), np.full((rows, hq), -np.inf)
-    spread, big, pieces = np.zeros((rows, hq, D)), np.zeros((rows, hq)), np.zeros((rows, hq, D))
+    K, V = (put(case.codes[x]).view(torch.float8_e4m3fn).double() * put(case.scale[x]).double()[:, :, None, None]
+            for x in "kv")
+    scale_v, table, q = put(case.scale["v"]).double(), put(case.table).long(), put(q).double()
+    f64 = dict(dtype=torch.float64, device=dev)
+    out, lse = torch.zeros(rows, hq, D, **f64), torch.full((rows, hq), -np.inf, **f64)
+    spread, big, pieces = torch.zeros_like(out), torch.zeros(rows, hq, **f64), torch.zeros_like(out)
     for b in range(len(case.lengths)):
-        for r in range(case.cu[b], case.cu[b + 1]):
-            t = np.asarray(seen(b, int(case.lengths[b]) + r - case.cu[b]), np.int64)
-            j = t // page
-            width = case.table.shape[1]
-            ids = np.where(j < width, case.table[b, np.minimum(j, width - 1)], -1)
-            ok = (ids >= 0) & (ids < n)
-            t, ids = t[ok], ids[ok]
-            if len(t) == 0:
-                continue
-            for h in range(heads):
-                vs = case.scale["v"][ids, h].astype(np.float64)
-                kk = ref.decode(case.codes["k"][ids, h, t % page]) * case.scale["k"][ids, h].astype(np.float64)[:, None]
-                vv = ref.decode(case.codes["v"][ids, h, t % page]) * vs[:, None]
-                g = slice(h * group, (h + 1) * group)
-                s = scale * (q[r, g] @ kk.T)
-                m = s.max(1, keepdims=True)
-                p = np.exp(s - m)
-                l = p.sum(1, keepdims=True)
-                out[r, g], spread[r, g] = p @ vv / l, p @ np.abs(vv) / l
-                w = p * vs[None, :]
-                off = np.minimum(w, np.maximum(2.0 ** -8 * w, 2.0 ** -16 * w.max(1, keepdims=True)))
-                pieces[r, g] = (off / vs[None, :]) @ np.abs(vv) / l
-                lse[r, g] = (m + np.log(l))[:, 0]
-                big[r, g] = abs(scale) * (np.abs(q[r, g]) @ np.abs(kk).T).max(1)
-    return out, lse, spread, big, pieces
+        r0, r1 = int(case.cu[b]), int(case.cu[b + 1])
+        if r1 <= r0:
+            continue
+        tokens = [np.asarray(seen(b, int(case.lengths[b]) + i), np.int64) for i in range(r1 - r0)]
+        t = np.unique(np.concatenate(tokens))
+        hide = put(np.stack([~np.isin(t, x) for x in tokens]))
+        t = put(t)
+        j = t // page
+        ids = torch.where(j < table.shape[1], table[b, j.clamp(max=table.shape[1] - 1)], -1)
+        there = (ids >= 0) & (ids < n)
+        ids = ids.clamp(0, n - 1)
+        hide = (hide | ~there)[None, None]                                 # [1, 1, w, T]
+        k, v = (x[ids, :, t % page].transpose(0, 1) for x in (K, V))       # [heads, T, D]
+        k, v = k.masked_fill(~there[None, :, None], 0.0), v.masked_fill(~there[None, :, None], 0.0)
+        vs = scale_v[ids].T[:, None, None]                                 # [heads, 1, 1, T]
+        x = q[r0:r1].view(r1 - r0, heads, group, D).permute(1, 2, 0, 3)    # [heads, group, w, D]
+        s = (scale * (x @ k[:, None].mT)).masked_fill(hide, -np.inf)
+        m = s.amax(-1, keepdim=True)
+        p = torch.exp(s - torch.where(torch.isinf(m), 0.0, m))
+        l = p.sum(-1, keepdim=True)
+        some = l > 0
+        w = p * vs
+        off = torch.minimum(w, torch.maximum(2.0 ** -8 * w, 2.0 ** -16 * w.amax(-1, keepdim=True))) / vs
+        over = torch.where(some, l, 1.0)
+        back = lambda y: y.permute(2, 0, 1, 3).reshape(r1 - r0, hq, -1)     # noqa: E731
+        out[r0:r1] = back(p @ v[:, None] / over)
+        spread[r0:r1] = back(p @ v[:, None].abs() / over)
+        pieces[r0:r1] = back(off @ v[:, None].abs() / over)
+        lse[r0:r1] = back(torch.where(some, m + torch.log(over), -np.inf))[..., 0]
+        sums = (x.abs() @ k[:, None].abs().mT * abs(scale)).masked_fill(hide, 0.0)
+        big[r0:r1] = back(sums.amax(-1, keepdim=True))[..., 0]
+    return tuple(y.cpu().numpy() for y in (out, lse, spread, big, pieces))
 
 
 def check(case, dtype, q, out, lse, seen, *, joined=False, scale=None):

@@ -1,7 +1,11 @@
 """dspark_attend_shared against 64 bits over every request's whole context: one group and several, few
 rows and many on either side of the prefix, prefixes of one page to many tiles and ends inside a tile;
 groups that make no sense attend alone; pages out of range, queries that are no numbers, strides,
-graphs, two calls in a row; the refusals."""
+graphs, two calls in a row; the refusals.
+
+Prefixes are computed apart only where that saves 6000 tiles of 128 tokens and a head: `heavy` adds a
+group of 64 single tokens behind a prefix that is long enough for it, so that the others' odd sizes
+are met in that form too."""
 import ctypes
 
 import numpy as np
@@ -32,7 +36,7 @@ def test_refuses_on_the_host(lib):
         return rc, bd.last_error()
 
     need = bd.dspark_attend_shared_workspace_bytes(3, 4, 2, 64, 2)
-    assert need == bd.dspark_attend_workspace_bytes(2, 64) + 3 * 4 * 65 * 4 + 8
+    assert need == bd.dspark_attend_workspace_bytes(2, 64) + 3 * 4 * 65 * 4 + 12
     for code, kw, word in [(-1, dict(groups=-1), "groups"), (-1, dict(gcu=None), "group_cu"),
                            (-1, dict(prefix=None), "prefix"), (-1, dict(gcu=4097), "group_cu"),
                            (-1, dict(wb=need - 1), "workspace"), (-1, dict(ws=4104), "workspace"),
@@ -49,17 +53,27 @@ class Shared(Case):
     """groups: (requests, prefix) of consecutive groups from request 0 on; own: tokens of each request
     after its prefix."""
 
-    def __init__(self, seed, w, own, groups, heads, group, dim, page, **kw):
-        front = np.zeros(len(w), np.int64)
+    def __init__(self, seed, w, own, groups, heads, group, dim, page, heavy=True, **kw):
+        w, own, groups = list(w), list(own), list(groups)
+        self.light = len(w)
+        if heavy:
+            tiles = -(-6000 // (63 * heads))
+            w, own, groups = w + [1] * 64, own + [i % 5 for i in range(64)], groups + [(64, 128 * tiles)]
+        # pages for the prefix of a group's first request and for every request's own tokens
+        front, leads = np.zeros(len(w), np.int64), np.arange(len(w))
         b = 0
         for n, p in groups:
-            front[b:b + n] = p
+            front[b:b + n], leads[b:b + n] = p, b
             b += n
-        super().__init__(seed, w, front + np.asarray(own), heads, group, dim, page, **kw)
-        b = 0
-        for n, p in groups:
-            self.table[b:b + n, :p // page] = self.table[b, :p // page]
-            b += n
+        mine = np.where(leads == np.arange(len(w)), front, 0)
+        super().__init__(seed, w, mine + np.asarray(own), heads, group, dim, page, **kw)
+        first = self.table
+        self.table = np.full((len(w), first.shape[1] + int(front.max()) // page), -7, np.int32)
+        for b in range(len(w)):
+            at, skip = front[b] // page, mine[b] // page
+            self.table[b, :at] = first[leads[b], :at]
+            self.table[b, at:at + first.shape[1] - skip] = first[b, skip:]
+        self.lengths = (front + np.asarray(own)).astype(np.int32)
         self.group_cu = np.cumsum([0] + [n for n, _ in groups]).astype(np.int32)
         self.prefix = np.asarray([p for _, p in groups], np.int32)
 
@@ -121,16 +135,35 @@ def test_shared(lib, shape):
 
 
 @gpu
+@pytest.mark.parametrize("shape", [SHAPES[2], SHAPES[4], SHAPES[7]])
+@pytest.mark.parametrize("reach", [0, 100000])
+def test_not_worth_it(lib, shape, reach):
+    """Small calls attend alone, said by the host (a narrow page table) or on the device."""
+    c = Shared(11, *shape, heavy=False)
+    if reach:
+        c.table = np.concatenate([c.table, np.full((len(c.lengths), reach // c.page), -7, np.int32)], 1)
+    out, lse = c.hold()
+    dev = torch.device("cuda:0")
+    t = lambda a: torch.as_tensor(np.ascontiguousarray(a)).to(dev)         # noqa: E731
+    cache = bd.PagedCache(t(c.codes["k"]), t(c.codes["v"]), t(c.scale["k"]), t(c.scale["v"]), t(c.table))
+    q = torch.as_tensor(c.q).to(torch.bfloat16).to(dev)
+    want = torch.full_like(q, 5.0)
+    ws = torch.zeros(bd.dspark_attend_workspace_bytes(c.heads, c.dim), dtype=torch.uint8, device=dev)
+    bd.dspark_attend(cache, q, want, t(c.cu), t(c.lengths), ws)
+    np.testing.assert_array_equal(out, want.double().cpu().numpy())
+
+
+@gpu
 @pytest.mark.parametrize("shape", [SHAPES[2], SHAPES[4]])
 def test_fp32_attends_alone(lib, shape):
-    Shared(1, *shape).hold(torch.float32)
+    Shared(1, *shape, heavy=False).hold(torch.float32)
 
 
 @gpu
 @pytest.mark.parametrize("dim", [16, 96, 256])
 def test_other_head_sizes(lib, dim):
     for dtype in BOTH:
-        Shared(dim, [3, 1], [40, 7], [(2, 64)], 2, 3, dim, 16).hold(dtype)
+        Shared(dim, [3, 1], [40, 7], [(2, 64)], 2, 3, dim, 16, heavy=False).hold(dtype)
 
 
 def base(seed=2):
@@ -151,52 +184,68 @@ def test_a_prefix_counts_in_whole_pages(lib):
                                   "empty"])
 def test_groups_that_attend_alone(lib, what):
     """Whatever the groups say, a row sees its request's tokens."""
-    c = base(3)
-    status = 0
+    c = base(3)                              # groups of 3, 2 and 64 requests; 12 rows, then 64
+    every = lambda b, pos: np.arange(pos + 1)                              # noqa: E731
     if what == "one":                        # groups of one request
-        c.group_cu, c.prefix = np.arange(6, dtype=np.int32), np.full(5, 160, np.int32)
+        c.group_cu = np.concatenate([np.arange(6), [69]]).astype(np.int32)
+        c.prefix = np.concatenate([[160] * 3, [320] * 2, c.prefix[2:]]).astype(np.int32)
     elif what == "none":
-        c.prefix[:] = 0
+        c.prefix[:2] = 0
     elif what == "short":                    # a request with fewer tokens than the prefix
-        c.lengths[1] = 100
+        c.lengths[1], c.lengths[20] = 100, 0
     elif what == "negative":
-        c.prefix[:] = [-16, -(1 << 31)]
+        c.prefix[:2] = [-16, -(1 << 31)]
     elif what == "long":                     # past the page table
-        c.prefix[:] = [1 << 30, 2 ** 31 - 1]
+        c.prefix[:2] = [1 << 30, 2 ** 31 - 1]
     elif what == "gap":                      # requests before, between and behind the groups
-        c.group_cu, c.prefix = np.asarray([1, 3, 3], np.int32), np.asarray([160, 64], np.int32)
+        c.group_cu[:3] = [1, 3, 3]
+        c.group_cu[2:] = [5, 60]
+        c.prefix[:2] = [160, 0]
     elif what == "outside":                  # requests that are none
-        c.group_cu = np.asarray([0, 3, 9], np.int32)
-    elif what == "backwards":
-        c.group_cu = np.asarray([3, 0, 5], np.int32)
-        c.prefix[:] = [160, 64]
-        c.table[3:, :4] = c.table[0, :4]     # requests 0 to 4 now share 64 tokens
-    elif what == "rows":                     # packed rows of a group that end behind the buffer
-        c.cu[5] = c.rows + 3
-        status = bd.STATUS_BAD_ROWS
+        c.group_cu[3] = 70
+        c.prefix[1] = 320
+    elif what == "backwards":                # the first and second group are empty or nonsense
+        c.group_cu[:3] = [3, 0, 5]
+        c.prefix[:2] = [160, 64]
+        c.table[3:5, :4] = c.table[0, :4]    # requests 0 to 4 now share 64 tokens
+    elif what == "rows":                     # packed rows that end behind the buffer
+        c.cu[69] = c.rows + 3
         q, out, lse, st = c.go(torch.bfloat16)
-        assert st == status
-        c.cu[5] = 10                         # request 4 got nothing written
-        forms_ref.check(c, torch.bfloat16, q, out, lse, lambda b, pos: np.arange(pos + 1), joined=True)
+        assert st == bd.STATUS_BAD_ROWS
+        c.cu[69] = c.cu[68]                  # the last request got nothing written
+        forms_ref.check(c, torch.bfloat16, q, out, lse, every, joined=True)
         return
-    elif what == "empty":                    # no rows in the first group, no groups at all
+    elif what == "empty":                    # no rows in the first group; then no groups at all
         c = Shared(4, [0, 0, 2, 3], [30, 5, 200, 64], [(2, 160), (2, 320)], 2, 4, 64, 16)
         c.hold()
         c.group_cu, c.prefix = np.zeros(1, np.int32), np.zeros(0, np.int32)
-    c.hold(status=status)
+    c.hold()
+
+
+@gpu
+def test_rows_of_no_request_inside_a_group(lib):
+    """A request of a shared group whose rows run backwards is not written; the others are, whole."""
+    c = base(12)
+    c.cu[1:3] = [6, 5]                       # request 0: rows 0 .. 5, more than its pages hold; request 1: none
+    q, out, lse, st = c.go(torch.bfloat16)
+    assert st == bd.STATUS_BAD_ROWS | bd.STATUS_BAD_PAGE
+    c.cu[1:3] = [5, 5]                       # row 5 is request 0's and request 2's
+    want = forms_ref.attend(c, q, c.dim ** -0.5, lambda b, pos: np.arange(pos + 1))[0]
+    np.testing.assert_allclose(out[:5], want[:5], atol=0.02, rtol=0.02)
+    np.testing.assert_allclose(out[6:76], want[6:76], atol=0.02, rtol=0.02)
 
 
 @gpu
 def test_bad_pages(lib):
     c = base(5)
     c.table[:3, 4] = c.n                     # in the first prefix
-    c.table[3:, 0] = -1
+    c.table[3:5, 0] = -1
     c.table[2, 17] = 10 ** 6                 # one of request 2's own
     c.hold(status=bd.STATUS_BAD_PAGE)
     c = Shared(6, [2, 1, 70], [0, 0, 20], [(3, 64)], 1, 4, 64, 64)
-    c.table[:, 0] = -1                       # nothing of the prefix: the own tokens alone
+    c.table[:3, 0] = -1                      # nothing of the prefix: the own tokens alone
     out, lse = c.hold(status=bd.STATUS_BAD_PAGE)
-    c.table[:] = -1                          # nothing at all
+    c.table[:3] = -1                         # nothing at all
     _, lse = c.hold(status=bd.STATUS_BAD_PAGE)
     assert np.isneginf(lse[:73]).all()
 
