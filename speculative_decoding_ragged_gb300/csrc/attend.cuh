@@ -32,7 +32,8 @@ struct AttendCall {
     int last_tile;             // the last 128-token tile of them
     void* ws;
     int32_t* status;
-    int sinks;                 // kSinks
+    int sinks;                 // kSinks, and their blocks
+    int sink_blocks;
     // kPrefix, kSuffix. In a kPrefix call B is the number of groups.
     int requests;
     const int32_t* group_cu;   // a group's requests: group_cu[g] .. group_cu[g + 1] - 1

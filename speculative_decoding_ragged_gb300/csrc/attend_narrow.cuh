@@ -622,12 +622,8 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                 const int64_t bh = static_cast<int64_t>(id) * A.c.heads + h;
                 return make_float2(A.c.k_scale[bh], A.c.v_scale[bh]);
             };
-            // block number n of a piece: tiles may be left out
-            auto real_block = [&](const Piece& p, int n) -> int {
-                return SEE == kSinks && n >= sink_tiles(A) * per_tile ? n + p.from * per_tile : n;
-            };
             auto id_of = [&](const Piece& p, int n) -> int {        // -1: dead, not there, or not a page
-                const int j = real_block(p, n);
+                const int j = real_block<SEE>(A, n, p.from);
                 if (n >= (p.k0 + p.n) * per_tile ||
                     j >= (stored_tokens<SEE>(p.len, p.w) + A.c.page - 1) / A.c.page ||
                     ((j + 1) * A.c.page <= p.first_seen && !(SEE == kSinks && j * A.c.page < A.sinks))) return -1;
@@ -672,7 +668,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     }
                     const int src = j0 + (lane & (per_tile - 1));
                     const int my_id = __shfl_sync(0xffffffffu, id, src);
-                    const bool there = lane < per_tile && real_block(pc, base + src) < total_blocks;
+                    const bool there = lane < per_tile && real_block<SEE>(A, base + src, pc.from) < total_blocks;
                     const int count = __popc(__ballot_sync(0xffffffffu, there));
                     const int row = my_id < 0 ? beyond : (my_id * A.c.heads + h) * A.c.page;
 #pragma unroll 1
@@ -861,7 +857,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                 t.t = pc.k0 * kTile + token;
 #pragma unroll 1
                 for (int k = 0; k < n; ++k, ++it, t.t += kTile) {
-                    if constexpr (SEE == kSinks) t.t = real_tile<SEE>(A, pc.k0 + k, pc.from) * kTile + token;
+                    if constexpr (SEE == kSinks) t.t = real_token<SEE>(A, (pc.k0 + k) * kTile + token, pc.from);
                     const int token0 = t.t - token;
                     ok = ok && mbar_wait(smem_addr(&sm.full[slot]), phase, stalled) &&
                          mbar_wait(smem_addr(&sm.s_full[it & 1]), (it >> 1) & 1, stalled);
@@ -869,8 +865,8 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                     tc_fence_after();
                     t.n = sm.nums[num][my_block];
                     if (++num == kNums) num = 0;
-                    const bool mask = token0 + kTile - 1 > first_pos ||
-                                      (token0 < last_lo && !(SEE == kSinks && token0 + kTile <= A.sinks));
+                    const bool mask = SEE == kSinks ? masked_tile<SEE>(A, pc.k0 + k, pc.from, last_lo, first_pos)
+                                                    : token0 + kTile - 1 > first_pos || token0 < last_lo;
                     ok = soften<D, R, SEE>(sm, grp, piece & 3, l, sm.tmem + lanes + 64 * (it & 1), o_addr, t, mask, k, it,
                                            A.sinks, stalled) && ok;
                     tc_fence_before();

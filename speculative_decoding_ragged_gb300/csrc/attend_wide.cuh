@@ -61,7 +61,7 @@ struct Smem {
     struct {
         int k0, n;         // its tiles
         int lo, hi;        // tokens from lo to hi are seen by all its rows; hi is the first row's position
-        int skip;          // kSinks: the tiles left out
+        int skip;          // kSinks: the blocks left out
     } span;
     int stored;            // the request's tokens
     uint32_t tmem;
@@ -123,13 +123,14 @@ __device__ __forceinline__ bool soften(Smem<D, SEE>& sm, Row& r, uint32_t lanes,
             x[g + j + 1] = y.y;
         }
     }
-    const int token0 = real_tile<SEE>(A, sm.span.k0 + k, sm.span.skip) * kTile;
-    if (token0 + kTile - 1 > sm.span.hi ||
-        (token0 < sm.span.lo && !(SEE == kSinks && token0 + kTile <= A.sinks))) {
+    if (masked_tile<SEE>(A, sm.span.k0 + k, sm.span.skip, sm.span.lo, sm.span.hi)) {
+        const int number0 = (sm.span.k0 + k) * kTile;
+        // the window's tokens; of a tile with sinks the numbers before them lie before every window so
+        const int token0 = SEE == kSinks ? number0 + sm.span.skip * A.c.page : number0;
         const int pos = sm.span.hi + sm.after[row];
         const int first = first_seen_at<SEE>(A, pos, sm.span.lo);
         const uint32_t at = static_cast<uint32_t>(token0 - first), span = static_cast<uint32_t>(pos - first);
-        const int sinks = SEE == kSinks ? min(A.sinks, pos + 1) - token0 : 0;
+        const int sinks = SEE == kSinks ? min(A.sinks, pos + 1) - number0 : 0;
 #pragma unroll
         for (int j = 0; j < kTile; ++j)
             if (at + j > span && !(SEE == kSinks && j < sinks)) x[j] = -INFINITY;
@@ -472,12 +473,8 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                 // 32 blocks at a time, one per lane; the next 32 are fetched while these load
                 const int first_block = wk.k0 * per_tile;
                 int base = first_block;
-                // block number n of the piece: tiles may be left out
-                auto real_block = [&](int n) -> int {
-                    return SEE == kSinks && n >= sink_tiles(A) * per_tile ? n + wk.from * per_tile : n;
-                };
                 auto id_of = [&](int n) -> int {        // -1: dead, not there, or not a page
-                    const int j = real_block(n);
+                    const int j = real_block<SEE>(A, n, wk.from);
                     if (j >= total_blocks ||
                         ((j + 1) * A.c.page <= lo && !(SEE == kSinks && j * A.c.page < A.sinks))) return -1;
                     const int id = j < A.c.width ? table[j] : -1;
@@ -502,7 +499,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                     const int my_id = __shfl_sync(0xffffffffu, id, src);
                     const float ks = __shfl_sync(0xffffffffu, sc.x, src);
                     const float vs = __shfl_sync(0xffffffffu, sc.y, src);
-                    const int block = real_block(base + src);
+                    const int block = real_block<SEE>(A, base + src, wk.from);
                     const bool there = lane < per_tile && block < total_blocks;
                     const int count = __popc(__ballot_sync(0xffffffffu, there));
                     const int row = my_id < 0 ? beyond : (my_id * A.c.heads + wk.h) * A.c.page;
@@ -662,7 +659,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
                     ok = __all_sync(0xffffffffu, ok);
                     if (ok)
                         widen<D, SEE>(sm, sm.ring[s], row,
-                                      real_tile<SEE>(A, sm.span.k0 + k, sm.span.skip) * kTile + row < sm.stored);
+                                      real_token<SEE>(A, (sm.span.k0 + k) * kTile + row, sm.span.skip) < sm.stored);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     tc_fence_before();
                     __syncwarp();

@@ -190,6 +190,7 @@ int dspark_attend_sinks(const dspark_cache* cache, const void* q, int64_t q_stri
         return fail(DSPARK_ERR_INVALID_ARG, "%s: sinks = %d outside [0, %d]", fn, sinks, INT32_MAX - 256);
     if (!go) return DSPARK_OK;
     A.sinks = sinks;
+    A.sink_blocks = (sinks + cache->page - 1) / cache->page;
     // without a window every row sees its first tokens anyway
     return dspark::launch_attend(A, window > 0 && sinks > 0 ? dspark::kSinks : dspark::kAll, static_cast<int>(dtype),
                                  stream);
