@@ -74,6 +74,13 @@ class DSparkStep:
                          row_prob=row_prob, temperature=temperature, seed=seed, step=step,
                          status=self.status)
 
+    def adjust(self, target: torch.Tensor, block_tokens: torch.Tensor, how: bd.Adjustments,
+               out: Optional[torch.Tensor] = None, prepare=False):
+        """Penalties, biases and masks on the rows that verify reads, in place unless `out` is given."""
+        return bd.dspark_adjust(target, target if out is None else out, block_tokens, how,
+                                cu_seqlens=self.cu if self.mode == "compact" else None,
+                                status=self.status, prepare=prepare)
+
     def scatter(self):
         bd.dspark_scatter(self.committed, self.accept_len, self.out_tokens, self.out_len,
                           self.status)
