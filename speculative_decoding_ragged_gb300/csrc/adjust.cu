@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;                      // 16-byte units a thread has in flight
+constexpr int kEach = 2;                       // listed tokens a lane adjusts at a time
 constexpr int kMaxSlice = 7168, kMinSlice = 1024;
 static_assert(kMinSlice % (32 * kUnits * 8) == 0 && kMaxSlice % kMinSlice == 0, "slices of whole parts");
 // A token's word: uses in the answer, whether the prompt has it, whether it is a draft, 1 + the index of
@@ -309,23 +310,41 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
             *reinterpret_cast<uint4*>(y + t) = e[k];
         }
         if (!counts) continue;
-        // the part's listed tokens, over what the warp wrote
+        // the part's listed tokens, over what the warp wrote: kEach a lane at a time, their loads at once
         const int m = listed[now_part];
         __syncwarp();
 #pragma unroll 1
-        for (int k = lane; k < m; k += 32) {
-            const int t = list[p0 + k];
-            const uint32_t its = word[t] & ~kDraft, entry = its >> kBiasShift;
-            uint32_t uses = its & kUses;
-            for (int j = 1; j <= now_i; ++j) uses += draft[j] == t;
-            // a later row's draft; a token that is not allowed
-            if ((its | uses) == 0 || (row_mask != nullptr && !(mask_bits<1>(row_mask, v0 + t) & 1))) continue;
-            float z = E::up(x[t]);
-            const float add = entry ? bias[entry - 1] : 0.0f;
-            if ((its & kPrompt) | uses) z = z > 0.0f ? z / rep : z * rep;
-            if (uses) z -= fmaf(frequency, static_cast<float>(uses), presence);
-            if (entry) z += add;
-            y[t] = E::down(z);
+        for (int k0 = lane; k0 < m; k0 += 32 * kEach) {
+            int t[kEach];
+            uint32_t its[kEach], uses[kEach];
+            bool apply[kEach];
+            T old[kEach];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int k = k0 + 32 * e;
+                t[e] = list[p0 + min(k, m - 1)];
+                its[e] = word[t[e]] & ~kDraft;
+                uses[e] = its[e] & kUses;
+                // not: a token that is not allowed
+                apply[e] = k < m && (row_mask == nullptr || (mask_bits<1>(row_mask, v0 + t[e]) & 1));
+                old[e] = x[t[e]];
+            }
+            for (int j = 1; j <= now_i; ++j) {
+                const int d = draft[j];
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) uses[e] += d == t[e];
+            }
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                if (!apply[e] || (its[e] | uses[e]) == 0) continue;        // nor: a later row's draft
+                const uint32_t entry = its[e] >> kBiasShift;
+                float z = E::up(old[e]);
+                const float add = entry ? bias[entry - 1] : 0.0f;
+                if ((its[e] & kPrompt) | uses[e]) z = z > 0.0f ? z / rep : z * rep;
+                if (uses[e]) z -= fmaf(frequency, static_cast<float>(uses[e]), presence);
+                if (entry) z += add;
+                y[t[e]] = E::down(z);
+            }
         }
     }
     // Masks that allow nothing: row i's is looked at by slice i % slices.
