@@ -41,6 +41,7 @@ def test_refuses_on_the_host(lib):
             (-1, dict(how=None), "how"), (-1, dict(dt=7), "dtype"), (-1, dict(rows=-1), "rows=-1"),
             (-1, dict(V=0), "V=0"), (-1, dict(B=-1), "B=-1"), (-1, dict(gamma=0), "gamma=0"),
             (-1, dict(gamma=33), "gamma=33"), (-2, dict(B=8193), "B = 8193"),
+            (-2, dict(V=2 ** 29, xs=1 << 30, ys=1 << 30), "V = "),
             (-1, dict(xs=99), "row strides"), (-1, dict(ys=99), "row strides"),
             (-1, dict(y=4096, ys=101), "in place"), (-1, dict(cu=None, rows=5), "cu_seqlens"),
             (-1, dict(history_cap=-1), "history_cap"), (-2, dict(history_cap=524001), "history_cap"),
@@ -191,7 +192,7 @@ class Case:
         assert (out[same] == want[same]).all()             # untouched logits keep their bits
 
 
-# slices of 1024 tokens (few requests) to 4096 (304 requests and more); odd vocabularies put the rows
+# slices of 1024 tokens (few requests) to 7168 (304 requests and more); odd vocabularies put the rows
 # at every alignment
 @gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -218,6 +219,63 @@ def test_places_and_strides(lib, dtype, offset, extra, in_place):
         assert (got["wide"][:, :offset] == 7).all()
     if extra:
         assert (got["wide"][:, offset + c.V:] == 7).all()
+
+
+# Batches large enough for the largest slices (7168 tokens); row strides are padded so that odd
+# vocabularies' rows lie on 16-byte boundaries too.
+LARGE = [([1] * 310, 1), ([2, 0, 1] * 110, 7), ([3, 1] * 160, 33), ([2] * 310, 515), ([1, 4] * 80, 7169),
+         ([5, 2, 8] * 21, 40003), ([2] * 40, 60000)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("w,V", LARGE)
+def test_large_calls(lib, dtype, w, V):
+    c = Case(V, w, V)
+    got = c.run(dtype, extra=-V % 8)
+    c.check(got, dtype)
+    assert got["status"] == 0
+    again = c.run(dtype, extra=-V % 8, in_place=True)       # the same bits in place
+    M = int(c.cu[-1])
+    bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+    assert torch.equal(got["out"][:M].contiguous().view(bits), again["out"][:M].contiguous().view(bits))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("left_out", [("repetition", "presence", "frequency"), ("bias_tokens", "bias_values", "bias_len"),
+                                      ("mask", "mask_row"), ("mask_row",),
+                                      ("repetition", "presence", "frequency", "bias_tokens", "bias_values", "bias_len")])
+def test_large_calls_without_parts(lib, dtype, left_out):
+    c = Case(14, [2, 1] * 155, 3001, masks=470 if "mask_row" in left_out else 7).without(*left_out)
+    c.x[c.rng.random(c.x.shape) < 0.05] = np.nan
+    c.x[c.rng.random(c.x.shape) < 0.05] = -np.inf
+    if "bias_values" in c.h:
+        c.h["bias_values"][np.isinf(c.h["bias_values"])] = 1.0
+    got = c.run(dtype, extra=-3001 % 8)
+    c.check(got, dtype)
+    assert got["status"] == 0
+
+
+@gpu
+def test_large_calls_with_forbidden_rows(lib):
+    """Masks that forbid whole parts and whole rows, mask rows out of range, requests that are none."""
+    c = Case(15, [2, 3] * 60, 20480, masks=6).without("bias_tokens", "bias_values", "bias_len")
+    c.h["mask"][0] = 0
+    c.h["mask"][1] = 0
+    c.h["mask"][1, 639] = -1 << 31               # the last token alone
+    c.h["mask"][2] = -1
+    c.h["mask"][2, 32:64] = 0                    # one part of 1024 tokens
+    c.h["mask"][3] = 0
+    c.h["mask"][3, 31:33] = 1
+    got = c.run(torch.bfloat16)
+    c.check(got, torch.bfloat16)
+    assert got["status"] == (bd.STATUS_NO_TOKEN if (c.h["mask_row"][:300] == 0).any() else 0)
+    c.h["mask_row"][7] = 6
+    c.cu[-1] += 100
+    got = c.run(torch.bfloat16)
+    assert got["status"] & bd.STATUS_BAD_ROWS
+    assert torch.equal(got["out"][c.cu[-2]:], got["before"][c.cu[-2]:])
 
 
 PENALTIES = ("repetition", "presence", "frequency")
