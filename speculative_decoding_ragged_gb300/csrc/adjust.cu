@@ -9,7 +9,21 @@
 // No sort, no hash, no order that matters: counts are integers, and of several biases for one token the
 // last one counts.
 //
+// Bound by HBM: a row is read and written once. 256 windows of 1 to 8 rows over 151936 tokens in bf16: a copy
+// takes 105 us, with drafts 106, with 150 biases a request too 111, with histories of 64 to 4096 tokens 124
+// (5.6 TB/s). What the histories add is the adjusting of the listed tokens (a warp's instructions, whose
+// logits come from L1 or L2) and the counting's round trips; the first of each array is therefore fetched
+// before its length is known, and the counting runs under the warps' first loads. 320 rows under grammars:
+// 28.8 us, 7 TB/s of the bytes counted with every logit read; parts that are forbidden whole are not. One
+// window of 8 rows: 5.0 us, launch and three dependent loads.
+// Tried and slower for the 256 windows: four warps that count for eight that stream in a persistent grid
+// (187 to 295 us: what waits for the counts then reads back what was written), the rows through shared
+// memory by bulk copies (151), granules of 512 bytes dealt out to the slices, so that common tokens do not
+// lie in one (150), all rows of a part adjusted together (162), a lane for each word of a bit array in place
+// of lists (157, and 23 us for one window: common tokens lie together).
+//
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -18,6 +32,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;                      // 16-byte units a thread has in flight
+constexpr int64_t kFewCtas = 4;                // per SM, where requests are few
 constexpr int kEach = 2;                       // listed tokens a lane adjusts at a time
 constexpr int kMaxSlice = 7168, kMinSlice = 1024;
 static_assert(kMinSlice % (32 * kUnits * 8) == 0 && kMaxSlice % kMinSlice == 0, "slices of whole parts");
@@ -123,9 +138,11 @@ struct Element<DSPARK_F32> {
         return allow >> k & 1 ? x : kLowest;
     }
 };
-template <int DT>
-__global__ void __launch_bounds__(kThreads, 4)
-adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place)
+// COUNTING: the call has penalties or biases, MASKED: it has masks. A call without one of them is spared
+// its code and registers: 256 windows without masks 143 -> 124 us, grammars alone 35 -> 29 us.
+template <int DT, bool COUNTING, bool MASKED, bool IN_PLACE>
+__global__ void __launch_bounds__(kThreads, COUNTING ? 4 : 5)
+adjust_kernel(const __grid_constant__ AdjustCall A)
 {
     typedef Element<DT> E;
     typedef typename E::type T;
@@ -140,7 +157,7 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
     const int v0 = slice * A.slice, nv = min(A.slice, A.V - v0);
     uint32_t* word = sm;                       // these only where something counts
     uint16_t* list = reinterpret_cast<uint16_t*>(word + A.slice);
-    if (counting) {
+    if constexpr (COUNTING) {
         for (int i = tid; i < A.slice / 4; i += kThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
         if (tid < kMaxSlice / kPart) listed[tid] = 0;
         __syncthreads();
@@ -162,7 +179,9 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
     const int32_t* history = nullptr;
     const float* bias = h.bias_values + static_cast<int64_t>(b) * h.bias_cap;
     Four first;
-    if (counting) {
+    int first_id = -1;
+    float first_bias = 0.0f;
+    if constexpr (COUNTING) {
         rep = penalty_of(h.repetition, b, 1.0f, true, &bits);
         presence = penalty_of(h.presence, b, 0.0f, false, &bits);
         frequency = penalty_of(h.frequency, b, 0.0f, false, &bits);
@@ -174,10 +193,16 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
             n = clamped(h.history_len[b], h.history_cap, &bits);
             if (h.prompt_len != nullptr) n_prompt = clamped(h.prompt_len[b], n, &bits);
         }
-        if (h.bias_tokens != nullptr) n_bias = clamped(h.bias_len[b], h.bias_cap, &bits);
+        if (h.bias_tokens != nullptr) {
+            if (tid < h.bias_cap) {
+                first_id = h.bias_tokens[static_cast<int64_t>(b) * h.bias_cap + tid];
+                first_bias = bias[tid];
+            }
+            n_bias = clamped(h.bias_len[b], h.bias_cap, &bits);
+        }
     }
     const bool penalties = rep != 1.0f || presence != 0.0f || frequency != 0.0f;
-    const bool counts = w > 0 && (penalties || n_bias > 0);
+    const bool counts = COUNTING && w > 0 && (penalties || n_bias > 0);
 
     auto count = [&]() {
         // the place of token v in the slice, or -1
@@ -192,9 +217,9 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
         };
         const int32_t* ids = h.bias_tokens + static_cast<int64_t>(b) * h.bias_cap;
         for (int j = tid; j < n_bias; j += kThreads) {
-            const int t = place(ids[j]);
+            const int t = place(j == tid ? first_id : ids[j]);
             if (t < 0) continue;
-            if (!(bias[j] < INFINITY)) { bits |= DSPARK_STATUS_BAD_VALUE; continue; }      // -inf bans a token
+            if (!((j == tid ? first_bias : bias[j]) < INFINITY)) { bits |= DSPARK_STATUS_BAD_VALUE; continue; }      // -inf bans a token
             meet(t, atomicMax(&word[t], static_cast<uint32_t>(j + 1) << kBiasShift));
         }
         if (n_bias > 0) __syncthreads();       // the maximum is over biases alone
@@ -206,7 +231,8 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
         Four now = first;
 #pragma unroll 1
         for (int j = 4 * tid - shift; penalties && j < n; j += 4 * kThreads) {
-            const Four next = four_of(history, j + 4 * kThreads, h.history_cap);
+            Four next = now;
+            if (j + 4 * kThreads < n) next = four_of(history, j + 4 * kThreads, h.history_cap);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (static_cast<uint32_t>(j + e) >= static_cast<uint32_t>(n)) continue;
@@ -219,7 +245,7 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
     };
     // The mask row of packed row r, or none.
     auto mask_of = [&](int r) -> const uint32_t* {
-        if (h.mask == nullptr) return nullptr;
+        if (!MASKED) return nullptr;
         const int m = h.mask_row != nullptr ? h.mask_row[r] : r;
         if (m >= 0 && m < h.mask_rows) return h.mask + m * h.mask_stride;
         if (m != -1) bits |= DSPARK_STATUS_BAD_ROWS;
@@ -227,14 +253,14 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
     };
     // A warp takes kPart tokens of a row at a time; its part of the mask row is fetched one part ahead,
     // and the counting runs under its first loads.
-    const int parts = in_place && h.mask == nullptr && !counts ? 0 : (nv + kPart - 1) / kPart;
+    const int parts = IN_PLACE && !MASKED && !counts ? 0 : (nv + kPart - 1) / kPart;
     int i = 0, part = tid >> 5;
     const uint32_t* mask = nullptr;
     uint32_t ahead = 0;
     auto settle = [&]() {
         if (parts == 0) i = w;
         while (i < w && part >= parts) { part -= parts; ++i; }
-        if (i >= w || h.mask == nullptr) return;
+        if (!MASKED || i >= w) return;
         mask = mask_of(r0 + i);
         const int v = part * kPart + lane * 32;
         ahead = mask != nullptr && v < min(nv, (part + 1) * kPart) ? __ldg(mask + (v0 + v) / 32) : 0;
@@ -245,7 +271,7 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
     while (i < w || to_count) {
         const bool some = i < w;
         const int r = r0 + i, p0 = part * kPart, now_i = i, now_part = part;
-        const uint32_t* row_mask = mask;
+        const uint32_t* row_mask = MASKED ? mask : nullptr;
         const uint32_t mine = ahead;           // word `lane` of the part's mask
         const T* x = static_cast<const T*>(A.x) + r * A.xs + v0;
         T* y = static_cast<T*>(A.y) + r * A.ys + v0;
@@ -258,15 +284,15 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
 #pragma unroll
             for (int k = 0; k < kUnits; ++k) {
                 allow[k] = kAll;
-                if (row_mask != nullptr)
+                if (MASKED && row_mask != nullptr)
                     allow[k] = __shfl_sync(0xffffffffu, mine, (k * 32 + lane) * N / 32) >> (lane * N & 31) & kAll;
             }
 #pragma unroll
             for (int k = 0; k < kUnits; ++k)
-                if (allow[k] != 0 && !(in_place && allow[k] == kAll))
+                if (allow[k] != 0 && !(IN_PLACE && allow[k] == kAll))
                     e[k] = *(reinterpret_cast<const uint4*>(x + p0) + k * 32 + lane);
         }
-        if (to_count) {
+        if (COUNTING && to_count) {
             count();
             to_count = false;
         }
@@ -283,24 +309,24 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
             head = alike ? min(end, p0 + static_cast<int>(((16 - (ay & 15)) & 15) / sizeof(T))) : end;
             tail = head + (end - head) / N * N;
             auto single = [&](int t) {
-                const bool allowed = row_mask == nullptr || (mask_bits<1>(row_mask, v0 + t) & 1);
+                const bool allowed = !MASKED || row_mask == nullptr || (mask_bits<1>(row_mask, v0 + t) & 1);
                 if (!allowed) y[t] = E::kLowest;
-                else if (!in_place) y[t] = x[t];
+                else if (!IN_PLACE) y[t] = x[t];
             };
             for (int t = p0 + lane; t < head; t += 32) single(t);
             if (tail + lane < end) single(tail + lane);
 #pragma unroll
             for (int k = 0; k < kUnits; ++k) {
                 const int t = head + (k * 32 + lane) * N;
-                allow[k] = t >= tail || row_mask == nullptr ? kAll : mask_bits<N>(row_mask, v0 + t) & kAll;
-                if (t < tail && allow[k] != 0 && !(in_place && allow[k] == kAll))
+                allow[k] = t >= tail || !MASKED || row_mask == nullptr ? kAll : mask_bits<N>(row_mask, v0 + t) & kAll;
+                if (t < tail && allow[k] != 0 && !(IN_PLACE && allow[k] == kAll))
                     e[k] = *reinterpret_cast<const uint4*>(x + t);
             }
         }
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             const int t = head + (k * 32 + lane) * N;
-            if (t >= tail || (in_place && allow[k] == kAll)) continue;
+            if (t >= tail || (IN_PLACE && allow[k] == kAll)) continue;
             if (allow[k] != kAll) {
                 e[k].x = E::blend(e[k].x, allow[k], 0);
                 e[k].y = E::blend(e[k].y, allow[k], 1);
@@ -309,7 +335,7 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
             }
             *reinterpret_cast<uint4*>(y + t) = e[k];
         }
-        if (!counts) continue;
+        if (!COUNTING || !counts) continue;
         // the part's listed tokens, over what the warp wrote: kEach a lane at a time, their loads at once
         const int m = listed[now_part];
         __syncwarp();
@@ -326,7 +352,7 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
                 its[e] = word[t[e]] & ~kDraft;
                 uses[e] = its[e] & kUses;
                 // not: a token that is not allowed
-                apply[e] = k < m && (row_mask == nullptr || (mask_bits<1>(row_mask, v0 + t[e]) & 1));
+                apply[e] = k < m && (!MASKED || row_mask == nullptr || (mask_bits<1>(row_mask, v0 + t[e]) & 1));
                 old[e] = x[t[e]];
             }
             for (int j = 1; j <= now_i; ++j) {
@@ -348,7 +374,7 @@ adjust_kernel(const __grid_constant__ AdjustCall A, bool counting, bool in_place
         }
     }
     // Masks that allow nothing: row i's is looked at by slice i % slices.
-    if (h.mask != nullptr) {
+    if constexpr (MASKED) {
         const int words = (A.V + 31) / 32;
         const uint32_t last = A.V % 32 ? (1u << (A.V % 32)) - 1 : 0xffffffffu;     // bits of the last word
         for (int i = slice; i < w; i += A.slices) {
@@ -371,14 +397,25 @@ int launch_adjust(AdjustCall& A, int dtype, cudaStream_t stream)
     if (rc != DSPARK_OK) return rc;
     const bool counting = A.h.repetition != nullptr || A.h.presence != nullptr || A.h.frequency != nullptr ||
                           A.h.bias_tokens != nullptr;
-    // Slices of one size, in steps of kMinSlice: as few as kMaxSlice allows, or (few requests) so many
-    // that there are two CTAs for each SM.
-    const int64_t least = ceil_div(A.V, kMaxSlice), wanted = ceil_div(2ll * dev.sm_count, A.B);
+    // Slices of one size, in steps of kMinSlice: as few as kMaxSlice allows, since each counts the whole
+    // history (4096 tokens instead of 7168: 140 -> 161 us for the 256 windows), or, where requests are few, so
+    // many that there are kFewCtas CTAs for each SM (33 requests over 32003 tokens: 20 us, 28 with two).
+    const int64_t least = ceil_div(A.V, kMaxSlice), wanted = ceil_div(kFewCtas * dev.sm_count, A.B);
     A.slice = static_cast<int>(ceil_div(ceil_div(A.V, least > wanted ? least : wanted), kMinSlice) * kMinSlice);
     A.slices = static_cast<int>(ceil_div(A.V, A.slice));           // each holds a token
-    auto kernel = dtype == DSPARK_BF16 ? adjust_kernel<DSPARK_BF16> : adjust_kernel<DSPARK_F32>;
+    const bool masked = A.h.mask != nullptr;
+    auto pick = [&](auto dt, auto in_place) {
+        constexpr int DT = decltype(dt)::value;
+        constexpr bool P = decltype(in_place)::value;
+        return counting ? (masked ? adjust_kernel<DT, true, true, P> : adjust_kernel<DT, true, false, P>)
+                        : (masked ? adjust_kernel<DT, false, true, P> : adjust_kernel<DT, false, false, P>);
+    };
+    const std::integral_constant<int, DSPARK_BF16> bf16;
+    const std::integral_constant<int, DSPARK_F32> f32;
+    auto kernel = A.x == A.y ? (dtype == DSPARK_BF16 ? pick(bf16, std::true_type{}) : pick(f32, std::true_type{}))
+                             : (dtype == DSPARK_BF16 ? pick(bf16, std::false_type{}) : pick(f32, std::false_type{}));
     return launch_pdl("adjust", kernel, dim3(static_cast<unsigned>(A.B) * A.slices), dim3(kThreads),
-                      counting ? slice_bytes(A.slice) : 0, stream, A, counting, A.x == A.y);
+                      counting ? slice_bytes(A.slice) : 0, stream, A);
 }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
