@@ -234,3 +234,41 @@ def test_a_replayed_graph_takes_other_workspaces_beside_it(dev):
     for loop, w in zip(loops, want):
         M = int(loop.step.cu[-1])
         assert torch.equal(loop.attention.out[:M], w[:M])
+
+
+@gpu
+@pytest.mark.parametrize("form", ["sinks", "shared"])
+@pytest.mark.parametrize("w", [3, 60])                 # units of few rows and of many
+def test_pages_past_32_bit_offsets(dev, form, w):
+    """The same pages in a small cache and at the end of one of more than 2^32 bytes: the same bits."""
+    heads, page, dim, group = 4, 64, 128, 2
+    B, prefix, own = (2, 0, 700) if form == "sinks" else (40, 6400, 90)
+    rng = np.random.default_rng(w)
+    front, mine = prefix // page, -(-(own + w) // page)
+    n = front + B * mine
+    table = np.concatenate([np.tile(np.arange(front), (B, 1)), front + np.arange(B * mine).reshape(B, mine)], 1)
+    put = lambda a: torch.as_tensor(np.ascontiguousarray(a)).to(dev)      # noqa: E731
+    k, v = (put(rng.integers(0, 0x78, (n, heads, page, dim), dtype=np.uint8)) for _ in range(2))
+    scale = put(rng.uniform(1e-4, 1e-3, (n, heads)).astype(np.float32))
+    g = torch.Generator(device=dev).manual_seed(w)
+    q = torch.randn(B * w, heads * group, dim, generator=g, device=dev).bfloat16()
+    i32 = dict(dtype=torch.int32, device=dev)
+    cu = torch.arange(0, B * w + 1, w, **i32)
+    lengths = torch.full((B,), prefix + own, **i32)
+    size = bd.dspark_attend_shared_workspace_bytes(B * w, heads * group, heads, dim, B)
+    ws, results = torch.empty(size, dtype=torch.uint8, device=dev), []
+    for at in (0, (1 << 32) // (heads * page * dim) + 5):
+        pages = [torch.zeros(at + n, heads, page, dim, dtype=torch.uint8, device=dev) for _ in range(2)]
+        scales = torch.ones(at + n, heads, device=dev)
+        for to, x in zip((*pages, scales), (k, v, scale)):
+            to[at:] = x
+        cache = bd.PagedCache(*pages, scales, scales, put((table + at).astype(np.int32)))
+        out, status = torch.zeros_like(q), torch.zeros(1, **i32)
+        if form == "sinks":
+            bd.dspark_attend_sinks(cache, q, out, cu, lengths, ws, window=300, sinks=70, status=status)
+        else:
+            bd.dspark_attend_shared(cache, q, out, cu, lengths, torch.tensor([0, B], **i32),
+                                    torch.tensor([prefix], **i32), ws, status=status)
+        results.append(out)
+        assert int(status.item()) == 0
+    assert torch.isfinite(results[0]).all() and torch.equal(*results)
