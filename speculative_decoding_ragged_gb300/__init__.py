@@ -7,7 +7,8 @@ implemented as hand-written CUDA kernels in libdspark.so (C ABI: include/dspark.
 package is the ctypes binding (`_binding`), the in-tree build (`build`), a buffer-owning step
 runner (`step`) and the seeded synthetic workloads (`synth`).
 """
-from ._binding import (BF16, CAP_ACCEPT, COMPACT, F32, MODES, STATIC, CostTable, DSparkError,  # noqa: F401
-                       PagedCache, Rope, dspark_append, dspark_attend,
+from ._binding import (BF16, CAP_ACCEPT, COMPACT, F32, MODES, STATIC, Adjustments, CostTable, DSparkError,  # noqa: F401
+                       PagedCache, Rope, dspark_adjust, dspark_append, dspark_attend, dspark_attend_shared,
+                       dspark_attend_shared_workspace_bytes, dspark_attend_sinks,
                        dspark_attend_workspace_bytes, dspark_pack, dspark_rotate, dspark_scatter, dspark_schedule, dspark_verify,
                        dspark_verify_workspace_bytes, last_error, lib, version)

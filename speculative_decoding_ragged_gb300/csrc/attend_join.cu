@@ -10,7 +10,7 @@ namespace {
 // where the parts are few: its lanes read the parts' references and sums, dim / 4 lanes add up the
 // parts, up to 16 loads in flight. Prompts' units have 128 rows and mostly two parts, so that a warp's
 // time is its rows' round trips: with a row at a time, its references read before its parts, two
-// prompts' pieces took 37 us, now 11.
+// prompts' pieces took 37 us, now 12.
 constexpr int kJoinWarps = 8;
 constexpr int kFewParts = 4, kFewRows = 4;
 

@@ -25,7 +25,7 @@
 // Bound by HBM: 2 D bytes per token and cache head. What else showed in clock stamps was cold
 // code (about 16 cycles per instruction the first time), hence one walker, rolled loops where
 // registers allow them. 192 single tokens over 1 to 8 thousand, 8 heads of 128: 6.5 TB/s, 97 % of a
-// copy. 256 windows of 1 to 8 over 128 to 2048: 116 us, 3.3 TB/s: a unit has about nine tiles, of about
+// copy. 256 windows of 1 to 8 over 128 to 2048: 113 us, 3.4 TB/s: a unit has about nine tiles, of about
 // 2500 cycles each, and changing units costs 9000, the start 15 to 25 thousand.
 #pragma once
 

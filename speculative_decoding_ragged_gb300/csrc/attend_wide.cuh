@@ -21,7 +21,7 @@
 //
 // Bound: sixteen products of about 101 cycles a tile at D = 128, 1616 cycles a tile and SM, and the
 // softmax, which takes a CTA about 4250 cycles a tile, 2100 with two of them. Two prompts' pieces of
-// about 2000 rows, 32 query heads of 128 over 8 heads, after 4 to 8 thousand tokens: 507 us, 0.93
+// about 2000 rows, 32 query heads of 128 over 8 heads, after 4 to 8 thousand tokens: 482 us, 0.98
 // PFLOP/s of the plain form's 16-bit products. Its registers are tight: ptxas places the same
 // source's scores well or badly (640 us with the queries loaded in two halves).
 #pragma once
