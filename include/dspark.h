@@ -586,8 +586,8 @@ int dspark_attend_sinks(const dspark_cache* cache, const void* q, int64_t q_stri
  * same pages: their table entries are alike, and the call may read any of them. prefix is taken in whole
  * pages (a page that is appended to is not shared). Results are dspark_attend's over the same cache
  * without a window: a row sees every token up to its own. Requests in no group, or in a group of
- * one, those with fewer tokens in the cache than the prefix, and groups whose numbers make no sense
- * (a prefix that passes the page table or is negative, requests outside [0, B)) attend alone.
+ * one, those with fewer tokens in the cache than the prefix, and groups whose prefix passes the page
+ * table or is negative attend alone; so does every request where group_cu decreases or leaves [0, B].
  *
  * group_cu [groups + 1] int32, non-decreasing; prefix [groups] int32 (both may be NULL where groups is 0);
  * the rest as in dspark_attend. workspace: at least dspark_attend_shared_workspace_bytes(rows, q_heads,

@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(AttendCall A)
         // kSinks: the pieces from the sinks' last to the window's first are left out
         const int sink_pieces = SEE == kSinks ? (min(A.sinks, first) + 31) / 32 : 0;
         const int64_t skip = SEE == kSinks ? max(0, first / 32 - sink_pieces) * 32 : 0;
-        for (int64_t t0 = (SEE == kSinks ? 0 : (first / 32) * 32) + static_cast<int64_t>(warp) * 32; t0 + skip <= pos || t0 < sink_pieces * 32;
+        const int from = SEE == kSinks ? 0 : (first / 32) * 32;
+        for (int64_t t0 = from + static_cast<int64_t>(warp) * 32; t0 + skip <= pos || t0 < sink_pieces * 32;
              t0 += kWarps * 32) {
             const int64_t t = t0 + lane + (t0 < sink_pieces * 32 ? 0 : skip);
             bool see = (t >= first || (SEE == kSinks && t < A.sinks)) && t <= pos;

@@ -355,7 +355,7 @@ constexpr int kUnitCost = R < kTile ? 4 : 6;
 // kSinks: the sinks' blocks and the window's follow one another, so that neither the blocks between
 // nor the start of the window's first tile take tiles: token (block) number u of a unit is u of the
 // request up to the sinks' last block, and u + the blocks left out behind it. Tiles of whole 128
-// tokens for each took 147 us where this takes 130 (256 windows of 1 to 8 rows over 128 to 8192, 1024 and
+// tokens for each took 147 us where this takes 128 (256 windows of 1 to 8 rows over 128 to 8192, 1024 and
 // 4 visible).
 struct Shape {                   // a unit's visible tiles [a, z]; kSinks: the blocks left out
     int a, z, skip;

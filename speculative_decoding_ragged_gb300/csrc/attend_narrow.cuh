@@ -49,7 +49,7 @@ constexpr int weight_row(int R) { return R == 32 ? 32 : 64; }
 
 // A run's part of one unit.
 struct Piece {
-    int b, h, len, w;
+    int b, h, len, w;    // b: the row of the page table
     int row0, flat0;     // the request's first packed row; the unit's first (position, head)
     int rows;
     int k0, n;           // tiles
@@ -509,7 +509,7 @@ static __device__ __noinline__ void put_query(const AttendCall& A, Smem<D, R, SE
 template <int R, int SEE>
 __device__ __forceinline__ void describe(const AttendCall& A, const Walk<R, SEE>& wk, Piece& p)
 {
-    p.b = wk.b;
+    p.b = SEE == kPrefix ? A.group_cu[wk.b] : wk.b;
     p.h = wk.h;
     p.len = wk.len;
     p.w = wk.w;
@@ -627,7 +627,7 @@ attend_narrow_kernel(const __grid_constant__ AttendCall A, const __grid_constant
                 if (n >= (p.k0 + p.n) * per_tile ||
                     j >= (stored_tokens<SEE>(p.len, p.w) + A.c.page - 1) / A.c.page ||
                     ((j + 1) * A.c.page <= p.first_seen && !(SEE == kSinks && j * A.c.page < A.sinks))) return -1;
-                const int id = j < A.c.width ? table_row<SEE>(A, p.b)[j] : -1;
+                const int id = j < A.c.width ? A.c.table[static_cast<int64_t>(p.b) * A.c.width + j] : -1;
                 if (id < 0 || id >= A.c.n_pages) { bad = 1; return -1; }
                 return id;
             };

@@ -19,27 +19,44 @@ namespace {
 constexpr int64_t kWorth = 6000;
 
 // Whether the groups' prefixes are worth it; every request's first own token; no row has a part yet.
+// Groups that are not in order, or whose rows are more than there are, are not computed apart at all: the
+// cut of the prefixes' kernels counts on that.
 constexpr int kPlanThreads = 256;
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttendCall A)
 {
-    __shared__ int64_t saved[kPlanThreads / 32];
+    __shared__ int64_t saved[kPlanThreads / 32], members[kPlanThreads / 32];
     pdl_wait_and_trigger();
     const int tid = threadIdx.x;
     const int at = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
     for (int i = at; i < A.rows * A.q_heads; i += step) A.part_lse[i] = __uint_as_float(kNoPart);
-    int64_t tiles = 0;                           // each CTA adds them up for itself
+    int64_t tiles = 0, rows = 0;                 // each CTA adds them up for itself
+    bool orderly = true;
     for (int g = tid; g < A.B; g += kPlanThreads) {
-        const int64_t n = static_cast<int64_t>(A.group_cu[g + 1]) - A.group_cu[g];
-        if (n > 1 && n <= A.requests && A.prefix[g] > 0 && A.prefix[g] <= A.reach)
-            tiles += (n - 1) * ((A.prefix[g] + kTile - 1) / kTile);
+        const int b0 = A.group_cu[g], b1 = A.group_cu[g + 1];
+        orderly = orderly && b0 >= 0 && b1 >= b0 && b1 <= A.requests;
+        int r0, w, n;
+        group_shape(A, g, &r0, &w, &n);
+        if (w > 0) {
+            tiles += (b1 - b0 - 1ll) * ((n + kTile - 1) / kTile);
+            rows += w;
+        }
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, off);
-    if ((tid & 31) == 0) saved[tid >> 5] = tiles;
-    __syncthreads();
-    tiles = 0;
-    for (int i = 0; i < kPlanThreads / 32; ++i) tiles += saved[i];
-    const bool worth = tiles * A.c.heads >= kWorth;
+    for (int off = 16; off > 0; off >>= 1) {
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, off);
+        rows += __shfl_xor_sync(0xffffffffu, rows, off);
+    }
+    if ((tid & 31) == 0) {
+        saved[tid >> 5] = tiles;
+        members[tid >> 5] = rows;
+    }
+    orderly = __syncthreads_and(orderly);
+    tiles = rows = 0;
+    for (int i = 0; i < kPlanThreads / 32; ++i) {
+        tiles += saved[i];
+        rows += members[i];
+    }
+    const bool worth = orderly && rows <= A.rows && tiles * A.c.heads >= kWorth;
     if (at == 0) A.from[A.requests] = worth;
     for (int b = at; b < A.requests; b += step) {
         int lo = 0, hi = A.B;                    // the last group that starts at or before b
