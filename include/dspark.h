@@ -535,7 +535,8 @@ int dspark_append(const dspark_cache* cache, const dspark_rope* rope, const void
  * [0, n_pages), or in a block >= width, are not seen (DSPARK_STATUS_BAD_PAGE); pages wholly
  * before every row's window are not looked at (their entries may be stale). A negative length
  * counts as 0 (DSPARK_STATUS_BAD_LENGTH); a request whose rows lie outside [0, rows) or run
- * backwards gets nothing written (DSPARK_STATUS_BAD_ROWS). What stale slots hold, NaN codes
+ * backwards gets nothing written (DSPARK_STATUS_BAD_ROWS), and where others' rows then overlap so often that
+ * the work passes 2^30 tiles no request does. What stale slots hold, NaN codes
  * included, does not matter; NaN codes in a token that some row of the call sees may reach
  * every row of its request (dspark_append writes none).
  * Rows at or past cu_seqlens[B] are not written.

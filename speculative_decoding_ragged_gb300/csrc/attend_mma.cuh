@@ -577,6 +577,22 @@ __device__ __forceinline__ void find_start(const AttendCall& A, Walk<R, SEE>& k,
         k.piece(A, t0);
     }
 }
+// Requests whose rows run backwards let the others' overlap, so that they may be more than the packed rows
+// and their line longer than an int, which places_fit counts on: such a call has no line (fp32 sums:
+// the line is refused from 2^30 places on, and an int ends at 2^31). `size`: a thread's places.
+template <int NT>
+static __device__ __noinline__ bool line_fits(float size, int* scan)
+{
+    const int tid = threadIdx.x;
+    float* sums = reinterpret_cast<float*>(scan);
+    for (int d = 16; d > 0; d >>= 1) size += __shfl_xor_sync(0xffffffffu, size, d);
+    __syncthreads();                             // scan has been read
+    if ((tid & 31) == 0) sums[tid >> 5] = size;
+    __syncthreads();
+    float all = 0;
+    for (int i = 0; i < NT / 32; ++i) all += sums[i];
+    return all < 0x1p30f;
+}
 template <int R, int SEE, int NT>
 __device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R, SEE>& cut)
 {
@@ -592,6 +608,7 @@ __device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R, SEE>& cut)
     const int per = (A.B + groups - 1) / groups;
     const int b0 = min(tid / gr.size * per, A.B), b1 = min(b0 + per, A.B);
     int mine = 0, per_head = 1;
+    float size = 0;
     Walk<R, SEE> k;
     if (tid == 0) cut.walk.n = 0;
 #pragma unroll 1
@@ -600,6 +617,7 @@ __device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R, SEE>& cut)
         rows_of<SEE>(A, b, &k.row0, &k.w, &k.len, &k.from, &bits);
         per_head = group_places<R, SEE>(A, k.w, k.len, k.from, gr);
         mine += gr.g == 0 ? per_head * A.c.heads : 0;
+        size += gr.g == 0 ? static_cast<float>(per_head * A.c.heads) : 0.0f;
     }
     int upto = mine;
 #pragma unroll
@@ -608,14 +626,15 @@ __device__ __forceinline__ int cut_line(const AttendCall& A, Cut<R, SEE>& cut)
         if (lane >= d) upto += y;
     }
     if (lane == 31) cut.scan[warp] = upto;
-    __syncthreads();
+    const bool disorder = __syncthreads_or(bits & DSPARK_STATUS_BAD_ROWS);
     int sums = lane < NT / 32 ? cut.scan[lane] : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, sums, d);
         if (lane >= d) sums += y;
     }
-    const int total = __shfl_sync(0xffffffffu, sums, NT / 32 - 1);
+    int total = __shfl_sync(0xffffffffu, sums, NT / 32 - 1);
+    if (disorder && !line_fits<NT>(size, cut.scan)) total = 0;
     const int before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
     int from = (warp > 0 ? before : 0) + upto - mine;
     const int run = static_cast<int>((static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x);

@@ -236,6 +236,55 @@ def test_rows_of_no_request_inside_a_group(lib):
 
 
 @gpu
+def test_rows_that_are_more_than_there_are(lib):
+    """Where cu_seqlens runs backwards, groups' rows may overlap: no group is then computed apart, and the
+    rows of one request only are whole."""
+    c = base(13)                             # 12 rows of requests 0 to 4, 64 of 5 to 68
+    c.cu[3] = 60                             # request 2: rows 5 .. 59, more than its pages hold; request 3: none
+    q, out, lse, st = c.go(torch.bfloat16)
+    assert st == bd.STATUS_BAD_ROWS | bd.STATUS_BAD_PAGE
+    c.cu[3:5] = [5, 10]                      # for the formula: request 2 none; 3 rows 5 .. 9, not looked at
+    want = forms_ref.attend(c, q, c.dim ** -0.5, lambda b, pos: np.arange(pos + 1))[0]
+    for rows in (slice(0, 5), slice(60, 76)):
+        np.testing.assert_allclose(out[rows], want[rows], atol=0.02, rtol=0.02)
+    assert (out[76:] == 5.0).all()
+
+
+@gpu
+@pytest.mark.parametrize("form", ["plain", "sinks", "shared"])
+@pytest.mark.parametrize("rows,hq,page", [(2048, 64, 64), (200, 8, 128)])
+def test_rows_that_overlap_without_end(lib, form, rows, hq, page):
+    """Every other request has all the rows, over so many tokens that the work passes 32 bits: nothing is
+    written."""
+    B, dim, width = 1024, 64, 32768
+    dev = torch.device("cuda:0")
+    z = lambda *s, **k: torch.zeros(*s, device=dev, **k)                   # noqa: E731
+    cu = torch.tensor([0, rows] * (B // 2) + [rows], dtype=torch.int32, device=dev)
+    table = z(B, width, dtype=torch.int32)
+    reach = width * page
+    codes = [z(4, 1, page, dim, dtype=torch.uint8) for _ in range(2)]
+    scales = [torch.ones(4, 1, device=dev) for _ in range(2)]
+    cache = bd.PagedCache(*codes, *scales, table)
+    lengths = torch.full((B,), reach - rows, dtype=torch.int32, device=dev)
+    q = z(rows, hq, dim, dtype=torch.bfloat16)
+    out = torch.full_like(q, 5.0)
+    st = z(1, dtype=torch.int32)
+    if form == "shared":
+        ws = z(bd.dspark_attend_shared_workspace_bytes(rows, hq, 1, dim, B), dtype=torch.uint8)
+        gcu, prefix = (torch.tensor(x, dtype=torch.int32, device=dev) for x in ([0, B], [100 * page]))
+        bd.dspark_attend_shared(cache, q, out, cu, lengths, gcu, prefix, ws, status=st)
+    else:
+        ws = z(bd.dspark_attend_workspace_bytes(1, dim), dtype=torch.uint8)
+        if form == "plain":
+            bd.dspark_attend(cache, q, out, cu, lengths, ws, status=st)
+        else:
+            bd.dspark_attend_sinks(cache, q, out, cu, lengths, ws, window=reach, sinks=4, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == bd.STATUS_BAD_ROWS
+    assert bool((out == 5.0).all())
+
+
+@gpu
 def test_bad_pages(lib):
     c = base(5)
     c.table[:3, 4] = c.n                     # in the first prefix
