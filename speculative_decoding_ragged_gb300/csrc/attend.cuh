@@ -78,7 +78,8 @@ __device__ __forceinline__ void group_shape(const AttendCall& A, int g, int* row
     const int n = A.prefix[g] / A.c.page * A.c.page;
     *row0 = *w = 0;
     *len = n;
-    if (b0 < 0 || b1 > A.requests || b1 - b0 < 2 || n <= 0 || n > A.reach) return;
+    // in an order in which no difference passes 32 bits, whatever the numbers are
+    if (b0 < 0 || b1 < b0 || b1 > A.requests || b1 - b0 < 2 || n <= 0 || n > A.reach) return;
     const int r0 = A.cu[b0], r1 = A.cu[b1];
     if (r0 < 0 || r1 < r0 || r1 > A.rows) return;
     *row0 = r0;
