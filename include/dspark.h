@@ -583,12 +583,14 @@ int dspark_attend_sinks(const dspark_cache* cache, const void* q, int64_t q_stri
 /* ---------------------------------------------------------------------------------------
  * dspark_attend_shared — dspark_attend for requests that share a prefix, whose keys and values are then
  * read once for all rows of its requests instead of once for each. Group g is the requests
- * group_cu[g] .. group_cu[g + 1] - 1; the first prefix[g] tokens of each are the same tokens in the
- * same pages: their table entries are alike, and the call may read any of them. prefix is taken in whole
- * pages (a page that is appended to is not shared). Results are dspark_attend's over the same cache
+ * group_cu[g] .. group_cu[g + 1] - 1; the first prefix[g] tokens of each that has rows and so many
+ * tokens in the cache are the same tokens in the same pages: their table entries are alike, and the call
+ * may read any of them. The other requests of a group may have anything in their tables. prefix is taken in
+ * whole pages (a page that is appended to is not shared). Results are dspark_attend's over the same cache
  * without a window: a row sees every token up to its own. Requests in no group, or in a group of
  * one, those with fewer tokens in the cache than the prefix, and groups whose prefix passes the page
- * table or is negative attend alone; so does every request where group_cu decreases or leaves [0, B].
+ * table or is negative attend alone; so does every request where group_cu decreases or leaves [0, B], or
+ * where the groups' rows run backwards.
  *
  * group_cu [groups + 1] int32, non-decreasing; prefix [groups] int32 (both may be NULL where groups is 0);
  * the rest as in dspark_attend. workspace: at least dspark_attend_shared_workspace_bytes(rows, q_heads,

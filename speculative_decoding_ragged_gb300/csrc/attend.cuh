@@ -38,7 +38,9 @@ struct AttendCall {
     int requests;
     const int32_t* group_cu;   // a group's requests: group_cu[g] .. group_cu[g + 1] - 1
     const int32_t* prefix;     // its shared tokens
-    int32_t* from;             // [requests + 1] a request's first token that is its own; 0: all are.
+    int32_t* from;             // [requests + 1] a request's first token that is its own; 0: all are, and
+                               // so where negative, which a group's first request only is: minus the
+                               // group's first request that has the prefix (group_lead).
                                // The last: whether prefixes are computed apart at all
     float* part_lse;           // [rows * q_heads] what the own tokens give each row: log2 of the sum
     float* part;               // [rows * q_heads, dim] and the quotient
@@ -85,31 +87,37 @@ __device__ __forceinline__ void group_shape(const AttendCall& A, int g, int* row
     *row0 = r0;
     *w = r1 - r0;
 }
-// The same of a call's groups, none where it does not pay.
-__device__ __forceinline__ void group_rows(const AttendCall& A, int g, int* row0, int* w, int* len)
+// Whose table row a group's prefix is read by: its first request that has the prefix and rows. What stands
+// in the others' rows is not known (an emptied slot's may be another request's pages by now).
+__device__ __forceinline__ int group_lead(const AttendCall& A, int g)
+{
+    const int b0 = A.group_cu[g], x = A.from[b0];
+    return x < 0 ? -x : b0;
+}
+// The same of a call's groups, none where it does not pay; *lead: see above.
+__device__ __forceinline__ void group_rows(const AttendCall& A, int g, int* row0, int* w, int* len, int* lead)
 {
     group_shape(A, g, row0, w, len);
     if (A.from[A.requests] == 0) *w = 0;
+    if (*w > 0) *lead = group_lead(A, g);
 }
-// What a call takes as its requests; *from: the first token that is seen at all (kSuffix).
+// What a call takes as its requests; *from: the first token that is seen at all (kSuffix), the request that
+// is read (kPrefix).
 template <int SEE>
 __device__ __forceinline__ void rows_of(const AttendCall& A, int b, int* row0, int* w, int* len, int* from, int* bits)
 {
     if constexpr (SEE == kPrefix) {
-        group_rows(A, b, row0, w, len);
+        group_rows(A, b, row0, w, len, from);
     } else {
         request_rows(A, b, row0, w, len, bits);
-        if constexpr (SEE == kSuffix) *from = A.from[b];
+        if constexpr (SEE == kSuffix) *from = max(A.from[b], 0);
     }
 }
-// The tokens of a "request" that are in the cache, its table's row, a row's position.
+// The tokens of a "request" that are in the cache, whose table row it reads (from: rows_of's), a row's position.
 template <int SEE>
 __device__ __forceinline__ int stored_tokens(int len, int w) { return SEE == kPrefix ? len : len + w; }
 template <int SEE>
-__device__ __forceinline__ const int32_t* table_row(const AttendCall& A, int b)
-{
-    return A.c.table + static_cast<int64_t>(SEE == kPrefix ? A.group_cu[b] : b) * A.c.width;
-}
+__device__ __forceinline__ int table_of(int b, int from) { return SEE == kPrefix ? from : b; }
 template <int SEE>
 __device__ __forceinline__ int position(int len, int i) { return SEE == kPrefix ? len - 1 : len + i; }
 // The first token that a row at this position sees, sinks apart.

@@ -437,7 +437,8 @@ template <int R, int SEE>
 struct Walk {
     int b, h, qt, nq;
     int row0, w, len;
-    int from;                    // kSuffix: the first own token; kSinks: the unit's blocks left out
+    int from;                    // kSuffix: the first own token; kSinks: the unit's blocks left out;
+                                 // kPrefix: the request whose table row is read
     int a, z, k0, n;             // the unit's tiles [a, z]; this piece: n tiles from k0
     int unit;                    // the unit's first place on the line
     int stop;                    // the run's end on the line

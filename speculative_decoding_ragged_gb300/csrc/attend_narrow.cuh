@@ -509,7 +509,7 @@ static __device__ __noinline__ void put_query(const AttendCall& A, Smem<D, R, SE
 template <int R, int SEE>
 __device__ __forceinline__ void describe(const AttendCall& A, const Walk<R, SEE>& wk, Piece& p)
 {
-    p.b = SEE == kPrefix ? A.group_cu[wk.b] : wk.b;
+    p.b = table_of<SEE>(wk.b, wk.from);
     p.h = wk.h;
     p.len = wk.len;
     p.w = wk.w;

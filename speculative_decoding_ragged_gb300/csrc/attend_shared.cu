@@ -18,62 +18,74 @@ namespace {
 // tiles: 573 and 130.
 constexpr int64_t kWorth = 6000;
 
-// Whether the groups' prefixes are worth it; every request's first own token; no row has a part yet.
-// Groups that are not in order, or whose rows are more than there are, are not computed apart at all: the
-// cut of the prefixes' kernels counts on that.
-constexpr int kPlanThreads = 256;
+// Whether the groups' prefixes are worth it; every request's first own token, and whose pages are read for
+// a group (the first CTA); no row has a part yet (the others).
+// A request joins its group where its rows are the group's too and all of the prefix lies before them: the
+// prefix is then in its table. What stands in the table of one that does not join is not known. The first
+// that joins is the one before which the last that does lies in front of the group; requests are taken in
+// order, a thread each.
+// Groups that are not in order, or whose rows are not, are not computed apart at all: the cut of the prefixes'
+// kernels counts on rows that are no more than the call's.
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttendCall A)
 {
-    __shared__ int64_t saved[kPlanThreads / 32], members[kPlanThreads / 32];
+    __shared__ int saved[kPlanWarps];
+    __shared__ int last[2][kPlanWarps];          // the last request of each warp's that joins, or -1
     pdl_wait_and_trigger();
-    const int tid = threadIdx.x;
-    const int at = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
-    for (int i = at; i < A.rows * A.q_heads; i += step) A.part_lse[i] = __uint_as_float(kNoPart);
-    int64_t tiles = 0, rows = 0;                 // each CTA adds them up for itself
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x > 0) {
+        const int step = (gridDim.x - 1) * kPlanThreads;
+        for (int i = (blockIdx.x - 1) * kPlanThreads + tid; i < A.rows * A.q_heads; i += step)
+            A.part_lse[i] = __uint_as_float(kNoPart);
+        return;
+    }
+    int tiles = 0;                               // times the heads no more than the own tokens' line may have
     bool orderly = true;
     for (int g = tid; g < A.B; g += kPlanThreads) {
         const int b0 = A.group_cu[g], b1 = A.group_cu[g + 1];
-        orderly = orderly && b0 >= 0 && b1 >= b0 && b1 <= A.requests;
+        orderly = orderly && b0 >= 0 && b1 >= b0 && b1 <= A.requests && A.cu[b0] <= A.cu[b1];
         int r0, w, n;
         group_shape(A, g, &r0, &w, &n);
-        if (w > 0) {
-            tiles += (b1 - b0 - 1ll) * ((n + kTile - 1) / kTile);
-            rows += w;
+        if (w > 0) tiles += (b1 - b0 - 1) * ((n + kTile - 1) / kTile);
+    }
+    int before = -1;                             // the last request of earlier rounds that joins
+    for (int base = 0; base < A.requests; base += kPlanThreads) {
+        const int b = base + tid, round = base / kPlanThreads & 1;
+        int b0 = 0, n = 0;
+        bool joins = false;
+        if (b < A.requests) {
+            int row0, w, len, bits = 0;          // their loads under the search's
+            request_rows(A, b, &row0, &w, &len, &bits);
+            int lo = 0, hi = A.B;                // the last group that starts at or before b
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (A.group_cu[mid] <= b) lo = mid; else hi = mid;
+            }
+            b0 = A.group_cu[lo];
+            if (b0 <= b && b < A.group_cu[lo + 1]) {
+                int r0, group_w;
+                group_shape(A, lo, &r0, &group_w, &n);
+                joins = group_w > 0 && w > 0 && row0 >= r0 && row0 + w <= r0 + group_w && len >= n;
+            }
+            A.from[b] = joins ? n : 0;
         }
+        const uint32_t mask = __ballot_sync(0xffffffffu, joins);
+        if (lane == 0) last[round][warp] = mask != 0 ? base + warp * 32 + 31 - __clz(mask) : -1;
+        __syncthreads();
+        const int its = lane < kPlanWarps ? last[round][lane] : -1;
+        int earlier = max(before, __reduce_max_sync(0xffffffffu, lane < warp ? its : -1));
+        before = max(before, __reduce_max_sync(0xffffffffu, its));
+        const uint32_t below = mask & ((1u << lane) - 1);
+        if (below != 0) earlier = base + warp * 32 + 31 - __clz(below);
+        if (joins && earlier < b0 && b > b0) A.from[b0] = -b;
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        tiles += __shfl_xor_sync(0xffffffffu, tiles, off);
-        rows += __shfl_xor_sync(0xffffffffu, rows, off);
-    }
-    if ((tid & 31) == 0) {
-        saved[tid >> 5] = tiles;
-        members[tid >> 5] = rows;
-    }
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    if (lane == 0) saved[warp] = tiles;
     orderly = __syncthreads_and(orderly);
-    tiles = rows = 0;
-    for (int i = 0; i < kPlanThreads / 32; ++i) {
-        tiles += saved[i];
-        rows += members[i];
-    }
-    const bool worth = orderly && rows <= A.rows && tiles * A.c.heads >= kWorth;
-    if (at == 0) A.from[A.requests] = worth;
-    for (int b = at; b < A.requests; b += step) {
-        int lo = 0, hi = A.B;                    // the last group that starts at or before b
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (A.group_cu[mid] <= b) lo = mid; else hi = mid;
-        }
-        // its prefix, if the group is computed apart, its rows are the request's too and all of the
-        // prefix lies before the request's rows
-        int from = 0;
-        if (worth && A.group_cu[lo] <= b && b < A.group_cu[lo + 1]) {
-            int r0, w, n;
-            group_shape(A, lo, &r0, &w, &n);
-            if (w > 0 && A.cu[b] >= r0 && A.cu[b] <= A.cu[b + 1] && A.cu[b + 1] <= r0 + w && A.lengths[b] >= n) from = n;
-        }
-        A.from[b] = from;
-    }
+    tiles = __reduce_add_sync(0xffffffffu, lane < kPlanWarps ? saved[lane] : 0);
+    const bool worth = orderly && static_cast<int64_t>(tiles) * A.c.heads >= kWorth;
+    if (tid == 0) A.from[A.requests] = worth;
+    for (int b = tid; !worth && b < A.requests; b += kPlanThreads) A.from[b] = 0;
 }
 
 }  // namespace
@@ -104,9 +116,8 @@ int launch_attend_shared(const AttendCall& A, const int32_t* group_cu, const int
     own.from = reinterpret_cast<int32_t*>(own.part_lse + static_cast<int64_t>(A.rows) * A.q_heads);
     AttendCall shared = own;
     shared.B = groups;
-    const int64_t items = static_cast<int64_t>(A.rows) * A.q_heads > A.B ? static_cast<int64_t>(A.rows) * A.q_heads : A.B;
-    const int64_t ctas = ceil_div(items, kPlanThreads);
-    int rc = launch_pdl("attend plan", plan_kernel, dim3(static_cast<unsigned>(ctas < 64 ? ctas : 64)),
+    const int64_t ctas = ceil_div(static_cast<int64_t>(A.rows) * A.q_heads, kPlanThreads);
+    int rc = launch_pdl("attend plan", plan_kernel, dim3(static_cast<unsigned>(ctas < 64 ? ctas : 64) + 1),
                         dim3(kPlanThreads), 0, stream, shared);
     if (rc == DSPARK_OK) rc = launch_attend_mma(own, kSuffix, stream);
     return rc == DSPARK_OK ? launch_attend_mma(shared, kPrefix, stream) : rc;

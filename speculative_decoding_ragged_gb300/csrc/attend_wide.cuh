@@ -467,7 +467,7 @@ attend_wide_kernel(const __grid_constant__ AttendCall A, const __grid_constant__
             int bad = 0, issued = 0;
             bool ok = true;
             do {
-                const int32_t* table = table_row<SEE>(A, wk.b);
+                const int32_t* table = A.c.table + static_cast<int64_t>(table_of<SEE>(wk.b, wk.from)) * A.c.width;
                 const int total_blocks = (stored_tokens<SEE>(wk.len, wk.w) + A.c.page - 1) / A.c.page;
                 const int lo = wk.first_seen(A);
                 // 32 blocks at a time, one per lane; the next 32 are fetched while these load

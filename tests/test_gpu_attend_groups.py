@@ -1,8 +1,10 @@
-"""dspark_attend_shared's groups: numbers that are no requests, whatever their size."""
+"""dspark_attend_shared's groups: numbers that are no requests, whatever their size; first members that
+have no rows, or fewer tokens than the prefix, and table rows of which nothing is said."""
 import numpy as np
 import pytest
 import torch
 
+import forms_ref
 from speculative_decoding_ragged_gb300 import _binding as bd
 from test_gpu_attend_shared import Shared
 
@@ -28,11 +30,26 @@ def alone(c):
     return out.double().cpu().numpy()
 
 
+def saved(c):
+    """Tiles of 128 tokens and a head that are not read again, over the members that have the prefix and rows."""
+    n = 0
+    for g, p in enumerate(c.prefix // c.page * c.page):
+        b = np.arange(c.group_cu[g], c.group_cu[g + 1])
+        joins = ((c.lengths[b] >= p) & (np.diff(c.cu)[b] > 0)).sum()
+        n += max(int(joins) - 1, 0) * -(-int(p) // 128) * c.heads
+    return n
+
+
 def mixed(seed, w=None, more=70):
     """Groups of 3, 2 and `more` requests; enough tiles are saved where a few of the last are left out."""
     w = [2, 3, 1, 4, 2] + [1] * more if w is None else w
     return Shared(seed, w, [30, 5, 200, 64, 0] + [i % 5 for i in range(more)],
                   [(3, 160), (2, 320), (more, 128 * 48)], 2, 4, 128, 16, heavy=False)
+
+
+def other_pages(c, b, at):
+    """Request b's entries from `at` on are other pages of the cache."""
+    c.table[b, at:] = np.random.default_rng(b).integers(0, c.n, c.table.shape[1] - at)
 
 
 @gpu
@@ -45,3 +62,56 @@ def test_numbers_that_are_no_requests(lib, numbers):
     c.prefix = np.full(len(numbers) - 1, 128, np.int32)
     out, _ = c.hold()
     np.testing.assert_array_equal(out, alone(c))
+
+
+@gpu
+@pytest.mark.parametrize("what", ["short", "empty", "retired", "several", "wrong rows"])
+def test_first_members_without_the_prefix(lib, what):
+    """A group's pages are read by a member that has them."""
+    w = [2, 3, 1, 4, 2] + [1] * 70
+    if what in ("empty", "retired"):
+        w[0] = w[3] = w[5] = 0
+    if what == "several":
+        w[6] = w[7] = 0
+    c = mixed(22, w)
+    if what == "short":                          # fewer tokens than the prefix: other pages behind them
+        c.lengths[[0, 3, 5]] = 100, 1, 40
+        for b, at in ((0, 7), (3, 1), (5, 3)):
+            other_pages(c, b, at)
+    elif what == "empty":                        # slots without tokens or pages
+        c.lengths[[0, 3, 5]] = 0
+        c.table[[0, 3, 5]] = -7
+    elif what == "retired":                      # slots whose lengths are as they were, their pages others'
+        for b in (0, 3, 5):
+            other_pages(c, b, 0)
+    elif what == "several":
+        c.lengths[5:8] = 0, 40, 100000
+        other_pages(c, 5, 1)
+        c.table[6:8] = c.n
+    else:                                        # a first member whose rows run backwards
+        c.cu[5:7] = [12, 8]                      # request 5 has none; request 6 has its row and 5's and request 4's
+        c.w[5], c.w[6] = 0, 5
+        other_pages(c, 5, 0)
+        assert saved(c) >= 6000
+        q, out, lse, st = c.go(torch.bfloat16)
+        assert st & bd.STATUS_BAD_ROWS
+        want = forms_ref.attend(c, q, c.dim ** -0.5, lambda b, pos: np.arange(pos + 1))[0]
+        np.testing.assert_allclose(out[14:82], want[14:82], atol=0.02, rtol=0.02)
+        return
+    assert saved(c) >= 6000
+    out, lse = c.hold()
+    assert not np.array_equal(out, alone(c))     # prefixes were computed apart
+
+
+@gpu
+def test_first_members_among_many(lib):
+    """More requests than threads plan them; the first that has the prefix comes late."""
+    w = [0] * 990 + [1] * 10 + [0] * 100 + [1] * 400 + [3, 0]
+    B = len(w)
+    c = Shared(23, w, [i % 3 for i in range(B)], [(1000, 64), (500, 1040), (2, 32)], 2, 2, 64, 16, heavy=False)
+    for b in np.flatnonzero(np.asarray(w) == 0):
+        c.lengths[b] = (0, 50, 100000)[b % 3]
+        c.table[b] = -7 if b % 2 else (b * 31 + np.arange(c.table.shape[1])) % c.n
+    assert saved(c) >= 6000
+    out, lse = c.hold()
+    assert not np.array_equal(out, alone(c))
