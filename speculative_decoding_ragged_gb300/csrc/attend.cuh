@@ -88,18 +88,20 @@ __device__ __forceinline__ void group_shape(const AttendCall& A, int g, int* row
     *w = r1 - r0;
 }
 // Whose table row a group's prefix is read by: its first request that has the prefix and rows. What stands
-// in the others' rows is not known (an emptied slot's may be another request's pages by now).
+// in the others' rows is not known (an emptied slot's may be another request's pages by now). -1: none has.
 __device__ __forceinline__ int group_lead(const AttendCall& A, int g)
 {
     const int b0 = A.group_cu[g], x = A.from[b0];
-    return x < 0 ? -x : b0;
+    return x < 0 ? -x : x > 0 ? b0 : -1;
 }
-// The same of a call's groups, none where it does not pay; *lead: see above.
+// The same of the groups that are computed apart: those that some request joins, none where it does not
+// pay (all of `from` is 0). *lead: see above.
 __device__ __forceinline__ void group_rows(const AttendCall& A, int g, int* row0, int* w, int* len, int* lead)
 {
     group_shape(A, g, row0, w, len);
-    if (A.from[A.requests] == 0) *w = 0;
-    if (*w > 0) *lead = group_lead(A, g);
+    if (*w <= 0) return;
+    *lead = group_lead(A, g);
+    if (*lead < 0) *w = 0;
 }
 // What a call takes as its requests; *from: the first token that is seen at all (kSuffix), the request that
 // is read (kPrefix).

@@ -39,14 +39,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttendCall A)
             A.part_lse[i] = __uint_as_float(kNoPart);
         return;
     }
-    int tiles = 0;                               // times the heads no more than the own tokens' line may have
+    int tiles = 0;                               // saved; times the heads no more than the line may have
     bool orderly = true;
     for (int g = tid; g < A.B; g += kPlanThreads) {
         const int b0 = A.group_cu[g], b1 = A.group_cu[g + 1];
         orderly = orderly && b0 >= 0 && b1 >= b0 && b1 <= A.requests && A.cu[b0] <= A.cu[b1];
-        int r0, w, n;
-        group_shape(A, g, &r0, &w, &n);
-        if (w > 0) tiles += (b1 - b0 - 1) * ((n + kTile - 1) / kTile);
     }
     int before = -1;                             // the last request of earlier rounds that joins
     for (int base = 0; base < A.requests; base += kPlanThreads) {
@@ -77,7 +74,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttendCall A)
         before = max(before, __reduce_max_sync(0xffffffffu, its));
         const uint32_t below = mask & ((1u << lane) - 1);
         if (below != 0) earlier = base + warp * 32 + 31 - __clz(below);
-        if (joins && earlier < b0 && b > b0) A.from[b0] = -b;
+        if (joins && earlier >= b0) tiles += (n + kTile - 1) / kTile;    // what it does not read again
+        else if (joins && b > b0) A.from[b0] = -b;
     }
     tiles = __reduce_add_sync(0xffffffffu, tiles);
     if (lane == 0) saved[warp] = tiles;

@@ -1,5 +1,6 @@
 """dspark_attend_shared's groups: numbers that are no requests, whatever their size; first members that
-have no rows, or fewer tokens than the prefix, and table rows of which nothing is said."""
+have no rows, or fewer tokens than the prefix, and table rows of which nothing is said; members that do
+not count."""
 import numpy as np
 import pytest
 import torch
@@ -115,3 +116,25 @@ def test_first_members_among_many(lib):
     assert saved(c) >= 6000
     out, lse = c.hold()
     assert not np.array_equal(out, alone(c))
+
+
+@gpu
+def test_a_prefix_that_no_member_has(lib):
+    """Nobody sees its pages: nothing is said of them, whatever the table holds."""
+    c = mixed(24)
+    c.lengths[:3] = 100, 0, 30
+    for b, at in ((0, 7), (1, 1), (2, 2)):
+        c.table[b, at:] = -7
+    c.lengths[3:5] = 319, 0                      # a token too few
+    c.table[4, 1:] = c.n
+    c.hold()
+
+
+@gpu
+def test_members_without_the_prefix_do_not_count(lib):
+    """Whether it pays is a matter of the members that join."""
+    c = mixed(25)
+    c.lengths[7:65] = 100
+    assert 0 < saved(c) < 6000
+    out, _ = c.hold()
+    np.testing.assert_array_equal(out, alone(c))
