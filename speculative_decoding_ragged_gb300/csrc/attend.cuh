@@ -52,8 +52,9 @@ size_t attend_shared_workspace_bytes(int rows, int q_heads, int dim, int B);
 int launch_attend(const AttendCall& A, See see, int dtype, cudaStream_t stream);
 int launch_attend_shared(const AttendCall& A, const int32_t* group_cu, const int32_t* prefix, int groups, int dtype,
                          cudaStream_t stream);
-// The tensor-core kernel: whether it serves a call, and its launch.
+// The tensor-core kernel: whether it serves a call, whether its line of tiles can hold it, and its launch.
 bool attend_mma_serves(const AttendCall& A, int dtype);
+bool attend_mma_fits(const AttendCall& A);
 int launch_attend_mma(const AttendCall& A, See see, cudaStream_t stream);
 
 // Request b's packed rows [row0, row0 + w) and its length, checked: w = 0 for one whose rows are

@@ -217,6 +217,14 @@ bool attend_mma_serves(const AttendCall& A, int dtype)
     return dtype == DSPARK_BF16 && (A.c.dim == 64 || A.c.dim == 128) && A.c.n_pages > 0;
 }
 
+// Whether a call's line fits an int, whatever the lengths.
+bool attend_mma_fits(const AttendCall& A)
+{
+    const int R = unit_rows(A), cost = R < kTile ? kUnitCost<8> : kUnitCost<kTile>;
+    const int64_t units = static_cast<int64_t>(A.rows) * A.q_heads / R + static_cast<int64_t>(A.B) * A.c.heads;
+    return units * (A.last_tile + 1 + cost) <= INT32_MAX / 2;
+}
+
 size_t attend_workspace_bytes(int dim)
 {
     if (dim != 64 && dim != 128) return 16;
@@ -227,13 +235,8 @@ namespace {
 template <int SEE>
 int launch_both(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 {
-    // By the requests' average of (position, head) rows: up to 32 the narrow kernel (64 requests over
-    // 2048 tokens, 8 heads of 128: at 16 rows 74 us, wide 120; at 32 87 and 126), where it takes one
-    // unit per request and head. From 33 on, two units and more, wide (48 rows: 138 and 131; 256 requests
-    // over 512: 206 and 175; 128 rows: 248 and 155).
-    const bool narrow = static_cast<int64_t>(A.rows) * A.group <= 32ll * A.B;
-    const int rc = narrow ? launch_attend_narrow<SEE>(A, ctas, device, stream)
-                          : launch_attend_wide<SEE>(A, ctas, device, stream);
+    const int rc = unit_rows(A) < kTile ? launch_attend_narrow<SEE>(A, ctas, device, stream)
+                                        : launch_attend_wide<SEE>(A, ctas, device, stream);
     if (rc != DSPARK_OK) return rc;
     return launch_pdl("attend join", A.c.dim == 128 ? attend_join_kernel<128, SEE> : attend_join_kernel<64, SEE>,
                       dim3(ctas), dim3(kJoinWarps * 32), 0, stream, A);
@@ -242,6 +245,8 @@ int launch_both(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 
 int launch_attend_mma(const AttendCall& A, See see, cudaStream_t stream)
 {
+    if (!attend_mma_fits(A))
+        return fail(DSPARK_ERR_UNSUPPORTED, "dspark_attend: rows, heads and pages beyond what one call can cut");
     DeviceInfo dev;
     const int rc = current_device(&dev);
     if (rc != DSPARK_OK) return rc;

@@ -348,7 +348,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 // A unit of n tiles takes kUnitCost + n places on the line: starting and finishing a unit costs a
 // CTA about as much as that many tiles, and runs of equal length should take equal time. Tile k is
 // at place kUnitCost + k of its unit. Run i holds the places [i * run, (i + 1) * run). The host
-// makes sure that a line's length fits an int (places_fit).
+// makes sure that a line's length fits an int (attend_mma_fits).
 template <int R>
 constexpr int kUnitCost = R < kTile ? 4 : 6;
 
@@ -424,12 +424,15 @@ __device__ __forceinline__ int head_places(const AttendCall& A, int w, int len, 
     }
     return n;
 }
-// Whether a call's line fits an int, whatever the lengths.
-template <int R>
-inline bool places_fit(const AttendCall& A)
+// Rows per unit: 8, 16 or 32 for the narrow kernel, kTile for the wide one. By the requests' average of
+// (position, head) rows: what a call's windows are is known on the device only, and a longer one is several
+// units. Up to 32 the narrow kernel (64 requests over 2048 tokens, 8 heads of 128: at 16 rows 74 us, wide 120;
+// at 32 87 and 126), where it takes one unit per request and head. From 33 on, two units and more, wide (48
+// rows: 138 and 131; 256 requests over 512: 206 and 175; 128 rows: 248 and 155).
+inline int unit_rows(const AttendCall& A)
 {
-    const int64_t units = (static_cast<int64_t>(A.rows) * A.q_heads) / R + static_cast<int64_t>(A.B) * A.c.heads;
-    return units * (A.last_tile + 1 + kUnitCost<R>) <= INT32_MAX / 2;
+    const int64_t rows = static_cast<int64_t>(A.rows) * A.group;
+    return rows <= 8ll * A.B ? 8 : rows <= 16ll * A.B ? 16 : rows <= 32ll * A.B ? 32 : kTile;
 }
 
 // The units of one run in order.
@@ -579,7 +582,7 @@ __device__ __forceinline__ void find_start(const AttendCall& A, Walk<R, SEE>& k,
     }
 }
 // Requests whose rows run backwards let the others' overlap, so that they may be more than the packed rows
-// and their line longer than an int, which places_fit counts on: such a call has no line (fp32 sums:
+// and their line longer than an int, which attend_mma_fits counts on: such a call has no line (fp32 sums:
 // the line is refused from 2^30 places on, and an int ends at 2^31). `size`: a thread's places.
 template <int NT>
 static __device__ __noinline__ bool line_fits(float size, int* scan)

@@ -935,8 +935,6 @@ int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
         }
         ready_device = device;
     }
-    if (!places_fit<R>(A))
-        return fail(DSPARK_ERR_UNSUPPORTED, "dspark_attend: rows, heads and pages beyond what one call can cut");
     CUtensorMap k_map, v_map;
     int rc = encode_cache(&k_map, A.c.k, A.c);
     if (rc == DSPARK_OK) rc = encode_cache(&v_map, A.c.v, A.c);
@@ -950,16 +948,14 @@ int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 template <int SEE>
 int launch_attend_narrow(const AttendCall& A, int ctas, int device, cudaStream_t stream)
 {
-    // Rows per unit by the requests' average: what a call's windows are is known on the device only,
-    // and a longer one is several units.
-    const int64_t rows = static_cast<int64_t>(A.rows) * A.group;
+    const int rows = unit_rows(A);
     if (A.c.dim == 128)
-        return rows <= 8ll * A.B ? launch<128, 8, SEE>(A, ctas, device, stream)
-             : rows <= 16ll * A.B ? launch<128, 16, SEE>(A, ctas, device, stream)
-                                  : launch<128, 32, SEE>(A, ctas, device, stream);
-    return rows <= 8ll * A.B ? launch<64, 8, SEE>(A, ctas, device, stream)
-         : rows <= 16ll * A.B ? launch<64, 16, SEE>(A, ctas, device, stream)
-                              : launch<64, 32, SEE>(A, ctas, device, stream);
+        return rows == 8 ? launch<128, 8, SEE>(A, ctas, device, stream)
+             : rows == 16 ? launch<128, 16, SEE>(A, ctas, device, stream)
+                          : launch<128, 32, SEE>(A, ctas, device, stream);
+    return rows == 8 ? launch<64, 8, SEE>(A, ctas, device, stream)
+         : rows == 16 ? launch<64, 16, SEE>(A, ctas, device, stream)
+                      : launch<64, 32, SEE>(A, ctas, device, stream);
 }
 
 }  // namespace dspark

@@ -99,12 +99,12 @@ size_t attend_shared_workspace_bytes(int rows, int q_heads, int dim, int B)
 
 // Types and head sizes of the fp32 kernel have no such form: it attends over the whole contexts. So do
 // calls whose page tables are too small for any prefix to be worth computing apart (4 windows of 4 rows
-// behind 1000 tokens: 14 us alone, 33 apart, 21 with a plan that says so).
+// behind 1000 tokens: 14 us alone, 33 apart, 21 with a plan that says so), and calls with so many groups
+// that the prefixes' line could not hold them. All of that is known before anything is enqueued.
 int launch_attend_shared(const AttendCall& A, const int32_t* group_cu, const int32_t* prefix, int groups, int dtype,
                          cudaStream_t stream)
 {
     const int64_t most = (A.B - 1ll) * ((A.reach + kTile - 1ll) / kTile) * A.c.heads;
-    if (groups == 0 || most < kWorth || !attend_mma_serves(A, dtype)) return launch_attend(A, kAll, dtype, stream);
     AttendCall own = A;
     own.requests = A.B;
     own.group_cu = group_cu;
@@ -114,6 +114,8 @@ int launch_attend_shared(const AttendCall& A, const int32_t* group_cu, const int
     own.from = reinterpret_cast<int32_t*>(own.part_lse + static_cast<int64_t>(A.rows) * A.q_heads);
     AttendCall shared = own;
     shared.B = groups;
+    if (groups == 0 || most < kWorth || !attend_mma_serves(A, dtype) || !attend_mma_fits(own) || !attend_mma_fits(shared))
+        return launch_attend(A, kAll, dtype, stream);
     const int64_t ctas = ceil_div(static_cast<int64_t>(A.rows) * A.q_heads, kPlanThreads);
     int rc = launch_pdl("attend plan", plan_kernel, dim3(static_cast<unsigned>(ctas < 64 ? ctas : 64) + 1),
                         dim3(kPlanThreads), 0, stream, shared);

@@ -705,8 +705,6 @@ int launch(const AttendCall& A, int ctas, int device, cudaStream_t stream)
         }
         ready_device = device;
     }
-    if (!places_fit<kRows>(A))
-        return fail(DSPARK_ERR_UNSUPPORTED, "dspark_attend: rows, heads and pages beyond what one call can cut");
     CUtensorMap k_map, v_map;
     int rc = encode_cache(&k_map, A.c.k, A.c);
     if (rc == DSPARK_OK) rc = encode_cache(&v_map, A.c.v, A.c);

@@ -1,6 +1,6 @@
 """dspark_attend_shared's groups: numbers that are no requests, whatever their size; first members that
 have no rows, or fewer tokens than the prefix, and table rows of which nothing is said; members that do
-not count."""
+not count; far more groups than requests."""
 import numpy as np
 import pytest
 import torch
@@ -138,3 +138,19 @@ def test_members_without_the_prefix_do_not_count(lib):
     assert 0 < saved(c) < 6000
     out, _ = c.hold()
     np.testing.assert_array_equal(out, alone(c))
+
+
+@gpu
+def test_far_more_groups_than_requests(lib):
+    """Empty groups, so many that the prefixes' line is longer than a call can cut: as dspark_attend."""
+    c = mixed(26)
+    n = 10_000_000
+    tiles = -(-c.table.shape[1] * c.page // 128)
+    assert n * c.heads * (tiles + 4) > 1 << 30
+    c.group_cu = np.concatenate([np.zeros(n, np.int32), c.group_cu])
+    c.prefix = np.concatenate([np.full(n, 128, np.int32), c.prefix])
+    out, _ = c.hold()
+    np.testing.assert_array_equal(out, alone(c))
+    c.group_cu, c.prefix = c.group_cu[n - 100:], c.prefix[n - 100:]         # a hundred of them
+    out, _ = c.hold()
+    assert not np.array_equal(out, alone(c))
