@@ -97,9 +97,10 @@ class CachedAttention:
 
 
 class DecodeLoop:
-    """`prompt` tokens (whole pages) stand before every request's own, in the same pages; `repetition`,
-    `presence`, `frequency` (one number for all requests) and `mask` (a grammar's allowed tokens, [words]
-    int32, for every row) are dspark_adjust's."""
+    """`prompt` tokens (whole pages; self.prompt) stand before every request's own, in the same pages;
+    `repetition`, `presence`, `frequency` (one number for all requests) and `mask` (a grammar's allowed
+    tokens, [words] int32, for every row) are dspark_adjust's. A loop that adjusts keeps whole histories in
+    step.out_tokens: the prompt, the first anchor, then what is committed; any other what is committed."""
 
     def __init__(self, B: int, gamma: int, V: int, *, width: int = 256, q_heads: int = 8,
                  kv_heads: int = 2, dim: int = 64, page: int = 16, max_len: int = 512,
@@ -131,22 +132,29 @@ class DecodeLoop:
         shared = (torch.tensor([0, B], **i32), torch.tensor([prompt], **i32)) if prompt else None
         self.rope = bd.Rope.make(dim, device=dev)
         tiers = sorted({B, B * (gamma + 1) // 2, B * gamma})
+        adjusts = (repetition, presence, frequency) != (1.0, 0.0, 0.0) or mask is not None
+        before = prompt + 1 if adjusts else 0                # tokens of a history that no step commits
         self.step = DSparkStep(B, gamma, V, tiers, 1.0, 1e-3 * np.arange(B + 1),
-                               1e-3 * np.arange(B * gamma + 1), out_cap=max_len, device=dev)
+                               1e-3 * np.arange(B * gamma + 1), out_cap=before + max_len, device=dev)
         self.attention = CachedAttention(self.step.packed_cap, q_heads, kv_heads, dim, table,
                                          B * blocks + front.numel(), page, self.rope, window=window,
                                          sinks=sinks, shared=shared)
         self.lengths = torch.full((B,), prompt, **i32)
         self.anchor = torch.randint(V, (B,), generator=gen, dtype=torch.int32).to(dev)
         self.slots = torch.arange(gamma, **i32)
+        self.prompt = torch.randint(V, (prompt,), generator=gen).to(dev)
         if prompt:
-            self.fill(torch.randint(V, (prompt,), generator=gen).to(dev))
+            self.fill(self.prompt)
         self.how = None
-        if (repetition, presence, frequency) != (1.0, 0.0, 0.0) or mask is not None:
+        if adjusts:
+            self.step.out_tokens[:, :prompt] = self.prompt
+            self.step.out_tokens[:, prompt] = self.anchor
+            self.step.out_len.fill_(before)
             each = lambda x: torch.full((B,), x, dtype=torch.float32, device=dev)    # noqa: E731
             rows = torch.zeros(self.step.packed_cap, **i32) if mask is not None else None
             self.how = bd.Adjustments(
-                history=self.step.out_tokens, history_len=self.step.out_len, repetition=each(repetition),
+                history=self.step.out_tokens, history_len=self.step.out_len,
+                prompt_len=torch.full((B,), prompt, **i32), repetition=each(repetition),
                 presence=each(presence), frequency=each(frequency),
                 mask=mask[None] if mask is not None else None, mask_row=rows)
 
