@@ -622,7 +622,8 @@ size_t dspark_attend_shared_workspace_bytes(int rows, int q_heads, int heads, in
  * out = logits, for each token v of the row in fp32 and in this order:
  *   seen(v):     x = x / repetition[b] where x > 0, else x * repetition[b]
  *   c(v) > 0:    x = x - (frequency[b] * c(v) + presence[b])
- *   a bias:      x = x + bias_values[b, j], j the last of the request's biases for v
+ *   a bias:      x = x + bias_values[b, j], j the last of the request's biases for v;
+ *                where that is -inf x = -inf, whatever it was (NaN too): the token is banned
  *   not allowed: x = -inf, whatever it was (NaN too)
  * and one rounding to the type of out. Logits that nothing applies to keep their bits. Each part is
  * left out where its arrays are NULL (repetition NULL: 1; presence, frequency NULL: 0; prompt_len
@@ -630,7 +631,7 @@ size_t dspark_attend_shared_workspace_bytes(int rows, int q_heads, int heads, in
  *   history [B, history_cap] int32, history_len [B], prompt_len [B] int32: histories as
  *       dspark_scatter keeps them (the prompt's tokens first)
  *   repetition, presence, frequency [B] fp32
- *   bias_tokens [B, bias_cap] int32, bias_values [B, bias_cap] fp32, bias_len [B] int32; -inf bans
+ *   bias_tokens [B, bias_cap] int32, bias_values [B, bias_cap] fp32, bias_len [B] int32
  *   mask [mask_rows, mask_stride] 32-bit words, bit v % 32 of word v / 32: token v is allowed
  *       (bits past V do not matter); row r goes by mask row mask_row[r] (-1: none), or by mask row r
  *       where mask_row is NULL. Rows may share mask rows.

@@ -368,7 +368,7 @@ adjust_kernel(const __grid_constant__ AdjustCall A)
                 const float add = entry ? bias[entry - 1] : 0.0f;
                 if ((its[e] & kPrompt) | uses[e]) z = z > 0.0f ? z / rep : z * rep;
                 if (uses[e]) z -= fmaf(frequency, static_cast<float>(uses[e]), presence);
-                if (entry) z += add;
+                if (entry) z = add == -INFINITY ? add : z + add;     // a ban holds for +inf and NaN too
                 y[t[e]] = E::down(z);
             }
         }
