@@ -1,6 +1,6 @@
 """dspark_attend_shared's groups: numbers that are no requests, whatever their size; first members that
 have no rows, or fewer tokens than the prefix, and table rows of which nothing is said; members that do
-not count; far more groups than requests."""
+not count; far more groups than requests; every kernel that the prefixes and the own tokens can take."""
 import numpy as np
 import pytest
 import torch
@@ -154,3 +154,40 @@ def test_far_more_groups_than_requests(lib):
     c.group_cu, c.prefix = c.group_cu[n - 100:], c.prefix[n - 100:]         # a hundred of them
     out, _ = c.hold()
     assert not np.array_equal(out, alone(c))
+
+
+def unit_rows(rows, group, n):
+    """The kernel that n requests (or groups) of together `rows` rows and a cache head's `group` query heads take:
+    the narrow one of 8, 16 or 32 rows a unit, the wide one of 128."""
+    return next((r for r in (8, 16, 32) if rows * group <= r * n), 128)
+
+
+def many(n, size, w, group, heads, dim, page, prefix, seed):
+    """n groups of about `size` requests with windows of about w."""
+    rng = np.random.default_rng(seed)
+    sizes = size + rng.integers(-1, 2, n)
+    ws = np.maximum(w + rng.integers(-1, 1, sizes.sum()) * (rng.random(sizes.sum()) < 0.3), 1)
+    own = rng.integers(0, 40, sizes.sum()) * (rng.random(sizes.sum()) < 0.5)
+    return Shared(seed, ws, own, [(int(s), prefix) for s in sizes], heads, group, dim, page, heavy=False)
+
+
+# n, size, w, group, heads, dim, page, prefix; the rows of a prefix's units and of an own unit
+KERNELS = [((30, 6, 1, 1, 8, 128, 16, 720), 8, 8), ((30, 6, 2, 1, 8, 128, 32, 704), 16, 8),
+           ((30, 6, 2, 2, 8, 128, 16, 720), 32, 8), ((32, 6, 1, 1, 8, 64, 16, 656), 8, 8),
+           ((32, 6, 2, 1, 8, 64, 64, 704), 16, 8), ((40, 5, 3, 2, 8, 64, 16, 592), 32, 8),
+           ((160, 6, 1, 1, 8, 128, 64, 128), 8, 8), ((160, 6, 2, 2, 8, 64, 16, 112), 32, 8),
+           ((260, 3, 1, 2, 8, 64, 32, 192), 8, 8),
+           ((2, 10, 8, 3, 2, 128, 64, 21760), 128, 32), ((2, 16, 12, 4, 2, 64, 64, 13952), 128, 128),
+           ((3, 12, 6, 4, 2, 64, 16, 13040), 128, 32)]
+
+
+@gpu
+@pytest.mark.parametrize("shape,prefix_rows,own_rows", KERNELS)
+def test_every_kernel(lib, shape, prefix_rows, own_rows):
+    c = many(*shape, seed=sum(shape))
+    assert unit_rows(c.rows, shape[3], len(c.prefix)) == prefix_rows
+    assert unit_rows(c.rows, shape[3], len(c.lengths)) == own_rows
+    assert saved(c) >= 6000
+    out, _ = c.hold()
+    assert not np.array_equal(out, alone(c))
+    np.testing.assert_array_equal(c.go(torch.bfloat16, lse=False, fill=0xFF)[1], out)
