@@ -1,9 +1,11 @@
-"""dspark_adjust: a bias of -inf bans its token whatever the logit is."""
+"""dspark_adjust: a bias of -inf bans its token whatever the logit is, and rows that are left without a
+token through verify, greedy and stochastic."""
 import numpy as np
 import pytest
 import torch
 
 from speculative_decoding_ragged_gb300 import _binding as bd
+from speculative_decoding_ragged_gb300.decode import DecodeLoop
 
 from gpu_util import device
 
@@ -49,6 +51,34 @@ def test_a_bias_of_minus_infinity_bans(dtype, in_place, masked):
         assert (np.isnan(got[rows][:, rest]) == np.isnan(want)).all()
         fine = np.isfinite(want)
         # one sum in fp32 and one rounding to the type
-        err = np.abs(got[rows][:, rest] - want)[fine]
+        err = np.abs(got[rows][:, rest][fine] - want[fine])
         assert (err <= (2.0 ** -24 + torch.finfo(dtype).eps / 2) * (np.abs(want[fine]) + 4)).all()
     assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("stochastic", [False, True])
+@pytest.mark.parametrize("V", [64, 700])
+def test_rows_without_a_token(stochastic, V):
+    """A grammar that allows nothing is flagged, and what verify commits is a token of the vocabulary all
+    the same: the first one where it is greedy."""
+    dev = device()
+    loop = DecodeLoop(4, 3, V, mask=torch.zeros(-(-V // 32), dtype=torch.int32, device=dev), device=dev)
+    step = loop.step
+    step.stochastic = stochastic
+    step.workspace = torch.zeros(bd.dspark_verify_workspace_bytes(4, 3, V, stochastic), dtype=torch.uint8, device=dev)
+    draft = torch.zeros(4, 2, V, dtype=torch.bfloat16, device=dev) if stochastic else None
+    for k in range(3):
+        tokens, conf = loop.draft()
+        step.schedule_pack(conf, tokens)
+        logits = loop.target()
+        step.adjust(logits, tokens, loop.how)
+        M = int(step.cu[-1])
+        assert bool(torch.isneginf(logits[:M]).all())
+        step.verify_scatter(logits, tokens, draft, seed=5, step=k)
+        L, committed = step.accept_len.tolist(), step.committed.tolist()
+        for n, row in zip(L, committed):
+            assert 1 <= n <= 3 and all(0 <= t < V for t in row[:n]) and row[n:] == [-1] * (3 - n)
+            if not stochastic:
+                assert row[:n] == [0] * n
+        loop.advance()
+    assert int(step.status.item()) == bd.STATUS_NO_TOKEN
