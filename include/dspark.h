@@ -627,7 +627,8 @@ size_t dspark_attend_shared_workspace_bytes(int rows, int q_heads, int heads, in
  *   not allowed: x = -inf, whatever it was (NaN too)
  * and one rounding to the type of out. Logits that nothing applies to keep their bits. Each part is
  * left out where its arrays are NULL (repetition NULL: 1; presence, frequency NULL: 0; prompt_len
- * NULL: 0; history NULL: the drafts alone). A request with neutral penalties has its history not read.
+ * NULL: 0; history NULL: the drafts alone). A request with neutral penalties may
+ * have anything in its history.
  *   history [B, history_cap] int32, history_len [B], prompt_len [B] int32: histories as
  *       dspark_scatter keeps them (the prompt's tokens first)
  *   repetition, presence, frequency [B] fp32

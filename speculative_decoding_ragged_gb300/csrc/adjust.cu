@@ -10,11 +10,12 @@
 // last one counts.
 //
 // Bound by HBM: a row is read and written once. 256 windows of 1 to 8 rows over 151936 tokens in bf16: a copy
-// takes 105 us, with drafts 106, with 150 biases a request too 111, with histories of 64 to 4096 tokens 124
+// takes 105 us, with drafts 106, with 150 biases a request too 111, with histories of 64 to 4096 tokens 123-126
 // (5.6 TB/s). What the histories add is the adjusting of the listed tokens (a warp's instructions, whose
 // logits come from L1 or L2) and the counting's round trips; the first of each array is therefore fetched
 // before its length is known, and the counting runs under the warps' first loads. 320 rows under grammars:
-// 28.8 us, 7 TB/s of the bytes counted with every logit read; parts that are forbidden whole are not. One
+// 28.8 us, 7 TB/s of the bytes counted with every logit read; parts that are forbidden whole are not (4.6 TB/s
+// of what must move). In place, where what changes is written only, 77 and 24 us. One
 // window of 8 rows: 5.0 us, launch and three dependent loads.
 // Tried and slower for the 256 windows: four warps that count for eight that stream in a persistent grid
 // (187 to 295 us: what waits for the counts then reads back what was written), the rows through shared

@@ -5,8 +5,8 @@
 // rows, and leave each row's quotient and log2 sum in the workspace; the prefixes follow, group by group
 // in units of up to 128 rows of any of its requests, and join. So the join is paid by the kernel with
 // few, long units, whose parts are joined from the workspace anyway: with the own tokens last, each of
-// their many short units waited for 16 KB of the prefix's results (256 windows of 1 to 8 rows: 136 us
-// for 72).
+// their many short units waited for 16 KB of the prefix's results (own tokens of 256 windows of 1 to 8 rows:
+// 136 us, now 78).
 #include "attend_mma.cuh"
 
 namespace dspark {
@@ -15,7 +15,7 @@ namespace {
 // A prefix computed apart costs a kernel's start and its join, about 25 us; a tile of 128 tokens and a
 // head that is not read again saves about 4 ns (2500 cycles on 304 CTAs). 84 answers in 12 groups behind
 // 300 to 5000 tokens, 3800 tiles saved: 40 us alone, 47 apart; 192 single tokens behind 16384, 195 thousand
-// tiles: 573 and 130.
+// tiles: 573 and 125.
 constexpr int64_t kWorth = 6000;
 
 // Whether the groups' prefixes are worth it; every request's first own token, and whose pages are read for
